@@ -1,0 +1,160 @@
+// act8.cu -- activation checkpoints in 8 bits: int8 codes with a power-of-two scale for each
+// 128 elements of a row (include/mcemu_ops.h).
+//
+// Bound by HBM: 3 bytes an element from bf16.  The scale is a power of two so that a code
+// times its scale has seven significant bits and is exact in bfloat16: the weight
+// gradient's matrix operand needs no second rounding.
+#include "ops_common.cuh"
+
+namespace mcemu {
+namespace {
+
+constexpr int kBlock = MCEMU_ACT8_BLOCK;
+
+// Largest exponent of a type: 127 * 2^e is finite in it.
+template <class T> constexpr int kTopExp = 121;
+template <> constexpr int kTopExp<__half> = 9;
+
+// The least e >= -120 with amax <= 127 * 2^e, at most `top`; MCEMU_ACT8_NAN for a NaN or an
+// infinity; -7 for a block of zeros.  amax = m * 2^(x - 127) with m in [1, 2) gives
+// e = x - 127 - 6, one more when m > 127/64.
+__device__ __forceinline__ int exponent_of(float amax, int top) {
+  const uint32_t u = __float_as_uint(amax) & 0x7FFFFFFFu;
+  if (u >= 0x7F800000u) return MCEMU_ACT8_NAN;
+  if (u == 0) return -7;
+  const int e = (int)(u >> 23) - 133 + ((u & 0x7FFFFFu) > 0x7E0000u);
+  return e < -120 ? -120 : e > top ? top : e;
+}
+__device__ __forceinline__ int8_t code_of(float x, float inv) {
+  return (int8_t)max(-127, min(127, __float2int_rn(x * inv)));
+}
+// 2^-e for e in [-120, 121]; 0 for a block that is not finite, whose codes do not matter.
+__device__ __forceinline__ float inverse_of(int e) {
+  return e == MCEMU_ACT8_NAN ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// One warp to 32 * VEC consecutive elements of a row (VEC 8: two blocks, VEC 4: one), so
+// that 128 / VEC lanes share a block.
+template <class T, int VEC>
+__global__ void __launch_bounds__(256) compress_kernel(int64_t tasks, int per_row, int H, const T *__restrict__ x,
+                                                       int64_t ldx, int8_t *__restrict__ q, int64_t ldq,
+                                                       int8_t *__restrict__ e, int64_t lde) {
+  const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (task >= tasks) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = task / per_row;
+  const int i = ((int)(task - row * per_row) * 32 + lane) * VEC;
+  const bool in = i < H;
+  Vec<T, VEC> v;
+  float amax = 0.f;
+  if (in) {
+    v = load_vec<T, VEC>(x + row * ldx + i);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) amax = max_nan(amax, fabsf(to_f(v.v[j])));
+  }
+#pragma unroll
+  for (int o = kBlock / VEC / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  if (!in) return;
+  const int ex = exponent_of(amax, kTopExp<T>);
+  const float inv = inverse_of(ex);
+  Vec<int8_t, VEC> o;
+#pragma unroll
+  for (int j = 0; j < VEC; j++) o.v[j] = code_of(to_f(v.v[j]), inv);
+  store_vec(q + row * ldq + i, o);
+  if (i % kBlock == 0) e[row * lde + i / kBlock] = (int8_t)ex;
+}
+
+// Rows that no vector fits: a warp to a block, element by element.
+template <class T>
+__global__ void __launch_bounds__(256) compress_any_kernel(int64_t tasks, int per_row, int H, const T *__restrict__ x,
+                                                           int64_t ldx, int8_t *__restrict__ q, int64_t ldq,
+                                                           int8_t *__restrict__ e, int64_t lde) {
+  const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (task >= tasks) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = task / per_row;
+  const int b = (int)(task - row * per_row);
+  float v[4], amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const int i = b * kBlock + j * 32 + lane;
+    v[j] = i < H ? to_f(x[row * ldx + i]) : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; j++) amax = max_nan(amax, fabsf(v[j]));
+  amax = warp_max(amax);
+  const int ex = exponent_of(amax, kTopExp<T>);
+  const float inv = inverse_of(ex);
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const int i = b * kBlock + j * 32 + lane;
+    if (i < H) q[row * ldq + i] = code_of(v[j], inv);
+  }
+  if (lane == 0) e[row * lde + b] = (int8_t)ex;
+}
+
+template <class T, int VEC>
+__global__ void __launch_bounds__(256) expand_kernel(int64_t tasks, int per_row, const int8_t *__restrict__ q,
+                                                     int64_t ldq, const int8_t *__restrict__ e, int64_t lde,
+                                                     T *__restrict__ x, int64_t ldx) {
+  const int64_t task = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (task >= tasks) return;
+  const int64_t row = task / per_row;
+  const int i = (int)(task - row * per_row) * VEC;
+  const Vec<int8_t, VEC> v = load_vec<int8_t, VEC>(q + row * ldq + i);
+  const float s = act8_scale(e[row * lde + i / kBlock]);
+  Vec<T, VEC> o;
+#pragma unroll
+  for (int j = 0; j < VEC; j++) o.v[j] = from_f<T>((float)v.v[j] * s);
+  store_vec(x + row * ldx + i, o);
+}
+
+unsigned blocks_for(int64_t threads) { return (unsigned)((threads + 255) / 256); }
+
+template <class T>
+int compress_typed(int T_, int H, const void *x, int64_t ldx, int8_t *q, int64_t ldq, int8_t *e, int64_t lde,
+                   cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  if (H % V == 0 && rows16(x, ldx, sizeof(T)) && rows_on(q, ldq, 1, V)) {
+    const int per_row = (H + 32 * V - 1) / (32 * V);
+    const int64_t tasks = (int64_t)T_ * per_row;
+    compress_kernel<T, V><<<blocks_for(tasks * 32), 256, 0, st>>>(tasks, per_row, H, (const T *)x, ldx, q, ldq, e, lde);
+  } else {
+    const int per_row = (H + kBlock - 1) / kBlock;
+    const int64_t tasks = (int64_t)T_ * per_row;
+    compress_any_kernel<T><<<blocks_for(tasks * 32), 256, 0, st>>>(tasks, per_row, H, (const T *)x, ldx, q, ldq, e, lde);
+  }
+  return launch_status();
+}
+
+template <class T>
+int expand_typed(int T_, int H, const int8_t *q, int64_t ldq, const int8_t *e, int64_t lde, void *x, int64_t ldx,
+                 cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const bool wide = H % V == 0 && rows16(x, ldx, sizeof(T)) && rows_on(q, ldq, 1, V);
+  const int per_row = wide ? H / V : H;
+  const int64_t tasks = (int64_t)T_ * per_row;
+  if (wide) expand_kernel<T, V><<<blocks_for(tasks), 256, 0, st>>>(tasks, per_row, q, ldq, e, lde, (T *)x, ldx);
+  else expand_kernel<T, 1><<<blocks_for(tasks), 256, 0, st>>>(tasks, per_row, q, ldq, e, lde, (T *)x, ldx);
+  return launch_status();
+}
+
+}  // namespace
+
+int launch_act8_compress(int fmt, int T, int H, const void *x, int64_t ldx, int8_t *q, int64_t ldq, int8_t *e,
+                         int64_t lde, void *stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  return fmt == MCEMU_FP32   ? compress_typed<float>(T, H, x, ldx, q, ldq, e, lde, st)
+         : fmt == MCEMU_FP16 ? compress_typed<__half>(T, H, x, ldx, q, ldq, e, lde, st)
+                             : compress_typed<__nv_bfloat16>(T, H, x, ldx, q, ldq, e, lde, st);
+}
+
+int launch_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t ldq, const int8_t *e, int64_t lde, void *x,
+                       int64_t ldx, void *stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  return fmt == MCEMU_FP32   ? expand_typed<float>(T, H, q, ldq, e, lde, x, ldx, st)
+         : fmt == MCEMU_FP16 ? expand_typed<__half>(T, H, q, ldq, e, lde, x, ldx, st)
+                             : expand_typed<__nv_bfloat16>(T, H, q, ldq, e, lde, x, ldx, st);
+}
+
+}  // namespace mcemu
