@@ -1,21 +1,312 @@
 // int8_linear.cu -- product of 8-bit integers with a scale for each token and channel
 // (include/mcemu_ops.h has the formula).
+//
+// sm_103a has no fast 8-bit integer matrix instruction, so the sums run on the 16-bit floating
+// one, exactly: an 8-bit integer is a binary16 number, a product is below 2^14 + 1, and a sum
+// of 1024 products is an integer of at most 2^24, which fp32 accumulators hold without
+// rounding (every partial sum too, in any order).  Every 1024 products the accumulators are
+// therefore taken out of tensor memory and added to int32 sums in registers.
 #include "ops_common.cuh"
+#include "tc.cuh"
 
 namespace mcemu {
 namespace {
 
-__device__ __forceinline__ void put_y(const LinearArgs &a, int m, int n, int acc) {
+__device__ __forceinline__ void put_y(const LinearArgs &a, int m, int n, int acc, float sw, float bias) {
   const int64_t at = (int64_t)m * a.ldy + n;
   if (a.out_fmt == MCEMU_INT32) {
     ((int32_t *)a.y)[at] = acc;
     return;
   }
-  float v = __fmul_rn(__fmul_rn((float)acc, a.sx[m]), a.sw[n]);
-  if (a.bias) v = __fadd_rn(v, a.bias[n]);
+  float v = __fmul_rn(__fmul_rn((float)acc, a.sx[m]), sw);
+  if (a.bias) v = __fadd_rn(v, bias);
   if (a.out_fmt == MCEMU_FP32) ((float *)a.y)[at] = v;
   else if (a.out_fmt == MCEMU_FP16) ((__half *)a.y)[at] = __float2half_rn(v);
   else ((__nv_bfloat16 *)a.y)[at] = __float2bfloat16_rn(v);
+}
+
+// Sixteen tokens of one channel.
+__device__ __forceinline__ void put_y16(const LinearArgs &a, int m0, int n, const int *acc, float sw, float bias) {
+#pragma unroll
+  for (int x = 0; x < 16; x++)
+    if (m0 + x < a.M) put_y(a, m0 + x, n, acc[x], sw, bias);
+}
+
+// Four signed bytes to four binary16 numbers, exactly: b + 128 in the low mantissa bits of
+// 1024, less 1152.
+__device__ __forceinline__ void half4(uint32_t b, uint32_t &lo, uint32_t &hi) {
+  b ^= 0x80808080u;
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+  uint32_t l = __byte_perm(b, 0x64646464u, 0x4140), h = __byte_perm(b, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*(__half2 *)&l, off), y = __hsub2(*(__half2 *)&h, off);
+  lo = *(const uint32_t *)&x;
+  hi = *(const uint32_t *)&y;
+}
+
+// ---------------------------------------------------------------------------
+// Matrix kernel.  A tile is 128 channels a CTA (operand A) by BN tokens (operand B, split
+// between the CTAs of a pair); CG CTAs work on CG * 128 channels.  Eight worker warps read
+// both operands 64 k at a time, widen them to binary16 and store them in the swizzle; one
+// thread issues the matrix instructions; the workers take the accumulators out, one half of
+// the columns to each four warps, and write the tile.  Two sets of accumulators let the
+// matrix unit run on meanwhile.
+// ---------------------------------------------------------------------------
+constexpr int kStage = 64;                    // k of a stage: one 128-byte swizzle row
+constexpr int kChunk = 1024 / kStage;         // stages between two transfers to int32
+constexpr int kWorkers = 256;
+
+template <int CG, int BN>
+struct Shape {
+  static constexpr int kRowsB = BN / CG;                        // token rows this CTA stages
+  static constexpr int kRows = 128 + kRowsB;
+  static constexpr int kBytes = kRows * 128;                    // of one stage
+  static constexpr int kStages = kBytes >= 32768 ? 5 : kBytes >= 24576 ? 6 : 8;
+  static constexpr int kLoads = kRows * 4 / kWorkers;           // 16-byte pieces of a stage per worker
+  static constexpr bool kMove = BN >= 128;                      // registers move to the workers
+  static constexpr int kThreads = kMove ? 384 : kWorkers + 32;
+  static constexpr int kSmem = kStages * kBytes + 1024 + 256;
+};
+
+struct MatArgs {
+  LinearArgs a;
+  int tiles_n, tiles_m;      // tiles over channels and tokens
+};
+
+template <int CG, int BN>
+__global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(const MatArgs g) {
+  using S = Shape<CG, BN>;
+  static_assert(S::kLoads * kWorkers == S::kRows * 4, "whole pieces per worker");
+  extern __shared__ uint8_t raw[];
+  const LinearArgs &a = g.a;
+  const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t bars = base + S::kStages * S::kBytes;
+  const uint32_t full = bars, empty = full + 8 * S::kStages, acc_full = empty + 8 * S::kStages,
+                 acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0 : tc::cta_rank();
+  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; s++) {
+      tc::mbar_init(full + 8 * s, 8 * CG);
+      tc::mbar_init(empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; s++) {
+      tc::mbar_init(acc_full + 8 * s, 1);
+      tc::mbar_init(acc_empty + 8 * s, 8 * CG);
+    }
+    tc::mbar_init(drain, 1);
+    tc::mbar_init_fence();
+  }
+  if (warp == 8) tc::tmem_alloc<CG>(slot, 512);
+  tc::fence_before();
+  if constexpr (CG == 1) __syncthreads();
+  else tc::cluster_sync();
+  tc::fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+
+  const int stages = (a.K + 2 * kStage - 1) / (2 * kStage) * 2, chunks = (stages + kChunk - 1) / kChunk;
+  const int tiles = g.tiles_n * g.tiles_m;
+  bool dead = false;
+
+  if (warp >= 8) {
+    if constexpr (S::kMove) tc::give_registers();
+    if (warp == 8 && lane == 0 && rank == 0) {
+      constexpr uint32_t ins = tc::instruction(128 * CG, BN, 0, 0, 0);
+      uint32_t it = 0, ch = 0;
+      for (int tile = unit; tile < tiles && !dead; tile += units) {
+        for (int c = 0; c < chunks && !dead; c++, ch++) {
+          const uint32_t set = ch & 1;
+          tc::mbar_wait(acc_empty + 8 * set, ((ch >> 1) & 1) ^ 1, dead);
+          tc::fence_after();
+          const int n = min(kChunk, stages - c * kChunk);
+          for (int i = 0; i < n && !dead; i++, it++) {
+            const uint32_t s = it % S::kStages;
+            tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1, dead);
+            tc::fence_after();
+            if (dead) break;
+            const uint32_t at = base + s * S::kBytes;
+            const uint64_t da = tc::operand(at, 16, 1024), db = tc::operand(at + 128 * 128, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < kStage / 16; k++)
+              tc::mma<CG>(tmem + set * 256, da + 2 * k, db + 2 * k, ins, (i | k) != 0);
+            tc::commit<CG>(empty + 8 * s);
+          }
+          tc::commit<CG>(acc_full + 8 * set);
+        }
+      }
+      bool late = false;                       // everything issued has to end before the memory is given back
+      tc::commit_here<CG>(drain);
+      tc::mbar_wait(drain, 0, late);
+    }
+    __syncwarp();
+  } else {
+    if constexpr (S::kMove) tc::take_registers();
+    // pieces of a stage: piece p of a row is k 16p .. 16p + 15
+    const int piece = threadIdx.x & 3, row0 = threadIdx.x >> 2;
+    uint32_t store[S::kLoads];
+#pragma unroll
+    for (int j = 0; j < S::kLoads; j++) {
+      const int r = row0 + 64 * j;
+      store[j] = (r >> 3) * 1024 + (r & 7) * 128 + (((2 * piece) ^ (r & 7)) << 4);
+    }
+    const int8_t *src[S::kLoads];
+    bool have[S::kLoads];
+    int ltile = unit, lk = 0;                  // the load cursor runs two stages ahead of the store
+    auto aim = [&]() {
+      if (ltile >= tiles) {
+#pragma unroll
+        for (int j = 0; j < S::kLoads; j++) have[j] = false;
+        return;
+      }
+      const int n0 = (ltile % g.tiles_n) * (128 * CG) + rank * 128, m0 = (ltile / g.tiles_n) * BN + rank * S::kRowsB;
+#pragma unroll
+      for (int j = 0; j < S::kLoads; j++) {
+        const int r = row0 + 64 * j;
+        if (r < 128) {
+          have[j] = n0 + r < a.N;
+          src[j] = a.w + (int64_t)(n0 + r) * a.ldw + 16 * piece;
+        } else {
+          have[j] = m0 + r - 128 < a.M;
+          src[j] = a.x + (int64_t)(m0 + r - 128) * a.ldx + 16 * piece;
+        }
+      }
+    };
+    auto load = [&](uint4 (&v)[S::kLoads]) {
+      const bool in = lk * kStage + 16 * piece < a.K;
+#pragma unroll
+      for (int j = 0; j < S::kLoads; j++) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (have[j] && in) v[j] = __ldg((const uint4 *)(src[j] + (int64_t)lk * kStage));
+      }
+      if (++lk == stages) {
+        lk = 0;
+        ltile += units;
+        aim();
+      }
+    };
+    uint32_t it = 0, ch = 0;
+    int tile = unit, c = 0, i = 0;             // the store cursor: tile, chunk of it, stage of the chunk
+    int acc[BN / 2];
+#pragma unroll
+    for (int j = 0; j < BN / 2; j++) acc[j] = 0;
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * (BN / 2);
+    auto step = [&](uint4 (&v)[S::kLoads]) {
+      const uint32_t s = it % S::kStages;
+      tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1, dead);
+      const uint32_t at = base + s * S::kBytes;
+#pragma unroll
+      for (int j = 0; j < S::kLoads; j++) {
+        uint32_t h[8];
+        half4(v[j].x, h[0], h[1]);
+        half4(v[j].y, h[2], h[3]);
+        half4(v[j].z, h[4], h[5]);
+        half4(v[j].w, h[6], h[7]);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + store[j]), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                     "r"(h[3])
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (store[j] ^ 16)), "r"(h[4]), "r"(h[5]),
+                     "r"(h[6]), "r"(h[7])
+                     : "memory");
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_lead<CG>(full + 8 * s);
+      load(v);
+      it++;
+    };
+    uint4 va[S::kLoads], vb[S::kLoads];
+    aim();
+    load(va);
+    load(vb);
+    int done_tile = 0;                         // of the chunk that waits to be taken out
+    bool done_last = false;
+    for (;;) {
+      const bool more = tile < tiles;
+      if (more) {
+        step(va);
+        step(vb);
+      }
+      // A chunk is taken out once the next one is two pairs of stages along (or all there), so
+      // that the matrix unit has work meanwhile; the last one, at the end.
+      const int n = min(kChunk, stages - c * kChunk);
+      if (ch > 0 && (!more || i == min(4, n) - 2)) {
+        const uint32_t set = (ch - 1) & 1;
+        tc::mbar_wait(acc_full + 8 * set, ((ch - 1) >> 1) & 1, dead);
+        __syncwarp();
+        tc::fence_after();
+        const bool write = done_last;
+        const int n = (done_tile % g.tiles_n) * (128 * CG) + rank * 128 + (warp & 3) * 32 + lane;
+        const int m0 = (done_tile / g.tiles_n) * BN + (warp >> 2) * (BN / 2);
+        const float sw = write && a.sw && n < a.N ? a.sw[n] : 0.f, bias = write && a.bias && n < a.N ? a.bias[n] : 0.f;
+#pragma unroll
+        for (int j = 0; j < BN / 2; j += 16) {
+          float v[16];
+          tc::tmem_load16(mine + set * 256 + j, v);
+          tc::tmem_wait();
+#pragma unroll
+          for (int x = 0; x < 16; x++) acc[j + x] += __float2int_rn(v[x]);
+          if (write) {
+            if (n < a.N) put_y16(a, m0 + j, n, &acc[j], sw, bias);
+#pragma unroll
+            for (int x = 0; x < 16; x++) acc[j + x] = 0;
+          }
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_lead<CG>(acc_empty + 8 * set);
+      }
+      if (!more) break;
+      i += 2;
+      if (i == n) {
+        done_tile = tile;
+        done_last = c == chunks - 1;
+        i = 0;
+        ch++;
+        if (++c == chunks) {
+          c = 0;
+          tile += units;
+        }
+      }
+    }
+  }
+  tc::fence_before();
+  if constexpr (CG == 1) __syncthreads();
+  else tc::cluster_sync();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::tmem_free<CG>(tmem, 512);
+  }
+}
+
+template <int CG, int BN>
+int go_matrix(const LinearArgs &a, cudaStream_t st) {
+  using S = Shape<CG, BN>;
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MCEMU_ERR_CUDA;
+  if (dev >= 64 || !ready[dev].load()) {
+    if (cudaFuncSetAttribute(matrix_kernel<CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+      return MCEMU_ERR_CUDA;
+    if (dev < 64) ready[dev].store(true);
+  }
+  MatArgs g{a, (a.N + 128 * CG - 1) / (128 * CG), (a.M + BN - 1) / BN};
+  const int64_t tiles = (int64_t)g.tiles_n * g.tiles_m;
+  if (tiles > INT32_MAX / 2) return MCEMU_ERR_UNSUPPORTED;
+  const int units = (int)(tiles < sm_count() / CG ? tiles : sm_count() / CG);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * CG);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, matrix_kernel<CG, BN>, g) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
 }
 
 // 32 x 32 outputs to a block of 256 threads, four to a thread.
@@ -43,16 +334,25 @@ __global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
 #pragma unroll
   for (int r = 0; r < 4; r++) {
     const int m = m0 + ty + 8 * r, n = n0 + tx;
-    if (m < a.M && n < a.N) put_y(a, m, n, acc[r]);
+    if (m < a.M && n < a.N) put_y(a, m, n, acc[r], a.sw ? a.sw[n] : 0.f, a.bias ? a.bias[n] : 0.f);
   }
 }
 
 }  // namespace
 
+int int8_linear_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_timeouts(st, got); }
+
 size_t int8_linear_workspace(int M, int N, int K) { return 0; }
 
 int launch_int8_linear(const LinearArgs &a, void *ws, void *stream) {
-  linear_kernel<<<dim3((a.N + 31) / 32, (a.M + 31) / 32), 256, 0, (cudaStream_t)stream>>>(a);
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool rows = rows16(a.x, a.ldx, 1) && rows16(a.w, a.ldw, 1) && a.K % 16 == 0 && a.K > 0;
+  if (rows && a.M > 16) {
+    if (a.M <= 64) return go_matrix<1, 64>(a, st);
+    if (a.M <= 128) return go_matrix<1, 128>(a, st);
+    return go_matrix<2, 256>(a, st);
+  }
+  linear_kernel<<<dim3((a.N + 31) / 32, (a.M + 31) / 32), 256, 0, st>>>(a);
   return launch_status();
 }
 

@@ -1,6 +1,8 @@
 // ops.h -- host-side launchers of the 8-bit layer operators, called by the C ABI
 // (ops_api.cu) after its argument checks.
 #pragma once
+#include <cuda_runtime.h>
+
 #include <cstddef>
 #include <cstdint>
 
@@ -46,6 +48,8 @@ struct LinearArgs {
   void *y;
   int out_fmt;
 };
+// Whether a bounded device wait of these kernels gave up since the last question.
+int int8_linear_timeouts(cudaStream_t st, unsigned int *got);
 size_t int8_linear_workspace(int M, int N, int K);
 int launch_int8_linear(const LinearArgs &a, void *ws, void *stream);
 

@@ -140,3 +140,9 @@ extern "C" int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t
   WgradArgs a{T, N, K, dy, q, e, lddy, ldq, lde, lddw, dW, out_fmt, accumulate};
   return launch_act8_wgrad(a, workspace, stream);
 }
+
+extern "C" int mcemu_ops_check(void *stream) {
+  unsigned int linear = 0;
+  if (int8_linear_timeouts((cudaStream_t)stream, &linear) != MCEMU_OK) return MCEMU_ERR_CUDA;
+  return linear ? MCEMU_ERR_TIMEOUT : MCEMU_OK;
+}

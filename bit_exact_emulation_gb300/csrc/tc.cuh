@@ -1,0 +1,178 @@
+// tc.cuh -- PTX of sm_103a's fifth-generation tensor cores as the 8-bit layer products use
+// it: mbarriers with bounded waits, tensor memory, the matrix instruction and its shared-memory
+// operands in the 128-byte swizzle.  CG is the number of CTAs (1 or 2) that issue as one.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mcemu_ops.h"
+
+namespace mcemu {
+namespace tc {
+
+// Set when a wait gave up (one to a translation unit; mcemu_ops_check reads and clears them).
+static __device__ unsigned int g_timeouts = 0;
+
+// The flag's value once `st` is done, and 0 in its place.
+inline int take_timeouts(cudaStream_t st, unsigned int *got) {
+  const unsigned int zero = 0;
+  if (cudaMemcpyFromSymbolAsync(got, g_timeouts, sizeof *got, 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaMemcpyToSymbolAsync(g_timeouts, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
+    return MCEMU_ERR_CUDA;
+  return cudaStreamSynchronize(st) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
+}
+
+// Moves the registers of a block of three warpgroups, 168 a thread at launch, from the third
+// to the two that hold accumulators: 2 * 232 + 40 = 3 * 168.
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- mbarriers ---------------------------------------------------------------
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_init_fence() {
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+// Arrives on the barrier at the same offset in CTA 0 of the cluster (this CTA for CG 1).
+template <int CG>
+__device__ __forceinline__ void mbar_arrive_lead(uint32_t bar) {
+  if constexpr (CG == 1) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+  } else {
+    asm volatile(
+        "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, 0;\n"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase of `parity` to end.  Gives up after two seconds: `dead` is then set, the
+// flag too, and later waits return at once, so that the kernel runs to its end on what it has.
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = now_ns();
+  for (int i = 0; i < 1 << 26; i++) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 63) == 63 && now_ns() - t0 > 2000000000ull) break;
+  }
+  atomicExch(&g_timeouts, 1u);
+  return false;
+}
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool &dead) {
+  if (dead) return;
+#pragma unroll 1
+  for (int i = 0; i < 64; i++)
+    if (mbar_try(bar, parity)) return;
+  dead = !mbar_wait_long(bar, parity);
+}
+
+// ---- fences ------------------------------------------------------------------
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// ---- tensor memory (whole warps) ------------------------------------------------
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t cols) {
+  if constexpr (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+}
+// 16 consecutive columns of the warp's 32 lanes; complete after tmem_wait().
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- matrix instruction ------------------------------------------------------
+// Shared-memory operand in 128-byte swizzle: rows of 128 bytes, eight to an atom of 1024.
+// K-major (a row is 64 elements of K): `far` unused, `near` = 1024 between groups of eight
+// rows.  MN-major (a row is 64 elements of M or N, eight k to an atom): `far` from one 64 of
+// M or N to the next, `near` from one eight of k to the next.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t far, uint32_t near) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(far >> 4) << 16 | (uint64_t)(near >> 4) << 32 | 1ull << 46 |
+         2ull << 61;
+}
+// Instruction word of kind::f16: fp32 accumulators, binary16 (0) or bfloat16 (1) operands,
+// each K-major (0) or MN-major (1).
+__host__ __device__ constexpr uint32_t instruction(int m, int n, int bf16, int a_mn, int b_mn) {
+  return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 |
+         (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t ins, bool add) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(ins), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(ins), "r"((uint32_t)add)
+        : "memory");
+}
+// Arrives on `bar` (of both CTAs for CG 2) once every matrix instruction issued so far is done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// The same on this CTA's barrier alone.
+template <int CG>
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  if constexpr (CG == 1) commit<1>(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+}  // namespace tc
+}  // namespace mcemu

@@ -35,6 +35,7 @@ SYMBOLS = {
     "mcemu_act8_expand": (_I, [_I] * 3 + [_V, _L] * 3 + [_V]),
     "mcemu_act8_wgrad": (_I, [_I] * 3 + [_V, _L] * 3 + [_I, _I, _V, _L, _V, _Z, _V]),
     "mcemu_act8_wgrad_workspace": (_Z, [_I] * 3),
+    "mcemu_ops_check": (_I, [_V]),
 }
 _FMT_OF = {torch.float16: FMT["fp16"], torch.bfloat16: FMT["bf16"], torch.float32: FMT["fp32"]}
 _OUT = {"int8": (FMT["int8"], torch.int8), "e4m3": (FMT["e4m3"], torch.float8_e4m3fn),
@@ -272,3 +273,9 @@ def act8_wgrad(dy, q, e, out: str = "fp32", dW=None, accumulate: bool = False, w
     _run(w, "mcemu_act8_wgrad", T, N, K, pdy, lddy, pq, ldq, pe, lde, FMT[out], int(bool(accumulate)), pd, ldd, pws,
          nws, st)
     return dW
+
+
+def check():
+    """Waits for the current stream; raises (status 6) when a bounded wait inside one of the
+    product kernels gave up since the last call, which leaves that launch's results invalid."""
+    _run("check", "mcemu_ops_check", torch.cuda.current_stream().cuda_stream)

@@ -118,6 +118,12 @@ int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t lddy, cons
                      void *workspace, size_t ws_bytes, void *stream);
 size_t mcemu_act8_wgrad_workspace(int T, int N, int K);
 
+/* Waits for `stream`.  MCEMU_ERR_TIMEOUT when a wait inside one of the product
+ * kernels gave up on the current device since the last call of this function
+ * (each wait is bounded by two seconds; the results of that launch are not
+ * valid), MCEMU_OK otherwise.  Synchronous; not needed for ordering. */
+int mcemu_ops_check(void *stream);
+
 #ifdef __cplusplus
 }
 #endif

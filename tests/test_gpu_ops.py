@@ -618,3 +618,9 @@ def test_python_refusals(O):
         with pytest.raises(E):
             bad()
     torch.cuda.synchronize()
+
+
+def test_no_wait_gave_up(O):
+    x, w = torch.ones(200, 2048, dtype=torch.int8, device="cuda"), torch.ones(300, 2048, dtype=torch.int8, device="cuda")
+    assert torch.all(O.int8_linear(x, None, w, None, out="int32") == 2048)
+    O.check()
