@@ -6,8 +6,7 @@
 // of 1024 products is an integer of at most 2^24, which fp32 accumulators hold without
 // rounding (every partial sum too, in any order).  Every 1024 products the accumulators are
 // therefore taken out of tensor memory and added to int32 sums in registers.
-#include "ops_common.cuh"
-#include "tc.cuh"
+#include "panel.cuh"
 
 namespace mcemu {
 namespace {
@@ -44,8 +43,7 @@ __device__ __forceinline__ void half4(uint32_t b, uint32_t &lo, uint32_t &hi) {
 }
 
 // ---------------------------------------------------------------------------
-// Matrix kernel.  A tile is 128 channels a CTA (operand A) by BN tokens (operand B, split
-// between the CTAs of a pair); CG CTAs work on CG * 128 channels.  Eight worker warps read
+// Matrix kernel.  A tile is 128 channels (operand A) by BN tokens (operand B).  Eight worker warps read
 // both operands 64 k at a time, widen them to binary16 and store them in the swizzle; one
 // thread issues the matrix instructions; the workers take the accumulators out, one half of
 // the columns to each four warps, and write the tile.  Two sets of accumulators let the
@@ -55,9 +53,9 @@ constexpr int kStage = 64;                    // k of a stage: one 128-byte swiz
 constexpr int kChunk = 1024 / kStage;         // stages between two transfers to int32
 constexpr int kWorkers = 256;
 
-template <int CG, int BN>
+template <int BN>
 struct Shape {
-  static constexpr int kRowsB = BN / CG;                        // token rows this CTA stages
+  static constexpr int kRowsB = BN;                             // token rows
   static constexpr int kRows = 128 + kRowsB;
   static constexpr int kBytes = kRows * 128;                    // of one stage
   static constexpr int kStages = kBytes >= 32768 ? 5 : kBytes >= 24576 ? 6 : 8;
@@ -72,9 +70,9 @@ struct MatArgs {
   int tiles_n, tiles_m;      // tiles over channels and tokens
 };
 
-template <int CG, int BN>
-__global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(const MatArgs g) {
-  using S = Shape<CG, BN>;
+template <int BN>
+__global__ void __launch_bounds__(Shape<BN>::kThreads, 1) matrix_kernel(const MatArgs g) {
+  using S = Shape<BN>;
   static_assert(S::kLoads * kWorkers == S::kRows * 4, "whole pieces per worker");
   extern __shared__ uint8_t raw[];
   const LinearArgs &a = g.a;
@@ -83,25 +81,23 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
   const uint32_t full = bars, empty = full + 8 * S::kStages, acc_full = empty + 8 * S::kStages,
                  acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 1 ? 0 : tc::cta_rank();
-  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+  const int unit = blockIdx.x, units = gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; s++) {
-      tc::mbar_init(full + 8 * s, 8 * CG);
+      tc::mbar_init(full + 8 * s, 8);
       tc::mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < 2; s++) {
       tc::mbar_init(acc_full + 8 * s, 1);
-      tc::mbar_init(acc_empty + 8 * s, 8 * CG);
+      tc::mbar_init(acc_empty + 8 * s, 8);
     }
     tc::mbar_init(drain, 1);
     tc::mbar_init_fence();
   }
-  if (warp == 8) tc::tmem_alloc<CG>(slot, 512);
+  if (warp == 8) tc::tmem_alloc<1>(slot, 512);
   tc::fence_before();
-  if constexpr (CG == 1) __syncthreads();
-  else tc::cluster_sync();
+  __syncthreads();
   tc::fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
@@ -112,8 +108,8 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
 
   if (warp >= 8) {
     if constexpr (S::kMove) tc::give_registers();
-    if (warp == 8 && lane == 0 && rank == 0) {
-      constexpr uint32_t ins = tc::instruction(128 * CG, BN, 0, 0, 0);
+    if (warp == 8 && lane == 0) {
+      constexpr uint32_t ins = tc::instruction(128, BN, 0, 0, 0);
       uint32_t it = 0, ch = 0;
       for (int tile = unit; tile < tiles && !dead; tile += units) {
         for (int c = 0; c < chunks && !dead; c++, ch++) {
@@ -130,14 +126,14 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
             const uint64_t da = tc::operand(at, 16, 1024), db = tc::operand(at + 128 * 128, 16, 1024);
 #pragma unroll
             for (int k = 0; k < kStage / 16; k++)
-              tc::mma<CG>(tmem + set * 256, da + 2 * k, db + 2 * k, ins, (i | k) != 0);
-            tc::commit<CG>(empty + 8 * s);
+              tc::mma<1>(tmem + set * 256, da + 2 * k, db + 2 * k, ins, (i | k) != 0);
+            tc::commit<1>(empty + 8 * s);
           }
-          tc::commit<CG>(acc_full + 8 * set);
+          tc::commit<1>(acc_full + 8 * set);
         }
       }
       bool late = false;                       // everything issued has to end before the memory is given back
-      tc::commit_here<CG>(drain);
+      tc::commit<1>(drain);
       tc::mbar_wait(drain, 0, late);
     }
     __syncwarp();
@@ -160,7 +156,7 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
         for (int j = 0; j < S::kLoads; j++) have[j] = false;
         return;
       }
-      const int n0 = (ltile % g.tiles_n) * (128 * CG) + rank * 128, m0 = (ltile / g.tiles_n) * BN + rank * S::kRowsB;
+      const int n0 = (ltile % g.tiles_n) * 128, m0 = (ltile / g.tiles_n) * BN;
 #pragma unroll
       for (int j = 0; j < S::kLoads; j++) {
         const int r = row0 + 64 * j;
@@ -212,7 +208,7 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
       }
       tc::fence_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_lead<CG>(full + 8 * s);
+      if (lane == 0) tc::mbar_arrive(full + 8 * s);
       load(v);
       it++;
     };
@@ -237,7 +233,7 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
         __syncwarp();
         tc::fence_after();
         const bool write = done_last;
-        const int n = (done_tile % g.tiles_n) * (128 * CG) + rank * 128 + (warp & 3) * 32 + lane;
+        const int n = (done_tile % g.tiles_n) * 128 + (warp & 3) * 32 + lane;
         const int m0 = (done_tile / g.tiles_n) * BN + (warp >> 2) * (BN / 2);
         const float sw = write && a.sw && n < a.N ? a.sw[n] : 0.f, bias = write && a.bias && n < a.N ? a.bias[n] : 0.f;
 #pragma unroll
@@ -255,7 +251,7 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_lead<CG>(acc_empty + 8 * set);
+        if (lane == 0) tc::mbar_arrive(acc_empty + 8 * set);
       }
       if (!more) break;
       i += 2;
@@ -272,41 +268,112 @@ __global__ void __launch_bounds__(Shape<CG, BN>::kThreads, 1) matrix_kernel(cons
     }
   }
   tc::fence_before();
-  if constexpr (CG == 1) __syncthreads();
-  else tc::cluster_sync();
+  __syncthreads();
   if (warp == 8) {
     tc::fence_after();
-    tc::tmem_free<CG>(tmem, 512);
+    tc::tmem_free<1>(tmem, 512);
   }
 }
 
-template <int CG, int BN>
+template <int BN>
 int go_matrix(const LinearArgs &a, cudaStream_t st) {
-  using S = Shape<CG, BN>;
+  using S = Shape<BN>;
   static std::atomic<bool> ready[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MCEMU_ERR_CUDA;
   if (dev >= 64 || !ready[dev].load()) {
-    if (cudaFuncSetAttribute(matrix_kernel<CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(matrix_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
       return MCEMU_ERR_CUDA;
     if (dev < 64) ready[dev].store(true);
   }
-  MatArgs g{a, (a.N + 128 * CG - 1) / (128 * CG), (a.M + BN - 1) / BN};
+  MatArgs g{a, (a.N + 127) / 128, (a.M + BN - 1) / BN};
   const int64_t tiles = (int64_t)g.tiles_n * g.tiles_m;
   if (tiles > INT32_MAX / 2) return MCEMU_ERR_UNSUPPORTED;
-  const int units = (int)(tiles < sm_count() / CG ? tiles : sm_count() / CG);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(units * CG);
-  cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, matrix_kernel<CG, BN>, g) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
+  matrix_kernel<BN><<<(unsigned)(tiles < sm_count() ? tiles : sm_count()), S::kThreads, S::kSmem, st>>>(g);
+  return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Large products: both operands are widened to binary16 panels once (3 bytes of traffic an
+// element, against a conversion for every tile that reads it), and pairs of CTAs multiply
+// the panels with nothing but copies and matrix instructions in the loop.
+// ---------------------------------------------------------------------------
+struct Widen {
+  const int8_t *src;
+  int64_t ld;
+  int rows, blocks;          // rows, and 128-row blocks of the panel
+  uint8_t *to;
+};
+
+// Sixteen bytes of a row of K from k on, zeros beyond its end; any alignment, no access
+// outside the row.
+__device__ __forceinline__ uint4 row16(const int8_t *row, int k, int K, bool wide) {
+  if (wide && k + 16 <= K) return __ldg((const uint4 *)(row + k));
+  uint32_t w[4] = {0, 0, 0, 0};
+  const int off = (int)((uintptr_t)(row + k) & 3);
+  if (k >= off && k - off + 20 <= K) {          // five whole words around the sixteen bytes
+    const uint32_t *p = (const uint32_t *)(row + k - off);
+    uint32_t v[5];
+#pragma unroll
+    for (int i = 0; i < 5; i++) v[i] = __ldg(p + i);
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+      if (k + i < K) w[i >> 2] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One tile (128 rows by 64 k) to a block.
+__global__ void __launch_bounds__(256) widen_kernel(const Widen x, const Widen w, int K, int ktiles, bool wide) {
+  int64_t tile = blockIdx.x;
+  const int64_t mine = (int64_t)x.blocks * ktiles;
+  const Widen &o = tile < mine ? x : w;
+  if (tile >= mine) tile -= mine;
+  const int block = (int)(tile / ktiles), kt = (int)(tile - (int64_t)block * ktiles);
+  uint8_t *to = o.to + tile * panel::kTileBytes;
+#pragma unroll
+  for (int j = 0; j < 2; j++) {
+    const int piece = threadIdx.x & 3, r = (threadIdx.x >> 2) + 64 * j, row = block * 128 + r;
+    const int k = kt * 64 + 16 * piece;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < o.rows && k < K) v = row16(o.src + (int64_t)row * o.ld, k, K, wide);
+    uint4 lo, hi;
+    half4(v.x, lo.x, lo.y);
+    half4(v.y, lo.z, lo.w);
+    half4(v.z, hi.x, hi.y);
+    half4(v.w, hi.z, hi.w);
+    const int at = r * 128 + (((2 * piece) ^ (r & 7)) << 4);
+    *(uint4 *)(to + at) = lo;
+    *(uint4 *)(to + (at ^ 16)) = hi;
+  }
+}
+
+struct LinearEp {
+  using Sum = int;
+  LinearArgs a;
+  static __device__ __forceinline__ void add(int &s, float v) { s += __float2int_rn(v); }
+  __device__ __forceinline__ void store(int n, int m0, const int *sum, int) const {
+    if (n >= a.N) return;
+    const float sw = a.sw ? __ldg(a.sw + n) : 0.f, bias = a.bias ? __ldg(a.bias + n) : 0.f;
+    put_y16(a, m0, n, sum, sw, bias);
+  }
+};
+
+int blocks128(int rows) { return (rows + 255) / 256 * 2; }
+int ktiles_of(int K) { return (K + 63) / 64; }
+
+int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
+  const int kt = ktiles_of(a.K);
+  Widen x{a.x, a.ldx, a.M, blocks128(a.M), (uint8_t *)ws};
+  Widen w{a.w, a.ldw, a.N, blocks128(a.N), x.to + (int64_t)x.blocks * kt * panel::kTileBytes};
+  const int64_t tiles = (int64_t)(x.blocks + w.blocks) * kt;
+  if (tiles > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+  widen_kernel<<<(unsigned)tiles, 256, 0, st>>>(x, w, a.K, kt, wide);
+  panel::Args g{w.to, x.to, kt, w.blocks / 2, x.blocks / 2, 1, kt, 1024 / panel::kTileK};
+  return panel::launch<LinearEp, 0, 0>(g, LinearEp{a}, st);
 }
 
 // 32 x 32 outputs to a block of 256 threads, four to a thread.
@@ -342,15 +409,21 @@ __global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
 
 int int8_linear_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_timeouts(st, got); }
 
-size_t int8_linear_workspace(int M, int N, int K) { return 0; }
+// Products that go through panels: more than 16 tokens, and either enough of them to pay for
+// the panels or rows that are not on 16-byte boundaries.
+static bool by_panels(int M, int K, bool rows) { return M > 16 && K > 0 && (M > 256 || !rows || K % 16 != 0); }
 
-int launch_int8_linear(const LinearArgs &a, void *ws, void *stream) {
+size_t int8_linear_workspace(int M, int N, int K, int rows) {
+  if (!by_panels(M, K, rows != 0)) return 0;
+  return (size_t)(blocks128(M) + blocks128(N)) * ktiles_of(K) * panel::kTileBytes;
+}
+
+int launch_int8_linear(const LinearArgs &a, bool rows, void *ws, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
-  const bool rows = rows16(a.x, a.ldx, 1) && rows16(a.w, a.ldw, 1) && a.K % 16 == 0 && a.K > 0;
-  if (rows && a.M > 16) {
-    if (a.M <= 64) return go_matrix<1, 64>(a, st);
-    if (a.M <= 128) return go_matrix<1, 128>(a, st);
-    return go_matrix<2, 256>(a, st);
+  if (by_panels(a.M, a.K, rows)) return go_panels(a, rows, ws, st);
+  if (a.M > 16 && a.K > 0) {
+    if (a.M <= 64) return go_matrix<64>(a, st);
+    return go_matrix<128>(a, st);
   }
   linear_kernel<<<dim3((a.N + 31) / 32, (a.M + 31) / 32), 256, 0, st>>>(a);
   return launch_status();

@@ -44,17 +44,17 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_init_fence() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
-// Arrives on the barrier at the same offset in CTA 0 of the cluster (this CTA for CG 1).
-template <int CG>
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrives on the barrier at the same offset in CTA 0 of the cluster.  The release covers what
+// this thread has seen, so a thread that waits on its own CTA's barrier and then calls this
+// passes the whole CTA's work on.
 __device__ __forceinline__ void mbar_arrive_lead(uint32_t bar) {
-  if constexpr (CG == 1) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-  } else {
-    asm volatile(
-        "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, 0;\n"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar)
-        : "memory");
-  }
+  asm volatile(
+      "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, 0;\n"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -91,6 +91,14 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool &d
   for (int i = 0; i < 64; i++)
     if (mbar_try(bar, parity)) return;
   dead = !mbar_wait_long(bar, parity);
+}
+
+// Copies `bytes` (a multiple of 16, both ends on 16-byte boundaries) from global memory into
+// this CTA's shared memory and counts them on its barrier.
+__device__ __forceinline__ void bulk_load(uint32_t to, const void *from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "l"(from), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 // ---- fences ------------------------------------------------------------------
