@@ -370,10 +370,14 @@ int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
   Widen x{a.x, a.ldx, a.M, blocks128(a.M), (uint8_t *)ws};
   Widen w{a.w, a.ldw, a.N, blocks128(a.N), x.to + (int64_t)x.blocks * kt * panel::kTileBytes};
   const int64_t tiles = (int64_t)(x.blocks + w.blocks) * kt;
-  if (tiles > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+  if (!panel::panel_fits(x.blocks, kt) || !panel::panel_fits(w.blocks, kt)) return MCEMU_ERR_UNSUPPORTED;
   widen_kernel<<<(unsigned)tiles, 256, 0, st>>>(x, w, a.K, kt, wide);
-  panel::Args g{w.to, x.to, kt, w.blocks / 2, x.blocks / 2, 1, kt, 1024 / panel::kTileK};
-  return panel::launch<LinearEp, 0, 0>(g, LinearEp{a}, st);
+  CUtensorMap mw, mx;
+  int rc = panel::panel_map(&mw, w.to, w.blocks, kt);
+  if (rc == MCEMU_OK) rc = panel::panel_map(&mx, x.to, x.blocks, kt);
+  if (rc != MCEMU_OK) return rc;
+  panel::Args g{kt, w.blocks / 2, x.blocks / 2, 1, kt, 1024 / panel::kTileK};
+  return panel::launch<LinearEp, 0, 0, 0>(g, mw, mx, LinearEp{a}, st);
 }
 
 // 32 x 32 outputs to a block of 256 threads, four to a thread.

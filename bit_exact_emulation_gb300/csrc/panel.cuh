@@ -1,15 +1,19 @@
-// panel.cuh -- product of two operands laid out as panels, on pairs of CTAs.
+// panel.cuh -- product of two operands in 16-bit floating point on pairs of CTAs.
 //
-// A panel is an operand cut into tiles of 128 rows by 64 k, each tile the 16 KB image that
-// the matrix instruction reads from shared memory (128-byte swizzle), tiles of one 128-row
-// block following one another along k.  A stage of the pipeline is then two bulk copies of
-// 16 KB with no address arithmetic, no alignment left to check and no tensor map.
+// An operand is either a panel, cut beforehand into tiles of 128 rows by 64 k, each the 16 KB
+// image that the matrix instruction reads from shared memory (128-byte swizzle), tiles of
+// one 128-row block following one another along k; or (MN-major only) a matrix in global
+// memory, k by rows, from which the copy engine makes the same images.
 //
 // A pair computes 256 rows of A by 256 rows of B: each CTA holds 128 rows of both (32 KB a
 // stage) and 128 x 256 accumulators, twice, so that one set is drained while the other
 // fills.  The accumulators leave tensor memory every `chunk` stages and are added up in
 // registers, in whatever type the caller's sums need; the matrix unit alone would drop the
 // low bits of long sums (it truncates, it does not round).
+//
+// Both CTAs' copies count on the issuing CTA's barrier, by the hardware.  Passing a stage on by
+// a thread's arrival on the other CTA's barrier, with the release that it takes, measured
+// 0.95 us a stage in place of NEWSTAGE.
 #pragma once
 #include "ops_common.cuh"
 #include "tc.cuh"
@@ -25,7 +29,6 @@ constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
 constexpr int kThreads = 384;                 // eight warps drain, one loads, one issues, one relays
 
 struct Args {
-  const uint8_t *a, *b;      // panels
   int ka;                    // tiles along k
   int tiles_a, tiles_b;      // 256-row tiles of either operand
   int splits, per_split;     // parts of the sum, k tiles to a part
@@ -50,15 +53,30 @@ __device__ __forceinline__ Unit unit_at(const Args &g, int u) {
   return r;
 }
 
+// Copies the two operands' part of stage k for this CTA.  DIRECT: B is a matrix in memory.
+template <int DIRECT>
+__device__ __forceinline__ void load_stage(const Args &g, const CUtensorMap *ma, const CUtensorMap *mb, const Unit &w,
+                                           int rank, int k, uint32_t at, uint32_t bar) {
+  tc::box_load_pair(at, ma, 0, ((2 * w.ta + rank) * g.ka + k) * 128, bar);
+  if constexpr (DIRECT) {
+    const int x = w.tb * 256 + rank * 128;
+    tc::box_load_pair(at + kTileBytes, mb, x, k * kTileK, bar);
+    tc::box_load_pair(at + kTileBytes + 8192, mb, x + 64, k * kTileK, bar);
+  } else {
+    tc::box_load_pair(at + kTileBytes, mb, 0, ((2 * w.tb + rank) * g.ka + k) * 128, bar);
+  }
+}
+
 // Ep: `Ep::Sum` is the type of the register sums; add(Sum &, float) takes one accumulator;
 // store(row of A, row of B, 16 sums along B, split) writes 16 outputs.  MN: operands are
 // MN-major; BF16: bfloat16 (else binary16).
-template <class Ep, int MN, int BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kernel(const Args g, const Ep ep) {
+template <class Ep, int MN, int BF16, int DIRECT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    panel_kernel(const Args g, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                 const Ep ep) {
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t full = base + kStages * kStageBytes, empty = full + 8 * kStages, peer = empty + 8 * kStages,
-                 acc_full = peer + 8 * kStages, acc_empty = acc_full + 16, peer_acc = acc_empty + 16,
+  const uint32_t full = base + kStages * kStageBytes, empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, peer_acc = acc_empty + 16,
                  drain = peer_acc + 16, slot = drain + 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cta_rank();
@@ -68,7 +86,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kernel(
     for (int s = 0; s < kStages; s++) {
       tc::mbar_init(full + 8 * s, 1);
       tc::mbar_init(empty + 8 * s, 1);
-      tc::mbar_init(peer + 8 * s, 1);
     }
     for (int s = 0; s < 2; s++) {
       tc::mbar_init(acc_full + 8 * s, 1);
@@ -90,22 +107,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kernel(
     uint32_t it = 0;
     for (int u = first; u < units; u += step) {
       const Unit w = unit_at(g, u);
-      const uint8_t *pa = g.a + ((int64_t)(2 * w.ta + rank) * g.ka) * kTileBytes;
-      const uint8_t *pb = g.b + ((int64_t)(2 * w.tb + rank) * g.ka) * kTileBytes;
       for (int k = w.k0; k < w.k1 && !dead; k++, it++) {
-        const uint32_t s = it % kStages, at = base + s * kStageBytes;
+        const uint32_t s = it % kStages;
         tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, dead);
         if (dead) break;
-        tc::mbar_expect(full + 8 * s, kStageBytes);
-        tc::bulk_load(at, pa + (int64_t)k * kTileBytes, kTileBytes, full + 8 * s);
-        tc::bulk_load(at + kTileBytes, pb + (int64_t)k * kTileBytes, kTileBytes, full + 8 * s);
+        if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * kStageBytes);
+        load_stage<DIRECT>(g, &ma, &mb, w, rank, k, base + s * kStageBytes, full + 8 * s);
       }
     }
-    // copies in flight end before the block does
-    bool late = false;
-    for (uint32_t s = 0; s < kStages && s < it; s++) {
-      const uint32_t last = it - 1 - (it - 1 - s) % kStages;        // the last use of slot s
-      tc::mbar_wait(full + 8 * s, (last / kStages) & 1, late);
+    if (rank == 0) {                          // both CTAs' copies end before either leaves
+      bool late = false;
+      for (uint32_t s = 0; s < kStages && s < it; s++) {
+        const uint32_t last = it - 1 - (it - 1 - s) % kStages;      // the last use of slot s
+        tc::mbar_wait(full + 8 * s, (last / kStages) & 1, late);
+      }
     }
   } else if (warp == 9 && lane == 0 && rank == 0) {   // issues the pair's matrix instructions
     constexpr uint32_t ins = tc::instruction(256, 256, BF16, MN, MN);
@@ -121,7 +136,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kernel(
         for (int i = 0; i < n; i++, it++) {
           const uint32_t s = it % kStages, at = base + s * kStageBytes, fp = (it / kStages) & 1;
           tc::mbar_wait(full + 8 * s, fp, dead);
-          tc::mbar_wait(peer + 8 * s, fp, dead);
           if (dead) break;
           tc::fence_after();
           if constexpr (MN) {
@@ -142,17 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kernel(
     bool late = false;                        // everything issued ends before the memory is given back
     tc::commit_here<2>(drain);
     tc::mbar_wait(drain, 0, late);
-  } else if (warp == 9 && lane == 0) {        // tells the issuing CTA that this CTA's stage is there
-    uint32_t it = 0;
-    for (int u = first; u < units; u += step) {
-      const Unit w = unit_at(g, u);
-      for (int k = w.k0; k < w.k1; k++, it++) {
-        const uint32_t s = it % kStages;
-        tc::mbar_wait(full + 8 * s, (it / kStages) & 1, dead);
-        if (!dead) tc::mbar_arrive_lead(peer + 8 * s);
-      }
-    }
-  } else if (warp == 10 && lane == 0 && rank == 1) {  // ... and that its accumulators are drained
+  } else if (warp == 10 && lane == 0 && rank == 1) {  // tells the issuing CTA that this CTA's accumulators are drained
     uint32_t ch = 0;
     for (int u = first; u < units; u += step) {
       const Unit w = unit_at(g, u);
@@ -201,20 +205,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) kernel(
   }
 }
 
-template <class Ep, int MN, int BF16>
-int launch(const Args &g, const Ep &ep, cudaStream_t st) {
+// Tensor map of a panel of `blocks` 128-row blocks.
+inline int panel_map(CUtensorMap *map, const void *panel, int blocks, int ktiles) {
+  return tc::tensor_map(map, panel, 64, (uint64_t)blocks * ktiles * 128, 64, 128, false);
+}
+// What fits a panel: its rows are counted in 32 bits.
+inline bool panel_fits(int64_t blocks, int64_t ktiles) { return blocks * ktiles * 128 <= INT32_MAX; }
+
+template <class Ep, int MN, int BF16, int DIRECT>
+int launch(const Args &g, const CUtensorMap &ma, const CUtensorMap &mb, const Ep &ep, cudaStream_t st) {
   static std::atomic<bool> ready[64];
+  const auto kernel = panel_kernel<Ep, MN, BF16, DIRECT>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MCEMU_ERR_CUDA;
   if (dev >= 64 || !ready[dev].load()) {
-    if (cudaFuncSetAttribute(kernel<Ep, MN, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
       return MCEMU_ERR_CUDA;
     if (dev < 64) ready[dev].store(true);
   }
   const int64_t units = (int64_t)g.tiles_a * g.tiles_b * g.splits;
   if (units > INT32_MAX / 4) return MCEMU_ERR_UNSUPPORTED;
   const int pairs = (int)(units < sm_count() / 2 ? units : sm_count() / 2);
-  kernel<Ep, MN, BF16><<<2 * pairs, kThreads, kSmem, st>>>(g, ep);
+  kernel<<<2 * pairs, kThreads, kSmem, st>>>(g, ma, mb, ep);
   return launch_status();
 }
 

@@ -2,8 +2,11 @@
 // it: mbarriers with bounded waits, tensor memory, the matrix instruction and its shared-memory
 // operands in the 128-byte swizzle.  CG is the number of CTAs (1 or 2) that issue as one.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "../../include/mcemu_ops.h"
 
@@ -20,6 +23,32 @@ inline int take_timeouts(cudaStream_t st, unsigned int *got) {
       cudaMemcpyToSymbolAsync(g_timeouts, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
     return MCEMU_ERR_CUDA;
   return cudaStreamSynchronize(st) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
+}
+
+// Tensor map of a row-major matrix of 16-bit elements: `cols` x `rows`, `ld` elements between
+// rows (a multiple of 8, as is the base of 16 bytes), boxes of 64 columns by `box` rows, stored
+// plainly or in the 128-byte swizzle.  The driver's encoder is looked up once.
+inline int tensor_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box,
+                      bool swizzle) {
+  using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<void *> known{nullptr};
+  void *f = known.load();
+  if (!f) {
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess || !f)
+      return MCEMU_ERR_CUDA;
+    known.store(f);
+  }
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
+  const cuuint32_t boxes[2] = {64, box}, ones[2] = {1, 1};
+  return ((Encode)f)(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, boxes, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MCEMU_OK
+             : MCEMU_ERR_CUDA;
 }
 
 // Moves the registers of a block of three warpgroups, 168 a thread at launch, from the third
@@ -93,12 +122,16 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool &d
   dead = !mbar_wait_long(bar, parity);
 }
 
-// Copies `bytes` (a multiple of 16, both ends on 16-byte boundaries) from global memory into
-// this CTA's shared memory and counts them on its barrier.
-__device__ __forceinline__ void bulk_load(uint32_t to, const void *from, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
-               "l"(from), "r"(bytes), "r"(bar)
-               : "memory");
+// Copies a box of a two-dimensional tensor map, from element (x, y) on, into this CTA's shared
+// memory and counts its bytes on the barrier at the same offset in CTA 0 of the pair.  Elements
+// outside the tensor read as zeros and count too.
+__device__ __forceinline__ void box_load_pair(uint32_t to, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .b32 b;\nmapa.shared::cluster.u32 b, %4, 0;\n"
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[b];\n}" ::"r"(to),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 
 // ---- fences ------------------------------------------------------------------
