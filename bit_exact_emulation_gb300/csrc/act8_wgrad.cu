@@ -1,49 +1,179 @@
 // act8_wgrad.cu -- a linear layer's weight gradient from the 8-bit checkpoint of its input
 // (include/mcemu_ops.h has the formula).
-#include "ops_common.cuh"
+//
+// A product of dY^T (N x T) and the checkpoint (T x K) over the tokens.  A code times its
+// power-of-two scale is a bfloat16 number, so the checkpoint is widened once to a bfloat16 panel
+// (3 bytes of traffic an element) and the product is the matrix unit's, with exact operands.
+// Both operands are read with the tokens outermost as they lie in memory (MN-major); dY
+// needs no panel of its own unless its rows miss 16-byte boundaries.
+#include "panel.cuh"
 
 namespace mcemu {
 namespace {
 
-// 32 x 32 outputs to a block of 256 threads, four to a thread.
-__global__ void __launch_bounds__(256) wgrad_kernel(const WgradArgs a) {
-  __shared__ float ds[32][33], xs[32][33];
-  const int n0 = blockIdx.y * 32, k0 = blockIdx.x * 32;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int t0 = 0; t0 < a.T; t0 += 32) {
+// The image of 64 tokens by 128 columns: two halves of 64 columns, 8 KB each, a token's 64
+// columns in 128 bytes.  Where 16-byte unit u (of 16) of token t lies in it:
+__device__ __forceinline__ int image_at(int t, int u) {
+  return (u >> 3) * 8192 + (t >> 3) * 1024 + (t & 7) * 128 + (((u & 7) ^ (t & 7)) << 4);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *(const uint32_t *)&v;
+}
+
+// Checkpoint to panel, one image (64 tokens by one block of 128) to a block of threads: 16
+// codes a thread, twice.
+__global__ void __launch_bounds__(256) widen_kernel(const WgradArgs a, int ttiles, bool wide, uint8_t *__restrict__ to) {
+  const int64_t tile = blockIdx.x;
+  const int block = (int)(tile / ttiles), tt = (int)(tile - (int64_t)block * ttiles);
+  to += tile * panel::kTileBytes;
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
-      const int i = ty + 8 * r, t = t0 + i, n = n0 + tx, k = k0 + tx;
-      ds[i][tx] = t < a.T && n < a.N ? __uint_as_float((uint32_t)a.dy[(int64_t)t * a.lddy + n] << 16) : 0.f;
-      xs[i][tx] = t < a.T && k < a.K ? (float)a.q[(int64_t)t * a.ldq + k] *
-                                           act8_scale(a.e[(int64_t)t * a.lde + k / MCEMU_ACT8_BLOCK])
-                                     : 0.f;
+  for (int j = 0; j < 2; j++) {
+    const int piece = threadIdx.x & 7, r = (threadIdx.x >> 3) + 32 * j, t = tt * 64 + r;
+    const int k = block * 128 + 16 * piece;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    float s = 0.f;
+    if (t < a.T && k < a.K) {
+      v = row16(a.q + (int64_t)t * a.ldq, k, a.K, wide);
+      s = act8_scale(a.e[(int64_t)t * a.lde + block]);
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int i = 0; i < 32; i++)
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
 #pragma unroll
-      for (int r = 0; r < 4; r++) acc[r] = fmaf(ds[i][ty + 8 * r], xs[i][tx], acc[r]);
-    __syncthreads();
+    for (int i = 0; i < 8; i++) {
+      const int b = (int)(w[i >> 1] >> (16 * (i & 1)));
+      o[i] = bf16x2((float)(int8_t)b * s, (float)(int8_t)(b >> 8) * s);
+    }
+    *(uint4 *)(to + image_at(r, 2 * piece)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *(uint4 *)(to + image_at(r, 2 * piece + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
   }
+}
+
+// dY to a panel, for rows that the copy engine cannot read: eight elements a thread, four times.
+__global__ void __launch_bounds__(256) copy_kernel(const WgradArgs a, int ttiles, uint8_t *__restrict__ to) {
+  const int64_t tile = blockIdx.x;
+  const int block = (int)(tile / ttiles), tt = (int)(tile - (int64_t)block * ttiles);
+  to += tile * panel::kTileBytes;
 #pragma unroll
-  for (int r = 0; r < 4; r++) {
-    const int n = n0 + ty + 8 * r, k = k0 + tx;
-    if (n >= a.N || k >= a.K) continue;
-    const int64_t at = (int64_t)n * a.lddw + k;
-    if (a.out_fmt == MCEMU_FP32) ((float *)a.dW)[at] = a.accumulate ? ((float *)a.dW)[at] + acc[r] : acc[r];
-    else ((__nv_bfloat16 *)a.dW)[at] = __float2bfloat16_rn(acc[r]);
+  for (int j = 0; j < 4; j++) {
+    const int unit = threadIdx.x & 15, r = (threadIdx.x >> 4) + 16 * j, t = tt * 64 + r, n = block * 128 + 8 * unit;
+    uint32_t o[4] = {0, 0, 0, 0};
+    if (t < a.T) {
+      const uint16_t *p = a.dy + (int64_t)t * a.lddy + n;
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        if (n + i < a.N) o[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+    }
+    *(uint4 *)(to + image_at(r, unit)) = make_uint4(o[0], o[1], o[2], o[3]);
   }
+}
+
+__device__ __forceinline__ void put(const WgradArgs &a, int64_t at, float v) {
+  if (a.out_fmt == MCEMU_FP32) ((float *)a.dW)[at] = a.accumulate ? ((float *)a.dW)[at] + v : v;
+  else ((__nv_bfloat16 *)a.dW)[at] = __float2bfloat16_rn(v);
+}
+
+struct WgradEp {
+  using Sum = float;
+  WgradArgs a;
+  float *parts;              // [splits][N][K] when the sum is split
+  static __device__ __forceinline__ void add(float &s, float v) { s += v; }
+  __device__ __forceinline__ void store(int k, int n0, const float *sum, int split) const {
+    if (k >= a.K) return;
+    if (parts) {
+      float *p = parts + ((int64_t)split * a.N + n0) * a.K + k;
+#pragma unroll
+      for (int x = 0; x < 16; x++)
+        if (n0 + x < a.N) p[(int64_t)x * a.K] = sum[x];
+    } else {
+#pragma unroll
+      for (int x = 0; x < 16; x++)
+        if (n0 + x < a.N) put(a, (int64_t)(n0 + x) * a.lddw + k, sum[x]);
+    }
+  }
+};
+
+// Parts of the sum over the tokens, added in order.
+__global__ void __launch_bounds__(256) join_kernel(const WgradArgs a, const float *__restrict__ parts, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, size = (int64_t)a.N * a.K;
+  if (i >= size) return;
+  float s = parts[i];
+  for (int p = 1; p < splits; p++) s += parts[p * size + i];
+  put(a, i / a.K * a.lddw + i % a.K, s);
+}
+
+// No tokens: a gradient of zeros.
+__global__ void __launch_bounds__(256) zero_kernel(const WgradArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < (int64_t)a.N * a.K) put(a, i / a.K * a.lddw + i % a.K, 0.f);
+}
+
+#ifndef WCHUNK
+#define WCHUNK 16
+#endif
+constexpr int kChunk = WCHUNK;                // 64-token stages between two drains
+
+struct Plan {
+  int ttiles, blocks_k, blocks_n, splits, per_split;
+  int64_t panel_x, panel_dy, parts;          // bytes
+};
+Plan plan_of(int T, int N, int K, bool direct) {
+  Plan p;
+  p.ttiles = (T + 63) / 64;
+  p.blocks_k = (K + 255) / 256 * 2;
+  p.blocks_n = (N + 255) / 256 * 2;
+  // A product of few tiles is split along the tokens until the pairs of CTAs have work, down to
+  // sixteen stages a part.
+  const int64_t tiles = (int64_t)(p.blocks_k / 2) * (p.blocks_n / 2), pairs = 76;
+  int64_t s = tiles >= pairs ? 1 : pairs / tiles;
+  if (s > p.ttiles / 16) s = p.ttiles / 16;
+  if (s < 1) s = 1;
+  p.per_split = (int)((p.ttiles + s - 1) / s);
+  p.per_split = (p.per_split + kChunk - 1) / kChunk * kChunk;
+  p.splits = (p.ttiles + p.per_split - 1) / p.per_split;
+  p.panel_x = (int64_t)p.blocks_k * p.ttiles * panel::kTileBytes;
+  p.panel_dy = direct ? 0 : (int64_t)p.blocks_n * p.ttiles * panel::kTileBytes;
+  p.parts = p.splits > 1 ? (int64_t)p.splits * N * K * 4 : 0;
+  return p;
 }
 
 }  // namespace
 
-size_t act8_wgrad_workspace(int T, int N, int K) { return 0; }
+int act8_wgrad_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_timeouts(st, got); }
 
-int launch_act8_wgrad(const WgradArgs &a, void *ws, void *stream) {
-  wgrad_kernel<<<dim3((a.K + 31) / 32, (a.N + 31) / 32), 256, 0, (cudaStream_t)stream>>>(a);
-  return launch_status();
+size_t act8_wgrad_workspace(int T, int N, int K, bool direct) {
+  const Plan p = plan_of(T, N, K, direct);
+  return (size_t)(p.panel_x + p.panel_dy + p.parts);
+}
+
+int launch_act8_wgrad(const WgradArgs &a, bool direct, void *ws, void *stream) {
+  cudaStream_t st = (cudaStream_t)stream;
+  const int64_t size = (int64_t)a.N * a.K, blocks = (size + 255) / 256;
+  if (blocks > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+  if (a.T == 0) {
+    zero_kernel<<<(unsigned)blocks, 256, 0, st>>>(a);
+    return launch_status();
+  }
+  const Plan p = plan_of(a.T, a.N, a.K, direct);
+  if (!panel::panel_fits(p.blocks_k, p.ttiles) || !panel::panel_fits(p.blocks_n, p.ttiles)) return MCEMU_ERR_UNSUPPORTED;
+  uint8_t *px = (uint8_t *)ws, *pdy = px + p.panel_x;
+  float *parts = p.splits > 1 ? (float *)(pdy + p.panel_dy) : nullptr;
+  CUtensorMap mx, md;
+  int rc = panel::panel_map(&mx, px, p.blocks_k, p.ttiles);
+  if (rc == MCEMU_OK)
+    rc = direct ? tc::tensor_map(&md, a.dy, a.N, a.T, a.lddy, 64, true) : panel::panel_map(&md, pdy, p.blocks_n, p.ttiles);
+  if (rc != MCEMU_OK) return rc;
+  widen_kernel<<<(unsigned)(p.blocks_k * p.ttiles), 256, 0, st>>>(a, p.ttiles, rows16(a.q, a.ldq, 1), px);
+  if (!direct) copy_kernel<<<(unsigned)(p.blocks_n * p.ttiles), 256, 0, st>>>(a, p.ttiles, pdy);
+  const panel::Args g{p.ttiles, p.blocks_k / 2, p.blocks_n / 2, p.splits, p.per_split, kChunk};
+  rc = direct ? panel::launch<WgradEp, 1, 1, 1>(g, mx, md, WgradEp{a, parts}, st)
+              : panel::launch<WgradEp, 1, 1, 0>(g, mx, md, WgradEp{a, parts}, st);
+  if (rc == MCEMU_OK && parts) {
+    join_kernel<<<(unsigned)blocks, 256, 0, st>>>(a, parts, p.splits);
+    rc = launch_status();
+  }
+  return rc;
 }
 
 }  // namespace mcemu

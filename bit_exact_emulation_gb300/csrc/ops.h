@@ -50,8 +50,8 @@ struct LinearArgs {
 };
 // Whether a bounded device wait of these kernels gave up since the last question.
 int int8_linear_timeouts(cudaStream_t st, unsigned int *got);
+size_t int8_linear_workspace(int M, int N, int K);
 // rows: every row of x and w starts on a 16-byte boundary.
-size_t int8_linear_workspace(int M, int N, int K, int rows);
 int launch_int8_linear(const LinearArgs &a, bool rows, void *ws, void *stream);
 
 struct WgradArgs {
@@ -62,7 +62,9 @@ struct WgradArgs {
   void *dW;
   int out_fmt, accumulate;
 };
-size_t act8_wgrad_workspace(int T, int N, int K);
-int launch_act8_wgrad(const WgradArgs &a, void *ws, void *stream);
+int act8_wgrad_timeouts(cudaStream_t st, unsigned int *got);
+// direct: every row of dy starts on a 16-byte boundary.
+size_t act8_wgrad_workspace(int T, int N, int K, bool direct);
+int launch_act8_wgrad(const WgradArgs &a, bool direct, void *ws, void *stream);
 
 }  // namespace mcemu

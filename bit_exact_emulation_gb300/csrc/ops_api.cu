@@ -97,8 +97,8 @@ extern "C" int mcemu_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t
   return launch_act8_expand(fmt, T, H, q, ldq, e, lde, x, ldx, stream);
 }
 
-extern "C" size_t mcemu_int8_linear_workspace(int M, int N, int K, int rows_aligned) {
-  return M < 1 || N < 1 || K < 1 || K > 131071 ? 0 : int8_linear_workspace(M, N, K, rows_aligned);
+extern "C" size_t mcemu_int8_linear_workspace(int M, int N, int K) {
+  return M < 1 || N < 1 || K < 1 || K > 131071 ? 0 : int8_linear_workspace(M, N, K);
 }
 
 extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t ldx, const float *sx,
@@ -115,14 +115,14 @@ extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t l
   const size_t s = out_fmt == MCEMU_INT32 ? 4 : bytes_of(out_fmt);
   if (!aligned(y, s) || !aligned(sx, 4) || !aligned(sw, 4) || !aligned(bias, 4)) return MCEMU_ERR_ALIGNMENT;
   const bool rows = aligned(x, 16) && aligned(w, 16) && ldx % 16 == 0 && ldw % 16 == 0;
-  const int st = check_ws(workspace, ws_bytes, mcemu_int8_linear_workspace(M, N, K, rows));
+  const int st = check_ws(workspace, ws_bytes, mcemu_int8_linear_workspace(M, N, K));
   if (st != MCEMU_OK) return st;
   LinearArgs a{M, N, K, x, w, ldx, ldw, ldy, sx, sw, bias, y, out_fmt};
   return launch_int8_linear(a, rows, workspace, stream);
 }
 
-extern "C" size_t mcemu_act8_wgrad_workspace(int T, int N, int K) {
-  return T < 1 || N < 1 || K < 1 ? 0 : act8_wgrad_workspace(T, N, K);
+extern "C" size_t mcemu_act8_wgrad_workspace(int T, int N, int K, int dy_rows_aligned) {
+  return T < 1 || N < 1 || K < 1 ? 0 : act8_wgrad_workspace(T, N, K, dy_rows_aligned != 0);
 }
 
 extern "C" int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t lddy, const int8_t *q, int64_t ldq,
@@ -136,14 +136,17 @@ extern "C" int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t
   if ((T > 0 && (!dy || !q || !e)) || !dW) return MCEMU_ERR_INVALID_ARG;
   if (lddy < N || ldq < K || lde < blocks_of(K) || lddw < K) return MCEMU_ERR_INVALID_ARG;
   if (!aligned(dy, 2) || !aligned(dW, bytes_of(out_fmt))) return MCEMU_ERR_ALIGNMENT;
-  const int st = check_ws(workspace, ws_bytes, mcemu_act8_wgrad_workspace(T, N, K));
+  const bool direct = aligned(dy, 16) && lddy % 8 == 0;
+  const int st = check_ws(workspace, ws_bytes, mcemu_act8_wgrad_workspace(T, N, K, direct));
   if (st != MCEMU_OK) return st;
   WgradArgs a{T, N, K, dy, q, e, lddy, ldq, lde, lddw, dW, out_fmt, accumulate};
-  return launch_act8_wgrad(a, workspace, stream);
+  return launch_act8_wgrad(a, direct, workspace, stream);
 }
 
 extern "C" int mcemu_ops_check(void *stream) {
-  unsigned int linear = 0;
-  if (int8_linear_timeouts((cudaStream_t)stream, &linear) != MCEMU_OK) return MCEMU_ERR_CUDA;
-  return linear ? MCEMU_ERR_TIMEOUT : MCEMU_OK;
+  unsigned int linear = 0, wgrad = 0;
+  if (int8_linear_timeouts((cudaStream_t)stream, &linear) != MCEMU_OK ||
+      act8_wgrad_timeouts((cudaStream_t)stream, &wgrad) != MCEMU_OK)
+    return MCEMU_ERR_CUDA;
+  return linear || wgrad ? MCEMU_ERR_TIMEOUT : MCEMU_OK;
 }

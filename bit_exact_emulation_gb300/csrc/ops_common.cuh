@@ -53,6 +53,27 @@ __device__ __forceinline__ float act8_scale(int e) {
   return __int_as_float(e == MCEMU_ACT8_NAN ? 0x7FC00000 : (e + 127) << 23);
 }
 
+// Sixteen bytes of a row of K from k on, zeros beyond its end; any alignment, no access
+// outside the row.
+__device__ __forceinline__ uint4 row16(const int8_t *row, int k, int K, bool wide) {
+  if (wide && k + 16 <= K) return __ldg((const uint4 *)(row + k));
+  uint32_t w[4] = {0, 0, 0, 0};
+  const int off = (int)((uintptr_t)(row + k) & 3);
+  if (k >= off && k - off + 20 <= K) {          // five whole words around the sixteen bytes
+    const uint32_t *p = (const uint32_t *)(row + k - off);
+    uint32_t v[5];
+#pragma unroll
+    for (int i = 0; i < 5; i++) v[i] = __ldg(p + i);
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+      if (k + i < K) w[i >> 2] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Multiprocessors of the current device, looked up once per device.
 inline int sm_count() {
   static std::atomic<int> known[64];

@@ -26,7 +26,7 @@ constexpr int kTileK = 64;
 constexpr int kStages = 6;
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
-constexpr int kThreads = 384;                 // eight warps drain, one loads, one issues, one relays
+constexpr int kThreads = 384;                 // eight warps drain, one loads, one issues, two are idle
 
 struct Args {
   int ka;                    // tiles along k
@@ -76,8 +76,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  const Ep ep) {
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t full = base + kStages * kStageBytes, empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, peer_acc = acc_empty + 16,
-                 drain = peer_acc + 16, slot = drain + 8;
+  const uint32_t full = base + kStages * kStageBytes, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+                 acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cta_rank();
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1, units = g.tiles_a * g.tiles_b * g.splits;
@@ -89,8 +89,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; s++) {
       tc::mbar_init(acc_full + 8 * s, 1);
-      tc::mbar_init(acc_empty + 8 * s, 8);
-      tc::mbar_init(peer_acc + 8 * s, 1);
+      tc::mbar_init(acc_empty + 8 * s, 16);
     }
     tc::mbar_init(drain, 1);
     tc::mbar_init_fence();
@@ -103,6 +102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
   bool dead = false;
 
+  if (warp >= 8) tc::give_registers();
   if (warp == 8 && lane == 0) {               // loads this CTA's half of both operands
     uint32_t it = 0;
     for (int u = first; u < units; u += step) {
@@ -128,9 +128,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int u = first; u < units && !dead; u += step) {
       const Unit w = unit_at(g, u);
       for (int k = w.k0; k < w.k1 && !dead; k += g.chunk, ch++) {
-        const uint32_t set = ch & 1, ph = ((ch >> 1) & 1) ^ 1;
-        tc::mbar_wait(acc_empty + 8 * set, ph, dead);
-        tc::mbar_wait(peer_acc + 8 * set, ph, dead);
+        const uint32_t set = ch & 1;
+        tc::mbar_wait(acc_empty + 8 * set, ((ch >> 1) & 1) ^ 1, dead);
         tc::fence_after();
         const int n = min(g.chunk, w.k1 - k);
         for (int i = 0; i < n; i++, it++) {
@@ -156,17 +155,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool late = false;                        // everything issued ends before the memory is given back
     tc::commit_here<2>(drain);
     tc::mbar_wait(drain, 0, late);
-  } else if (warp == 10 && lane == 0 && rank == 1) {  // tells the issuing CTA that this CTA's accumulators are drained
-    uint32_t ch = 0;
-    for (int u = first; u < units; u += step) {
-      const Unit w = unit_at(g, u);
-      for (int k = w.k0; k < w.k1; k += g.chunk, ch++) {
-        const uint32_t set = ch & 1;
-        tc::mbar_wait(acc_empty + 8 * set, (ch >> 1) & 1, dead);
-        if (!dead) tc::mbar_arrive_lead(peer_acc + 8 * set);
-      }
-    }
   } else if (warp < 8) {
+    tc::take_registers();
     const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * 128;
     uint32_t ch = 0;
     for (int u = first; u < units; u += step) {
@@ -177,23 +167,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int ra = w.ta * 256 + rank * 128 + (warp & 3) * 32 + lane, rb = w.tb * 256 + (warp >> 2) * 128;
       for (int k = w.k0; k < w.k1; k += g.chunk, ch++) {
         const uint32_t set = ch & 1;
-        const bool last = k + g.chunk >= w.k1;
         tc::mbar_wait(acc_full + 8 * set, (ch >> 1) & 1, dead);
         __syncwarp();
         tc::fence_after();
+        float v[2][16];
+        tc::tmem_load16(mine + set * 256, v[0]);
 #pragma unroll
         for (int j = 0; j < 128; j += 16) {
-          float v[16];
-          tc::tmem_load16(mine + set * 256 + j, v);
           tc::tmem_wait();
+          if (j + 16 < 128) tc::tmem_load16(mine + set * 256 + j + 16, v[(j >> 4) + 1 & 1]);
 #pragma unroll
-          for (int x = 0; x < 16; x++) Ep::add(sum[j + x], v[x]);
-          if (last) ep.store(ra, rb + j, &sum[j], w.split);
+          for (int x = 0; x < 16; x++) Ep::add(sum[j + x], v[(j >> 4) & 1][x]);
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(acc_empty + 8 * set);
+        if (lane == 0) tc::mbar_arrive_lead(acc_empty + 8 * set);
       }
+      // the matrix unit has both sets to go on with meanwhile
+#pragma unroll
+      for (int j = 0; j < 128; j += 16) ep.store(ra, rb + j, &sum[j], w.split);
     }
   }
   __syncwarp();

@@ -52,9 +52,9 @@ inline int tensor_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_
 }
 
 // Moves the registers of a block of three warpgroups, 168 a thread at launch, from the third
-// to the two that hold accumulators: 2 * 232 + 40 = 3 * 168.
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 232;"); }
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 40;"); }
+// to the two that hold sums: 2 * 224 + 56 = 3 * 168.
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -76,13 +76,13 @@ __device__ __forceinline__ void mbar_init_fence() {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrives on the barrier at the same offset in CTA 0 of the cluster.  The release covers what
-// this thread has seen, so a thread that waits on its own CTA's barrier and then calls this
-// passes the whole CTA's work on.
+// Arrives on the barrier at the same offset in CTA 0 of the pair.  Relaxed: it orders no
+// memory accesses.  What it announces are tensor-memory reads, which are complete (tmem_wait)
+// and ordered by the fence before it.  A release at cluster scope costs a microsecond here.
 __device__ __forceinline__ void mbar_arrive_lead(uint32_t bar) {
   asm volatile(
       "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, 0;\n"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar)
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {

@@ -30,11 +30,11 @@ SYMBOLS = {
     "mcemu_rmsnorm_backward": (_I, [_I] * 4 + [_V, _L] * 5 + [_V, _V, _V, _L, _V, _V, _Z, _V]),
     "mcemu_rmsnorm_backward_workspace": (_Z, [_I] * 2),
     "mcemu_int8_linear": (_I, [_I] * 3 + [_V, _L, _V, _V, _L, _V, _V, _I, _V, _L, _V, _Z, _V]),
-    "mcemu_int8_linear_workspace": (_Z, [_I] * 4),
+    "mcemu_int8_linear_workspace": (_Z, [_I] * 3),
     "mcemu_act8_compress": (_I, [_I] * 3 + [_V, _L] * 3 + [_V]),
     "mcemu_act8_expand": (_I, [_I] * 3 + [_V, _L] * 3 + [_V]),
     "mcemu_act8_wgrad": (_I, [_I] * 3 + [_V, _L] * 3 + [_I, _I, _V, _L, _V, _Z, _V]),
-    "mcemu_act8_wgrad_workspace": (_Z, [_I] * 3),
+    "mcemu_act8_wgrad_workspace": (_Z, [_I] * 4),
     "mcemu_ops_check": (_I, [_V]),
 }
 _FMT_OF = {torch.float16: FMT["fp16"], torch.bfloat16: FMT["bf16"], torch.float32: FMT["fp32"]}
@@ -209,8 +209,7 @@ def int8_linear(x, sx, weight, sw, bias=None, out: str = "bf16", y=None, workspa
     if y is None:
         y = torch.empty((M, N), dtype=dt, device=x.device)
     py, ldy = _matrix(w, "y", y, (dt,), (M, N))
-    ws, pws, nws = _workspace(lib().mcemu_int8_linear_workspace(M, N, K, int((px | ldx | pw | ldw) % 16 == 0)), x,
-                             workspace)
+    ws, pws, nws = _workspace(lib().mcemu_int8_linear_workspace(M, N, K), x, workspace)
     st = _same_device(w, x, weight, sx, sw, bias, y, ws)
     _run(w, "mcemu_int8_linear", M, N, K, px, ldx, psx, pw, ldw, psw, pb, INT32 if out == "int32" else FMT[out], py, ldy,
          pws, nws, st)
@@ -269,7 +268,8 @@ def act8_wgrad(dy, q, e, out: str = "fp32", dW=None, accumulate: bool = False, w
     if dW is None:
         dW = torch.empty((N, K), dtype=_DTYPE[out], device=dy.device)
     pd, ldd = _matrix(w, "dW", dW, (_DTYPE[out],), (N, K))
-    ws, pws, nws = _workspace(lib().mcemu_act8_wgrad_workspace(T, N, K), dy, workspace)
+    ws, pws, nws = _workspace(lib().mcemu_act8_wgrad_workspace(T, N, K, int(pdy % 16 == 0 and lddy % 8 == 0)), dy,
+                             workspace)
     st = _same_device(w, dy, q, e, dW, ws)
     _run(w, "mcemu_act8_wgrad", T, N, K, pdy, lddy, pq, ldq, pe, lde, FMT[out], int(bool(accumulate)), pd, ldd, pws,
          nws, st)

@@ -84,14 +84,12 @@ size_t mcemu_rmsnorm_backward_workspace(int T, int H);
  * acc itself; sx, sw and bias are then NULL.  x [M][K] (a token a row), w [N][K]
  * (a channel a row), sx [M], sw [N], y [M][N].  K <= 131071, so that no sum
  * overflows (else UNSUPPORTED); K = 0 gives sums of 0.
- * workspace: mcemu_int8_linear_workspace(M, N, K, rows_aligned) bytes, 16-byte
- * aligned; may be NULL where that is 0.  rows_aligned: 1 when every row of x and
- * of w starts on a 16-byte boundary (both pointers and leading dimensions are
- * multiples of 16), which needs less. */
+ * workspace: mcemu_int8_linear_workspace(M, N, K) bytes, 16-byte aligned; may be
+ * NULL where that is 0. */
 int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t ldx, const float *sx, const int8_t *w,
                       int64_t ldw, const float *sw, const float *bias, int out_fmt, void *y, int64_t ldy,
                       void *workspace, size_t ws_bytes, void *stream);
-size_t mcemu_int8_linear_workspace(int M, int N, int K, int rows_aligned);
+size_t mcemu_int8_linear_workspace(int M, int N, int K);
 
 /* ---- activation checkpoints ------------------------------------------------- */
 /* Elements of a row that share one exponent; a row of H has ceil(H / 128). */
@@ -113,12 +111,14 @@ int mcemu_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t ldq, const
  * accumulate = 1, FP32 only), for a linear layer y = x W^T with W [N][K] whose
  * input x [T][K] was kept as a checkpoint.  dy is BF16 [T][N]; dW is FP32 or BF16
  * [N][K].  Products are exact, sums are held in fp32, the result is rounded once.
- * workspace: mcemu_act8_wgrad_workspace(T, N, K) bytes, 16-byte aligned; may be
- * NULL where that is 0. */
+ * workspace: mcemu_act8_wgrad_workspace(T, N, K, dy_rows_aligned) bytes, 16-byte
+ * aligned; may be NULL where that is 0.  dy_rows_aligned: 1 when every row of dy
+ * starts on a 16-byte boundary (the pointer is a multiple of 16, lddy of 8),
+ * which needs less. */
 int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t lddy, const int8_t *q, int64_t ldq,
                      const int8_t *e, int64_t lde, int out_fmt, int accumulate, void *dW, int64_t lddw,
                      void *workspace, size_t ws_bytes, void *stream);
-size_t mcemu_act8_wgrad_workspace(int T, int N, int K);
+size_t mcemu_act8_wgrad_workspace(int T, int N, int K, int dy_rows_aligned);
 
 /* Waits for `stream`.  MCEMU_ERR_TIMEOUT when a wait inside one of the product
  * kernels gave up on the current device since the last call of this function
