@@ -33,64 +33,79 @@ __device__ __forceinline__ float inverse_of(int e) {
   return e == MCEMU_ACT8_NAN ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-// One warp to 32 * VEC consecutive elements of a row (VEC 8: two blocks, VEC 4: one), so
-// that 128 / VEC lanes share a block.
+// blockDim.x * VEC columns by blockDim.y * kRows rows to a block of 256 threads, kRows rows to a
+// thread so that as many loads are in flight; 128 / VEC neighbouring lanes share a block of 128.
+constexpr int kRows = 4;
+
 template <class T, int VEC>
-__global__ void __launch_bounds__(256) compress_kernel(int64_t tasks, int per_row, int H, const T *__restrict__ x,
-                                                       int64_t ldx, int8_t *__restrict__ q, int64_t ldq,
-                                                       int8_t *__restrict__ e, int64_t lde) {
-  const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (task >= tasks) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = task / per_row;
-  const int i = ((int)(task - row * per_row) * 32 + lane) * VEC;
-  const bool in = i < H;
-  Vec<T, VEC> v;
-  float amax = 0.f;
-  if (in) {
-    v = load_vec<T, VEC>(x + row * ldx + i);
+__global__ void __launch_bounds__(256) compress_kernel(int T_, int H, const T *__restrict__ x, int64_t ldx,
+                                                       int8_t *__restrict__ q, int64_t ldq, int8_t *__restrict__ e,
+                                                       int64_t lde) {
+  const int i = ((int)(blockIdx.y * blockDim.x) + threadIdx.x) * VEC;
+  const int64_t row0 = (int64_t)blockIdx.x * (blockDim.y * kRows) + threadIdx.y;
+  Vec<T, VEC> v[kRows];
+  bool in[kRows];
 #pragma unroll
-    for (int j = 0; j < VEC; j++) amax = max_nan(amax, fabsf(to_f(v.v[j])));
+  for (int r = 0; r < kRows; r++) {
+    const int64_t row = row0 + r * blockDim.y;
+    in[r] = i < H && row < T_;
+    if (in[r]) v[r] = load_vec<T, VEC>(x + row * ldx + i);
   }
 #pragma unroll
-  for (int o = kBlock / VEC / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  if (!in) return;
-  const int ex = exponent_of(amax, kTopExp<T>);
-  const float inv = inverse_of(ex);
-  Vec<int8_t, VEC> o;
+  for (int r = 0; r < kRows; r++) {
+    const int64_t row = row0 + r * blockDim.y;
+    float amax = 0.f;
+    if (in[r]) {
 #pragma unroll
-  for (int j = 0; j < VEC; j++) o.v[j] = code_of(to_f(v.v[j]), inv);
-  store_vec(q + row * ldq + i, o);
-  if (i % kBlock == 0) e[row * lde + i / kBlock] = (int8_t)ex;
+      for (int j = 0; j < VEC; j++) amax = max_nan(amax, fabsf(to_f(v[r].v[j])));
+    }
+#pragma unroll
+    for (int o = kBlock / VEC / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    if (!in[r]) continue;
+    const int ex = exponent_of(amax, kTopExp<T>);
+    const float inv = inverse_of(ex);
+    Vec<int8_t, VEC> o;
+#pragma unroll
+    for (int j = 0; j < VEC; j++) o.v[j] = code_of(to_f(v[r].v[j]), inv);
+    store_vec(q + row * ldq + i, o);
+    if (i % kBlock == 0) e[row * lde + i / kBlock] = (int8_t)ex;
+  }
 }
 
-// Rows that no vector fits: a warp to a block, element by element.
+// Rows that no vector fits: a warp to a block of 128, element by element; eight blocks of a
+// row by kRows rows to 256 threads.
 template <class T>
-__global__ void __launch_bounds__(256) compress_any_kernel(int64_t tasks, int per_row, int H, const T *__restrict__ x,
-                                                           int64_t ldx, int8_t *__restrict__ q, int64_t ldq,
-                                                           int8_t *__restrict__ e, int64_t lde) {
-  const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (task >= tasks) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = task / per_row;
-  const int b = (int)(task - row * per_row);
-  float v[4], amax = 0.f;
+__global__ void __launch_bounds__(256) compress_any_kernel(int T_, int H, const T *__restrict__ x, int64_t ldx,
+                                                           int8_t *__restrict__ q, int64_t ldq, int8_t *__restrict__ e,
+                                                           int64_t lde) {
+  const int lane = threadIdx.x & 31, b = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int64_t row0 = (int64_t)blockIdx.x * kRows;
+  if (b * kBlock >= H) return;
+  T v[kRows][4];
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int i = b * kBlock + j * 32 + lane;
-    v[j] = i < H ? to_f(x[row * ldx + i]) : 0.f;
+  for (int r = 0; r < kRows; r++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int i = b * kBlock + j * 32 + lane;
+      v[r][j] = i < H && row0 + r < T_ ? x[(row0 + r) * ldx + i] : from_f<T>(0.f);
+    }
+#pragma unroll
+  for (int r = 0; r < kRows; r++) {
+    const int64_t row = row0 + r;
+    if (row >= T_) break;
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; j++) amax = max_nan(amax, fabsf(to_f(v[r][j])));
+    amax = warp_max(amax);
+    const int ex = exponent_of(amax, kTopExp<T>);
+    const float inv = inverse_of(ex);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int i = b * kBlock + j * 32 + lane;
+      if (i < H) q[row * ldq + i] = code_of(to_f(v[r][j]), inv);
+    }
+    if (lane == 0) e[row * lde + b] = (int8_t)ex;
   }
-#pragma unroll
-  for (int j = 0; j < 4; j++) amax = max_nan(amax, fabsf(v[j]));
-  amax = warp_max(amax);
-  const int ex = exponent_of(amax, kTopExp<T>);
-  const float inv = inverse_of(ex);
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int i = b * kBlock + j * 32 + lane;
-    if (i < H) q[row * ldq + i] = code_of(v[j], inv);
-  }
-  if (lane == 0) e[row * lde + b] = (int8_t)ex;
 }
 
 template <class T, int VEC>
@@ -116,13 +131,16 @@ int compress_typed(int T_, int H, const void *x, int64_t ldx, int8_t *q, int64_t
                    cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   if (H % V == 0 && rows16(x, ldx, sizeof(T)) && rows_on(q, ldq, 1, V)) {
-    const int per_row = (H + 32 * V - 1) / (32 * V);
-    const int64_t tasks = (int64_t)T_ * per_row;
-    compress_kernel<T, V><<<blocks_for(tasks * 32), 256, 0, st>>>(tasks, per_row, H, (const T *)x, ldx, q, ldq, e, lde);
+    const int items = H / V;
+    int tx = 32;
+    while (tx < 256 && tx < items) tx *= 2;
+    const dim3 block(tx, 256 / tx), grid((T_ + block.y * kRows - 1) / (block.y * kRows), (items + tx - 1) / tx);
+    if (grid.y > 65535) return MCEMU_ERR_UNSUPPORTED;
+    compress_kernel<T, V><<<grid, block, 0, st>>>(T_, H, (const T *)x, ldx, q, ldq, e, lde);
   } else {
-    const int per_row = (H + kBlock - 1) / kBlock;
-    const int64_t tasks = (int64_t)T_ * per_row;
-    compress_any_kernel<T><<<blocks_for(tasks * 32), 256, 0, st>>>(tasks, per_row, H, (const T *)x, ldx, q, ldq, e, lde);
+    const dim3 grid((T_ + kRows - 1) / kRows, (H + 8 * kBlock - 1) / (8 * kBlock));
+    if (grid.y > 65535) return MCEMU_ERR_UNSUPPORTED;
+    compress_any_kernel<T><<<grid, 256, 0, st>>>(T_, H, (const T *)x, ldx, q, ldq, e, lde);
   }
   return launch_status();
 }

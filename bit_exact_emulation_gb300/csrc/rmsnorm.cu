@@ -10,7 +10,8 @@ namespace mcemu {
 namespace {
 
 constexpr float kAmaxFloor = 7.88860905221011805e-31f;   // 2^-100
-constexpr int kMaxPerThread = 32;                        // row elements a thread holds
+constexpr int kMaxThreads = 512, kMaxPerThread = 32;     // threads to a row, its elements a thread holds
+constexpr int kMaxRow = kMaxThreads * kMaxPerThread;
 
 template <class T, int VEC>
 __device__ __forceinline__ void load_w(const void *w, int w32, int64_t i, float (&f)[VEC]) {
@@ -74,25 +75,6 @@ __device__ __forceinline__ float top_of(int out_fmt) {
   return out_fmt == MCEMU_INT8 ? 127.f : out_fmt == MCEMU_E4M3 ? 448.f : 57344.f;
 }
 
-// h of one vector: the stored sum with a residual, x without.
-template <class T, int VEC>
-__device__ __forceinline__ void take_h(const NormArgs &a, int64_t row, int i, float (&f)[VEC]) {
-  const Vec<T, VEC> x = load_vec<T, VEC>((const T *)a.x + row * a.ldx + i);
-  if (a.res) {
-    const Vec<T, VEC> r = load_vec<T, VEC>((const T *)a.res + row * a.ldr + i);
-    Vec<T, VEC> h;
-#pragma unroll
-    for (int j = 0; j < VEC; j++) {
-      h.v[j] = from_f<T>(to_f(x.v[j]) + to_f(r.v[j]));
-      f[j] = to_f(h.v[j]);
-    }
-    store_vec((T *)a.h + row * a.ldh + i, h);
-  } else {
-#pragma unroll
-    for (int j = 0; j < VEC; j++) f[j] = to_f(x.v[j]);
-  }
-}
-
 __device__ __forceinline__ float finish_row(const NormArgs &a, int64_t row, float sum, float mx, bool lead) {
   const float rstd = 1.f / sqrtf(sum / (float)a.H + a.eps);
   const bool narrow = a.scale && (a.out_fmt == MCEMU_INT8 || a.out_fmt == MCEMU_E4M3 || a.out_fmt == MCEMU_E5M2);
@@ -105,30 +87,42 @@ __device__ __forceinline__ float finish_row(const NormArgs &a, int64_t row, floa
 }
 
 // A row in the registers of blockDim.x threads, PER vectors of VEC elements each;
-// blockDim.y rows to a block.
-template <class T, int VEC, int PER>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
-  __shared__ float2 part[32];
+// blockDim.y rows to a block.  All of a thread's loads are issued before its first store (h
+// may lie on x or res, so the compiler would keep them in order).
+template <class T, int VEC, int PER, bool RES>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) {
+  __shared__ float2 part[kMaxThreads / 32];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < a.T;
   float v[PER][VEC];
   float sum = 0.f, mx = 0.f;
   if (live) {
+    Vec<T, VEC> x[PER], r[PER];
+    const T *px = (const T *)a.x + row * a.ldx, *pr = (const T *)a.res + row * a.ldr;
 #pragma unroll
     for (int p = 0; p < PER; p++) {
       const int i = (p * blockDim.x + threadIdx.x) * VEC;
-      if (i < a.H) take_h<T, VEC>(a, row, i, v[p]);
+      if (i < a.H) {
+        x[p] = load_vec<T, VEC>(px + i);
+        if constexpr (RES) r[p] = load_vec<T, VEC>(pr + i);
+      }
     }
 #pragma unroll
     for (int p = 0; p < PER; p++) {
       const int i = (p * blockDim.x + threadIdx.x) * VEC;
       if (i >= a.H) continue;
+      if constexpr (RES) {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) x[p].v[j] = from_f<T>(to_f(x[p].v[j]) + to_f(r[p].v[j]));
+        store_vec((T *)a.h + row * a.ldh + i, x[p]);
+      }
       float w[VEC];
       load_w<T, VEC>(a.w, a.w32, i, w);
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
-        sum = fmaf(v[p][j], v[p][j], sum);
-        v[p][j] *= w[j];
+        const float h = to_f(x[p].v[j]);
+        sum = fmaf(h, h, sum);
+        v[p][j] = h * w[j];
         mx = max_nan(mx, fabsf(v[p][j]));
       }
     }
@@ -143,27 +137,39 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
   }
 }
 
-// Rows longer than 1024 threads hold: a block to a row, h read a second time.
-template <class T>
-__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
-  __shared__ float2 part[32];
+// Longer rows: a block to a row, h read a second time.
+template <class T, int VEC>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_long_kernel(const NormArgs a) {
+  __shared__ float2 part[kMaxThreads / 32];
   const int64_t row = blockIdx.x;
   float sum = 0.f, mx = 0.f;
-  for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-    float h[1], w[1];
-    take_h<T, 1>(a, row, i, h);
-    load_w<T, 1>(a.w, a.w32, i, w);
-    sum = fmaf(h[0], h[0], sum);
-    mx = max_nan(mx, fabsf(h[0] * w[0]));
+  for (int i = threadIdx.x * VEC; i < a.H; i += blockDim.x * VEC) {
+    Vec<T, VEC> x = load_vec<T, VEC>((const T *)a.x + row * a.ldx + i);
+    if (a.res) {
+      const Vec<T, VEC> r = load_vec<T, VEC>((const T *)a.res + row * a.ldr + i);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) x.v[j] = from_f<T>(to_f(x.v[j]) + to_f(r.v[j]));
+      store_vec((T *)a.h + row * a.ldh + i, x);
+    }
+    float w[VEC];
+    load_w<T, VEC>(a.w, a.w32, i, w);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) {
+      const float h = to_f(x.v[j]);
+      sum = fmaf(h, h, sum);
+      mx = max_nan(mx, fabsf(h * w[j]));
+    }
   }
   row_reduce(sum, mx, part);
   const float mul = finish_row(a, row, sum, mx, threadIdx.x == 0);
   const T *src = a.res ? (const T *)a.h + row * a.ldh : (const T *)a.x + row * a.ldx;
-  for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-    float v[1], w[1];
-    load_w<T, 1>(a.w, a.w32, i, w);
-    v[0] = to_f(src[i]) * w[0];
-    put<T, 1>(a.out_fmt, a.y, row * a.ldy + i, v, mul);
+  for (int i = threadIdx.x * VEC; i < a.H; i += blockDim.x * VEC) {
+    const Vec<T, VEC> x = load_vec<T, VEC>(src + i);
+    float v[VEC], w[VEC];
+    load_w<T, VEC>(a.w, a.w32, i, w);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) v[j] = to_f(x.v[j]) * w[j];
+    put<T, VEC>(a.out_fmt, a.y, row * a.ldy + i, v, mul);
   }
 }
 
@@ -177,18 +183,19 @@ Shape shape_of(int T, int H, int vec, int max_per) {
   const int items = (H + vec - 1) / vec;
   const int want = T >= 2 * sm_count() ? max_per : 1;
   int per = 1;
-  while (per < max_per && (per < want || (items + per - 1) / per > 1024)) per *= 2;
+  while (per < max_per && (per < want || (items + per - 1) / per > kMaxThreads)) per *= 2;
   while (per > 1 && (items + per / 2 - 1) / (per / 2) <= 32) per /= 2;      // a warp is enough
-  int threads = ((items + per - 1) / per + 31) / 32 * 32;
+  const int threads = ((items + per - 1) / per + 31) / 32 * 32;
   int rows = threads < 256 ? 256 / threads : 1;
-  if (rows > 8) rows = 8;
   if (T < rows * sm_count()) rows = 1;
   return {per, threads, rows};
 }
 
 template <class T, int VEC, int PER>
 void go(const NormArgs &a, const Shape &s, cudaStream_t st) {
-  rmsnorm_kernel<T, VEC, PER><<<(a.T + s.rows - 1) / s.rows, dim3(s.threads, s.rows), 0, st>>>(a);
+  const dim3 grid((a.T + s.rows - 1) / s.rows), block(s.threads, s.rows);
+  if (a.res) rmsnorm_kernel<T, VEC, PER, true><<<grid, block, 0, st>>>(a);
+  else rmsnorm_kernel<T, VEC, PER, false><<<grid, block, 0, st>>>(a);
 }
 
 template <class T>
@@ -197,14 +204,15 @@ int norm_typed(const NormArgs &a, cudaStream_t st) {
   const int ob = a.out_fmt == MCEMU_INT8 || a.out_fmt == MCEMU_E4M3 || a.out_fmt == MCEMU_E5M2 ? 1 : (int)sizeof(T);
   const bool wide = a.H % V == 0 && rows16(a.x, a.ldx, sizeof(T)) && rows16(a.res, a.ldr, sizeof(T)) &&
                     rows16(a.h, a.ldh, sizeof(T)) && rows16(a.w, 0, 4) && rows_on(a.y, a.ldy, ob, V * ob);
-  if (a.H > 1024 * kMaxPerThread) {
-    rmsnorm_long_kernel<T><<<a.T, 1024, 0, st>>>(a);
+  if (a.H > kMaxRow) {
+    if (wide) rmsnorm_long_kernel<T, V><<<a.T, kMaxThreads, 0, st>>>(a);
+    else rmsnorm_long_kernel<T, 1><<<a.T, kMaxThreads, 0, st>>>(a);
   } else if (wide) {
     const Shape s = shape_of(a.T, a.H, V, kMaxPerThread / V);
     if (s.per == 1) go<T, V, 1>(a, s, st);
     else if (s.per == 2) go<T, V, 2>(a, s, st);
-    else if (s.per == 4) go<T, V, 4>(a, s, st);
-    else go<T, V, 8>(a, s, st);
+    else if (s.per == 4 || V == 8) go<T, V, 4>(a, s, st);
+    else go<T, V, 32 / V>(a, s, st);
   } else {
     const Shape s = shape_of(a.T, a.H, 1, kMaxPerThread);
     if (s.per <= 2) go<T, 1, 2>(a, s, st);

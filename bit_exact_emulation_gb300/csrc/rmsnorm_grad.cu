@@ -10,23 +10,25 @@ namespace mcemu {
 namespace {
 
 constexpr int kMaxThreads = 512, kMaxPerThread = 32;
-constexpr int kMaxRow = kMaxThreads * kMaxPerThread;   // longest row held in registers
+constexpr int kMaxRow = kMaxThreads * kMaxPerThread;   // longest row held in registers, half of it without vectors
 
-// Groups of threads that keep a part of dw each.
-int groups_of(int T, int H) {
-  const int most = H <= 1024 ? 8 * 152 : H <= 4096 ? 4 * 152 : 2 * 152;
+// Blocks, each of which keeps a part of dw: as many as are resident, where there are rows for them.
+int blocks_of(int T, int H) {
+  const int most = H <= 2048 ? 4 * 152 : 2 * 152;
   return T < most ? T : most;
 }
 
+// Sum over the threads of a row (blockDim.x, whole warps); every row of the block calls it.
 __device__ __forceinline__ float row_sum(float x, float *part) {
   x = warp_sum(x);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return x;
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+  float *mine = part + threadIdx.y * warps;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = x;
   __syncthreads();
   x = 0.f;
-  for (int i = 0; i < warps; i++) x += part[i];
-  __syncthreads();
+  for (int i = 0; i < warps; i++) x += mine[i];
   return x;
 }
 
@@ -63,21 +65,15 @@ __device__ __forceinline__ void load_w(const NormGradArgs &a, int i, float (&f)[
   for (int j = 0; j < VEC; j++) f[j] = a.w32 ? ((const float *)a.w)[i + j] : to_f(((const T *)a.w)[i + j]);
 }
 
+// The vectors of a row that a thread holds, all loaded at once.
 template <class T, int VEC, int PER, bool CKPT>
-__global__ void __launch_bounds__(kMaxThreads) grad_kernel(const NormGradArgs a, float *__restrict__ parts) {
-  __shared__ float sh[32];
-  const int group = blockIdx.x * blockDim.y + threadIdx.y, groups = gridDim.x * blockDim.y;
-  float w[PER][VEC], dw[PER][VEC];
-#pragma unroll
-  for (int p = 0; p < PER; p++) {
-    const int i = (p * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; j++) dw[p][j] = w[p][j] = 0.f;
-    if (i < a.H) load_w<T, VEC>(a, i, w[p]);
-  }
-  for (int64_t row = group; row < a.T; row += groups) {
-    Vec<T, VEC> dy[PER], dr[PER];
-    Input<T, VEC, CKPT> in[PER];
+struct Row {
+  Vec<T, VEC> dy[PER], dr[PER];
+  Input<T, VEC, CKPT> in[PER];
+  float rstd;
+  __device__ __forceinline__ void load(const NormGradArgs &a, int64_t row) {
+    if (row >= a.T) return;
+    rstd = a.rstd[row];
 #pragma unroll
     for (int p = 0; p < PER; p++) {
       const int i = (p * blockDim.x + threadIdx.x) * VEC;
@@ -87,18 +83,43 @@ __global__ void __launch_bounds__(kMaxThreads) grad_kernel(const NormGradArgs a,
         if (a.dres) dr[p] = load_vec<T, VEC>((const T *)a.dres + row * a.lddr + i);
       }
     }
-    const float rstd = a.rstd[row];
+  }
+};
+
+// blockDim.y rows at a time to a block, PER vectors of a row to a thread.  Where the registers
+// allow it the next rows are loaded before the sum over the present ones is awaited.
+template <class T, int VEC, int PER, bool CKPT>
+__global__ void __launch_bounds__(kMaxThreads, VEC * PER <= 8 ? 2 : 1)
+    grad_kernel(const NormGradArgs a, float *__restrict__ parts) {
+  __shared__ float sh[32];
+  extern __shared__ float join[];               // [blockDim.y][H] with several rows to a block
+  float dw[PER][VEC];
+#pragma unroll
+  for (int p = 0; p < PER; p++)
+#pragma unroll
+    for (int j = 0; j < VEC; j++) dw[p][j] = 0.f;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
+  constexpr bool kAhead = VEC * PER <= (VEC > 1 ? 16 : 8);
+  Row<T, VEC, PER, CKPT> cur, nxt;
+  if (kAhead) cur.load(a, row0 + threadIdx.y);
+  for (; row0 < a.T; row0 += step) {
+    const int64_t row = row0 + threadIdx.y;
+    const bool live = row < a.T;
+    if (kAhead) nxt.load(a, row + step);
+    else cur.load(a, row);
     float dot = 0.f;
 #pragma unroll
     for (int p = 0; p < PER; p++) {
       const int i = (p * blockDim.x + threadIdx.x) * VEC;
-      if (i >= a.H) continue;
-      float z[VEC];
-      in[p].get(z, rstd);
+      if (i >= a.H || !live) continue;
+      float z[VEC], w[VEC];
+      cur.in[p].get(z, cur.rstd);
+      load_w<T, VEC>(a, i, w);
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
-        const float d = to_f(dy[p].v[j]);
-        dot = fmaf(d * w[p][j], z[j], dot);
+        const float d = to_f(cur.dy[p].v[j]);
+        dot = fmaf(d * w[j], z[j], dot);
         dw[p][j] = fmaf(d, z[j], dw[p][j]);
       }
     }
@@ -106,21 +127,24 @@ __global__ void __launch_bounds__(kMaxThreads) grad_kernel(const NormGradArgs a,
 #pragma unroll
     for (int p = 0; p < PER; p++) {
       const int i = (p * blockDim.x + threadIdx.x) * VEC;
-      if (i >= a.H) continue;
-      float z[VEC];
-      in[p].get(z, rstd);
+      if (i >= a.H || !live) continue;
+      float z[VEC], w[VEC];
+      cur.in[p].get(z, cur.rstd);
+      load_w<T, VEC>(a, i, w);
       Vec<T, VEC> o;
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
-        const float g = to_f(dy[p].v[j]) * w[p][j];
-        float x = rstd * (g - z[j] * mean);
-        if (a.dres) x += to_f(dr[p].v[j]);
+        float x = cur.rstd * (to_f(cur.dy[p].v[j]) * w[j] - z[j] * mean);
+        if (a.dres) x += to_f(cur.dr[p].v[j]);
         o.v[j] = from_f<T>(x);
       }
       store_vec((T *)a.dx + row * a.lddx + i, o);
     }
+    if (kAhead) cur = nxt;
   }
-  float *mine = parts + (int64_t)group * a.H;
+  // dx may lie on dy or dres: a block only writes rows that it has read
+  const bool several = blockDim.y > 1;
+  float *mine = several ? join + (int64_t)threadIdx.y * a.H : parts + (int64_t)blockIdx.x * a.H;
 #pragma unroll
   for (int p = 0; p < PER; p++) {
     const int i = (p * blockDim.x + threadIdx.x) * VEC;
@@ -128,6 +152,13 @@ __global__ void __launch_bounds__(kMaxThreads) grad_kernel(const NormGradArgs a,
 #pragma unroll
       for (int j = 0; j < VEC; j++) mine[i + j] = dw[p][j];
     }
+  }
+  if (!several) return;
+  __syncthreads();
+  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < a.H; i += blockDim.x * blockDim.y) {
+    float s = join[i];
+    for (unsigned r = 1; r < blockDim.y; r++) s += join[r * a.H + i];
+    parts[(int64_t)blockIdx.x * a.H + i] = s;
   }
 }
 
@@ -190,29 +221,32 @@ __global__ void __launch_bounds__(256) long_grad_kernel(const NormGradArgs a, co
 }
 
 template <class T, int VEC, int PER, bool CKPT>
-void go(const NormGradArgs &a, int groups, float *parts, cudaStream_t st) {
+int go(const NormGradArgs &a, float *parts, cudaStream_t st) {
   const int items = (a.H + VEC - 1) / VEC, threads = ((items + PER - 1) / PER + 31) / 32 * 32;
-  grad_kernel<T, VEC, PER, CKPT><<<groups, dim3(threads, 1), 0, st>>>(a, parts);
+  const int rows = threads < 256 && a.H <= 1024 ? 256 / threads : 1, most = blocks_of(a.T, a.H);
+  const int blocks = (a.T + rows - 1) / rows < most ? (a.T + rows - 1) / rows : most;
+  grad_kernel<T, VEC, PER, CKPT>
+      <<<blocks, dim3(threads, rows), rows > 1 ? rows * a.H * sizeof(float) : 0, st>>>(a, parts);
+  return blocks;
 }
 
 template <class T, bool CKPT>
 int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const int groups = groups_of(a.T, a.H);
+  int groups = blocks_of(a.T, a.H);
   const bool wide = a.H % V == 0 && rows16(a.dy, a.lddy, sizeof(T)) && rows16(a.dres, a.lddr, sizeof(T)) &&
                     rows16(a.dx, a.lddx, sizeof(T)) && rows16(a.h, a.ldh, sizeof(T)) && rows_on(a.q, a.ldq, 1, V);
-  if (a.H > kMaxRow) {
+  if (a.H > (wide ? kMaxRow : kMaxRow / 2)) {
     float *mean = ws + (int64_t)groups * a.H;
     long_mean_kernel<T, CKPT><<<groups, 512, 0, st>>>(a, mean);
     long_grad_kernel<T, CKPT><<<dim3(groups, (a.H + 255) / 256), 256, 0, st>>>(a, mean, ws);
   } else if (wide) {
-    if (a.H <= 4096) go<T, V, 8 / V, CKPT>(a, groups, ws, st);
-    else if (a.H <= 8192) go<T, V, 16 / V, CKPT>(a, groups, ws, st);
-    else go<T, V, 32 / V, CKPT>(a, groups, ws, st);
+    if (a.H <= 4096) groups = go<T, V, 8 / V, CKPT>(a, ws, st);
+    else if (a.H <= 8192) groups = go<T, V, 16 / V, CKPT>(a, ws, st);
+    else groups = go<T, V, 32 / V, CKPT>(a, ws, st);
   } else {
-    if (a.H <= 4096) go<T, 1, 8, CKPT>(a, groups, ws, st);
-    else if (a.H <= 8192) go<T, 1, 16, CKPT>(a, groups, ws, st);
-    else go<T, 1, 32, CKPT>(a, groups, ws, st);
+    if (a.H <= 4096) groups = go<T, 1, 8, CKPT>(a, ws, st);
+    else groups = go<T, 1, 16, CKPT>(a, ws, st);
   }
   join_kernel<<<(a.H + 31) / 32, dim3(32, 8), 0, st>>>(ws, groups, a.H, a.dw);
   return launch_status();
@@ -226,7 +260,7 @@ int grad_any(const NormGradArgs &a, float *ws, cudaStream_t st) {
 }  // namespace
 
 size_t rmsnorm_backward_workspace(int T, int H) {
-  return ((size_t)groups_of(T, H) * H + (H > kMaxRow ? T : 0)) * sizeof(float);
+  return ((size_t)blocks_of(T, H) * H + (H > kMaxRow / 2 ? T : 0)) * sizeof(float);
 }
 
 int launch_rmsnorm_backward(int fmt, const NormGradArgs &a, void *ws, void *stream) {

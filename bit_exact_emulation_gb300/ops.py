@@ -40,6 +40,7 @@ SYMBOLS = {
 _FMT_OF = {torch.float16: FMT["fp16"], torch.bfloat16: FMT["bf16"], torch.float32: FMT["fp32"]}
 _OUT = {"int8": (FMT["int8"], torch.int8), "e4m3": (FMT["e4m3"], torch.float8_e4m3fn),
         "e5m2": (FMT["e5m2"], torch.float8_e5m2)}
+_LINEAR_OUT = {"fp16": FMT["fp16"], "bf16": FMT["bf16"], "fp32": FMT["fp32"], "int32": INT32}
 _DTYPE = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32, "int32": torch.int32}
 _lib = None
 
@@ -57,55 +58,74 @@ def lib():
     return _lib
 
 
+_empty = torch.empty
+
+
 def _bad(where: str, why: str):
     raise McemuError(1, f"{where}: {why}")
 
 
-def _matrix(where, name, t, dtypes, shape=None):
-    """Data pointer and row stride of a matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda:
-        _bad(where, f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    if shape is not None and tuple(t.shape) != shape:
-        _bad(where, f"{name} must have the shape {shape}")
-    rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+def _device(where, t):
+    """The current device, on which `t` must be."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _bad(where, "tensors must be on the current CUDA device")
+    return dev
+
+
+def _stream(dev):
+    """Torch's current stream on its current device, as the C ABI takes it."""
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):       # the same number, 3 us sooner
+    _stream = torch._C._cuda_getCurrentRawStream
+
+
+def _matrix(where, name, t, dtypes, dev, shape=None):
+    """Data pointer and row stride of a matrix on the current device whose rows are contiguous."""
+    size = t.shape
+    if len(size) != 2 or t.dtype not in dtypes or t.get_device() != dev:
+        _bad(where, f"{name} must be a 2-D tensor of {' or '.join(map(str, dtypes))} on the current device (cuda:{dev})")
+    if shape is not None and size != shape:
+        _bad(where, f"{name} must have the shape {tuple(shape)}")
+    rows, cols = size
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (one != 1 and cols > 1) or ld < cols:
         _bad(where, f"{name} must have contiguous rows that do not overlap")
     return t.data_ptr(), ld
 
 
-def _vector(where, name, t, dtypes, n):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or not t.is_cuda or (n > 1 and t.stride(0) != 1):
-        _bad(where, f"{name} must be a contiguous CUDA vector of {n} {' or '.join(str(d) for d in dtypes)}")
+def _vector(where, name, t, dtypes, dev, n):
+    if t.shape != (n,) or t.dtype not in dtypes or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
+        _bad(where, f"{name} must be a contiguous vector of {n} {' or '.join(map(str, dtypes))} on the current device "
+                    f"(cuda:{dev})")
     return t.data_ptr()
 
 
-def _same_device(where, *tensors):
-    """The current stream, once every tensor is known to lie on its device."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            _bad(where, f"tensors must be on the current device (cuda:{dev})")
-    return torch.cuda.current_stream().cuda_stream
-
-
-def _run(where, name, *args):
-    st = getattr(lib(), name)(*args)
-    if st:
-        raise McemuError(st, where)
-
-
-def _workspace(need, like, workspace):
+def _workspace(where, need, dev, workspace):
+    """(tensor to keep until the launch, pointer, bytes) of the caller's workspace or a new one."""
     if need == 0:
         return None, None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = _empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _bad(where, f"workspace must be contiguous and on the current device (cuda:{dev})")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _ckpt(where, q, e, dev, T, H):
+    pq, ldq = _matrix(where, "q", q, _I8, dev, (T, H))
+    pe, lde = _matrix(where, "e", e, _I8, dev, (T, (H + ACT8_BLOCK - 1) // ACT8_BLOCK))
+    return pq, ldq, pe, lde
 
 
 _FLOATS = tuple(_FMT_OF)
 _F32 = (torch.float32,)
 _I8 = (torch.int8,)
+_BF16 = (torch.bfloat16,)
 
 
 def rmsnorm(x, weight, eps: float, residual=None, out: str = "int8", y=None, scale=None, rstd=None, h=None):
@@ -115,38 +135,50 @@ def rmsnorm(x, weight, eps: float, residual=None, out: str = "int8", y=None, sca
     norm; or "own": y has x's type and scale is None.  h is None without a residual; it may
     be passed as x or residual to add in place.  rstd [T] is what ``rmsnorm_backward`` takes."""
     w = "rmsnorm"
-    px, ldx = _matrix(w, "x", x, _FLOATS)
-    T, H = x.shape
-    if out != "own" and out not in _OUT:
+    dev = _device(w, x)
+    dtype = x.dtype
+    px, ldx = _matrix(w, "x", x, _FLOATS, dev)
+    size = T, H = x.shape
+    fmt = _FMT_OF[dtype]
+    if out == "own":
+        out_fmt, out_dtype = fmt, dtype
+    elif out in _OUT:
+        out_fmt, out_dtype = _OUT[out]
+    else:
         _bad(w, "out must be 'int8', 'e4m3', 'e5m2' or 'own'")
-    fmt = _FMT_OF[x.dtype]
-    out_fmt, out_dtype = _OUT.get(out, (fmt, x.dtype))
-    dev = x.device
-    pw = _vector(w, "weight", weight, (x.dtype, torch.float32), H)
+    pw = _vector(w, "weight", weight, (dtype, torch.float32), dev, H)
     pr = ldr = ph = ldh = ps = 0
     if residual is not None:
-        pr, ldr = _matrix(w, "residual", residual, (x.dtype,), (T, H))
+        pr, ldr = _matrix(w, "residual", residual, (dtype,), dev, size)
         if h is None:
-            h = torch.empty((T, H), dtype=x.dtype, device=dev)
-        ph, ldh = _matrix(w, "h", h, (x.dtype,), (T, H))
+            h = _empty(size, dtype=dtype, device=dev)
+            ph, ldh = h.data_ptr(), H
+        else:
+            ph, ldh = _matrix(w, "h", h, (dtype,), dev, size)
     elif h is not None:
         _bad(w, "h is written only with a residual")
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=dev)
-    py, ldy = _matrix(w, "y", y, (out_dtype,), (T, H))
+        y = _empty(size, dtype=out_dtype, device=dev)
+        py, ldy = y.data_ptr(), H
+    else:
+        py, ldy = _matrix(w, "y", y, (out_dtype,), dev, size)
     if out == "own":
         if scale is not None:
             _bad(w, "scale is written only for 8-bit outputs")
+    elif scale is None:
+        scale = _empty(T, dtype=torch.float32, device=dev)
+        ps = scale.data_ptr()
     else:
-        if scale is None:
-            scale = torch.empty(T, dtype=torch.float32, device=dev)
-        ps = _vector(w, "scale", scale, _F32, T)
+        ps = _vector(w, "scale", scale, _F32, dev, T)
     if rstd is None:
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    pd = _vector(w, "rstd", rstd, _F32, T)
-    st = _same_device(w, x, weight, residual, h, y, scale, rstd)
-    _run(w, "mcemu_rmsnorm", fmt, _FMT_OF[weight.dtype], out_fmt, T, H, px, ldx, pr, ldr, pw, eps, ph, ldh, py, ldy,
-         ps, pd, st)
+        rstd = _empty(T, dtype=torch.float32, device=dev)
+        pd = rstd.data_ptr()
+    else:
+        pd = _vector(w, "rstd", rstd, _F32, dev, T)
+    st = (_lib or lib()).mcemu_rmsnorm(fmt, _FMT_OF[weight.dtype], out_fmt, T, H, px, ldx, pr, ldr, pw, eps, ph, ldh, py,
+                                       ldy, ps, pd, _stream(dev))
+    if st:
+        raise McemuError(st, w)
     return y, scale, rstd, h
 
 
@@ -154,31 +186,37 @@ def rmsnorm_backward(dy, weight, rstd, h=None, ckpt=None, dres=None, dx=None, dw
     """(dx, dw): gradients of the norm's input (dres, the residual path's gradient, added) and
     of its weight (fp32).  The input is given as h or as a checkpoint ckpt = (q, e)."""
     w = "rmsnorm_backward"
-    pdy, lddy = _matrix(w, "dy", dy, _FLOATS)
-    T, H = dy.shape
+    dev = _device(w, dy)
+    dtype = dy.dtype
+    pdy, lddy = _matrix(w, "dy", dy, _FLOATS, dev)
+    size = T, H = dy.shape
     if (h is None) == (ckpt is None):
         _bad(w, "the norm's input is given as h or as ckpt")
-    pw = _vector(w, "weight", weight, (dy.dtype, torch.float32), H)
-    prs = _vector(w, "rstd", rstd, _F32, T)
+    pw = _vector(w, "weight", weight, (dtype, torch.float32), dev, H)
+    prs = _vector(w, "rstd", rstd, _F32, dev, T)
     ph = ldh = pq = ldq = pe = lde = pr = ldr = 0
-    q = e = None
     if h is not None:
-        ph, ldh = _matrix(w, "h", h, (dy.dtype,), (T, H))
+        ph, ldh = _matrix(w, "h", h, (dtype,), dev, size)
     else:
-        q, e = ckpt
-        pq, ldq, pe, lde = _ckpt(w, q, e, T, H)
+        pq, ldq, pe, lde = _ckpt(w, *ckpt, dev, T, H)
     if dres is not None:
-        pr, ldr = _matrix(w, "dres", dres, (dy.dtype,), (T, H))
+        pr, ldr = _matrix(w, "dres", dres, (dtype,), dev, size)
     if dx is None:
-        dx = torch.empty((T, H), dtype=dy.dtype, device=dy.device)
-    pdx, lddx = _matrix(w, "dx", dx, (dy.dtype,), (T, H))
+        dx = _empty(size, dtype=dtype, device=dev)
+        pdx, lddx = dx.data_ptr(), H
+    else:
+        pdx, lddx = _matrix(w, "dx", dx, (dtype,), dev, size)
     if dw is None:
-        dw = torch.empty(H, dtype=torch.float32, device=dy.device)
-    pdw = _vector(w, "dw", dw, _F32, H)
-    ws, pws, nws = _workspace(lib().mcemu_rmsnorm_backward_workspace(T, H), dy, workspace)
-    st = _same_device(w, dy, weight, rstd, h, q, e, dres, dx, dw, ws)
-    _run(w, "mcemu_rmsnorm_backward", _FMT_OF[dy.dtype], _FMT_OF[weight.dtype], T, H, pdy, lddy, pr, ldr, ph, ldh, pq,
-         ldq, pe, lde, prs, pw, pdx, lddx, pdw, pws, nws, st)
+        dw = _empty(H, dtype=torch.float32, device=dev)
+        pdw = dw.data_ptr()
+    else:
+        pdw = _vector(w, "dw", dw, _F32, dev, H)
+    L = _lib or lib()
+    ws, pws, nws = _workspace(w, L.mcemu_rmsnorm_backward_workspace(T, H), dev, workspace)
+    st = L.mcemu_rmsnorm_backward(_FMT_OF[dtype], _FMT_OF[weight.dtype], T, H, pdy, lddy, pr, ldr, ph, ldh, pq, ldq, pe,
+                                  lde, prs, pw, pdx, lddx, pdw, pws, nws, _stream(dev))
+    if st:
+        raise McemuError(st, w)
     return dx, dw
 
 
@@ -187,11 +225,12 @@ def int8_linear(x, sx, weight, sw, bias=None, out: str = "bf16", y=None, workspa
     exact.  ``out`` is "bf16", "fp16" or "fp32"; "int32" gives the sums themselves (sx, sw and
     bias None)."""
     w = "int8_linear"
-    px, ldx = _matrix(w, "x", x, _I8)
+    dev = _device(w, x)
+    px, ldx = _matrix(w, "x", x, _I8, dev)
+    pw, ldw = _matrix(w, "weight", weight, _I8, dev)
     M, K = x.shape
-    pw, ldw = _matrix(w, "weight", weight, _I8)
-    N = weight.shape[0]
-    if weight.shape[1] != K:
+    N, k = weight.shape
+    if k != K:
         _bad(w, f"weight must have {K} columns")
     if out not in _DTYPE:
         _bad(w, "out must be 'bf16', 'fp16', 'fp32' or 'int32'")
@@ -199,56 +238,62 @@ def int8_linear(x, sx, weight, sw, bias=None, out: str = "bf16", y=None, workspa
     if out == "int32":
         if sx is not None or sw is not None or bias is not None:
             _bad(w, "sums in int32 take neither scales nor a bias")
+    elif sx is None or sw is None:
+        _bad(w, "scales are missing")
     else:
-        if sx is None or sw is None:
-            _bad(w, "scales are missing")
-        psx, psw = _vector(w, "sx", sx, _F32, M), _vector(w, "sw", sw, _F32, N)
+        psx, psw = _vector(w, "sx", sx, _F32, dev, M), _vector(w, "sw", sw, _F32, dev, N)
         if bias is not None:
-            pb = _vector(w, "bias", bias, _F32, N)
-    dt = _DTYPE[out]
+            pb = _vector(w, "bias", bias, _F32, dev, N)
     if y is None:
-        y = torch.empty((M, N), dtype=dt, device=x.device)
-    py, ldy = _matrix(w, "y", y, (dt,), (M, N))
-    ws, pws, nws = _workspace(lib().mcemu_int8_linear_workspace(M, N, K), x, workspace)
-    st = _same_device(w, x, weight, sx, sw, bias, y, ws)
-    _run(w, "mcemu_int8_linear", M, N, K, px, ldx, psx, pw, ldw, psw, pb, INT32 if out == "int32" else FMT[out], py, ldy,
-         pws, nws, st)
+        y = _empty((M, N), dtype=_DTYPE[out], device=dev)
+        py, ldy = y.data_ptr(), N
+    else:
+        py, ldy = _matrix(w, "y", y, (_DTYPE[out],), dev, (M, N))
+    L = _lib or lib()
+    ws, pws, nws = _workspace(w, L.mcemu_int8_linear_workspace(M, N, K), dev, workspace)
+    st = L.mcemu_int8_linear(M, N, K, px, ldx, psx, pw, ldw, psw, pb, _LINEAR_OUT[out], py, ldy, pws, nws, _stream(dev))
+    if st:
+        raise McemuError(st, w)
     return y
-
-
-def _ckpt(where, q, e, T, H):
-    pq, ldq = _matrix(where, "q", q, _I8, (T, H))
-    pe, lde = _matrix(where, "e", e, _I8, (T, -(-H // ACT8_BLOCK)))
-    return pq, ldq, pe, lde
 
 
 def act8_compress(x, q=None, e=None):
     """(q, e): int8 codes [T, H] and exponents [T, ceil(H / 128)] with x ~ q * 2^e."""
     w = "act8_compress"
-    px, ldx = _matrix(w, "x", x, _FLOATS)
-    T, H = x.shape
+    dev = _device(w, x)
+    px, ldx = _matrix(w, "x", x, _FLOATS, dev)
+    size = T, H = x.shape
+    blocks = (H + ACT8_BLOCK - 1) // ACT8_BLOCK
     if q is None:
-        q = torch.empty((T, H), dtype=torch.int8, device=x.device)
+        q = _empty(size, dtype=torch.int8, device=dev)
+        pq, ldq = q.data_ptr(), H
+    else:
+        pq, ldq = _matrix(w, "q", q, _I8, dev, size)
     if e is None:
-        e = torch.empty((T, -(-H // ACT8_BLOCK)), dtype=torch.int8, device=x.device)
-    pq, ldq, pe, lde = _ckpt(w, q, e, T, H)
-    st = _same_device(w, x, q, e)
-    _run(w, "mcemu_act8_compress", _FMT_OF[x.dtype], T, H, px, ldx, pq, ldq, pe, lde, st)
+        e = _empty((T, blocks), dtype=torch.int8, device=dev)
+        pe, lde = e.data_ptr(), blocks
+    else:
+        pe, lde = _matrix(w, "e", e, _I8, dev, (T, blocks))
+    st = (_lib or lib()).mcemu_act8_compress(_FMT_OF[x.dtype], T, H, px, ldx, pq, ldq, pe, lde, _stream(dev))
+    if st:
+        raise McemuError(st, w)
     return q, e
 
 
 def act8_expand(q, e, out: str = "bf16", x=None):
     """q * 2^e in "bf16", "fp16" or "fp32"."""
     w = "act8_expand"
+    dev = _device(w, q)
     if q.dim() != 2 or out not in ("bf16", "fp16", "fp32"):
         _bad(w, "q must be a matrix and out 'bf16', 'fp16' or 'fp32'")
     T, H = q.shape
-    pq, ldq, pe, lde = _ckpt(w, q, e, T, H)
+    pq, ldq, pe, lde = _ckpt(w, q, e, dev, T, H)
     if x is None:
-        x = torch.empty((T, H), dtype=_DTYPE[out], device=q.device)
-    px, ldx = _matrix(w, "x", x, (_DTYPE[out],), (T, H))
-    st = _same_device(w, q, e, x)
-    _run(w, "mcemu_act8_expand", FMT[out], T, H, pq, ldq, pe, lde, px, ldx, st)
+        x = _empty((T, H), dtype=_DTYPE[out], device=dev)
+    px, ldx = _matrix(w, "x", x, (_DTYPE[out],), dev, (T, H))
+    st = (_lib or lib()).mcemu_act8_expand(FMT[out], T, H, pq, ldq, pe, lde, px, ldx, _stream(dev))
+    if st:
+        raise McemuError(st, w)
     return x
 
 
@@ -257,26 +302,32 @@ def act8_wgrad(dy, q, e, out: str = "fp32", dW=None, accumulate: bool = False, w
     (bfloat16) and the checkpoint of its input [T, K].  With ``accumulate`` it is added to
     dW (fp32)."""
     w = "act8_wgrad"
-    pdy, lddy = _matrix(w, "dy", dy, (torch.bfloat16,))
+    dev = _device(w, dy)
+    pdy, lddy = _matrix(w, "dy", dy, _BF16, dev)
     T, N = dy.shape
     if q.dim() != 2 or q.shape[0] != T:
         _bad(w, f"q must be a matrix of {T} rows")
     K = q.shape[1]
-    pq, ldq, pe, lde = _ckpt(w, q, e, T, K)
+    pq, ldq, pe, lde = _ckpt(w, q, e, dev, T, K)
     if out not in ("bf16", "fp32") or (accumulate and (out != "fp32" or dW is None)):
         _bad(w, "out must be 'bf16' or 'fp32'; accumulate adds to an fp32 dW that is passed in")
     if dW is None:
-        dW = torch.empty((N, K), dtype=_DTYPE[out], device=dy.device)
-    pd, ldd = _matrix(w, "dW", dW, (_DTYPE[out],), (N, K))
-    ws, pws, nws = _workspace(lib().mcemu_act8_wgrad_workspace(T, N, K, int(pdy % 16 == 0 and lddy % 8 == 0)), dy,
-                             workspace)
-    st = _same_device(w, dy, q, e, dW, ws)
-    _run(w, "mcemu_act8_wgrad", T, N, K, pdy, lddy, pq, ldq, pe, lde, FMT[out], int(bool(accumulate)), pd, ldd, pws,
-         nws, st)
+        dW = _empty((N, K), dtype=_DTYPE[out], device=dev)
+        pd, ldd = dW.data_ptr(), K
+    else:
+        pd, ldd = _matrix(w, "dW", dW, (_DTYPE[out],), dev, (N, K))
+    L = _lib or lib()
+    ws, pws, nws = _workspace(w, L.mcemu_act8_wgrad_workspace(T, N, K, int(pdy % 16 == 0 and lddy % 8 == 0)), dev, workspace)
+    st = L.mcemu_act8_wgrad(T, N, K, pdy, lddy, pq, ldq, pe, lde, FMT[out], int(bool(accumulate)), pd, ldd, pws, nws,
+                            _stream(dev))
+    if st:
+        raise McemuError(st, w)
     return dW
 
 
 def check():
     """Waits for the current stream; raises (status 6) when a bounded wait inside one of the
     product kernels gave up since the last call, which leaves that launch's results invalid."""
-    _run("check", "mcemu_ops_check", torch.cuda.current_stream().cuda_stream)
+    st = (_lib or lib()).mcemu_ops_check(_stream(torch.cuda.current_device()))
+    if st:
+        raise McemuError(st, "check")
