@@ -25,12 +25,28 @@ __device__ __forceinline__ int exponent_of(float amax, int top) {
   const int e = (int)(u >> 23) - 133 + ((u & 0x7FFFFFu) > 0x7E0000u);
   return e < -120 ? -120 : e > top ? top : e;
 }
-__device__ __forceinline__ int8_t code_of(float x, float inv) {
-  return (int8_t)max(-127, min(127, __float2int_rn(x * inv)));
-}
 // 2^-e for e in [-120, 121]; 0 for a block that is not finite, whose codes do not matter.
 __device__ __forceinline__ float inverse_of(int e) {
   return e == MCEMU_ACT8_NAN ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
+}
+// x * 2^-e, kept within the codes' range: only a block at the top exponent can leave it.
+__device__ __forceinline__ float code_of(float x, float inv) { return fminf(fmaxf(x * inv, -127.f), 127.f); }
+
+// Largest magnitude of a vector.  16-bit types in pairs.
+template <class T, int V>
+__device__ __forceinline__ float amax_of(const Vec<T, V> &x) {
+  if constexpr (sizeof(T) == 2) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 m = __habs2(*(const T2 *)&x.v[0]);
+#pragma unroll
+    for (int i = 2; i < V; i += 2) m = __hmax2_nan(m, __habs2(*(const T2 *)&x.v[i]));
+    return max_nan(to_f(m.x), to_f(m.y));
+  } else {
+    float m = fabsf(x.v[0]);
+#pragma unroll
+    for (int i = 1; i < V; i++) m = max_nan(m, fabsf(x.v[i]));
+    return m;
+  }
 }
 
 // blockDim.x * VEC columns by blockDim.y * kRows rows to a block of 256 threads, kRows rows to a
@@ -54,19 +70,27 @@ __global__ void __launch_bounds__(256) compress_kernel(int T_, int H, const T *_
 #pragma unroll
   for (int r = 0; r < kRows; r++) {
     const int64_t row = row0 + r * blockDim.y;
-    float amax = 0.f;
-    if (in[r]) {
-#pragma unroll
-      for (int j = 0; j < VEC; j++) amax = max_nan(amax, fabsf(to_f(v[r].v[j])));
-    }
+    float amax = in[r] ? amax_of<T, VEC>(v[r]) : 0.f;
 #pragma unroll
     for (int o = kBlock / VEC / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     if (!in[r]) continue;
     const int ex = exponent_of(amax, kTopExp<T>);
     const float inv = inverse_of(ex);
     Vec<int8_t, VEC> o;
+    if (ex == kTopExp<T>) {
+      float c[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; j++) o.v[j] = code_of(to_f(v[r].v[j]), inv);
+      for (int j = 0; j < VEC; j++) c[j] = code_of(to_f(v[r].v[j]), inv);
+      o = to_int8<VEC>(c);
+    } else {
+      // a power of two scales without rounding, so that the sum with round_bits' constant may
+      // be one fused operation
+      uint32_t c[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; j++) c[j] = __float_as_uint(fmaf(to_f(v[r].v[j]), inv, 12582912.f));
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4) *(uint32_t *)&o.v[j] = bytes4(c[j], c[j + 1], c[j + 2], c[j + 3]);
+    }
     store_vec(q + row * ldq + i, o);
     if (i % kBlock == 0) e[row * lde + i / kBlock] = (int8_t)ex;
   }
@@ -102,7 +126,7 @@ __global__ void __launch_bounds__(256) compress_any_kernel(int T_, int H, const 
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       const int i = b * kBlock + j * 32 + lane;
-      if (i < H) q[row * ldq + i] = code_of(to_f(v[r][j]), inv);
+      if (i < H) q[row * ldq + i] = (int8_t)__float2int_rn(code_of(to_f(v[r][j]), inv));
     }
     if (lane == 0) e[row * lde + b] = (int8_t)ex;
   }

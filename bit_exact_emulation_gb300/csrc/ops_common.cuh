@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ops.h"
 
@@ -29,6 +30,115 @@ template <class T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec(const T *p) { return *reinterpret_cast<const Vec<T, V> *>(p); }
 template <class T, int V>
 __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &x) { *reinterpret_cast<Vec<T, V> *>(p) = x; }
+
+// Sums rounded to the type.  16-bit types in pairs: the sum of two such numbers rounds the same
+// straight to the type as through fp32 (where fp32 would round, the smaller operand lies below
+// half a step of the type).
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> add_vec(const Vec<T, V> &a, const Vec<T, V> &b) {
+  Vec<T, V> r;
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) *(T2 *)&r.v[i] = __hadd2_rn(*(const T2 *)&a.v[i], *(const T2 *)&b.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++) r.v[i] = from_f<T>(to_f(a.v[i]) + to_f(b.v[i]));
+  }
+  return r;
+}
+
+// Numbers of at most 2^22 in magnitude rounded to integers (ties to even) in the low bits of
+// the result: 1.5 * 2^23 puts the units digit last.  Two full-rate instructions where a
+// conversion is a quarter-rate one.
+__device__ __forceinline__ uint32_t round_bits(float x) { return __float_as_uint(__fadd_rn(x, 12582912.f)); }
+// Four of them to bytes.
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// V numbers of at most 127 in magnitude to signed bytes (a NaN gives some byte).
+template <int V>
+__device__ __forceinline__ Vec<int8_t, V> to_int8(const float (&x)[V]) {
+  Vec<int8_t, V> r;
+  if constexpr (V == 1) {
+    r.v[0] = (int8_t)__float2int_rn(x[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *(uint32_t *)&r.v[i] = bytes4(round_bits(x[i]), round_bits(x[i + 1]), round_bits(x[i + 2]), round_bits(x[i + 3]));
+  }
+  return r;
+}
+
+// V signed bytes to fp32, exactly: a byte plus 128 as the last digits of 2^23, less 2^23 + 128.
+template <int V>
+__device__ __forceinline__ void bytes_to_f(const Vec<int8_t, V> &q, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = (float)q.v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const uint32_t b = *(const uint32_t *)&q.v[i] ^ 0x80808080u;
+#pragma unroll
+      for (int j = 0; j < 4; j++) f[i + j] = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + j)) - 8388736.f;
+    }
+  }
+}
+
+// Elements i .. i + V - 1 of a row of n.  With SHIFT the vectors of a row start on 16-byte
+// boundaries of memory and not of the row, so that the first and the last may lie partly outside
+// it (zeros there, nothing written); i may be negative.
+template <class T, int V, bool SHIFT>
+__device__ __forceinline__ Vec<T, V> load_part(const T *row, int i, int n) {
+  if (!SHIFT || (i >= 0 && i + V <= n)) return load_vec<T, V>(row + i);
+  Vec<T, V> x;
+#pragma unroll
+  for (int j = 0; j < V; j++) x.v[j] = i + j >= 0 && i + j < n ? row[i + j] : T(0);
+  return x;
+}
+template <class T, int V, bool SHIFT>
+__device__ __forceinline__ void store_part(T *row, int i, int n, const Vec<T, V> &x) {
+  if (!SHIFT || (i >= 0 && i + V <= n)) {
+    store_vec(row + i, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j++)
+      if (i + j >= 0 && i + j < n) row[i + j] = x.v[j];
+  }
+}
+// V weights from the i-th on, kept in fp32 (w32) or in T.
+template <class T, int VEC>
+__device__ __forceinline__ void load_w(const void *w, int w32, int64_t i, float (&f)[VEC]) {
+  if (w32) {
+    if constexpr (VEC == 8) {
+      const Vec<float, 4> lo = load_vec<float, 4>((const float *)w + i), hi = load_vec<float, 4>((const float *)w + i + 4);
+#pragma unroll
+      for (int j = 0; j < 4; j++) f[j] = lo.v[j], f[j + 4] = hi.v[j];
+    } else {
+      const Vec<float, VEC> x = load_vec<float, VEC>((const float *)w + i);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) f[j] = x.v[j];
+    }
+  } else {
+    const Vec<T, VEC> x = load_vec<T, VEC>((const T *)w + i);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) f[j] = to_f(x.v[j]);
+  }
+}
+
+// The same for a shifted vector.
+template <class T, int V, bool SHIFT>
+__device__ __forceinline__ void load_w_part(const void *w, int w32, int i, int n, float (&f)[V]) {
+  if constexpr (!SHIFT) {
+    load_w<T, V>(w, w32, i, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      const bool in = i + j >= 0 && i + j < n;
+      f[j] = !in ? 0.f : w32 ? __ldg((const float *)w + i + j) : to_f(((const T *)w)[i + j]);
+    }
+  }
+}
 
 // Maximum that keeps a NaN (fmaxf drops it).
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -92,6 +202,20 @@ inline int launch_status() { return cudaGetLastError() == cudaSuccess ? MCEMU_OK
 inline bool rows16(const void *p, int64_t ld, int elem_bytes) {
   return !p || (((uintptr_t)p & 15) == 0 && (ld * elem_bytes) % 16 == 0);
 }
+// Whether row-major operands can be walked in vectors of v elements that start on boundaries of
+// memory common to all: the same place against the boundary in every row.
+struct Walk {
+  int v, at = -1;
+  bool ok = true;
+  int64_t step = 0;
+  void add(const void *p, int64_t ld, int elem_bytes) {
+    if (!p) return;
+    const int here = (int)(((uintptr_t)p / elem_bytes) % v), s = (int)(ld % v);
+    if (at < 0) at = here, step = s;
+    else if (at != here || step != s) ok = false;
+  }
+  bool shifted() const { return at != 0 || step != 0; }
+};
 // The same for boundaries of n bytes.
 inline bool rows_on(const void *p, int64_t ld, int elem_bytes, int n) {
   return !p || (((uintptr_t)p & (n - 1)) == 0 && (ld * elem_bytes) % n == 0);

@@ -10,27 +10,9 @@ namespace mcemu {
 namespace {
 
 constexpr float kAmaxFloor = 7.88860905221011805e-31f;   // 2^-100
-constexpr int kMaxThreads = 512, kMaxPerThread = 32;     // threads to a row, its elements a thread holds
-constexpr int kMaxRow = kMaxThreads * kMaxPerThread;
-
-template <class T, int VEC>
-__device__ __forceinline__ void load_w(const void *w, int w32, int64_t i, float (&f)[VEC]) {
-  if (w32) {
-    if constexpr (VEC == 8) {
-      const Vec<float, 4> lo = load_vec<float, 4>((const float *)w + i), hi = load_vec<float, 4>((const float *)w + i + 4);
-#pragma unroll
-      for (int j = 0; j < 4; j++) f[j] = lo.v[j], f[j + 4] = hi.v[j];
-    } else {
-      const Vec<float, VEC> x = load_vec<float, VEC>((const float *)w + i);
-#pragma unroll
-      for (int j = 0; j < VEC; j++) f[j] = x.v[j];
-    }
-  } else {
-    const Vec<T, VEC> x = load_vec<T, VEC>((const T *)w + i);
-#pragma unroll
-    for (int j = 0; j < VEC; j++) f[j] = to_f(x.v[j]);
-  }
-}
+constexpr int kMaxThreads = 1024;             // to a row
+// Vectors of a row that a thread holds: registers for two blocks of 512 threads at least.
+template <int VEC> constexpr int kMaxPer = VEC == 1 ? 16 : 4;
 
 // Sum and maximum over the threads of a row (blockDim.x of them, whole warps).
 __device__ __forceinline__ void row_reduce(float &sum, float &mx, float2 *part) {
@@ -49,25 +31,32 @@ __device__ __forceinline__ void row_reduce(float &sum, float &mx, float2 *part) 
   }
 }
 
-// One vector of v = h * w to the output type.
-template <class T, int VEC>
-__device__ __forceinline__ void put(int out_fmt, void *y, int64_t at, const float (&v)[VEC], float mul) {
-  if (out_fmt == MCEMU_INT8) {
-    Vec<int8_t, VEC> o;
+// One vector of the output row: v * mul in its type.
+template <class T, int VEC, bool SHIFT>
+__device__ __forceinline__ void put(const NormArgs &a, int64_t row, int i, float (&v)[VEC], float mul) {
 #pragma unroll
-    for (int j = 0; j < VEC; j++) o.v[j] = (int8_t)__float2int_rn(v[j] * mul);
-    store_vec((int8_t *)y + at, o);
-  } else if (out_fmt == MCEMU_E4M3 || out_fmt == MCEMU_E5M2) {
+  for (int j = 0; j < VEC; j++) v[j] *= mul;
+  if (a.out_fmt == MCEMU_INT8) {
+    store_part<int8_t, VEC, SHIFT>((int8_t *)a.y + row * a.ldy, i, a.H, to_int8<VEC>(v));
+  } else if (a.out_fmt == MCEMU_E4M3 || a.out_fmt == MCEMU_E5M2) {
     Vec<uint8_t, VEC> o;
+    if constexpr (VEC == 1) {
+      o.v[0] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, a.out_fmt == MCEMU_E4M3 ? __NV_E4M3 : __NV_E5M2);
+    } else if (a.out_fmt == MCEMU_E4M3) {
 #pragma unroll
-    for (int j = 0; j < VEC; j++)
-      o.v[j] = __nv_cvt_float_to_fp8(v[j] * mul, __NV_SATFINITE, out_fmt == MCEMU_E4M3 ? __NV_E4M3 : __NV_E5M2);
-    store_vec((uint8_t *)y + at, o);
+      for (int j = 0; j < VEC; j += 2)
+        *(uint16_t *)&o.v[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[j], v[j + 1]), __NV_SATFINITE, __NV_E4M3);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; j += 2)
+        *(uint16_t *)&o.v[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[j], v[j + 1]), __NV_SATFINITE, __NV_E5M2);
+    }
+    store_part<uint8_t, VEC, SHIFT>((uint8_t *)a.y + row * a.ldy, i, a.H, o);
   } else {
     Vec<T, VEC> o;
 #pragma unroll
-    for (int j = 0; j < VEC; j++) o.v[j] = from_f<T>(v[j] * mul);
-    store_vec((T *)y + at, o);
+    for (int j = 0; j < VEC; j++) o.v[j] = from_f<T>(v[j]);
+    store_part<T, VEC, SHIFT>((T *)a.y + row * a.ldy, i, a.H, o);
   }
 }
 
@@ -87,43 +76,44 @@ __device__ __forceinline__ float finish_row(const NormArgs &a, int64_t row, floa
 }
 
 // A row in the registers of blockDim.x threads, PER vectors of VEC elements each;
-// blockDim.y rows to a block.  All of a thread's loads are issued before its first store (h
-// may lie on x or res, so the compiler would keep them in order).
-template <class T, int VEC, int PER, bool RES>
+// blockDim.y rows to a block.  h is held in its own type and v = h * w computed twice: the
+// registers of fp32 copies would halve the threads in flight, and with them the bandwidth (98 us
+// in place of NORMNOW for 8192 x 8192 bf16 with a residual).  All of a thread's loads are issued before
+// its first store (h may lie on x or res, so the compiler would keep them in order).
+template <class T, int VEC, int PER, bool RES, bool SHIFT>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) {
   __shared__ float2 part[kMaxThreads / 32];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < a.T;
-  float v[PER][VEC];
+  const T *px = (const T *)a.x + row * a.ldx, *pr = (const T *)a.res + row * a.ldr;
+  const int back = SHIFT ? (int)(((uintptr_t)px / sizeof(T)) % VEC) : 0;     // of the first vector
+  Vec<T, VEC> h[PER];
   float sum = 0.f, mx = 0.f;
   if (live) {
-    Vec<T, VEC> x[PER], r[PER];
-    const T *px = (const T *)a.x + row * a.ldx, *pr = (const T *)a.res + row * a.ldr;
+    Vec<T, VEC> r[PER];
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = (p * blockDim.x + threadIdx.x) * VEC;
+      const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
       if (i < a.H) {
-        x[p] = load_vec<T, VEC>(px + i);
-        if constexpr (RES) r[p] = load_vec<T, VEC>(pr + i);
+        h[p] = load_part<T, VEC, SHIFT>(px, i, a.H);
+        if constexpr (RES) r[p] = load_part<T, VEC, SHIFT>(pr, i, a.H);
       }
     }
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = (p * blockDim.x + threadIdx.x) * VEC;
+      const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
       if (i >= a.H) continue;
       if constexpr (RES) {
-#pragma unroll
-        for (int j = 0; j < VEC; j++) x[p].v[j] = from_f<T>(to_f(x[p].v[j]) + to_f(r[p].v[j]));
-        store_vec((T *)a.h + row * a.ldh + i, x[p]);
+        h[p] = add_vec<T, VEC>(h[p], r[p]);
+        store_part<T, VEC, SHIFT>((T *)a.h + row * a.ldh, i, a.H, h[p]);
       }
       float w[VEC];
-      load_w<T, VEC>(a.w, a.w32, i, w);
+      load_w_part<T, VEC, SHIFT>(a.w, a.w32, i, a.H, w);
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
-        const float h = to_f(x[p].v[j]);
-        sum = fmaf(h, h, sum);
-        v[p][j] = h * w[j];
-        mx = max_nan(mx, fabsf(v[p][j]));
+        const float f = to_f(h[p].v[j]);
+        sum = fmaf(f, f, sum);
+        mx = max_nan(mx, fabsf(f * w[j]));
       }
     }
   }
@@ -132,8 +122,13 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) 
   const float mul = finish_row(a, row, sum, mx, threadIdx.x == 0);
 #pragma unroll
   for (int p = 0; p < PER; p++) {
-    const int i = (p * blockDim.x + threadIdx.x) * VEC;
-    if (i < a.H) put<T, VEC>(a.out_fmt, a.y, row * a.ldy + i, v[p], mul);
+    const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
+    if (i >= a.H) continue;
+    float w[VEC];
+    load_w_part<T, VEC, SHIFT>(a.w, a.w32, i, a.H, w);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) w[j] *= to_f(h[p].v[j]);
+    put<T, VEC, SHIFT>(a, row, i, w, mul);
   }
 }
 
@@ -146,9 +141,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_long_kernel(const NormArg
   for (int i = threadIdx.x * VEC; i < a.H; i += blockDim.x * VEC) {
     Vec<T, VEC> x = load_vec<T, VEC>((const T *)a.x + row * a.ldx + i);
     if (a.res) {
-      const Vec<T, VEC> r = load_vec<T, VEC>((const T *)a.res + row * a.ldr + i);
-#pragma unroll
-      for (int j = 0; j < VEC; j++) x.v[j] = from_f<T>(to_f(x.v[j]) + to_f(r.v[j]));
+      x = add_vec<T, VEC>(x, load_vec<T, VEC>((const T *)a.res + row * a.ldr + i));
       store_vec((T *)a.h + row * a.ldh + i, x);
     }
     float w[VEC];
@@ -169,18 +162,18 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_long_kernel(const NormArg
     load_w<T, VEC>(a.w, a.w32, i, w);
 #pragma unroll
     for (int j = 0; j < VEC; j++) v[j] = to_f(x.v[j]) * w[j];
-    put<T, VEC>(a.out_fmt, a.y, row * a.ldy + i, v, mul);
+    put<T, VEC, false>(a, row, i, v, mul);
   }
 }
 
 struct Shape {
   int per, threads, rows;
 };
-// Threads to a row and vectors to a thread.  Many rows: up to 32 elements a thread, so
-// that a thread has several loads in flight; few rows: as many threads as the row feeds,
-// for latency.
+// Threads to a row and vectors to a thread.  Many rows: as many vectors a thread as it can
+// hold, so that it has several loads in flight; few rows: as many threads as the row feeds, for
+// latency.
 Shape shape_of(int T, int H, int vec, int max_per) {
-  const int items = (H + vec - 1) / vec;
+  const int items = H / vec + (H % vec != 0);
   const int want = T >= 2 * sm_count() ? max_per : 1;
   int per = 1;
   while (per < max_per && (per < want || (items + per - 1) / per > kMaxThreads)) per *= 2;
@@ -191,34 +184,44 @@ Shape shape_of(int T, int H, int vec, int max_per) {
   return {per, threads, rows};
 }
 
-template <class T, int VEC, int PER>
+template <class T, int VEC, int PER, bool SHIFT>
 void go(const NormArgs &a, const Shape &s, cudaStream_t st) {
   const dim3 grid((a.T + s.rows - 1) / s.rows), block(s.threads, s.rows);
-  if (a.res) rmsnorm_kernel<T, VEC, PER, true><<<grid, block, 0, st>>>(a);
-  else rmsnorm_kernel<T, VEC, PER, false><<<grid, block, 0, st>>>(a);
+  if (a.res) rmsnorm_kernel<T, VEC, PER, true, SHIFT><<<grid, block, 0, st>>>(a);
+  else rmsnorm_kernel<T, VEC, PER, false, SHIFT><<<grid, block, 0, st>>>(a);
 }
 
 template <class T>
 int norm_typed(const NormArgs &a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int ob = a.out_fmt == MCEMU_INT8 || a.out_fmt == MCEMU_E4M3 || a.out_fmt == MCEMU_E5M2 ? 1 : (int)sizeof(T);
-  const bool wide = a.H % V == 0 && rows16(a.x, a.ldx, sizeof(T)) && rows16(a.res, a.ldr, sizeof(T)) &&
-                    rows16(a.h, a.ldh, sizeof(T)) && rows16(a.w, 0, 4) && rows_on(a.y, a.ldy, ob, V * ob);
-  if (a.H > kMaxRow) {
-    if (wide) rmsnorm_long_kernel<T, V><<<a.T, kMaxThreads, 0, st>>>(a);
-    else rmsnorm_long_kernel<T, 1><<<a.T, kMaxThreads, 0, st>>>(a);
-  } else if (wide) {
-    const Shape s = shape_of(a.T, a.H, V, kMaxPerThread / V);
-    if (s.per == 1) go<T, V, 1>(a, s, st);
-    else if (s.per == 2) go<T, V, 2>(a, s, st);
-    else if (s.per == 4 || V == 8) go<T, V, 4>(a, s, st);
-    else go<T, V, 32 / V>(a, s, st);
+  Walk walk{V};
+  walk.add(a.x, a.ldx, sizeof(T));
+  walk.add(a.res, a.ldr, sizeof(T));
+  walk.add(a.h, a.ldh, sizeof(T));
+  walk.add(a.y, a.ldy, ob);
+  const bool wide = walk.ok && !walk.shifted() && a.H % V == 0 && rows16(a.w, 0, 4);
+  // Vectors where every operand's rows lie alike against 16-byte boundaries (contiguous ones
+  // do, whatever H); 8191 x 5003 bf16 with a residual: SHIFTNOW us, one element at a time 149.
+  const bool shift = walk.ok && !wide && a.H >= 64;
+  const int vec = wide || shift ? V : 1, max_per = wide || shift ? kMaxPer<V> : kMaxPer<1>;
+  const int span = shift ? a.H + V - 1 : a.H;
+  if ((int64_t)span > (int64_t)kMaxThreads * max_per * vec) {
+    if (wide) rmsnorm_long_kernel<T, V><<<a.T, 512, 0, st>>>(a);
+    else rmsnorm_long_kernel<T, 1><<<a.T, 512, 0, st>>>(a);
+    return launch_status();
+  }
+  const Shape s = shape_of(a.T, span, vec, max_per);
+  if (wide) {
+    if (s.per == 1) go<T, V, 1, false>(a, s, st);
+    else if (s.per == 2) go<T, V, 2, false>(a, s, st);
+    else go<T, V, 4, false>(a, s, st);
+  } else if (shift) {
+    if (s.per <= 2) go<T, V, 2, true>(a, s, st);
+    else go<T, V, 4, true>(a, s, st);
   } else {
-    const Shape s = shape_of(a.T, a.H, 1, kMaxPerThread);
-    if (s.per <= 2) go<T, 1, 2>(a, s, st);
-    else if (s.per <= 8) go<T, 1, 8>(a, s, st);
-    else if (s.per == 16) go<T, 1, 16>(a, s, st);
-    else go<T, 1, 32>(a, s, st);
+    if (s.per <= 4) go<T, 1, 4, false>(a, s, st);
+    else go<T, 1, 16, false>(a, s, st);
   }
   return launch_status();
 }
