@@ -86,8 +86,10 @@ __global__ void __launch_bounds__(256) compress_kernel(int T_, int H, const T *_
       // a power of two scales without rounding, so that the sum with round_bits' constant may
       // be one fused operation
       uint32_t c[VEC];
+      float f[VEC];
+      unpack<T, VEC>(v[r], f);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) c[j] = __float_as_uint(fmaf(to_f(v[r].v[j]), inv, 12582912.f));
+      for (int j = 0; j < VEC; j++) c[j] = __float_as_uint(fmaf(f[j], inv, 12582912.f));
 #pragma unroll
       for (int j = 0; j < VEC; j += 4) *(uint32_t *)&o.v[j] = bytes4(c[j], c[j + 1], c[j + 2], c[j + 3]);
     }

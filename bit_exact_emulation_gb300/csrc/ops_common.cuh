@@ -31,6 +31,45 @@ __device__ __forceinline__ Vec<T, V> load_vec(const T *p) { return *reinterpret_
 template <class T, int V>
 __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &x) { *reinterpret_cast<Vec<T, V> *>(p) = x; }
 
+// A vector to fp32; 16-bit types a register's two halves at a time.
+template <class T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V> &x, float (&f)[V]) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const uint32_t u = *(const uint32_t *)&x.v[i];
+      f[i] = __uint_as_float(u << 16);
+      f[i + 1] = __uint_as_float(u & 0xFFFF0000u);
+    }
+  } else if constexpr (std::is_same<T, __half>::value && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 p = __half22float2(*(const __half2 *)&x.v[i]);
+      f[i] = p.x;
+      f[i + 1] = p.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++) f[i] = to_f(x.v[i]);
+  }
+}
+// fp32 rounded to the type, 16-bit types in pairs.
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> pack(const float (&f)[V]) {
+  Vec<T, V> r;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) *(__nv_bfloat162 *)&r.v[i] = __floats2bfloat162_rn(f[i], f[i + 1]);
+  } else if constexpr (std::is_same<T, __half>::value && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) *(__half2 *)&r.v[i] = __floats2half2_rn(f[i], f[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++) r.v[i] = from_f<T>(f[i]);
+  }
+  return r;
+}
+
 // Sums rounded to the type.  16-bit types in pairs: the sum of two such numbers rounds the same
 // straight to the type as through fp32 (where fp32 would round, the smaller operand lies below
 // half a step of the type).
@@ -120,25 +159,52 @@ __device__ __forceinline__ void load_w(const void *w, int w32, int64_t i, float 
       for (int j = 0; j < VEC; j++) f[j] = x.v[j];
     }
   } else {
-    const Vec<T, VEC> x = load_vec<T, VEC>((const T *)w + i);
-#pragma unroll
-    for (int j = 0; j < VEC; j++) f[j] = to_f(x.v[j]);
+    unpack<T, VEC>(load_vec<T, VEC>((const T *)w + i), f);
   }
 }
 
-// The same for a shifted vector.
+// The same for a shifted vector of 16 bytes.  Weights in T come from the two aligned pieces of
+// memory around it, where both lie within the weights.
 template <class T, int V, bool SHIFT>
 __device__ __forceinline__ void load_w_part(const void *w, int w32, int i, int n, float (&f)[V]) {
   if constexpr (!SHIFT) {
     load_w<T, V>(w, w32, i, f);
   } else {
+    const char *p = (const char *)w + (int64_t)i * (int)sizeof(T);
+    const int off = (int)((uintptr_t)p & 15);
+    const char *lo = p - off;
+    if ((!w32 || sizeof(T) == 4) && lo >= (const char *)w && lo + 32 <= (const char *)w + (int64_t)n * (int)sizeof(T)) {
+      const uint4 a = __ldg((const uint4 *)lo), b = __ldg((const uint4 *)lo + 1);
+      uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < V; j++) {
-      const bool in = i + j >= 0 && i + j < n;
-      f[j] = !in ? 0.f : w32 ? __ldg((const float *)w + i + j) : to_f(((const T *)w)[i + j]);
+      for (int k = 0; k < 6; k++) v[k] = off & 8 ? v[k + 2] : v[k];
+#pragma unroll
+      for (int k = 0; k < 5; k++) v[k] = off & 4 ? v[k + 1] : v[k];
+      Vec<T, V> x;
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        *((uint32_t *)&x.v[0] + k) = sizeof(T) == 4 ? v[k] : __funnelshift_r(v[k], v[k + 1], 8 * (off & 2));
+      unpack<T, V>(x, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j++) {
+        const bool in = i + j >= 0 && i + j < n;
+        f[j] = !in ? 0.f : w32 ? __ldg((const float *)w + i + j) : to_f(((const T *)w)[i + j]);
+      }
     }
   }
 }
+
+// Asynchronous copies of 4, 8 or 16 bytes to shared memory by the thread that reads them there.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from) {
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
 
 // Maximum that keeps a NaN (fmaxf drops it).
 __device__ __forceinline__ float max_nan(float a, float b) {

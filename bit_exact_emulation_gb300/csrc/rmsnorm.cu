@@ -53,10 +53,7 @@ __device__ __forceinline__ void put(const NormArgs &a, int64_t row, int i, float
     }
     store_part<uint8_t, VEC, SHIFT>((uint8_t *)a.y + row * a.ldy, i, a.H, o);
   } else {
-    Vec<T, VEC> o;
-#pragma unroll
-    for (int j = 0; j < VEC; j++) o.v[j] = from_f<T>(v[j]);
-    store_part<T, VEC, SHIFT>((T *)a.y + row * a.ldy, i, a.H, o);
+    store_part<T, VEC, SHIFT>((T *)a.y + row * a.ldy, i, a.H, pack<T, VEC>(v));
   }
 }
 
@@ -107,13 +104,13 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) 
         h[p] = add_vec<T, VEC>(h[p], r[p]);
         store_part<T, VEC, SHIFT>((T *)a.h + row * a.ldh, i, a.H, h[p]);
       }
-      float w[VEC];
+      float w[VEC], f[VEC];
       load_w_part<T, VEC, SHIFT>(a.w, a.w32, i, a.H, w);
+      unpack<T, VEC>(h[p], f);
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
-        const float f = to_f(h[p].v[j]);
-        sum = fmaf(f, f, sum);
-        mx = max_nan(mx, fabsf(f * w[j]));
+        sum = fmaf(f[j], f[j], sum);
+        mx = max_nan(mx, fabsf(f[j] * w[j]));
       }
     }
   }
@@ -124,10 +121,11 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) 
   for (int p = 0; p < PER; p++) {
     const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
     if (i >= a.H) continue;
-    float w[VEC];
+    float w[VEC], f[VEC];
     load_w_part<T, VEC, SHIFT>(a.w, a.w32, i, a.H, w);
+    unpack<T, VEC>(h[p], f);
 #pragma unroll
-    for (int j = 0; j < VEC; j++) w[j] *= to_f(h[p].v[j]);
+    for (int j = 0; j < VEC; j++) w[j] *= f[j];
     put<T, VEC, SHIFT>(a, row, i, w, mul);
   }
 }

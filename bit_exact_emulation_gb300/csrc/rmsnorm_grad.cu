@@ -10,23 +10,28 @@ namespace mcemu {
 namespace {
 
 constexpr int kThreads = 512;                  // of a block
-constexpr int kMaxRow = 16384;                 // longest row held in registers, half of it without vectors
 
-// Blocks, each of which keeps a part of dw: one to a multiprocessor, where there are rows for them.
-int blocks_of(int T) { return T < 152 ? T : 152; }
+// Most blocks, each of which keeps a part of dw: one to a multiprocessor, more where a block is
+// one group of threads for a short row.
+int most_blocks(int T, int H) {
+  const int per_sm = H <= 2048 ? 8 : H <= 16384 ? 16384 / H : 1, most = 152 * per_sm;
+  return T < most ? T : most;
+}
 
-// Sum over the threads of a row (blockDim.x, whole warps), which wait for one another alone.
+// Sum over the TX threads of a row (whole warps), which wait for one another alone.
+template <int TX>
 __device__ __forceinline__ float row_sum(float x, float *part) {
   x = warp_sum(x);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return x;
-  float *mine = part + threadIdx.y * warps;
-  const int bar = threadIdx.y + 1;
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"((int)blockDim.x) : "memory");
-  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = x;
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"((int)blockDim.x) : "memory");
-  x = 0.f;
-  for (int i = 0; i < warps; i++) x += mine[i];
+  if constexpr (TX > 32) {
+    float *mine = part + threadIdx.y * (TX / 32);
+    const int bar = threadIdx.y + 1;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TX) : "memory");
+    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = x;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TX) : "memory");
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < TX / 32; i++) x += mine[i];
+  }
   return x;
 }
 
@@ -37,10 +42,7 @@ struct Input {
   __device__ __forceinline__ void load(const NormGradArgs &a, int64_t row, int i) {
     h = load_part<T, VEC, SHIFT>((const T *)a.h + row * a.ldh, i, a.H);
   }
-  __device__ __forceinline__ void get(float (&f)[VEC]) const {
-#pragma unroll
-    for (int j = 0; j < VEC; j++) f[j] = to_f(h.v[j]);
-  }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const { unpack<T, VEC>(h, f); }
   __device__ __forceinline__ float scale(int, int) const { return 1.f; }
 };
 template <class T, int VEC, bool SHIFT>
@@ -59,85 +61,116 @@ struct Input<T, VEC, true, SHIFT> {
   }
 };
 
-// The vectors of a row that a thread holds, all loaded at once.
-template <class T, int VEC, int PER, bool CKPT, bool SHIFT>
-struct Row {
-  Vec<T, VEC> dy[PER], dr[PER];
-  Input<T, VEC, CKPT, SHIFT> in[PER];
-  __device__ __forceinline__ void load(const NormGradArgs &a, int64_t row, int back) {
-#pragma unroll
-    for (int p = 0; p < PER; p++) {
-      const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
-      if (i < a.H) {
-        dy[p] = load_part<T, VEC, SHIFT>((const T *)a.dy + row * a.lddy, i, a.H);
-        in[p].load(a, row, i);
-        if (a.dres) dr[p] = load_part<T, VEC, SHIFT>((const T *)a.dres + row * a.lddr, i, a.H);
-      }
-    }
-  }
+// Where column k of dw lies in shared memory: a word is left out after every eight, so that lanes
+// eight (or four) columns apart meet different banks.
+__device__ __forceinline__ int padded(int k) { return k + (k >> 3); }
+
+// blockDim.y rows at a time to a block, TX threads to a row, PER vectors of it to a thread.  The
+// groups of threads that hold a row each run on their own.  A thread copies its pieces of the next
+// row into shared memory while it works on the present one, so that loads are in flight
+// throughout without a register for them.  TX is known to the compiler, so that the vectors
+// of a row lie at fixed distances; 32 elements a thread, where the row is long enough, keep what a
+// row costs on top of its elements small.  8192 x 4096 bf16 with a residual path: GRADNOW us;
+// rows loaded to registers when their turn comes 71; 8 elements a thread and TX a variable 86.
+template <class T, int VEC, int PER, bool CKPT>
+struct Stage {                                  // of kThreads threads
+  Vec<T, VEC> dy[PER][kThreads], dr[PER][kThreads];
+  typename std::conditional<CKPT, Vec<int8_t, VEC>, Vec<T, VEC>>::type in[PER][kThreads];
 };
 
-// blockDim.y rows at a time to a block, PER vectors of a row to a thread.  The groups of
-// threads that hold a row each run on their own, so that while one waits for its sum the others
-// load or store.  Many elements a thread (32 where the row is long enough) keep what a row costs
-// on top of its elements small: 8 took 57 instructions an element, and 86 us for 8192 x 4096
-// bf16 with a residual path in place of GRADNOW.
-template <class T, int VEC, int PER, bool CKPT>
+template <class T, int VEC, int PER, int TX, bool CKPT>
 __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a, float *__restrict__ parts) {
-  __shared__ float sh[32];
-  extern __shared__ float join[];               // [H]
+  using S = Stage<T, VEC, PER, CKPT>;
+  __shared__ float sh[kThreads / 32];
+  extern __shared__ __align__(16) uint8_t raw[];
+  S *stages = (S *)raw;
+  float *join = (float *)(raw + 2 * sizeof(S));  // [H] with several rows to a block
+  const int t = threadIdx.y * TX + threadIdx.x;
   float dw[PER][VEC];
 #pragma unroll
   for (int p = 0; p < PER; p++)
 #pragma unroll
     for (int j = 0; j < VEC; j++) dw[p][j] = 0.f;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < a.T; row += step) {
-    Row<T, VEC, PER, CKPT, false> cur;
-    cur.load(a, row, 0);
-    const float rstd = a.rstd[row];
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+
+  float rstd = 0.f, rstd_next = 0.f;
+  float scale[PER], scale_next[PER];
+  const auto fetch = [&](int64_t r, S &to) {
+#pragma unroll
+    for (int p = 0; p < PER; p++) {
+      const int i = (p * TX + threadIdx.x) * VEC;
+      if (i >= a.H) continue;
+      copy_async<16>(&to.dy[p][t], (const T *)a.dy + r * a.lddy + i);
+      if (a.dres) copy_async<16>(&to.dr[p][t], (const T *)a.dres + r * a.lddr + i);
+      if constexpr (CKPT) {
+        copy_async<VEC>(&to.in[p][t], a.q + r * a.ldq + i);
+        scale_next[p] = act8_scale(a.e[r * a.lde + i / MCEMU_ACT8_BLOCK]);
+      } else {
+        copy_async<16>(&to.in[p][t], (const T *)a.h + r * a.ldh + i);
+      }
+    }
+    rstd_next = a.rstd[r];
+  };
+  if (row < a.T) fetch(row, stages[0]);
+  copy_commit();
+  for (int s = 0; row < a.T; row += step, s ^= 1) {
+    rstd = rstd_next;
+#pragma unroll
+    for (int p = 0; p < PER; p++) scale[p] = CKPT ? scale_next[p] * rstd : rstd;      // z = f * scale
+    if (row + step < a.T) fetch(row + step, stages[s ^ 1]);
+    copy_commit();
+    copy_wait<1>();
+    const S &cur = stages[s];
+    const auto get = [&](int p, float (&f)[VEC]) {
+      if constexpr (CKPT) bytes_to_f<VEC>(cur.in[p][t], f);
+      else unpack<T, VEC>(cur.in[p][t], f);
+    };
     float dot = 0.f;
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = (p * blockDim.x + threadIdx.x) * VEC;
+      const int i = (p * TX + threadIdx.x) * VEC;
       if (i >= a.H) continue;
-      float f[VEC], w[VEC], some = 0.f;
-      cur.in[p].get(f);
+      float f[VEC], w[VEC], d[VEC], some = 0.f;
+      get(p, f);
+      unpack<T, VEC>(cur.dy[p][t], d);
       load_w<T, VEC>(a.w, a.w32, i, w);
-      const float s = cur.in[p].scale(i, 0) * rstd;      // z = f * s
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
-        const float d = to_f(cur.dy[p].v[j]), z = f[j] * s;
-        some = fmaf(d * w[j], z, some);
-        dw[p][j] = fmaf(d, z, dw[p][j]);
+        const float z = f[j] * scale[p];
+        some = fmaf(d[j] * w[j], z, some);
+        dw[p][j] = fmaf(d[j], z, dw[p][j]);
       }
       dot += some;
     }
-    const float mean = row_sum(dot, sh) / (float)a.H;
+    const float mean = row_sum<TX>(dot, sh) / (float)a.H;
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = (p * blockDim.x + threadIdx.x) * VEC;
+      const int i = (p * TX + threadIdx.x) * VEC;
       if (i >= a.H) continue;
-      float f[VEC], w[VEC];
-      cur.in[p].get(f);
+      float f[VEC], w[VEC], d[VEC];
+      get(p, f);
+      unpack<T, VEC>(cur.dy[p][t], d);
       load_w<T, VEC>(a.w, a.w32, i, w);
-      const float s = cur.in[p].scale(i, 0) * rstd;
-      Vec<T, VEC> o;
 #pragma unroll
-      for (int j = 0; j < VEC; j++) {
-        const float x = rstd * fmaf(-(f[j] * s), mean, to_f(cur.dy[p].v[j]) * w[j]);
-        o.v[j] = from_f<T>(a.dres ? x + to_f(cur.dr[p].v[j]) : x);
+      for (int j = 0; j < VEC; j++) f[j] = rstd * fmaf(-(f[j] * scale[p]), mean, d[j] * w[j]);
+      if (a.dres) {
+        unpack<T, VEC>(cur.dr[p][t], d);
+#pragma unroll
+        for (int j = 0; j < VEC; j++) f[j] += d[j];
       }
-      store_vec((T *)a.dx + row * a.lddx + i, o);
+      store_vec((T *)a.dx + row * a.lddx + i, pack<T, VEC>(f));
     }
   }
+  copy_wait<0>();
   // the groups' parts of dw, added in order
+  float *mine = parts + (int64_t)blockIdx.x * a.H;
   for (int g = 0; g < (int)blockDim.y; g++) {
-    float *to = blockDim.y > 1 ? join : parts + (int64_t)blockIdx.x * a.H;
+    float *to = blockDim.y > 1 ? join : mine;
     if ((int)threadIdx.y == g) {
 #pragma unroll
       for (int p = 0; p < PER; p++) {
-        const int i = (p * blockDim.x + threadIdx.x) * VEC;
+        const int i = (p * TX + threadIdx.x) * VEC;
         if (i < a.H) {
 #pragma unroll
           for (int j = 0; j < VEC; j++) to[i + j] = g ? to[i + j] + dw[p][j] : dw[p][j];
@@ -147,8 +180,79 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
     __syncthreads();
   }
   if (blockDim.y > 1)
-    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < a.H; i += blockDim.x * blockDim.y)
-      parts[(int64_t)blockIdx.x * a.H + i] = join[i];
+    for (int i = t; i < a.H; i += TX * blockDim.y) mine[i] = join[i];
+}
+
+// Rows that do not start on 16-byte boundaries, but all alike: the vectors start on boundaries of
+// memory, the columns of a thread change from row to row, and dw is kept in shared memory by the
+// one group of threads that a block then has.
+template <class T, int VEC, int PER, int TX, bool CKPT>
+__global__ void __launch_bounds__(kThreads, 1) shifted_kernel(const NormGradArgs a, float *__restrict__ parts) {
+  __shared__ float sh[kThreads / 32];
+  extern __shared__ float join[];               // [H], padded
+  for (int i = threadIdx.x; i < padded(a.H) + 1; i += TX) join[i] = 0.f;
+  __syncthreads();
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const T *pdy = (const T *)a.dy + row * a.lddy, *pdr = (const T *)a.dres + row * a.lddr;
+    const int first = threadIdx.x * VEC - (int)(((uintptr_t)pdy / sizeof(T)) % VEC);
+    Vec<T, VEC> dy[PER], dr[PER];
+    Input<T, VEC, CKPT, true> in[PER];
+#pragma unroll
+    for (int p = 0; p < PER; p++) {
+      const int i = first + p * TX * VEC;
+      if (i < a.H) {
+        dy[p] = load_part<T, VEC, true>(pdy, i, a.H);
+        in[p].load(a, row, i);
+        if (a.dres) dr[p] = load_part<T, VEC, true>(pdr, i, a.H);
+      }
+    }
+    const float rstd = a.rstd[row];
+    float dot = 0.f;
+#pragma unroll
+    for (int p = 0; p < PER; p++) {
+      const int i = first + p * TX * VEC;
+      if (i >= a.H) continue;
+      float f[VEC], w[VEC], d[VEC], some = 0.f;
+      in[p].get(f);
+      unpack<T, VEC>(dy[p], d);
+      load_w_part<T, VEC, true>(a.w, a.w32, i, a.H, w);
+      float old[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; j++) old[j] = i + j >= 0 && i + j < a.H ? join[padded(i + j)] : 0.f;
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const float z = f[j] * (in[p].scale(i, j) * rstd);
+        some = fmaf(d[j] * w[j], z, some);
+        old[j] = fmaf(d[j], z, old[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; j++)
+        if (i + j >= 0 && i + j < a.H) join[padded(i + j)] = old[j];
+      dot += some;
+    }
+    const float mean = row_sum<TX>(dot, sh) / (float)a.H;
+#pragma unroll
+    for (int p = 0; p < PER; p++) {
+      const int i = first + p * TX * VEC;
+      if (i >= a.H) continue;
+      float f[VEC], w[VEC], d[VEC];
+      in[p].get(f);
+      unpack<T, VEC>(dy[p], d);
+      load_w_part<T, VEC, true>(a.w, a.w32, i, a.H, w);
+#pragma unroll
+      for (int j = 0; j < VEC; j++)
+        f[j] = rstd * fmaf(-(f[j] * (in[p].scale(i, j) * rstd)), mean, d[j] * w[j]);
+      if (a.dres) {
+        unpack<T, VEC>(dr[p], d);
+#pragma unroll
+        for (int j = 0; j < VEC; j++) f[j] += d[j];
+      }
+      store_part<T, VEC, true>((T *)a.dx + row * a.lddx, i, a.H, pack<T, VEC>(f));
+    }
+    __syncthreads();                            // the next row's columns belong to other threads
+  }
+  float *mine = parts + (int64_t)blockIdx.x * a.H;
+  for (int i = threadIdx.x; i < a.H; i += TX) mine[i] = join[padded(i)];
 }
 
 // dw[j] = sum over the groups of parts[group][j]: 32 columns and eight strands of groups to
@@ -169,7 +273,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
   }
 }
 
-// Rows longer than a block holds: mean(g z) of each row, then dx and parts of dw by columns.
+// Rows longer than a block holds, or whose operands lie differently in memory: mean(g z) of each row, then dx and parts of dw by columns.
 template <class T, bool CKPT>
 __global__ void __launch_bounds__(512) long_mean_kernel(const NormGradArgs a, float *__restrict__ mean) {
   __shared__ float sh[32];
@@ -185,7 +289,7 @@ __global__ void __launch_bounds__(512) long_mean_kernel(const NormGradArgs a, fl
       load_w<T, 1>(a.w, a.w32, i, w);
       dot = fmaf(to_f(((const T *)a.dy)[row * a.lddy + i]) * w[0], z[0], dot);
     }
-    dot = row_sum(dot, sh);
+    dot = row_sum<512>(dot, sh);
     if (threadIdx.x == 0) mean[row] = dot / (float)a.H;
   }
 }
@@ -211,37 +315,69 @@ __global__ void __launch_bounds__(256) long_grad_kernel(const NormGradArgs a, co
   parts[(int64_t)blockIdx.x * a.H + i] = dw;
 }
 
-template <class T, int VEC, int PER, bool CKPT>
+template <class K>
+bool allow_smem(K kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ||
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+// Blocks launched, -1 after an error.
+template <class T, int VEC, int PER, int TX, bool CKPT, bool SHIFT>
 int go(const NormGradArgs &a, float *parts, cudaStream_t st) {
-  const int items = (a.H + VEC - 1) / VEC, threads = ((items + PER - 1) / PER + 31) / 32 * 32;
-  int rows = kThreads / threads;               // as many as fit, but first a block on every multiprocessor
-  if (rows > a.T / 152) rows = a.T / 152;
-  if (rows < 1) rows = 1;
-  if (rows > 15) rows = 15;                    // barriers
-  const int need = (a.T + rows - 1) / rows, blocks = need < blocks_of(a.T) ? need : blocks_of(a.T);
-  grad_kernel<T, VEC, PER, CKPT><<<blocks, dim3(threads, rows), rows > 1 ? a.H * sizeof(float) : 0, st>>>(a, parts);
-  return blocks;
+  if constexpr (SHIFT) {
+    const int blocks = most_blocks(a.T, a.H);
+    const size_t smem = (a.H + a.H / 8 + 2) * sizeof(float);
+    if (!allow_smem(shifted_kernel<T, VEC, PER, TX, CKPT>, smem)) return -1;
+    shifted_kernel<T, VEC, PER, TX, CKPT><<<blocks, TX, smem, st>>>(a, parts);
+    return blocks;
+  } else {
+    int rows = kThreads / TX;                  // as many as fit, but first a block on every multiprocessor
+    if (rows > a.T / 152) rows = a.T / 152;
+    if (rows < 1) rows = 1;
+    if (rows > 15) rows = 15;                  // barriers
+    const int need = (a.T + rows - 1) / rows, blocks = need < 152 ? need : 152;
+    const size_t smem = 2 * sizeof(Stage<T, VEC, PER, CKPT>) + (rows > 1 ? a.H * sizeof(float) : 0);
+    if (!allow_smem(grad_kernel<T, VEC, PER, TX, CKPT>, smem)) return -1;
+    grad_kernel<T, VEC, PER, TX, CKPT><<<blocks, dim3(TX, rows), smem, st>>>(a, parts);
+    return blocks;
+  }
+}
+
+// The group of threads for rows of H columns: 32 columns a thread (16 of fp32).
+template <class T, int VEC, bool CKPT, bool SHIFT>
+int pick(const NormGradArgs &a, int span, float *parts, cudaStream_t st) {
+  constexpr int P = (VEC == 4 ? 16 : 32) / VEC;
+  if (span <= 32 * VEC) return go<T, VEC, 1, 32, CKPT, SHIFT>(a, parts, st);
+  if (span <= 32 * VEC * P) return go<T, VEC, P, 32, CKPT, SHIFT>(a, parts, st);
+  if (span <= 64 * VEC * P) return go<T, VEC, P, 64, CKPT, SHIFT>(a, parts, st);
+  if (span <= 128 * VEC * P) return go<T, VEC, P, 128, CKPT, SHIFT>(a, parts, st);
+  if (span <= 256 * VEC * P) return go<T, VEC, P, 256, CKPT, SHIFT>(a, parts, st);
+  return go<T, VEC, P, 512, CKPT, SHIFT>(a, parts, st);
 }
 
 template <class T, bool CKPT>
 int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  int groups = blocks_of(a.T);
-  const bool wide = a.H % V == 0 && rows16(a.dy, a.lddy, sizeof(T)) && rows16(a.dres, a.lddr, sizeof(T)) &&
-                    rows16(a.dx, a.lddx, sizeof(T)) && rows16(a.h, a.ldh, sizeof(T)) && rows16(a.w, 0, 4) &&
-                    rows_on(a.q, a.ldq, 1, V);
-  if (a.H > (wide ? kMaxRow : kMaxRow / 2)) {
+  constexpr int V = 16 / sizeof(T), kMost = kThreads * (V == 4 ? 16 : 32);      // columns held in registers
+  int groups = most_blocks(a.T, a.H);
+  Walk walk{V};
+  walk.add(a.dy, a.lddy, sizeof(T));
+  walk.add(a.dres, a.lddr, sizeof(T));
+  walk.add(a.dx, a.lddx, sizeof(T));
+  walk.add(a.h, a.ldh, sizeof(T));
+  walk.add(a.q, a.ldq, 1);
+  const bool wide = walk.ok && !walk.shifted() && a.H % V == 0 && rows16(a.w, 0, 4) && a.H <= kMost;
+  // Rows that lie alike against 16-byte boundaries, as contiguous ones do whatever H is.
+  const bool shift = walk.ok && !wide && a.H >= 64 && a.H + V - 1 <= kMost;
+  if (wide) {
+    groups = pick<T, V, CKPT, false>(a, a.H, ws, st);
+  } else if (shift) {
+    groups = pick<T, V, CKPT, true>(a, a.H + V - 1, ws, st);
+  } else {
     float *mean = ws + (int64_t)groups * a.H;
     long_mean_kernel<T, CKPT><<<a.T < 152 * 4 ? a.T : 152 * 4, 512, 0, st>>>(a, mean);
     long_grad_kernel<T, CKPT><<<dim3(groups, (a.H + 255) / 256), 256, 0, st>>>(a, mean, ws);
-  } else if (wide) {
-    if (a.H <= 256) groups = go<T, V, 8 / V, CKPT>(a, ws, st);
-    else if (a.H <= 512 || (V == 4 && a.H <= 8192)) groups = go<T, V, 16 / V, CKPT>(a, ws, st);
-    else groups = go<T, V, 32 / V, CKPT>(a, ws, st);
-  } else {
-    if (a.H <= 1024) groups = go<T, 1, 4, CKPT>(a, ws, st);
-    else groups = go<T, 1, 16, CKPT>(a, ws, st);
   }
+  if (groups < 0) return MCEMU_ERR_CUDA;
   join_kernel<<<(a.H + 31) / 32, dim3(32, 8), 0, st>>>(ws, groups, a.H, a.dw);
   return launch_status();
 }
@@ -254,7 +390,7 @@ int grad_any(const NormGradArgs &a, float *ws, cudaStream_t st) {
 }  // namespace
 
 size_t rmsnorm_backward_workspace(int T, int H) {
-  return ((size_t)blocks_of(T) * H + (H > kMaxRow / 2 ? T : 0)) * sizeof(float);
+  return ((size_t)most_blocks(T, H) * H + T) * sizeof(float);
 }
 
 int launch_rmsnorm_backward(int fmt, const NormGradArgs &a, void *ws, void *stream) {
