@@ -35,7 +35,8 @@ __device__ __forceinline__ float row_sum(float x, float *part) {
   return x;
 }
 
-// h of one vector, as stored or from the checkpoint: get() gives f with h = f * scale(j).
+// h of one vector, as stored or from the checkpoint: f of get() times scale1() for the elements
+// j with first(i, j), times scale2() for the others (a shifted vector may lie in two blocks of 128).
 template <class T, int VEC, bool CKPT, bool SHIFT>
 struct Input {
   Vec<T, VEC> h;
@@ -43,22 +44,26 @@ struct Input {
     h = load_part<T, VEC, SHIFT>((const T *)a.h + row * a.ldh, i, a.H);
   }
   __device__ __forceinline__ void get(float (&f)[VEC]) const { unpack<T, VEC>(h, f); }
-  __device__ __forceinline__ float scale(int, int) const { return 1.f; }
+  __device__ __forceinline__ bool first(int, int) const { return true; }
+  __device__ __forceinline__ float scale1() const { return 1.f; }
+  __device__ __forceinline__ float scale2() const { return 1.f; }
 };
 template <class T, int VEC, bool SHIFT>
 struct Input<T, VEC, true, SHIFT> {
   Vec<int8_t, VEC> q;
-  int8_t e, e2;              // of the block of 128 where the vector begins, and of the one where it ends
+  int8_t e1, e2;
   __device__ __forceinline__ void load(const NormGradArgs &a, int64_t row, int i) {
     q = load_part<int8_t, VEC, SHIFT>(a.q + row * a.ldq, i, a.H);
     const int8_t *pe = a.e + row * a.lde;
-    e = pe[max(i, 0) / MCEMU_ACT8_BLOCK];
-    e2 = SHIFT ? pe[min(i + VEC - 1, a.H - 1) / MCEMU_ACT8_BLOCK] : e;
+    e1 = pe[max(i, 0) / MCEMU_ACT8_BLOCK];
+    e2 = SHIFT ? pe[min(i + VEC - 1, a.H - 1) / MCEMU_ACT8_BLOCK] : e1;
   }
   __device__ __forceinline__ void get(float (&f)[VEC]) const { bytes_to_f<VEC>(q, f); }
-  __device__ __forceinline__ float scale(int i, int j) const {
-    return act8_scale(SHIFT && ((i + j) & (MCEMU_ACT8_BLOCK - 1)) < j ? e2 : e);
+  __device__ __forceinline__ bool first(int i, int j) const {
+    return !SHIFT || j < MCEMU_ACT8_BLOCK - (i & (MCEMU_ACT8_BLOCK - 1));
   }
+  __device__ __forceinline__ float scale1() const { return act8_scale(e1); }
+  __device__ __forceinline__ float scale2() const { return act8_scale(e2); }
 };
 
 // Where column k of dw lies in shared memory: a word is left out after every eight, so that lanes
@@ -84,13 +89,24 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
   __shared__ float sh[kThreads / 32];
   extern __shared__ __align__(16) uint8_t raw[];
   S *stages = (S *)raw;
-  float *join = (float *)(raw + 2 * sizeof(S));  // [H] with several rows to a block
+  float *join = (float *)(raw + 2 * sizeof(S));  // [H], padded, with several rows to a block
   const int t = threadIdx.y * TX + threadIdx.x;
   float dw[PER][VEC];
 #pragma unroll
   for (int p = 0; p < PER; p++)
 #pragma unroll
     for (int j = 0; j < VEC; j++) dw[p][j] = 0.f;
+  Vec<T, VEC> wv[PER];                          // weights in T stay in registers, fp32 ones are read again
+  const bool keep = !a.w32 || sizeof(T) == 4;
+#pragma unroll
+  for (int p = 0; p < PER; p++) {
+    const int i = (p * TX + threadIdx.x) * VEC;
+    if (keep && i < a.H) wv[p] = load_vec<T, VEC>((const T *)a.w + i);
+  }
+  const auto weights = [&](int p, int i, float (&w)[VEC]) {
+    if (keep) unpack<T, VEC>(wv[p], w);
+    else load_w<T, VEC>(a.w, 1, i, w);
+  };
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
 
@@ -134,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
       float f[VEC], w[VEC], d[VEC], some = 0.f;
       get(p, f);
       unpack<T, VEC>(cur.dy[p][t], d);
-      load_w<T, VEC>(a.w, a.w32, i, w);
+      weights(p, i, w);
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
         const float z = f[j] * scale[p];
@@ -151,14 +167,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
       float f[VEC], w[VEC], d[VEC];
       get(p, f);
       unpack<T, VEC>(cur.dy[p][t], d);
-      load_w<T, VEC>(a.w, a.w32, i, w);
+      weights(p, i, w);
+      // rstd * (g - z * mean) + dres, the factors of f gathered
+      const float k = -(scale[p] * mean * rstd);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) f[j] = rstd * fmaf(-(f[j] * scale[p]), mean, d[j] * w[j]);
-      if (a.dres) {
-        unpack<T, VEC>(cur.dr[p][t], d);
+      for (int j = 0; j < VEC; j++) w[j] *= d[j];
+      if (a.dres) unpack<T, VEC>(cur.dr[p][t], d);
 #pragma unroll
-        for (int j = 0; j < VEC; j++) f[j] += d[j];
-      }
+      for (int j = 0; j < VEC; j++) f[j] = fmaf(f[j], k, a.dres ? fmaf(w[j], rstd, d[j]) : w[j] * rstd);
       store_vec((T *)a.dx + row * a.lddx + i, pack<T, VEC>(f));
     }
   }
@@ -166,29 +182,31 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
   // the groups' parts of dw, added in order
   float *mine = parts + (int64_t)blockIdx.x * a.H;
   for (int g = 0; g < (int)blockDim.y; g++) {
-    float *to = blockDim.y > 1 ? join : mine;
     if ((int)threadIdx.y == g) {
 #pragma unroll
       for (int p = 0; p < PER; p++) {
         const int i = (p * TX + threadIdx.x) * VEC;
         if (i < a.H) {
 #pragma unroll
-          for (int j = 0; j < VEC; j++) to[i + j] = g ? to[i + j] + dw[p][j] : dw[p][j];
+          for (int j = 0; j < VEC; j++) {
+            if (blockDim.y > 1) join[padded(i + j)] = g ? join[padded(i + j)] + dw[p][j] : dw[p][j];
+            else mine[i + j] = dw[p][j];
+          }
         }
       }
     }
     __syncthreads();
   }
   if (blockDim.y > 1)
-    for (int i = t; i < a.H; i += TX * blockDim.y) mine[i] = join[i];
+    for (int i = t; i < a.H; i += TX * blockDim.y) mine[i] = join[padded(i)];
 }
 
 // Rows that do not start on 16-byte boundaries, but all alike: the vectors start on boundaries of
 // memory, the columns of a thread change from row to row, and dw is kept in shared memory by the
 // one group of threads that a block then has.
 template <class T, int VEC, int PER, int TX, bool CKPT>
-__global__ void __launch_bounds__(kThreads, 1) shifted_kernel(const NormGradArgs a, float *__restrict__ parts) {
-  __shared__ float sh[kThreads / 32];
+__global__ void __launch_bounds__(TX) shifted_kernel(const NormGradArgs a, float *__restrict__ parts) {
+  __shared__ float sh[32];
   extern __shared__ float join[];               // [H], padded
   for (int i = threadIdx.x; i < padded(a.H) + 1; i += TX) join[i] = 0.f;
   __syncthreads();
@@ -216,18 +234,19 @@ __global__ void __launch_bounds__(kThreads, 1) shifted_kernel(const NormGradArgs
       in[p].get(f);
       unpack<T, VEC>(dy[p], d);
       load_w_part<T, VEC, true>(a.w, a.w32, i, a.H, w);
+      const float s1 = in[p].scale1() * rstd, s2 = in[p].scale2() * rstd;
       float old[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; j++) old[j] = i + j >= 0 && i + j < a.H ? join[padded(i + j)] : 0.f;
+      for (int j = 0; j < VEC; j++) old[j] = (unsigned)(i + j) < (unsigned)a.H ? join[padded(i + j)] : 0.f;
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
-        const float z = f[j] * (in[p].scale(i, j) * rstd);
+        const float z = f[j] * (in[p].first(i, j) ? s1 : s2);
         some = fmaf(d[j] * w[j], z, some);
         old[j] = fmaf(d[j], z, old[j]);
       }
 #pragma unroll
       for (int j = 0; j < VEC; j++)
-        if (i + j >= 0 && i + j < a.H) join[padded(i + j)] = old[j];
+        if ((unsigned)(i + j) < (unsigned)a.H) join[padded(i + j)] = old[j];
       dot += some;
     }
     const float mean = row_sum<TX>(dot, sh) / (float)a.H;
@@ -239,14 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1) shifted_kernel(const NormGradArgs
       in[p].get(f);
       unpack<T, VEC>(dy[p], d);
       load_w_part<T, VEC, true>(a.w, a.w32, i, a.H, w);
+      const float k1 = -(in[p].scale1() * rstd * mean * rstd), k2 = -(in[p].scale2() * rstd * mean * rstd);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) w[j] *= d[j];
+      if (a.dres) unpack<T, VEC>(dr[p], d);
 #pragma unroll
       for (int j = 0; j < VEC; j++)
-        f[j] = rstd * fmaf(-(f[j] * (in[p].scale(i, j) * rstd)), mean, d[j] * w[j]);
-      if (a.dres) {
-        unpack<T, VEC>(dr[p], d);
-#pragma unroll
-        for (int j = 0; j < VEC; j++) f[j] += d[j];
-      }
+        f[j] = fmaf(f[j], in[p].first(i, j) ? k1 : k2, a.dres ? fmaf(w[j], rstd, d[j]) : w[j] * rstd);
       store_part<T, VEC, true>((T *)a.dx + row * a.lddx, i, a.H, pack<T, VEC>(f));
     }
     __syncthreads();                            // the next row's columns belong to other threads
@@ -285,7 +303,7 @@ __global__ void __launch_bounds__(512) long_mean_kernel(const NormGradArgs a, fl
       float z[1], w[1];
       in.load(a, row, i);
       in.get(z);
-      z[0] *= in.scale(i, 0) * rstd;
+      z[0] *= in.scale1() * rstd;
       load_w<T, 1>(a.w, a.w32, i, w);
       dot = fmaf(to_f(((const T *)a.dy)[row * a.lddy + i]) * w[0], z[0], dot);
     }
@@ -306,7 +324,7 @@ __global__ void __launch_bounds__(256) long_grad_kernel(const NormGradArgs a, co
     float z[1];
     in.load(a, row, i);
     in.get(z);
-    z[0] *= in.scale(i, 0) * rstd;
+    z[0] *= in.scale1() * rstd;
     dw = fmaf(d, z[0], dw);
     float x = rstd * (d * w[0] - z[0] * mean[row]);
     if (a.dres) x += to_f(((const T *)a.dres)[row * a.lddr + i]);
@@ -336,22 +354,25 @@ int go(const NormGradArgs &a, float *parts, cudaStream_t st) {
     if (rows < 1) rows = 1;
     if (rows > 15) rows = 15;                  // barriers
     const int need = (a.T + rows - 1) / rows, blocks = need < 152 ? need : 152;
-    const size_t smem = 2 * sizeof(Stage<T, VEC, PER, CKPT>) + (rows > 1 ? a.H * sizeof(float) : 0);
+    const size_t smem = 2 * sizeof(Stage<T, VEC, PER, CKPT>) + (rows > 1 ? (a.H + a.H / 8 + 2) * sizeof(float) : 0);
     if (!allow_smem(grad_kernel<T, VEC, PER, TX, CKPT>, smem)) return -1;
     grad_kernel<T, VEC, PER, TX, CKPT><<<blocks, dim3(TX, rows), smem, st>>>(a, parts);
     return blocks;
   }
 }
 
-// The group of threads for rows of H columns: 32 columns a thread (16 of fp32).
+// The group of threads for rows of `span` columns.  32 columns a thread (16 of fp32) from the
+// shared copies; 16 (8) with SHIFT, which has them in registers.
 template <class T, int VEC, bool CKPT, bool SHIFT>
 int pick(const NormGradArgs &a, int span, float *parts, cudaStream_t st) {
-  constexpr int P = (VEC == 4 ? 16 : 32) / VEC;
+  constexpr int P = (VEC == 4 ? 16 : 32) / VEC / (SHIFT ? 2 : 1);
   if (span <= 32 * VEC) return go<T, VEC, 1, 32, CKPT, SHIFT>(a, parts, st);
   if (span <= 32 * VEC * P) return go<T, VEC, P, 32, CKPT, SHIFT>(a, parts, st);
   if (span <= 64 * VEC * P) return go<T, VEC, P, 64, CKPT, SHIFT>(a, parts, st);
   if (span <= 128 * VEC * P) return go<T, VEC, P, 128, CKPT, SHIFT>(a, parts, st);
   if (span <= 256 * VEC * P) return go<T, VEC, P, 256, CKPT, SHIFT>(a, parts, st);
+  if constexpr (SHIFT)
+    if (span > 512 * VEC * P) return go<T, VEC, P, 1024, CKPT, SHIFT>(a, parts, st);
   return go<T, VEC, P, 512, CKPT, SHIFT>(a, parts, st);
 }
 
