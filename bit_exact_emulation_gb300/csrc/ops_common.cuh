@@ -124,27 +124,6 @@ __device__ __forceinline__ void bytes_to_f(const Vec<int8_t, V> &q, float (&f)[V
   }
 }
 
-// Elements i .. i + V - 1 of a row of n.  With SHIFT the vectors of a row start on 16-byte
-// boundaries of memory and not of the row, so that the first and the last may lie partly outside
-// it (zeros there, nothing written); i may be negative.
-template <class T, int V, bool SHIFT>
-__device__ __forceinline__ Vec<T, V> load_part(const T *row, int i, int n) {
-  if (!SHIFT || (i >= 0 && i + V <= n)) return load_vec<T, V>(row + i);
-  Vec<T, V> x;
-#pragma unroll
-  for (int j = 0; j < V; j++) x.v[j] = i + j >= 0 && i + j < n ? row[i + j] : T(0);
-  return x;
-}
-template <class T, int V, bool SHIFT>
-__device__ __forceinline__ void store_part(T *row, int i, int n, const Vec<T, V> &x) {
-  if (!SHIFT || (i >= 0 && i + V <= n)) {
-    store_vec(row + i, x);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; j++)
-      if (i + j >= 0 && i + j < n) row[i + j] = x.v[j];
-  }
-}
 // V weights from the i-th on, kept in fp32 (w32) or in T.
 template <class T, int VEC>
 __device__ __forceinline__ void load_w(const void *w, int w32, int64_t i, float (&f)[VEC]) {
@@ -160,38 +139,6 @@ __device__ __forceinline__ void load_w(const void *w, int w32, int64_t i, float 
     }
   } else {
     unpack<T, VEC>(load_vec<T, VEC>((const T *)w + i), f);
-  }
-}
-
-// The same for a shifted vector of 16 bytes.  Weights in T come from the two aligned pieces of
-// memory around it, where both lie within the weights.
-template <class T, int V, bool SHIFT>
-__device__ __forceinline__ void load_w_part(const void *w, int w32, int i, int n, float (&f)[V]) {
-  if constexpr (!SHIFT) {
-    load_w<T, V>(w, w32, i, f);
-  } else {
-    const char *p = (const char *)w + (int64_t)i * (int)sizeof(T);
-    const int off = (int)((uintptr_t)p & 15);
-    const char *lo = p - off;
-    if ((!w32 || sizeof(T) == 4) && lo >= (const char *)w && lo + 32 <= (const char *)w + (int64_t)n * (int)sizeof(T)) {
-      const uint4 a = __ldg((const uint4 *)lo), b = __ldg((const uint4 *)lo + 1);
-      uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int k = 0; k < 6; k++) v[k] = off & 8 ? v[k + 2] : v[k];
-#pragma unroll
-      for (int k = 0; k < 5; k++) v[k] = off & 4 ? v[k + 1] : v[k];
-      Vec<T, V> x;
-#pragma unroll
-      for (int k = 0; k < 4; k++)
-        *((uint32_t *)&x.v[0] + k) = sizeof(T) == 4 ? v[k] : __funnelshift_r(v[k], v[k + 1], 8 * (off & 2));
-      unpack<T, V>(x, f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; j++) {
-        const bool in = i + j >= 0 && i + j < n;
-        f[j] = !in ? 0.f : w32 ? __ldg((const float *)w + i + j) : to_f(((const T *)w)[i + j]);
-      }
-    }
   }
 }
 
@@ -268,20 +215,6 @@ inline int launch_status() { return cudaGetLastError() == cudaSuccess ? MCEMU_OK
 inline bool rows16(const void *p, int64_t ld, int elem_bytes) {
   return !p || (((uintptr_t)p & 15) == 0 && (ld * elem_bytes) % 16 == 0);
 }
-// Whether row-major operands can be walked in vectors of v elements that start on boundaries of
-// memory common to all: the same place against the boundary in every row.
-struct Walk {
-  int v, at = -1;
-  bool ok = true;
-  int64_t step = 0;
-  void add(const void *p, int64_t ld, int elem_bytes) {
-    if (!p) return;
-    const int here = (int)(((uintptr_t)p / elem_bytes) % v), s = (int)(ld % v);
-    if (at < 0) at = here, step = s;
-    else if (at != here || step != s) ok = false;
-  }
-  bool shifted() const { return at != 0 || step != 0; }
-};
 // The same for boundaries of n bytes.
 inline bool rows_on(const void *p, int64_t ld, int elem_bytes, int n) {
   return !p || (((uintptr_t)p & (n - 1)) == 0 && (ld * elem_bytes) % n == 0);

@@ -11,8 +11,8 @@ namespace {
 
 constexpr float kAmaxFloor = 7.88860905221011805e-31f;   // 2^-100
 constexpr int kMaxThreads = 1024;             // to a row
-// Vectors of a row that a thread holds: registers for two blocks of 512 threads at least.
-template <int VEC> constexpr int kMaxPer = VEC == 1 ? 16 : 4;
+constexpr int kMaxPer = 4;                    // vectors of a row that a thread holds
+constexpr int kSingles = 16;                  // elements a thread holds where no vector fits
 
 // Sum and maximum over the threads of a row (blockDim.x of them, whole warps).
 __device__ __forceinline__ void row_reduce(float &sum, float &mx, float2 *part) {
@@ -32,12 +32,12 @@ __device__ __forceinline__ void row_reduce(float &sum, float &mx, float2 *part) 
 }
 
 // One vector of the output row: v * mul in its type.
-template <class T, int VEC, bool SHIFT>
+template <class T, int VEC>
 __device__ __forceinline__ void put(const NormArgs &a, int64_t row, int i, float (&v)[VEC], float mul) {
 #pragma unroll
   for (int j = 0; j < VEC; j++) v[j] *= mul;
   if (a.out_fmt == MCEMU_INT8) {
-    store_part<int8_t, VEC, SHIFT>((int8_t *)a.y + row * a.ldy, i, a.H, to_int8<VEC>(v));
+    store_vec((int8_t *)a.y + row * a.ldy + i, to_int8<VEC>(v));
   } else if (a.out_fmt == MCEMU_E4M3 || a.out_fmt == MCEMU_E5M2) {
     Vec<uint8_t, VEC> o;
     if constexpr (VEC == 1) {
@@ -51,9 +51,9 @@ __device__ __forceinline__ void put(const NormArgs &a, int64_t row, int i, float
       for (int j = 0; j < VEC; j += 2)
         *(uint16_t *)&o.v[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[j], v[j + 1]), __NV_SATFINITE, __NV_E5M2);
     }
-    store_part<uint8_t, VEC, SHIFT>((uint8_t *)a.y + row * a.ldy, i, a.H, o);
+    store_vec((uint8_t *)a.y + row * a.ldy + i, o);
   } else {
-    store_part<T, VEC, SHIFT>((T *)a.y + row * a.ldy, i, a.H, pack<T, VEC>(v));
+    store_vec((T *)a.y + row * a.ldy + i, pack<T, VEC>(v));
   }
 }
 
@@ -77,35 +77,34 @@ __device__ __forceinline__ float finish_row(const NormArgs &a, int64_t row, floa
 // registers of fp32 copies would halve the threads in flight, and with them the bandwidth (98 us
 // in place of NORMNOW for 8192 x 8192 bf16 with a residual).  All of a thread's loads are issued before
 // its first store (h may lie on x or res, so the compiler would keep them in order).
-template <class T, int VEC, int PER, bool RES, bool SHIFT>
+template <class T, int VEC, int PER, bool RES>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) {
   __shared__ float2 part[kMaxThreads / 32];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < a.T;
   const T *px = (const T *)a.x + row * a.ldx, *pr = (const T *)a.res + row * a.ldr;
-  const int back = SHIFT ? (int)(((uintptr_t)px / sizeof(T)) % VEC) : 0;     // of the first vector
   Vec<T, VEC> h[PER];
   float sum = 0.f, mx = 0.f;
   if (live) {
     Vec<T, VEC> r[PER];
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
+      const int i = (p * blockDim.x + threadIdx.x) * VEC;
       if (i < a.H) {
-        h[p] = load_part<T, VEC, SHIFT>(px, i, a.H);
-        if constexpr (RES) r[p] = load_part<T, VEC, SHIFT>(pr, i, a.H);
+        h[p] = load_vec<T, VEC>(px + i);
+        if constexpr (RES) r[p] = load_vec<T, VEC>(pr + i);
       }
     }
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
+      const int i = (p * blockDim.x + threadIdx.x) * VEC;
       if (i >= a.H) continue;
       if constexpr (RES) {
         h[p] = add_vec<T, VEC>(h[p], r[p]);
-        store_part<T, VEC, SHIFT>((T *)a.h + row * a.ldh, i, a.H, h[p]);
+        store_vec((T *)a.h + row * a.ldh + i, h[p]);
       }
       float w[VEC], f[VEC];
-      load_w_part<T, VEC, SHIFT>(a.w, a.w32, i, a.H, w);
+      load_w<T, VEC>(a.w, a.w32, i, w);
       unpack<T, VEC>(h[p], f);
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
@@ -119,14 +118,59 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) 
   const float mul = finish_row(a, row, sum, mx, threadIdx.x == 0);
 #pragma unroll
   for (int p = 0; p < PER; p++) {
-    const int i = (p * blockDim.x + threadIdx.x) * VEC - back;
+    const int i = (p * blockDim.x + threadIdx.x) * VEC;
     if (i >= a.H) continue;
     float w[VEC], f[VEC];
-    load_w_part<T, VEC, SHIFT>(a.w, a.w32, i, a.H, w);
+    load_w<T, VEC>(a.w, a.w32, i, w);
     unpack<T, VEC>(h[p], f);
 #pragma unroll
     for (int j = 0; j < VEC; j++) w[j] *= f[j];
-    put<T, VEC, SHIFT>(a, row, i, w, mul);
+    put<T, VEC>(a, row, i, w, mul);
+  }
+}
+
+// Rows that no vector fits: one element of every TX to a thread, at distances that the compiler
+// knows (with TX a variable the address of every access is computed anew: 8191 x 5003 bf16 with a
+// residual 149 us in place of SINGLENOW).
+template <class T, int TX, bool RES>
+__global__ void __launch_bounds__(TX < 256 ? 256 : TX) single_kernel(const NormArgs a) {
+  __shared__ float2 part[kMaxThreads / 32];
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int left = row < a.T ? a.H - (int)threadIdx.x : 0;       // elements p with p * TX < left
+  const int64_t i0 = threadIdx.x;
+  const T *px = (const T *)a.x + row * a.ldx + i0, *pr = (const T *)a.res + row * a.ldr + i0;
+  T h[kSingles], r[kSingles];
+  float v[kSingles], sum = 0.f, mx = 0.f;
+#pragma unroll
+  for (int p = 0; p < kSingles; p++) {
+    if (p * TX >= left) continue;
+    h[p] = px[p * TX];
+    if constexpr (RES) r[p] = pr[p * TX];
+  }
+#pragma unroll
+  for (int p = 0; p < kSingles; p++)
+    if (p * TX < left) v[p] = a.w32 ? ((const float *)a.w)[i0 + p * TX] : to_f(((const T *)a.w)[i0 + p * TX]);
+  T *ph = (T *)a.h + row * a.ldh + i0;
+#pragma unroll
+  for (int p = 0; p < kSingles; p++) {
+    if (p * TX >= left) continue;
+    if constexpr (RES) {
+      h[p] = from_f<T>(to_f(h[p]) + to_f(r[p]));
+      ph[p * TX] = h[p];
+    }
+    const float f = to_f(h[p]);
+    sum = fmaf(f, f, sum);
+    v[p] *= f;
+    mx = max_nan(mx, fabsf(v[p]));
+  }
+  row_reduce(sum, mx, part);
+  if (row >= a.T) return;
+  const float mul = finish_row(a, row, sum, mx, threadIdx.x == 0);
+#pragma unroll
+  for (int p = 0; p < kSingles; p++) {
+    if (p * TX >= left) continue;
+    float o[1] = {v[p]};
+    put<T, 1>(a, row, (int)i0 + p * TX, o, mul);
   }
 }
 
@@ -160,67 +204,62 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_long_kernel(const NormArg
     load_w<T, VEC>(a.w, a.w32, i, w);
 #pragma unroll
     for (int j = 0; j < VEC; j++) v[j] = to_f(x.v[j]) * w[j];
-    put<T, VEC, false>(a, row, i, v, mul);
+    put<T, VEC>(a, row, i, v, mul);
   }
 }
 
-struct Shape {
-  int per, threads, rows;
-};
 // Threads to a row and vectors to a thread.  Many rows: as many vectors a thread as it can
 // hold, so that it has several loads in flight; few rows: as many threads as the row feeds, for
 // latency.
-Shape shape_of(int T, int H, int vec, int max_per) {
-  const int items = H / vec + (H % vec != 0);
-  const int want = T >= 2 * sm_count() ? max_per : 1;
-  int per = 1;
-  while (per < max_per && (per < want || (items + per - 1) / per > kMaxThreads)) per *= 2;
-  while (per > 1 && (items + per / 2 - 1) / (per / 2) <= 32) per /= 2;      // a warp is enough
-  const int threads = ((items + per - 1) / per + 31) / 32 * 32;
+template <class T, int VEC, int PER>
+void go(const NormArgs &a, int items, cudaStream_t st) {
+  const int threads = ((items + PER - 1) / PER + 31) / 32 * 32;
   int rows = threads < 256 ? 256 / threads : 1;
-  if (T < rows * sm_count()) rows = 1;
-  return {per, threads, rows};
+  if (a.T < rows * sm_count()) rows = 1;
+  const dim3 grid((a.T + rows - 1) / rows), block(threads, rows);
+  if (a.res) rmsnorm_kernel<T, VEC, PER, true><<<grid, block, 0, st>>>(a);
+  else rmsnorm_kernel<T, VEC, PER, false><<<grid, block, 0, st>>>(a);
+}
+template <class T, int VEC>
+void go_vectors(const NormArgs &a, cudaStream_t st) {
+  const int items = a.H / VEC;
+  const bool many = a.T >= 2 * sm_count();
+  if (items <= 32 || (items <= kMaxThreads && !many)) go<T, VEC, 1>(a, items, st);
+  else if (items <= 64 || (items <= 2 * kMaxThreads && !many)) go<T, VEC, 2>(a, items, st);
+  else go<T, VEC, kMaxPer>(a, items, st);
 }
 
-template <class T, int VEC, int PER, bool SHIFT>
-void go(const NormArgs &a, const Shape &s, cudaStream_t st) {
-  const dim3 grid((a.T + s.rows - 1) / s.rows), block(s.threads, s.rows);
-  if (a.res) rmsnorm_kernel<T, VEC, PER, true, SHIFT><<<grid, block, 0, st>>>(a);
-  else rmsnorm_kernel<T, VEC, PER, false, SHIFT><<<grid, block, 0, st>>>(a);
+template <class T, int TX>
+void go_single(const NormArgs &a, cudaStream_t st) {
+  int rows = TX < 256 ? 256 / TX : 1;
+  if (a.T < rows * sm_count()) rows = 1;
+  const dim3 grid((a.T + rows - 1) / rows), block(TX, rows);
+  if (a.res) single_kernel<T, TX, true><<<grid, block, 0, st>>>(a);
+  else single_kernel<T, TX, false><<<grid, block, 0, st>>>(a);
+}
+template <class T>
+void go_singles(const NormArgs &a, cudaStream_t st) {
+  const int threads = (a.H + kSingles - 1) / kSingles;
+  if (threads <= 32) go_single<T, 32>(a, st);
+  else if (threads <= 64) go_single<T, 64>(a, st);
+  else if (threads <= 128) go_single<T, 128>(a, st);
+  else if (threads <= 256) go_single<T, 256>(a, st);
+  else if (threads <= 384) go_single<T, 384>(a, st);
+  else if (threads <= 512) go_single<T, 512>(a, st);
+  else if (threads <= 768) go_single<T, 768>(a, st);
+  else go_single<T, 1024>(a, st);
 }
 
 template <class T>
 int norm_typed(const NormArgs &a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
   const int ob = a.out_fmt == MCEMU_INT8 || a.out_fmt == MCEMU_E4M3 || a.out_fmt == MCEMU_E5M2 ? 1 : (int)sizeof(T);
-  Walk walk{V};
-  walk.add(a.x, a.ldx, sizeof(T));
-  walk.add(a.res, a.ldr, sizeof(T));
-  walk.add(a.h, a.ldh, sizeof(T));
-  walk.add(a.y, a.ldy, ob);
-  const bool wide = walk.ok && !walk.shifted() && a.H % V == 0 && rows16(a.w, 0, 4);
-  // Vectors where every operand's rows lie alike against 16-byte boundaries (contiguous ones
-  // do, whatever H); 8191 x 5003 bf16 with a residual: SHIFTNOW us, one element at a time 149.
-  const bool shift = walk.ok && !wide && a.H >= 64;
-  const int vec = wide || shift ? V : 1, max_per = wide || shift ? kMaxPer<V> : kMaxPer<1>;
-  const int span = shift ? a.H + V - 1 : a.H;
-  if ((int64_t)span > (int64_t)kMaxThreads * max_per * vec) {
-    if (wide) rmsnorm_long_kernel<T, V><<<a.T, 512, 0, st>>>(a);
-    else rmsnorm_long_kernel<T, 1><<<a.T, 512, 0, st>>>(a);
-    return launch_status();
-  }
-  const Shape s = shape_of(a.T, span, vec, max_per);
-  if (wide) {
-    if (s.per == 1) go<T, V, 1, false>(a, s, st);
-    else if (s.per == 2) go<T, V, 2, false>(a, s, st);
-    else go<T, V, 4, false>(a, s, st);
-  } else if (shift) {
-    if (s.per <= 2) go<T, V, 2, true>(a, s, st);
-    else go<T, V, 4, true>(a, s, st);
-  } else {
-    if (s.per <= 4) go<T, 1, 4, false>(a, s, st);
-    else go<T, 1, 16, false>(a, s, st);
-  }
+  const bool wide = a.H % V == 0 && rows16(a.x, a.ldx, sizeof(T)) && rows16(a.res, a.ldr, sizeof(T)) &&
+                    rows16(a.h, a.ldh, sizeof(T)) && rows16(a.w, 0, 4) && rows_on(a.y, a.ldy, ob, V * ob);
+  if (wide && a.H <= kMaxThreads * kMaxPer * V) go_vectors<T, V>(a, st);
+  else if (a.H <= kMaxThreads * kSingles) go_singles<T>(a, st);
+  else if (wide) rmsnorm_long_kernel<T, V><<<a.T, 512, 0, st>>>(a);
+  else rmsnorm_long_kernel<T, 1><<<a.T, 512, 0, st>>>(a);
   return launch_status();
 }
 

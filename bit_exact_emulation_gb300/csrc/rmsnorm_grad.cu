@@ -14,7 +14,7 @@ constexpr int kThreads = 512;                  // of a block
 // Most blocks, each of which keeps a part of dw: one to a multiprocessor, more where a block is
 // one group of threads for a short row.
 int most_blocks(int T, int H) {
-  const int per_sm = H <= 2048 ? 8 : H <= 16384 ? 16384 / H : 1, most = 152 * per_sm;
+  const int per_sm = H <= 1024 ? 16 : H <= 16384 ? 16384 / H : 1, most = 152 * per_sm;
   return T < most ? T : most;
 }
 
@@ -35,36 +35,14 @@ __device__ __forceinline__ float row_sum(float x, float *part) {
   return x;
 }
 
-// h of one vector, as stored or from the checkpoint: f of get() times scale1() for the elements
-// j with first(i, j), times scale2() for the others (a shifted vector may lie in two blocks of 128).
-template <class T, int VEC, bool CKPT, bool SHIFT>
-struct Input {
-  Vec<T, VEC> h;
-  __device__ __forceinline__ void load(const NormGradArgs &a, int64_t row, int i) {
-    h = load_part<T, VEC, SHIFT>((const T *)a.h + row * a.ldh, i, a.H);
-  }
-  __device__ __forceinline__ void get(float (&f)[VEC]) const { unpack<T, VEC>(h, f); }
-  __device__ __forceinline__ bool first(int, int) const { return true; }
-  __device__ __forceinline__ float scale1() const { return 1.f; }
-  __device__ __forceinline__ float scale2() const { return 1.f; }
-};
-template <class T, int VEC, bool SHIFT>
-struct Input<T, VEC, true, SHIFT> {
-  Vec<int8_t, VEC> q;
-  int8_t e1, e2;
-  __device__ __forceinline__ void load(const NormGradArgs &a, int64_t row, int i) {
-    q = load_part<int8_t, VEC, SHIFT>(a.q + row * a.ldq, i, a.H);
-    const int8_t *pe = a.e + row * a.lde;
-    e1 = pe[max(i, 0) / MCEMU_ACT8_BLOCK];
-    e2 = SHIFT ? pe[min(i + VEC - 1, a.H - 1) / MCEMU_ACT8_BLOCK] : e1;
-  }
-  __device__ __forceinline__ void get(float (&f)[VEC]) const { bytes_to_f<VEC>(q, f); }
-  __device__ __forceinline__ bool first(int i, int j) const {
-    return !SHIFT || j < MCEMU_ACT8_BLOCK - (i & (MCEMU_ACT8_BLOCK - 1));
-  }
-  __device__ __forceinline__ float scale1() const { return act8_scale(e1); }
-  __device__ __forceinline__ float scale2() const { return act8_scale(e2); }
-};
+// One element of the norm's input, from h or from the checkpoint.
+template <class T, bool CKPT>
+__device__ __forceinline__ float input_at(const NormGradArgs &a, int64_t row, int i) {
+  if constexpr (CKPT)
+    return (float)a.q[row * a.ldq + i] * act8_scale(a.e[row * a.lde + i / MCEMU_ACT8_BLOCK]);
+  else
+    return to_f(((const T *)a.h)[row * a.ldh + i]);
+}
 
 // Where column k of dw lies in shared memory: a word is left out after every eight, so that lanes
 // eight (or four) columns apart meet different banks.
@@ -89,7 +67,6 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
   __shared__ float sh[kThreads / 32];
   extern __shared__ __align__(16) uint8_t raw[];
   S *stages = (S *)raw;
-  float *join = (float *)(raw + 2 * sizeof(S));  // [H], padded, with several rows to a block
   const int t = threadIdx.y * TX + threadIdx.x;
   float dw[PER][VEC];
 #pragma unroll
@@ -179,119 +156,111 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
     }
   }
   copy_wait<0>();
-  // the groups' parts of dw, added in order
+  // the groups' parts of dw, side by side in the copies' memory, added in order
   float *mine = parts + (int64_t)blockIdx.x * a.H;
-  for (int g = 0; g < (int)blockDim.y; g++) {
-    if ((int)threadIdx.y == g) {
+  const int pitch = padded(a.H) + 1;
+  float *join = (float *)raw + threadIdx.y * pitch;
+  if (blockDim.y > 1) __syncthreads();
 #pragma unroll
-      for (int p = 0; p < PER; p++) {
-        const int i = (p * TX + threadIdx.x) * VEC;
-        if (i < a.H) {
+  for (int p = 0; p < PER; p++) {
+    const int i = (p * TX + threadIdx.x) * VEC;
+    if (i >= a.H) continue;
 #pragma unroll
-          for (int j = 0; j < VEC; j++) {
-            if (blockDim.y > 1) join[padded(i + j)] = g ? join[padded(i + j)] + dw[p][j] : dw[p][j];
-            else mine[i + j] = dw[p][j];
-          }
-        }
-      }
+    for (int j = 0; j < VEC; j++) {
+      if (blockDim.y > 1) join[padded(i + j)] = dw[p][j];
+      else mine[i + j] = dw[p][j];
     }
-    __syncthreads();
   }
-  if (blockDim.y > 1)
-    for (int i = t; i < a.H; i += TX * blockDim.y) mine[i] = join[padded(i)];
+  if (blockDim.y == 1) return;
+  __syncthreads();
+  for (int i = t; i < a.H; i += TX * blockDim.y) {
+    float s = ((float *)raw)[padded(i)];
+    for (int g = 1; g < (int)blockDim.y; g++) s += ((float *)raw)[g * pitch + padded(i)];
+    mine[i] = s;
+  }
 }
 
-// Rows that do not start on 16-byte boundaries, but all alike: the vectors start on boundaries of
-// memory, the columns of a thread change from row to row, and dw is kept in shared memory by the
-// one group of threads that a block then has.
-template <class T, int VEC, int PER, int TX, bool CKPT>
-__global__ void __launch_bounds__(TX) shifted_kernel(const NormGradArgs a, float *__restrict__ parts) {
+// Rows that no vector fits, at any strides: a group of TX threads to a block, one element of every
+// TX to a thread, so that a thread keeps its columns, their weights and its part of dw.
+template <class T, int PER, int TX, bool CKPT>
+__global__ void __launch_bounds__(TX) single_kernel(const NormGradArgs a, float *__restrict__ parts) {
   __shared__ float sh[32];
-  extern __shared__ float join[];               // [H], padded
-  for (int i = threadIdx.x; i < padded(a.H) + 1; i += TX) join[i] = 0.f;
+  __shared__ float scales[2][PER * TX / MCEMU_ACT8_BLOCK + 1];      // of this row's blocks of 128 and the next one's
+  const int i0 = threadIdx.x, blocks = (a.H + MCEMU_ACT8_BLOCK - 1) / MCEMU_ACT8_BLOCK;
+  float w[PER], dw[PER];
+#pragma unroll
+  for (int p = 0; p < PER; p++) {
+    const int i = i0 + p * TX;
+    dw[p] = w[p] = 0.f;
+    if (i < a.H) w[p] = a.w32 ? ((const float *)a.w)[i] : to_f(((const T *)a.w)[i]);
+  }
+  int64_t row = blockIdx.x;
+  if (CKPT && row < a.T)
+    for (int i = threadIdx.x; i < blocks; i += TX) scales[0][i] = act8_scale(a.e[row * a.lde + i]);
   __syncthreads();
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-    const T *pdy = (const T *)a.dy + row * a.lddy, *pdr = (const T *)a.dres + row * a.lddr;
-    const int first = threadIdx.x * VEC - (int)(((uintptr_t)pdy / sizeof(T)) % VEC);
-    Vec<T, VEC> dy[PER], dr[PER];
-    Input<T, VEC, CKPT, true> in[PER];
+  for (int s = 0; row < a.T; row += gridDim.x, s ^= 1) {
+    const T *pdy = (const T *)a.dy + row * a.lddy + i0, *pdr = (const T *)a.dres + row * a.lddr + i0;
+    const T *ph = (const T *)a.h + row * a.ldh + i0;
+    const int8_t *pq = a.q + row * a.ldq + i0;
+    T dy[PER], dr[PER];
+    typename std::conditional<CKPT, int8_t, T>::type in[PER];
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = first + p * TX * VEC;
-      if (i < a.H) {
-        dy[p] = load_part<T, VEC, true>(pdy, i, a.H);
-        in[p].load(a, row, i);
-        if (a.dres) dr[p] = load_part<T, VEC, true>(pdr, i, a.H);
-      }
+      if (i0 + p * TX >= a.H) continue;
+      dy[p] = pdy[p * TX];
+      if constexpr (CKPT) in[p] = pq[p * TX];
+      else in[p] = ph[p * TX];
+      if (a.dres) dr[p] = pdr[p * TX];
     }
     const float rstd = a.rstd[row];
-    float dot = 0.f;
+    if (CKPT && row + gridDim.x < a.T)
+      for (int i = threadIdx.x; i < blocks; i += TX)
+        scales[s ^ 1][i] = act8_scale(a.e[(row + gridDim.x) * a.lde + i]);
+    float z[PER], dot = 0.f;
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = first + p * TX * VEC;
-      if (i >= a.H) continue;
-      float f[VEC], w[VEC], d[VEC], some = 0.f;
-      in[p].get(f);
-      unpack<T, VEC>(dy[p], d);
-      load_w_part<T, VEC, true>(a.w, a.w32, i, a.H, w);
-      const float s1 = in[p].scale1() * rstd, s2 = in[p].scale2() * rstd;
-      float old[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; j++) old[j] = (unsigned)(i + j) < (unsigned)a.H ? join[padded(i + j)] : 0.f;
-#pragma unroll
-      for (int j = 0; j < VEC; j++) {
-        const float z = f[j] * (in[p].first(i, j) ? s1 : s2);
-        some = fmaf(d[j] * w[j], z, some);
-        old[j] = fmaf(d[j], z, old[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < VEC; j++)
-        if ((unsigned)(i + j) < (unsigned)a.H) join[padded(i + j)] = old[j];
-      dot += some;
+      z[p] = 0.f;
+      if (i0 + p * TX >= a.H) continue;
+      if constexpr (CKPT) z[p] = (float)in[p] * scales[s][(i0 + p * TX) / MCEMU_ACT8_BLOCK] * rstd;
+      else z[p] = to_f(in[p]) * rstd;
+      const float d = to_f(dy[p]);
+      dot = fmaf(d * w[p], z[p], dot);
+      dw[p] = fmaf(d, z[p], dw[p]);
     }
-    const float mean = row_sum<TX>(dot, sh) / (float)a.H;
+    if (TX == 32) __syncwarp();
+    const float k = -(row_sum<TX>(dot, sh) / (float)a.H) * rstd;
+    T *pdx = (T *)a.dx + row * a.lddx + i0;
 #pragma unroll
     for (int p = 0; p < PER; p++) {
-      const int i = first + p * TX * VEC;
-      if (i >= a.H) continue;
-      float f[VEC], w[VEC], d[VEC];
-      in[p].get(f);
-      unpack<T, VEC>(dy[p], d);
-      load_w_part<T, VEC, true>(a.w, a.w32, i, a.H, w);
-      const float k1 = -(in[p].scale1() * rstd * mean * rstd), k2 = -(in[p].scale2() * rstd * mean * rstd);
-#pragma unroll
-      for (int j = 0; j < VEC; j++) w[j] *= d[j];
-      if (a.dres) unpack<T, VEC>(dr[p], d);
-#pragma unroll
-      for (int j = 0; j < VEC; j++)
-        f[j] = fmaf(f[j], in[p].first(i, j) ? k1 : k2, a.dres ? fmaf(w[j], rstd, d[j]) : w[j] * rstd);
-      store_part<T, VEC, true>((T *)a.dx + row * a.lddx, i, a.H, pack<T, VEC>(f));
+      if (i0 + p * TX >= a.H) continue;
+      const float g = to_f(dy[p]) * w[p];
+      pdx[p * TX] = from_f<T>(fmaf(z[p], k, a.dres ? fmaf(g, rstd, to_f(dr[p])) : g * rstd));
     }
-    __syncthreads();                            // the next row's columns belong to other threads
   }
-  float *mine = parts + (int64_t)blockIdx.x * a.H;
-  for (int i = threadIdx.x; i < a.H; i += TX) mine[i] = join[padded(i)];
+#pragma unroll
+  for (int p = 0; p < PER; p++)
+    if (i0 + p * TX < a.H) parts[(int64_t)blockIdx.x * a.H + i0 + p * TX] = dw[p];
 }
 
-// dw[j] = sum over the groups of parts[group][j]: 32 columns and eight strands of groups to
-// a block, the strands joined in order.
-__global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ parts, int groups, int H, float *dw) {
-  __shared__ float sh[8][33];
+// dw[j] = sum over the blocks of parts[block][j]: 32 columns and 32 strands of blocks to a block
+// of threads, the strands joined in order.
+__global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ parts, int groups, int H, float *dw) {
+  __shared__ float sh[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (col < H)
-#pragma unroll 8
-    for (int g = threadIdx.y; g < groups; g += 8) s += parts[(int64_t)g * H + col];
+#pragma unroll 4
+    for (int g = threadIdx.y; g < groups; g += 32) s += parts[(int64_t)g * H + col];
   sh[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && col < H) {
 #pragma unroll
-    for (int i = 1; i < 8; i++) s += sh[i][threadIdx.x];
+    for (int i = 1; i < 32; i++) s += sh[i][threadIdx.x];
     dw[col] = s;
   }
 }
 
-// Rows longer than a block holds, or whose operands lie differently in memory: mean(g z) of each row, then dx and parts of dw by columns.
+// Rows longer than a block holds: mean(g z) of each row, then dx and parts of dw by columns.
 template <class T, bool CKPT>
 __global__ void __launch_bounds__(512) long_mean_kernel(const NormGradArgs a, float *__restrict__ mean) {
   __shared__ float sh[32];
@@ -299,11 +268,8 @@ __global__ void __launch_bounds__(512) long_mean_kernel(const NormGradArgs a, fl
     const float rstd = a.rstd[row];
     float dot = 0.f;
     for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
-      Input<T, 1, CKPT, false> in;
       float z[1], w[1];
-      in.load(a, row, i);
-      in.get(z);
-      z[0] *= in.scale1() * rstd;
+      z[0] = input_at<T, CKPT>(a, row, i) * rstd;
       load_w<T, 1>(a.w, a.w32, i, w);
       dot = fmaf(to_f(((const T *)a.dy)[row * a.lddy + i]) * w[0], z[0], dot);
     }
@@ -320,11 +286,8 @@ __global__ void __launch_bounds__(256) long_grad_kernel(const NormGradArgs a, co
   load_w<T, 1>(a.w, a.w32, i, w);
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const float rstd = a.rstd[row], d = to_f(((const T *)a.dy)[row * a.lddy + i]);
-    Input<T, 1, CKPT, false> in;
     float z[1];
-    in.load(a, row, i);
-    in.get(z);
-    z[0] *= in.scale1() * rstd;
+    z[0] = input_at<T, CKPT>(a, row, i) * rstd;
     dw = fmaf(d, z[0], dw);
     float x = rstd * (d * w[0] - z[0] * mean[row]);
     if (a.dres) x += to_f(((const T *)a.dres)[row * a.lddr + i]);
@@ -340,66 +303,53 @@ bool allow_smem(K kernel, size_t bytes) {
 }
 
 // Blocks launched, -1 after an error.
-template <class T, int VEC, int PER, int TX, bool CKPT, bool SHIFT>
+template <class T, int VEC, int PER, int TX, bool CKPT>
 int go(const NormGradArgs &a, float *parts, cudaStream_t st) {
-  if constexpr (SHIFT) {
-    const int blocks = most_blocks(a.T, a.H);
-    const size_t smem = (a.H + a.H / 8 + 2) * sizeof(float);
-    if (!allow_smem(shifted_kernel<T, VEC, PER, TX, CKPT>, smem)) return -1;
-    shifted_kernel<T, VEC, PER, TX, CKPT><<<blocks, TX, smem, st>>>(a, parts);
-    return blocks;
-  } else {
-    int rows = kThreads / TX;                  // as many as fit, but first a block on every multiprocessor
-    if (rows > a.T / 152) rows = a.T / 152;
-    if (rows < 1) rows = 1;
-    if (rows > 15) rows = 15;                  // barriers
-    const int need = (a.T + rows - 1) / rows, blocks = need < 152 ? need : 152;
-    const size_t smem = 2 * sizeof(Stage<T, VEC, PER, CKPT>) + (rows > 1 ? (a.H + a.H / 8 + 2) * sizeof(float) : 0);
-    if (!allow_smem(grad_kernel<T, VEC, PER, TX, CKPT>, smem)) return -1;
-    grad_kernel<T, VEC, PER, TX, CKPT><<<blocks, dim3(TX, rows), smem, st>>>(a, parts);
-    return blocks;
-  }
+  int rows = kThreads / TX;                    // as many as fit, but first a block on every multiprocessor
+  if (rows > a.T / 152) rows = a.T / 152;
+  if (rows < 1) rows = 1;
+  if (TX > 32 && rows > 15) rows = 15;         // barriers
+  const int need = (a.T + rows - 1) / rows, blocks = need < 152 ? need : 152;
+  const size_t smem = 2 * sizeof(Stage<T, VEC, PER, CKPT>);
+  static_assert(2 * sizeof(Stage<T, VEC, PER, CKPT>) >= kThreads / TX * (TX * PER * VEC * 9 / 8 + 2) * sizeof(float),
+                "the parts of dw fit the copies' memory");
+  if (!allow_smem(grad_kernel<T, VEC, PER, TX, CKPT>, smem)) return -1;
+  grad_kernel<T, VEC, PER, TX, CKPT><<<blocks, dim3(TX, rows), smem, st>>>(a, parts);
+  return blocks;
 }
-
-// The group of threads for rows of `span` columns.  32 columns a thread (16 of fp32) from the
-// shared copies; 16 (8) with SHIFT, which has them in registers.
-template <class T, int VEC, bool CKPT, bool SHIFT>
-int pick(const NormGradArgs &a, int span, float *parts, cudaStream_t st) {
-  constexpr int P = (VEC == 4 ? 16 : 32) / VEC / (SHIFT ? 2 : 1);
-  if (span <= 32 * VEC) return go<T, VEC, 1, 32, CKPT, SHIFT>(a, parts, st);
-  if (span <= 32 * VEC * P) return go<T, VEC, P, 32, CKPT, SHIFT>(a, parts, st);
-  if (span <= 64 * VEC * P) return go<T, VEC, P, 64, CKPT, SHIFT>(a, parts, st);
-  if (span <= 128 * VEC * P) return go<T, VEC, P, 128, CKPT, SHIFT>(a, parts, st);
-  if (span <= 256 * VEC * P) return go<T, VEC, P, 256, CKPT, SHIFT>(a, parts, st);
-  if constexpr (SHIFT)
-    if (span > 512 * VEC * P) return go<T, VEC, P, 1024, CKPT, SHIFT>(a, parts, st);
-  return go<T, VEC, P, 512, CKPT, SHIFT>(a, parts, st);
+template <class T, int TX, bool CKPT>
+int go_single(const NormGradArgs &a, float *parts, cudaStream_t st) {
+  const int blocks = most_blocks(a.T, a.H);
+  single_kernel<T, 16, TX, CKPT><<<blocks, TX, 0, st>>>(a, parts);
+  return blocks;
 }
 
 template <class T, bool CKPT>
 int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T), kMost = kThreads * (V == 4 ? 16 : 32);      // columns held in registers
+  constexpr int V = 16 / sizeof(T), P = (V == 4 ? 16 : 32) / V;       // 32 columns a thread, 16 of fp32
   int groups = most_blocks(a.T, a.H);
-  Walk walk{V};
-  walk.add(a.dy, a.lddy, sizeof(T));
-  walk.add(a.dres, a.lddr, sizeof(T));
-  walk.add(a.dx, a.lddx, sizeof(T));
-  walk.add(a.h, a.ldh, sizeof(T));
-  walk.add(a.q, a.ldq, 1);
-  const bool wide = walk.ok && !walk.shifted() && a.H % V == 0 && rows16(a.w, 0, 4) && a.H <= kMost;
-  // Rows that lie alike against 16-byte boundaries, as contiguous ones do whatever H is.
-  const bool shift = walk.ok && !wide && a.H >= 64 && a.H + V - 1 <= kMost;
-  if (wide) {
-    groups = pick<T, V, CKPT, false>(a, a.H, ws, st);
-  } else if (shift) {
-    groups = pick<T, V, CKPT, true>(a, a.H + V - 1, ws, st);
+  const bool wide = a.H % V == 0 && rows16(a.dy, a.lddy, sizeof(T)) && rows16(a.dres, a.lddr, sizeof(T)) &&
+                    rows16(a.dx, a.lddx, sizeof(T)) && rows16(a.h, a.ldh, sizeof(T)) && rows16(a.w, 0, 4) &&
+                    rows_on(a.q, a.ldq, 1, V);
+  if (wide && a.H <= kThreads * V * P) {
+    if (a.H <= 32 * V) groups = go<T, V, 1, 32, CKPT>(a, ws, st);
+    else if (a.H <= 32 * V * P) groups = go<T, V, P, 32, CKPT>(a, ws, st);
+    else if (a.H <= 64 * V * P) groups = go<T, V, P, 64, CKPT>(a, ws, st);
+    else if (a.H <= 128 * V * P) groups = go<T, V, P, 128, CKPT>(a, ws, st);
+    else if (a.H <= 256 * V * P) groups = go<T, V, P, 256, CKPT>(a, ws, st);
+    else groups = go<T, V, P, 512, CKPT>(a, ws, st);
+  } else if (a.H <= 16 * 512) {
+    if (a.H <= 16 * 32) groups = go_single<T, 32, CKPT>(a, ws, st);
+    else if (a.H <= 16 * 128) groups = go_single<T, 128, CKPT>(a, ws, st);
+    else if (a.H <= 16 * 256) groups = go_single<T, 256, CKPT>(a, ws, st);
+    else groups = go_single<T, 512, CKPT>(a, ws, st);
   } else {
     float *mean = ws + (int64_t)groups * a.H;
     long_mean_kernel<T, CKPT><<<a.T < 152 * 4 ? a.T : 152 * 4, 512, 0, st>>>(a, mean);
     long_grad_kernel<T, CKPT><<<dim3(groups, (a.H + 255) / 256), 256, 0, st>>>(a, mean, ws);
   }
   if (groups < 0) return MCEMU_ERR_CUDA;
-  join_kernel<<<(a.H + 31) / 32, dim3(32, 8), 0, st>>>(ws, groups, a.H, a.dw);
+  join_kernel<<<(a.H + 31) / 32, dim3(32, 32), 0, st>>>(ws, groups, a.H, a.dw);
   return launch_status();
 }
 
