@@ -78,6 +78,7 @@ struct Widen {
 // One tile (128 rows by 64 k) to a block.
 __global__ void __launch_bounds__(256) widen_kernel(const Widen x, const Widen w, int K, int ktiles, bool wide) {
   int64_t tile = blockIdx.x;
+  grid_go();
   const int64_t mine = (int64_t)x.blocks * ktiles;
   const Widen &o = tile < mine ? x : w;
   if (tile >= mine) tile -= mine;
@@ -132,13 +133,17 @@ int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Few tokens: the weights' bytes are what counts, and every warp widens what it reads in
-// registers.  A block takes 16 * CH channels by 8 * NT tokens; its eight warps share K, 64 at a
+// registers.  A block takes 16 channels by 8 * NT tokens; its eight warps share K, 64 at a
 // time in turn.  The warp-wide matrix instruction (m16n8k16, 1000 MAC a cycle and SM measured,
 // against 250 for its 8-bit form and for dp4a alike) takes four k of a row from a lane, and
 // which four is free as long as both operands agree: a lane reads 16 consecutive bytes of
 // its rows and feeds them to four instructions.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
+#ifndef FEW
+#define FEW 32
+#endif
+constexpr int kFew = FEW;                     // most tokens
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -147,18 +152,49 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-template <int OUT, int NT, int CH>
-__global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a, bool wide) {
-  constexpr int kAhead = NT * CH >= 8 ? 2 : 4;               // pieces of 64 k in flight
-  __shared__ int total[16 * CH][8 * NT + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16 * CH, m0 = blockIdx.y * 8 * NT;
-  for (int i = threadIdx.x; i < 16 * CH * (8 * NT + 1); i += blockDim.x) (&total[0][0])[i] = 0;
+// Sixteen bytes of a row from k on.  WIDE: rows start on 16-byte boundaries and K is a multiple
+// of 16.
+template <bool WIDE>
+__device__ __forceinline__ uint4 piece16(const int8_t *row, int k, int K, bool have) {
+  if constexpr (WIDE) {
+    return have && k < K ? __ldg((const uint4 *)(row + k)) : make_uint4(0, 0, 0, 0);
+  } else {
+    return have && k < K ? row16(row, k, K, false) : make_uint4(0, 0, 0, 0);
+  }
+}
 
-  const int8_t *wrow[2 * CH], *xrow[NT];
-  bool whave[2 * CH], xhave[NT];
+__device__ __forceinline__ void put_any(const LinearArgs &a, int m, int n, int acc, float sx, float sw, float bias) {
+  const int64_t at = (int64_t)m * a.ldy + n;
+  const bool biased = a.bias != nullptr;
+  if (a.out_fmt == MCEMU_BF16) ((__nv_bfloat16 *)a.y)[at] = scaled<MCEMU_BF16>(acc, sx, sw, biased, bias);
+  else if (a.out_fmt == MCEMU_FP16) ((__half *)a.y)[at] = scaled<MCEMU_FP16>(acc, sx, sw, biased, bias);
+  else if (a.out_fmt == MCEMU_FP32) ((float *)a.y)[at] = scaled<MCEMU_FP32>(acc, sx, sw, biased, bias);
+  else ((int32_t *)a.y)[at] = acc;
+}
+
+template <int NT, bool WIDE>
+__global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a) {
+  constexpr int kAhead = WIDE ? (NT == 1 ? 8 : 4) : 2;       // pieces of 64 k in flight
+  constexpr int kOut = 16 * 8 * NT;                          // outputs of a block
+  constexpr int kEach = (kOut + 32 * kWarps - 1) / (32 * kWarps);
+  __shared__ int part[kWarps][kOut];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 8 * NT;
+  // this thread's outputs (a channel, every sixteenth token), their factors asked for early
+  const int n = n0 + (threadIdx.x & 15);
+  const bool scales = a.out_fmt != MCEMU_INT32;
+  float sx[kEach];
 #pragma unroll
-  for (int r = 0; r < 2 * CH; r++) {
+  for (int i = 0; i < kEach; i++) {
+    const int m = m0 + (threadIdx.x >> 4) + 16 * i;
+    sx[i] = scales && m < a.M ? __ldg(a.sx + m) : 0.f;
+  }
+  const float sw = scales && n < a.N ? __ldg(a.sw + n) : 0.f, bias = scales && a.bias && n < a.N ? __ldg(a.bias + n) : 0.f;
+
+  const int8_t *wrow[2], *xrow[NT];
+  bool whave[2], xhave[NT];
+#pragma unroll
+  for (int r = 0; r < 2; r++) {
     whave[r] = n0 + 8 * r + g < a.N;
     wrow[r] = a.w + (whave[r] ? (int64_t)(n0 + 8 * r + g) * a.ldw : 0);
   }
@@ -167,117 +203,339 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a, bo
     xhave[j] = m0 + 8 * j + g < a.M;
     xrow[j] = a.x + (xhave[j] ? (int64_t)(m0 + 8 * j + g) * a.ldx : 0);
   }
-  float acc[CH][NT][4];
-  int sum[CH][NT][4];
+  float acc[NT][4];
+  int sum[NT][4];
 #pragma unroll
-  for (int i = 0; i < CH * NT * 4; i++) (&acc[0][0][0])[i] = 0.f, (&sum[0][0][0])[i] = 0;
+  for (int i = 0; i < NT * 4; i++) (&acc[0][0])[i] = 0.f, (&sum[0][0])[i] = 0;
 
   const int pieces = (a.K + 63) / 64;
   int since = 0;                                             // pieces since the sums were taken out
   for (int p = warp; p < pieces; p += kWarps * kAhead) {
-    uint4 w[kAhead][2 * CH], x[kAhead][NT];
+    uint4 w[kAhead][2], x[kAhead][NT];
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
       const int k = (p + u * kWarps) * 64 + 16 * t;
 #pragma unroll
-      for (int r = 0; r < 2 * CH; r++) {
-        w[u][r] = make_uint4(0, 0, 0, 0);
-        if (whave[r] && k < a.K) w[u][r] = row16(wrow[r], k, a.K, wide);
-      }
+      for (int r = 0; r < 2; r++) w[u][r] = piece16<WIDE>(wrow[r], k, a.K, whave[r]);
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-        x[u][j] = make_uint4(0, 0, 0, 0);
-        if (xhave[j] && k < a.K) x[u][j] = row16(xrow[j], k, a.K, wide);
-      }
+      for (int j = 0; j < NT; j++) x[u][j] = piece16<WIDE>(xrow[j], k, a.K, xhave[j]);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
-      const uint32_t *wu = &w[u][0].x, *xu = &x[u][0].x;
+      const uint32_t *w0 = &w[u][0].x, *w1 = &w[u][1].x, *xu = &x[u][0].x;
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        uint32_t af[CH][4];
-#pragma unroll
-        for (int c = 0; c < CH; c++) {
-          half4(wu[(2 * c) * 4 + q], af[c][0], af[c][2]);
-          half4(wu[(2 * c + 1) * 4 + q], af[c][1], af[c][3]);
-        }
+        uint32_t af[4];
+        half4(w0[q], af[0], af[2]);
+        half4(w1[q], af[1], af[3]);
 #pragma unroll
         for (int j = 0; j < NT; j++) {
           uint32_t bf[2];
           half4(xu[j * 4 + q], bf[0], bf[1]);
-#pragma unroll
-          for (int c = 0; c < CH; c++) mma16816(acc[c][j], af[c], bf);
+          mma16816(acc[j], af, bf);
         }
       }
     }
     since += kAhead;
     if (since + kAhead > 16 || p + kWarps * kAhead >= pieces) {   // 1024 products an accumulator at most
 #pragma unroll
-      for (int i = 0; i < CH * NT * 4; i++) {
-        (&sum[0][0][0])[i] += __float2int_rn((&acc[0][0][0])[i]);
-        (&acc[0][0][0])[i] = 0.f;
+      for (int i = 0; i < NT * 4; i++) {
+        (&sum[0][0])[i] += __float2int_rn((&acc[0][0])[i]);
+        (&acc[0][0])[i] = 0.f;
       }
       since = 0;
     }
   }
+#pragma unroll
+  for (int j = 0; j < NT; j++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) part[warp][(8 * j + 2 * t + (i & 1)) * 16 + 8 * (i >> 1) + g] = sum[j][i];
   __syncthreads();
 #pragma unroll
-  for (int c = 0; c < CH; c++)
+  for (int i = 0; i < kEach; i++) {
+    const int at = threadIdx.x + 32 * kWarps * i, m = m0 + (at >> 4);
+    if (at >= kOut || n >= a.N || m >= a.M) continue;
+    int total = part[0][at];
 #pragma unroll
-    for (int j = 0; j < NT; j++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) atomicAdd(&total[16 * c + 8 * (i >> 1) + g][8 * j + 2 * t + (i & 1)], sum[c][j][i]);
-  __syncthreads();
-  using T = typename OutType<OUT>::T;
-  for (int i = threadIdx.x; i < 16 * CH * 8 * NT; i += blockDim.x) {
-    const int n = n0 + i % (16 * CH), m = m0 + i / (16 * CH);
-    if (n < a.N && m < a.M) {
-      const float2 c = channel<OUT>(a, n);
-      ((T *)a.y)[(int64_t)m * a.ldy + n] = scaled<OUT>(total[i % (16 * CH)][i / (16 * CH)],
-                                                       OUT == MCEMU_INT32 ? 0.f : a.sx[m], c.x, a.bias != nullptr, c.y);
-    }
+    for (int p = 1; p < kWarps; p++) total += part[p][at];
+    put_any(a, m, n, total, sx[i], sw, bias);
   }
 }
 
-template <int OUT, int NT, int CH>
+template <int NT>
 int go_few(const LinearArgs &a, bool wide, cudaStream_t st) {
-  const dim3 grid((a.N + 16 * CH - 1) / (16 * CH), (a.M + 8 * NT - 1) / (8 * NT));
-  few_kernel<OUT, NT, CH><<<grid, 32 * kWarps, 0, st>>>(a, wide);
+  const dim3 grid((a.N + 15) / 16, (a.M + 8 * NT - 1) / (8 * NT));
+  if (wide) few_kernel<NT, true><<<grid, 32 * kWarps, 0, st>>>(a);
+  else few_kernel<NT, false><<<grid, 32 * kWarps, 0, st>>>(a);
   return launch_status();
 }
 
-// Products that go through panels.
-#ifndef MIN_PANEL
-#define MIN_PANEL 64
-#endif
-bool by_panels(int M, int K) { return M > MIN_PANEL && K > 0; }
+// ---------------------------------------------------------------------------
+// A batch of tokens, too few to pay for panels: a block takes 128 channels by BN tokens and a part
+// of K.  Eight worker warps read both operands 64 k at a time, kSets stages ahead, widen them to
+// binary16 and store them in the swizzle; one thread issues the matrix instructions.  The
+// blocks of a cluster share K, and each adds up its share of the tile out of the others' shared
+// memory, so that no second launch joins the parts.
+// ---------------------------------------------------------------------------
+constexpr int kStageK = 64;                   // k of a stage: one 128-byte swizzle row
+constexpr int kChunk = 1024 / kStageK;        // stages between two transfers to int32
+constexpr int kWorkers = 256;
+constexpr int kSets = 4;                      // stages whose loads are in flight
 
-template <int OUT>
-int go(const LinearArgs &a, bool rows, void *ws, cudaStream_t st) {
-  if (by_panels(a.M, a.K)) return go_panels<OUT>(a, rows, ws, st);
-  if (a.M <= 8) return go_few<OUT, 1, 1>(a, rows, st);
-  if (a.M <= 16) return go_few<OUT, 2, 1>(a, rows, st);
-  if (a.M <= 32) return go_few<OUT, 4, 2>(a, rows, st);
-  return go_few<OUT, 8, 2>(a, rows, st);
+template <int BN>
+struct Batch {
+  static constexpr int kRows = 128 + BN;
+  static constexpr int kBytes = kRows * 128;                    // of one stage
+  static constexpr int kStages = 4;
+  static constexpr int kLoads = (kRows * 4 + kWorkers - 1) / kWorkers;      // 16-byte pieces of a stage per worker
+  static constexpr int kColumns = BN < 32 ? 32 : BN;            // tensor memory, a power of two
+  static constexpr int kSmem = kStages * kBytes + 1024 + 256;   // also holds the tile's 128 * BN sums
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kWorkers + 32, BN <= 64 ? 2 : 1) batch_kernel(const LinearArgs a, int tiles_n, int per) {
+  using S = Batch<BN>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t full = base + S::kStages * S::kBytes, empty = full + 8 * S::kStages, acc_full = empty + 8 * S::kStages,
+                 acc_empty = acc_full + 8, drain = acc_empty + 8, slot = drain + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t parts = tc::cluster_size(), rank = tc::cta_rank();
+  const int tile = blockIdx.x / parts, n0 = (tile % tiles_n) * 128, m0 = (tile / tiles_n) * BN;
+  const int stages = (a.K + kStageK - 1) / kStageK, s0 = (int)rank * per;
+  const int s1 = s0 < stages ? s0 + min(per, (stages - s0 + kSets - 1) / kSets * kSets) : s0;   // whole rounds of loads
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; s++) {
+      tc::mbar_init(full + 8 * s, 8);
+      tc::mbar_init(empty + 8 * s, 1);
+    }
+    tc::mbar_init(acc_full, 1);
+    tc::mbar_init(acc_empty, 8);
+    tc::mbar_init(drain, 1);
+    tc::mbar_init_fence();
+  }
+  if (warp == 8) tc::tmem_alloc<1>(slot, S::kColumns);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+  bool dead = false;
+  int sum[BN / 2];
+#pragma unroll
+  for (int j = 0; j < BN / 2; j++) sum[j] = 0;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      constexpr uint32_t ins = tc::instruction(128, BN, 0, 0, 0);
+      uint32_t it = 0, ch = 0;
+      for (int c = s0; c < s1 && !dead; c += kChunk, ch++) {
+        tc::mbar_wait(acc_empty, (ch & 1) ^ 1, dead);
+        tc::fence_after();
+        const int n = min(kChunk, s1 - c);
+        for (int i = 0; i < n && !dead; i++, it++) {
+          const uint32_t s = it % S::kStages, at = base + s * S::kBytes;
+          tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1, dead);
+          if (dead) break;
+          tc::fence_after();
+          const uint64_t da = tc::operand(at, 16, 1024), db = tc::operand(at + 128 * 128, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kStageK / 16; k++) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, ins, (i | k) != 0);
+          tc::commit<1>(empty + 8 * s);
+        }
+        tc::commit<1>(acc_full);
+      }
+      bool late = false;                       // everything issued ends before the memory is given back
+      tc::commit<1>(drain);
+      tc::mbar_wait(drain, 0, late);
+    }
+    __syncwarp();
+  } else {
+    // pieces of a stage: piece p of a row is k 16p .. 16p + 15
+    const int piece = threadIdx.x & 3, row0 = threadIdx.x >> 2;
+    const int8_t *src[S::kLoads];
+    uint32_t store[S::kLoads];
+    bool have[S::kLoads], slots[S::kLoads];
+#pragma unroll
+    for (int j = 0; j < S::kLoads; j++) {
+      const int r = row0 + 64 * j;
+      slots[j] = r < S::kRows;
+      store[j] = (r >> 3) * 1024 + (r & 7) * 128 + (((2 * piece) ^ (r & 7)) << 4);
+      if (r < 128) {
+        have[j] = n0 + r < a.N;
+        src[j] = a.w + (have[j] ? (int64_t)(n0 + r) * a.ldw : 0);
+      } else {
+        have[j] = slots[j] && m0 + r - 128 < a.M;
+        src[j] = a.x + (have[j] ? (int64_t)(m0 + r - 128) * a.ldx : 0);
+      }
+    }
+    const auto load = [&](uint4 (&v)[S::kLoads], int s) {
+      const int k = s * kStageK + 16 * piece;
+#pragma unroll
+      for (int j = 0; j < S::kLoads; j++) v[j] = piece16<true>(src[j], k, a.K, have[j] && s < s1);
+    };
+    uint32_t it = 0;
+    const auto step = [&](uint4 (&v)[S::kLoads], int next) {
+      const uint32_t s = it % S::kStages, at = base + s * S::kBytes;
+      tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1, dead);
+#pragma unroll
+      for (int j = 0; j < S::kLoads; j++) {
+        if (!slots[j]) continue;
+        uint32_t h[8];
+        half4(v[j].x, h[0], h[1]);
+        half4(v[j].y, h[2], h[3]);
+        half4(v[j].z, h[4], h[5]);
+        half4(v[j].w, h[6], h[7]);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + store[j]), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                     "r"(h[3])
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (store[j] ^ 16)), "r"(h[4]), "r"(h[5]),
+                     "r"(h[6]), "r"(h[7])
+                     : "memory");
+      }
+      load(v, next);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full + 8 * s);
+      it++;
+    };
+    uint4 v[kSets][S::kLoads];
+#pragma unroll
+    for (int i = 0; i < kSets; i++) load(v[i], s0 + i);
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * (BN / 2);
+    uint32_t ch = 0;
+    for (int c = s0; c < s1; c += kChunk, ch++) {
+      const int e = min(s1, c + kChunk);
+      for (int s = c; s < e; s += kSets) {
+#pragma unroll
+        for (int i = 0; i < kSets; i++) step(v[i], s + i + kSets);
+      }
+      tc::mbar_wait(acc_full, ch & 1, dead);
+      __syncwarp();
+      tc::fence_after();
+#pragma unroll
+      for (int j = 0; j < BN / 2; j += 16) {
+        float f[16];
+        tc::tmem_load16(mine + j, f);
+        tc::tmem_wait();
+#pragma unroll
+        for (int x = 0; x < 16; x++) sum[j + x] += __float2int_rn(f[x]);
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(acc_empty);
+    }
+  }
+  // sums to shared memory (token by channel), then this block's tokens out of every block's
+  __syncthreads();
+  if (warp < 8) {
+    const uint32_t at = base + ((warp >> 2) * (BN / 2) * 128 + (warp & 3) * 32 + lane) * 4;
+#pragma unroll
+    for (int j = 0; j < BN / 2; j++)
+      asm volatile("st.shared.s32 [%0], %1;" ::"r"(at + j * 512), "r"(sum[j]) : "memory");
+  }
+  tc::cluster_sync();
+  if (warp < 8) {
+    // four channels of every eighth token to a thread; all blocks' parts asked for at once
+    const int r = lane * 4, n = n0 + r, share = BN / parts, end = min(a.M - m0, (int)(rank + 1) * share);
+    const bool scales = a.out_fmt != MCEMU_INT32;
+    float sw[4], bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      sw[i] = scales && n + i < a.N ? __ldg(a.sw + n + i) : 0.f;
+      bias[i] = scales && a.bias && n + i < a.N ? __ldg(a.bias + n + i) : 0.f;
+    }
+    for (int m = rank * share + warp; m < end; m += 8) {
+      const float sx = scales ? __ldg(a.sx + m0 + m) : 0.f;
+      int4 v[8];
+#pragma unroll
+      for (uint32_t p = 0; p < 8; p++)
+        if (p < parts) v[p] = tc::load_peer(base + (m * 128 + r) * 4, p);
+      int sum4[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (uint32_t p = 0; p < 8; p++)
+        if (p < parts) sum4[0] += v[p].x, sum4[1] += v[p].y, sum4[2] += v[p].z, sum4[3] += v[p].w;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (n + i < a.N) put_any(a, m0 + m, n + i, sum4[i], sx, sw[i], bias[i]);
+    }
+  }
+  tc::fence_before();
+  tc::cluster_sync();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::tmem_free<1>(tmem, S::kColumns);
+  }
+}
+
+template <int BN>
+int go_batch(const LinearArgs &a, cudaStream_t st) {
+  using S = Batch<BN>;
+  static std::atomic<bool> ready[64];
+  const auto kernel = batch_kernel<BN>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MCEMU_ERR_CUDA;
+  if (dev >= 64 || !ready[dev].load()) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+      return MCEMU_ERR_CUDA;
+    if (dev < 64) ready[dev].store(true);
+  }
+  const int tiles_n = (a.N + 127) / 128, stages = (a.K + kStageK - 1) / kStageK;
+  const int64_t tiles = (int64_t)tiles_n * ((a.M + BN - 1) / BN);
+  // Parts of K: a power of two of at most eight (a portable cluster), at least four stages each,
+  // until the blocks fill the multiprocessors.
+  const int room = sm_count() * (BN <= 64 ? 2 : 1);
+  int parts = 1;
+  while (parts < 8 && tiles * parts * 2 <= room && stages >= parts * 2 * 4) parts *= 2;
+  if (tiles * parts > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * parts));
+  cfg.blockDim = dim3(kWorkers + 32);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = parts;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t rc = cudaLaunchKernelEx(&cfg, kernel, a, tiles_n,
+                                            ((stages + parts - 1) / parts + kSets - 1) / kSets * kSets);
+  return rc == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
+}
+// Products that go through panels: more than one wave of the batch kernel's tiles, or rows that
+// its 16-byte loads do not fit.  WHY
+bool by_panels(int M, int N, int K, bool wide) {
+  return K > 0 && M > kFew && (!wide || (int64_t)((M + 127) / 128) * ((N + 127) / 128) > sm_count());
 }
 
 }  // namespace
 
 int int8_linear_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_timeouts(st, got); }
 
-size_t int8_linear_workspace(int M, int N, int K) {
-  if (!by_panels(M, K)) return 0;
+size_t int8_linear_workspace(int M, int N, int K, bool rows) {
+  if (!by_panels(M, N, K, rows && K % 16 == 0)) return 0;
   return (size_t)(blocks128(M) + blocks128(N)) * ktiles_of(K) * panel::kTileBytes;
 }
 
 int launch_int8_linear(const LinearArgs &a, bool rows, void *ws, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
-  switch (a.out_fmt) {
-    case MCEMU_INT32: return go<MCEMU_INT32>(a, rows, ws, st);
-    case MCEMU_FP32: return go<MCEMU_FP32>(a, rows, ws, st);
-    case MCEMU_FP16: return go<MCEMU_FP16>(a, rows, ws, st);
-    default: return go<MCEMU_BF16>(a, rows, ws, st);
+  const bool wide = rows && a.K % 16 == 0;
+  if (by_panels(a.M, a.N, a.K, wide)) {
+    switch (a.out_fmt) {
+      case MCEMU_INT32: return go_panels<MCEMU_INT32>(a, rows, ws, st);
+      case MCEMU_FP32: return go_panels<MCEMU_FP32>(a, rows, ws, st);
+      case MCEMU_FP16: return go_panels<MCEMU_FP16>(a, rows, ws, st);
+      default: return go_panels<MCEMU_BF16>(a, rows, ws, st);
+    }
   }
+  if (a.M <= 8) return go_few<1>(a, wide, st);
+  if (a.M <= 16) return go_few<2>(a, wide, st);
+  if (a.M <= kFew || a.K == 0) return go_few<4>(a, wide, st);
+  if (a.M <= 32) return go_batch<32>(a, st);
+  if (a.M <= 64) return go_batch<64>(a, st);
+  return go_batch<128>(a, st);
 }
 
 }  // namespace mcemu

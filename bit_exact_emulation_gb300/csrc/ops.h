@@ -50,8 +50,8 @@ struct LinearArgs {
 };
 // Whether a bounded device wait of these kernels gave up since the last question.
 int int8_linear_timeouts(cudaStream_t st, unsigned int *got);
-size_t int8_linear_workspace(int M, int N, int K);
 // rows: every row of x and w starts on a 16-byte boundary.
+size_t int8_linear_workspace(int M, int N, int K, bool rows);
 int launch_int8_linear(const LinearArgs &a, bool rows, void *ws, void *stream);
 
 struct WgradArgs {

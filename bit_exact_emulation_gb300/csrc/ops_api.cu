@@ -97,8 +97,8 @@ extern "C" int mcemu_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t
   return launch_act8_expand(fmt, T, H, q, ldq, e, lde, x, ldx, stream);
 }
 
-extern "C" size_t mcemu_int8_linear_workspace(int M, int N, int K) {
-  return M < 1 || N < 1 || K < 1 || K > 131071 ? 0 : int8_linear_workspace(M, N, K);
+extern "C" size_t mcemu_int8_linear_workspace(int M, int N, int K, int rows_aligned) {
+  return M < 1 || N < 1 || K < 1 || K > 131071 ? 0 : int8_linear_workspace(M, N, K, rows_aligned != 0);
 }
 
 extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t ldx, const float *sx,
@@ -115,7 +115,7 @@ extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t l
   const size_t s = out_fmt == MCEMU_INT32 ? 4 : bytes_of(out_fmt);
   if (!aligned(y, s) || !aligned(sx, 4) || !aligned(sw, 4) || !aligned(bias, 4)) return MCEMU_ERR_ALIGNMENT;
   const bool rows = aligned(x, 16) && aligned(w, 16) && ldx % 16 == 0 && ldw % 16 == 0;
-  const int st = check_ws(workspace, ws_bytes, mcemu_int8_linear_workspace(M, N, K));
+  const int st = check_ws(workspace, ws_bytes, mcemu_int8_linear_workspace(M, N, K, rows));
   if (st != MCEMU_OK) return st;
   LinearArgs a{M, N, K, x, w, ldx, ldw, ldy, sx, sw, bias, y, out_fmt};
   return launch_int8_linear(a, rows, workspace, stream);

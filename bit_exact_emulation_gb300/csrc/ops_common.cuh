@@ -209,6 +209,26 @@ inline int sm_count() {
   return n;
 }
 
+// A kernel that begins while the one before it on the stream still runs (programmatic dependent
+// launch): its set-up overlaps, and grid_wait() in it waits for that kernel's end and results.
+// The one before says with grid_go() that it may begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <class... P, class... A>
+int launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
+}
+
 inline int launch_status() { return cudaGetLastError() == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA; }
 
 // Whether a row-major operand's rows all start on 16-byte boundaries (an absent one does).

@@ -101,6 +101,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
   bool dead = false;
+  grid_go();
+  grid_wait();                                // the panels are the work of the kernel before
 
   if (warp >= 8) tc::give_registers();
   if (warp == 8 && lane == 0) {               // loads this CTA's half of both operands
@@ -218,8 +220,7 @@ int launch(const Args &g, const CUtensorMap &ma, const CUtensorMap &mb, const Ep
   const int64_t units = (int64_t)g.tiles_a * g.tiles_b * g.splits;
   if (units > INT32_MAX / 4) return MCEMU_ERR_UNSUPPORTED;
   const int pairs = (int)(units < sm_count() / 2 ? units : sm_count() / 2);
-  kernel<<<2 * pairs, kThreads, kSmem, st>>>(g, ma, mb, ep);
-  return launch_status();
+  return launch_early(kernel, dim3(2 * pairs), dim3(kThreads), kSmem, st, g, ma, mb, ep);
 }
 
 }  // namespace panel

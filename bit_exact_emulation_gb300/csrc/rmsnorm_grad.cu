@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
   extern __shared__ __align__(16) uint8_t raw[];
   S *stages = (S *)raw;
   const int t = threadIdx.y * TX + threadIdx.x;
+  grid_go();
   float dw[PER][VEC];
 #pragma unroll
   for (int p = 0; p < PER; p++)
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(TX) single_kernel(const NormGradArgs a, float 
   __shared__ float scales[2][PER * TX / MCEMU_ACT8_BLOCK + 1];      // of this row's blocks of 128 and the next one's
   const int i0 = threadIdx.x, blocks = (a.H + MCEMU_ACT8_BLOCK - 1) / MCEMU_ACT8_BLOCK;
   float w[PER], dw[PER];
+  grid_go();
 #pragma unroll
   for (int p = 0; p < PER; p++) {
     const int i = i0 + p * TX;
@@ -248,6 +250,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ pa
   __shared__ float sh[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
+  grid_wait();
   if (col < H)
 #pragma unroll 4
     for (int g = threadIdx.y; g < groups; g += 32) s += parts[(int64_t)g * H + col];
@@ -349,8 +352,8 @@ int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
     long_grad_kernel<T, CKPT><<<dim3(groups, (a.H + 255) / 256), 256, 0, st>>>(a, mean, ws);
   }
   if (groups < 0) return MCEMU_ERR_CUDA;
-  join_kernel<<<(a.H + 31) / 32, dim3(32, 32), 0, st>>>(ws, groups, a.H, a.dw);
-  return launch_status();
+  if (cudaGetLastError() != cudaSuccess) return MCEMU_ERR_CUDA;
+  return launch_early(join_kernel, dim3((a.H + 31) / 32), dim3(32, 32), 0, st, ws, groups, a.H, a.dw);
 }
 
 template <class T>

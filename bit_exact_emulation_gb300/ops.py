@@ -30,7 +30,7 @@ SYMBOLS = {
     "mcemu_rmsnorm_backward": (_I, [_I] * 4 + [_V, _L] * 5 + [_V, _V, _V, _L, _V, _V, _Z, _V]),
     "mcemu_rmsnorm_backward_workspace": (_Z, [_I] * 2),
     "mcemu_int8_linear": (_I, [_I] * 3 + [_V, _L, _V, _V, _L, _V, _V, _I, _V, _L, _V, _Z, _V]),
-    "mcemu_int8_linear_workspace": (_Z, [_I] * 3),
+    "mcemu_int8_linear_workspace": (_Z, [_I] * 4),
     "mcemu_act8_compress": (_I, [_I] * 3 + [_V, _L] * 3 + [_V]),
     "mcemu_act8_expand": (_I, [_I] * 3 + [_V, _L] * 3 + [_V]),
     "mcemu_act8_wgrad": (_I, [_I] * 3 + [_V, _L] * 3 + [_I, _I, _V, _L, _V, _Z, _V]),
@@ -250,7 +250,8 @@ def int8_linear(x, sx, weight, sw, bias=None, out: str = "bf16", y=None, workspa
     else:
         py, ldy = _matrix(w, "y", y, (_DTYPE[out],), dev, (M, N))
     L = _lib or lib()
-    ws, pws, nws = _workspace(w, L.mcemu_int8_linear_workspace(M, N, K), dev, workspace)
+    ws, pws, nws = _workspace(w, L.mcemu_int8_linear_workspace(M, N, K, (px | ldx | pw | ldw) % 16 == 0), dev,
+                             workspace)
     st = L.mcemu_int8_linear(M, N, K, px, ldx, psx, pw, ldw, psw, pb, _LINEAR_OUT[out], py, ldy, pws, nws, _stream(dev))
     if st:
         raise McemuError(st, w)

@@ -84,12 +84,14 @@ size_t mcemu_rmsnorm_backward_workspace(int T, int H);
  * acc itself; sx, sw and bias are then NULL.  x [M][K] (a token a row), w [N][K]
  * (a channel a row), sx [M], sw [N], y [M][N].  K <= 131071, so that no sum
  * overflows (else UNSUPPORTED); K = 0 gives sums of 0.
- * workspace: mcemu_int8_linear_workspace(M, N, K) bytes, 16-byte aligned; may be
- * NULL where that is 0. */
+ * workspace: mcemu_int8_linear_workspace(M, N, K, rows_aligned) bytes, 16-byte
+ * aligned; may be NULL where that is 0.  rows_aligned: 1 when every row of x and
+ * of w starts on a 16-byte boundary (both pointers and leading dimensions are
+ * multiples of 16), which needs less. */
 int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t ldx, const float *sx, const int8_t *w,
                       int64_t ldw, const float *sw, const float *bias, int out_fmt, void *y, int64_t ldy,
                       void *workspace, size_t ws_bytes, void *stream);
-size_t mcemu_int8_linear_workspace(int M, int N, int K);
+size_t mcemu_int8_linear_workspace(int M, int N, int K, int rows_aligned);
 
 /* ---- activation checkpoints ------------------------------------------------- */
 /* Elements of a row that share one exponent; a row of H has ceil(H / 128). */

@@ -126,9 +126,9 @@ def test_workspaces(L):
     """Sizes come without a device, are 0 for empty problems and do not wrap for large ones."""
     assert L.mcemu_rmsnorm_backward_workspace(0, 10) == 0
     assert L.mcemu_rmsnorm_backward_workspace(1 << 20, 16384) >= 16384 * 4
-    assert L.mcemu_int8_linear_workspace(0, 5, 5) == 0 and L.mcemu_act8_wgrad_workspace(5, 0, 5, 1) == 0
+    assert L.mcemu_int8_linear_workspace(0, 5, 5, 1) == 0 and L.mcemu_act8_wgrad_workspace(5, 0, 5, 1) == 0
     for M, N, K in ((1 << 20, 1 << 20, 131071), (1, 1 << 30, 4096), (1 << 30, 1, 4096)):
-        assert L.mcemu_int8_linear_workspace(M, N, K) < 1 << 62
+        assert L.mcemu_int8_linear_workspace(M, N, K, 0) < 1 << 62
 
 
 def test_cpu_tensors_are_refused(L):
