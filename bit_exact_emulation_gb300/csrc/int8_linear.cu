@@ -272,61 +272,65 @@ int go_few(const LinearArgs &a, bool wide, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 // A batch of tokens, too few to pay for panels: a block takes 128 channels by BN tokens and a part
-// of K.  Eight worker warps read both operands 64 k at a time, kSets stages ahead, widen them to
+// of K.  Worker warps read both operands 128 k at a time, kAhead stages ahead, widen them to
 // binary16 and store them in the swizzle; one thread issues the matrix instructions.  The
 // blocks of a cluster share K, and each adds up its share of the tile out of the others' shared
 // memory, so that no second launch joins the parts.
 // ---------------------------------------------------------------------------
-constexpr int kStageK = 64;                   // k of a stage: one 128-byte swizzle row
+constexpr int kStageK = 128;                  // k of a stage: two 128-byte swizzle rows, the first 64 k of all rows first
 constexpr int kChunk = 1024 / kStageK;        // stages between two transfers to int32
-constexpr int kWorkers = 256;
-constexpr int kSets = 4;                      // stages whose loads are in flight
 
 template <int BN>
 struct Batch {
+  static constexpr int kWorkers = 512;
+  static constexpr int kEach = BN / (kWorkers / 128);           // accumulator columns a worker drains
   static constexpr int kRows = 128 + BN;
-  static constexpr int kBytes = kRows * 128;                    // of one stage
-  static constexpr int kStages = 4;
-  static constexpr int kLoads = (kRows * 4 + kWorkers - 1) / kWorkers;      // 16-byte pieces of a stage per worker
-  static constexpr int kColumns = BN < 32 ? 32 : BN;            // tensor memory, a power of two
-  static constexpr int kSmem = kStages * kBytes + 1024 + 256;   // also holds the tile's 128 * BN sums
+  static constexpr int kHalf = kRows * 128, kBytes = 2 * kHalf; // of one stage
+  static constexpr int kStages = 2;
+  static constexpr int kPass = kWorkers / 8;                    // rows that the workers load at a time
+  static constexpr int kLoads = kRows / kPass;
+  static constexpr int kAhead = BN <= 64 ? 4 : 3;               // stages whose copies are in flight
+  static constexpr int kColumns = BN;                           // tensor memory: a power of two, 32 at least
+  static constexpr int kCopies = kAhead * kLoads * kWorkers * 16;
+  static constexpr int kSmem = kStages * kBytes + kCopies + 1024 + 256;     // also holds the tile's 128 * BN sums
 };
 
 template <int BN>
-__global__ void __launch_bounds__(kWorkers + 32, BN <= 64 ? 2 : 1) batch_kernel(const LinearArgs a, int tiles_n, int per) {
+__global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(const LinearArgs a, int tiles_n, int per) {
   using S = Batch<BN>;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t full = base + S::kStages * S::kBytes, empty = full + 8 * S::kStages, acc_full = empty + 8 * S::kStages,
-                 acc_empty = acc_full + 8, drain = acc_empty + 8, slot = drain + 8;
+  const uint32_t copies = base + S::kStages * S::kBytes, full = copies + S::kCopies, empty = full + 8 * S::kStages,
+                 acc_full = empty + 8 * S::kStages, acc_empty = acc_full + 8, drain = acc_empty + 8, slot = drain + 8;
+  constexpr int kMma = S::kWorkers / 32;        // the warp that issues
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t parts = tc::cluster_size(), rank = tc::cta_rank();
   const int tile = blockIdx.x / parts, n0 = (tile % tiles_n) * 128, m0 = (tile / tiles_n) * BN;
   const int stages = (a.K + kStageK - 1) / kStageK, s0 = (int)rank * per;
-  const int s1 = s0 < stages ? s0 + min(per, (stages - s0 + kSets - 1) / kSets * kSets) : s0;   // whole rounds of loads
+  const int s1 = max(s0, min(stages, s0 + per));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; s++) {
-      tc::mbar_init(full + 8 * s, 8);
+      tc::mbar_init(full + 8 * s, kMma);
       tc::mbar_init(empty + 8 * s, 1);
     }
     tc::mbar_init(acc_full, 1);
-    tc::mbar_init(acc_empty, 8);
+    tc::mbar_init(acc_empty, kMma);
     tc::mbar_init(drain, 1);
     tc::mbar_init_fence();
   }
-  if (warp == 8) tc::tmem_alloc<1>(slot, S::kColumns);
+  if (warp == kMma) tc::tmem_alloc<1>(slot, S::kColumns);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
   bool dead = false;
-  int sum[BN / 2];
+  int sum[S::kEach];
 #pragma unroll
-  for (int j = 0; j < BN / 2; j++) sum[j] = 0;
+  for (int j = 0; j < S::kEach; j++) sum[j] = 0;
 
-  if (warp == 8) {
+  if (warp == kMma) {
     if (lane == 0) {
       constexpr uint32_t ins = tc::instruction(128, BN, 0, 0, 0);
       uint32_t it = 0, ch = 0;
@@ -339,9 +343,12 @@ __global__ void __launch_bounds__(kWorkers + 32, BN <= 64 ? 2 : 1) batch_kernel(
           tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1, dead);
           if (dead) break;
           tc::fence_after();
-          const uint64_t da = tc::operand(at, 16, 1024), db = tc::operand(at + 128 * 128, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < kStageK / 16; k++) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, ins, (i | k) != 0);
+          for (int h = 0; h < 2; h++) {
+            const uint64_t da = tc::operand(at + h * S::kHalf, 16, 1024), db = tc::operand(at + h * S::kHalf + 128 * 128, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; k++) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, ins, (i | h | k) != 0);
+          }
           tc::commit<1>(empty + 8 * s);
         }
         tc::commit<1>(acc_full);
@@ -352,70 +359,78 @@ __global__ void __launch_bounds__(kWorkers + 32, BN <= 64 ? 2 : 1) batch_kernel(
     }
     __syncwarp();
   } else {
-    // pieces of a stage: piece p of a row is k 16p .. 16p + 15
-    const int piece = threadIdx.x & 3, row0 = threadIdx.x >> 2;
-    const int8_t *src[S::kLoads];
-    uint32_t store[S::kLoads];
-    bool have[S::kLoads], slots[S::kLoads];
+    // Pieces of a stage: piece p of a row is k 16p .. 16p + 15.  A warp reads whole 128-byte
+    // lines of four rows; eight lanes that store together hold two rows' pieces of one half,
+    // which lie in different banks.
+    const int piece = (lane & 3) + 4 * (lane >> 4), row0 = warp * 4 + ((lane >> 2) & 3);
+    const uint32_t store = (piece >> 2) * S::kHalf + (row0 >> 3) * 1024 + (row0 & 7) * 128 +
+                           (((2 * (piece & 3)) ^ (row0 & 7)) << 4);      // of row0; kPass rows on, 128 bytes each
+    const int8_t *pw = a.w + (int64_t)(n0 + row0) * a.ldw + 16 * piece, *px = a.x + (int64_t)(m0 + row0) * a.ldx + 16 * piece;
+    const int rows_w = a.N - n0 - row0, rows_x = a.M - m0 - row0;
+    // A thread copies its pieces ahead into places of its own, so that no barrier and no
+    // register waits for them (loaded to registers one stage ahead: 128 x 8192 x 4096 in 22 us in
+    // place of BATCHNOW).
+    const uint32_t place = copies + threadIdx.x * 16;
+    const auto copy = [&](int s) {
+      const int k = s < s1 ? s * kStageK : a.K;
+      const bool in = k + 16 * piece < a.K;
+      const uint32_t to = place + (uint32_t)((s - s0) % S::kAhead) * (S::kLoads * S::kWorkers * 16);
 #pragma unroll
-    for (int j = 0; j < S::kLoads; j++) {
-      const int r = row0 + 64 * j;
-      slots[j] = r < S::kRows;
-      store[j] = (r >> 3) * 1024 + (r & 7) * 128 + (((2 * piece) ^ (r & 7)) << 4);
-      if (r < 128) {
-        have[j] = n0 + r < a.N;
-        src[j] = a.w + (have[j] ? (int64_t)(n0 + r) * a.ldw : 0);
-      } else {
-        have[j] = slots[j] && m0 + r - 128 < a.M;
-        src[j] = a.x + (have[j] ? (int64_t)(m0 + r - 128) * a.ldx : 0);
+      for (int j = 0; j < S::kLoads; j++) {
+        const int r = S::kPass * j;                    // rows after row0
+        const bool is_w = r < 128, have = in && (is_w ? r < rows_w : r - 128 < rows_x);
+        const int8_t *from = !have ? a.w : is_w ? pw + r * a.ldw + k : px + (r - 128) * a.ldx + k;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + j * S::kWorkers * 16), "l"(from),
+                     "r"(have ? 16 : 0)
+                     : "memory");
       }
-    }
-    const auto load = [&](uint4 (&v)[S::kLoads], int s) {
-      const int k = s * kStageK + 16 * piece;
-#pragma unroll
-      for (int j = 0; j < S::kLoads; j++) v[j] = piece16<true>(src[j], k, a.K, have[j] && s < s1);
+      copy_commit();
     };
     uint32_t it = 0;
-    const auto step = [&](uint4 (&v)[S::kLoads], int next) {
+    const auto step = [&](int stage) {
       const uint32_t s = it % S::kStages, at = base + s * S::kBytes;
+      copy_wait<S::kAhead - 1>();
+      uint4 v[S::kLoads];
+      const uint32_t mine = place + (uint32_t)((stage - s0) % S::kAhead) * (S::kLoads * S::kWorkers * 16);
+#pragma unroll
+      for (int j = 0; j < S::kLoads; j++)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                     : "r"(mine + j * S::kWorkers * 16)
+                     : "memory");
       tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1, dead);
 #pragma unroll
       for (int j = 0; j < S::kLoads; j++) {
-        if (!slots[j]) continue;
         uint32_t h[8];
         half4(v[j].x, h[0], h[1]);
         half4(v[j].y, h[2], h[3]);
         half4(v[j].z, h[4], h[5]);
         half4(v[j].w, h[6], h[7]);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + store[j]), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + store + 128 * S::kPass * j), "r"(h[0]), "r"(h[1]), "r"(h[2]),
                      "r"(h[3])
                      : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (store[j] ^ 16)), "r"(h[4]), "r"(h[5]),
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (store ^ 16) + 128 * S::kPass * j), "r"(h[4]), "r"(h[5]),
                      "r"(h[6]), "r"(h[7])
                      : "memory");
       }
-      load(v, next);
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(full + 8 * s);
+      copy(stage + S::kAhead);
       it++;
     };
-    uint4 v[kSets][S::kLoads];
 #pragma unroll
-    for (int i = 0; i < kSets; i++) load(v[i], s0 + i);
-    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * (BN / 2);
+    for (int i = 0; i < S::kAhead; i++) copy(s0 + i);
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * S::kEach;
     uint32_t ch = 0;
     for (int c = s0; c < s1; c += kChunk, ch++) {
       const int e = min(s1, c + kChunk);
-      for (int s = c; s < e; s += kSets) {
-#pragma unroll
-        for (int i = 0; i < kSets; i++) step(v[i], s + i + kSets);
-      }
+      for (int s = c; s < e; s++) step(s);
       tc::mbar_wait(acc_full, ch & 1, dead);
       __syncwarp();
       tc::fence_after();
 #pragma unroll
-      for (int j = 0; j < BN / 2; j += 16) {
+      for (int j = 0; j < S::kEach; j += 16) {
         float f[16];
         tc::tmem_load16(mine + j, f);
         tc::tmem_wait();
@@ -427,17 +442,18 @@ __global__ void __launch_bounds__(kWorkers + 32, BN <= 64 ? 2 : 1) batch_kernel(
       if (lane == 0) tc::mbar_arrive(acc_empty);
     }
   }
+  copy_wait<0>();
   // sums to shared memory (token by channel), then this block's tokens out of every block's
   __syncthreads();
-  if (warp < 8) {
-    const uint32_t at = base + ((warp >> 2) * (BN / 2) * 128 + (warp & 3) * 32 + lane) * 4;
+  if (warp < kMma) {
+    const uint32_t at = base + ((warp >> 2) * S::kEach * 128 + (warp & 3) * 32 + lane) * 4;
 #pragma unroll
-    for (int j = 0; j < BN / 2; j++)
+    for (int j = 0; j < S::kEach; j++)
       asm volatile("st.shared.s32 [%0], %1;" ::"r"(at + j * 512), "r"(sum[j]) : "memory");
   }
   tc::cluster_sync();
-  if (warp < 8) {
-    // four channels of every eighth token to a thread; all blocks' parts asked for at once
+  if (warp < kMma) {
+    // four channels of every kMma-th token to a thread; all blocks' parts asked for at once
     const int r = lane * 4, n = n0 + r, share = BN / parts, end = min(a.M - m0, (int)(rank + 1) * share);
     const bool scales = a.out_fmt != MCEMU_INT32;
     float sw[4], bias[4];
@@ -446,7 +462,7 @@ __global__ void __launch_bounds__(kWorkers + 32, BN <= 64 ? 2 : 1) batch_kernel(
       sw[i] = scales && n + i < a.N ? __ldg(a.sw + n + i) : 0.f;
       bias[i] = scales && a.bias && n + i < a.N ? __ldg(a.bias + n + i) : 0.f;
     }
-    for (int m = rank * share + warp; m < end; m += 8) {
+    for (int m = rank * share + warp; m < end; m += kMma) {
       const float sx = scales ? __ldg(a.sx + m0 + m) : 0.f;
       int4 v[8];
 #pragma unroll
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(kWorkers + 32, BN <= 64 ? 2 : 1) batch_kernel(
   }
   tc::fence_before();
   tc::cluster_sync();
-  if (warp == 8) {
+  if (warp == kMma) {
     tc::fence_after();
     tc::tmem_free<1>(tmem, S::kColumns);
   }
@@ -483,15 +499,15 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
   }
   const int tiles_n = (a.N + 127) / 128, stages = (a.K + kStageK - 1) / kStageK;
   const int64_t tiles = (int64_t)tiles_n * ((a.M + BN - 1) / BN);
-  // Parts of K: a power of two of at most eight (a portable cluster), at least four stages each,
+  // Parts of K: a power of two of at most eight (a portable cluster), at least two stages each,
   // until the blocks fill the multiprocessors.
-  const int room = sm_count() * (BN <= 64 ? 2 : 1);
+  const int room = sm_count();
   int parts = 1;
-  while (parts < 8 && tiles * parts * 2 <= room && stages >= parts * 2 * 4) parts *= 2;
+  while (parts < 8 && tiles * parts * 2 <= room && stages >= parts * 4) parts *= 2;
   if (tiles * parts > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * parts));
-  cfg.blockDim = dim3(kWorkers + 32);
+  cfg.blockDim = dim3(S::kWorkers + 32);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -500,8 +516,7 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t rc = cudaLaunchKernelEx(&cfg, kernel, a, tiles_n,
-                                            ((stages + parts - 1) / parts + kSets - 1) / kSets * kSets);
+  const cudaError_t rc = cudaLaunchKernelEx(&cfg, kernel, a, tiles_n, (stages + parts - 1) / parts);
   return rc == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
 }
 // Products that go through panels: more than one wave of the batch kernel's tiles, or rows that
@@ -533,7 +548,6 @@ int launch_int8_linear(const LinearArgs &a, bool rows, void *ws, void *stream) {
   if (a.M <= 8) return go_few<1>(a, wide, st);
   if (a.M <= 16) return go_few<2>(a, wide, st);
   if (a.M <= kFew || a.K == 0) return go_few<4>(a, wide, st);
-  if (a.M <= 32) return go_batch<32>(a, st);
   if (a.M <= 64) return go_batch<64>(a, st);
   return go_batch<128>(a, st);
 }
