@@ -160,16 +160,10 @@ int launch_act8_wgrad(const WgradArgs &a, bool direct, void *ws, void *stream) {
   if (!panel::panel_fits(p.blocks_k, p.ttiles) || !panel::panel_fits(p.blocks_n, p.ttiles)) return MCEMU_ERR_UNSUPPORTED;
   uint8_t *px = (uint8_t *)ws, *pdy = px + p.panel_x;
   float *parts = p.splits > 1 ? (float *)(pdy + p.panel_dy) : nullptr;
-  CUtensorMap mx, md;
-  int rc = panel::panel_map(&mx, px, p.blocks_k, p.ttiles);
-  if (rc == MCEMU_OK)
-    rc = direct ? tc::tensor_map(&md, a.dy, a.N, a.T, a.lddy, 64, true) : panel::panel_map(&md, pdy, p.blocks_n, p.ttiles);
-  if (rc != MCEMU_OK) return rc;
   widen_kernel<<<(unsigned)(p.blocks_k * p.ttiles), 256, 0, st>>>(a, p.ttiles, rows16(a.q, a.ldq, 1), px);
   if (!direct) copy_kernel<<<(unsigned)(p.blocks_n * p.ttiles), 256, 0, st>>>(a, p.ttiles, pdy);
-  const panel::Args g{p.ttiles, p.blocks_k / 2, p.blocks_n / 2, p.splits, p.per_split, kChunk};
-  rc = direct ? panel::launch<WgradEp, 1, 1, 1>(g, mx, md, WgradEp{a, parts}, st)
-              : panel::launch<WgradEp, 1, 1, 0>(g, mx, md, WgradEp{a, parts}, st);
+  int rc = panel::launch<WgradEp, 1, 1>(px, a.K, pdy, a.N, direct ? a.dy : nullptr, a.lddy, a.T, p.ttiles, p.splits,
+                                    p.per_split, kChunk, WgradEp{a, parts}, st);
   if (rc == MCEMU_OK && parts)
     rc = launch_early(join_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, parts, p.splits);
   return rc;

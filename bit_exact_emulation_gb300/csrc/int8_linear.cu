@@ -123,12 +123,8 @@ int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
   const int64_t tiles = (int64_t)(x.blocks + w.blocks) * kt;
   if (!panel::panel_fits(x.blocks, kt) || !panel::panel_fits(w.blocks, kt)) return MCEMU_ERR_UNSUPPORTED;
   widen_kernel<<<(unsigned)tiles, 256, 0, st>>>(x, w, a.K, kt, wide);
-  CUtensorMap mw, mx;
-  int rc = panel::panel_map(&mw, w.to, w.blocks, kt);
-  if (rc == MCEMU_OK) rc = panel::panel_map(&mx, x.to, x.blocks, kt);
-  if (rc != MCEMU_OK) return rc;
-  panel::Args g{kt, w.blocks / 2, x.blocks / 2, 1, kt, 1024 / panel::kTileK};
-  return panel::launch<LinearEp<OUT>, 0, 0, 0>(g, mw, mx, LinearEp<OUT>{a}, st);
+  return panel::launch<LinearEp<OUT>, 0, 0>(w.to, a.N, x.to, a.M, nullptr, 0, a.K, kt, 1, kt, 1024 / panel::kTileK,
+                                            LinearEp<OUT>{a}, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -303,7 +299,7 @@ __global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(cons
   const uint32_t copies = base + S::kStages * S::kBytes, full = copies + S::kCopies, empty = full + 8 * S::kStages,
                  acc_full = empty + 8 * S::kStages, acc_empty = acc_full + 8, drain = acc_empty + 8, slot = drain + 8;
   constexpr int kMma = S::kWorkers / 32;        // the warp that issues
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc::warp_number(), lane = threadIdx.x & 31;
   const uint32_t parts = tc::cluster_size(), rank = tc::cta_rank();
   const int tile = blockIdx.x / parts, n0 = (tile % tiles_n) * 128, m0 = (tile / tiles_n) * BN;
   const int stages = (a.K + kStageK - 1) / kStageK, s0 = (int)rank * per;
@@ -325,22 +321,23 @@ __global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(cons
   tc::fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+  tmem = __shfl_sync(0xFFFFFFFFu, tmem, 0);
   bool dead = false;
   int sum[S::kEach];
 #pragma unroll
   for (int j = 0; j < S::kEach; j++) sum[j] = 0;
 
   if (warp == kMma) {
-    if (lane == 0) {
+    {
       constexpr uint32_t ins = tc::instruction(128, BN, 0, 0, 0);
       uint32_t it = 0, ch = 0;
       for (int c = s0; c < s1 && !dead; c += kChunk, ch++) {
-        tc::mbar_wait(acc_empty, (ch & 1) ^ 1, dead);
+        tc::mbar_wait_warp(acc_empty, (ch & 1) ^ 1, dead);
         tc::fence_after();
         const int n = min(kChunk, s1 - c);
         for (int i = 0; i < n && !dead; i++, it++) {
           const uint32_t s = it % S::kStages, at = base + s * S::kBytes;
-          tc::mbar_wait(full + 8 * s, (it / S::kStages) & 1, dead);
+          tc::mbar_wait_warp(full + 8 * s, (it / S::kStages) & 1, dead);
           if (dead) break;
           tc::fence_after();
 #pragma unroll
@@ -355,9 +352,8 @@ __global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(cons
       }
       bool late = false;                       // everything issued ends before the memory is given back
       tc::commit<1>(drain);
-      tc::mbar_wait(drain, 0, late);
+      tc::mbar_wait_warp(drain, 0, late);
     }
-    __syncwarp();
   } else {
     // Pieces of a stage: piece p of a row is k 16p .. 16p + 15.  A warp reads whole 128-byte
     // lines of four rows; eight lanes that store together hold two rows' pieces of one half,

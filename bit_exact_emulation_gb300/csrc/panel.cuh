@@ -5,9 +5,9 @@
 // one 128-row block following one another along k; or (MN-major only) a matrix in global
 // memory, k by rows, from which the copy engine makes the same images.
 //
-// A pair computes 256 rows of A by 256 rows of B: each CTA holds 128 rows of both (32 KB a
-// stage) and 128 x 256 accumulators, twice, so that one set is drained while the other
-// fills.  The accumulators leave tensor memory every `chunk` stages and are added up in
+// A pair computes 256 rows of A by BN (256 or 128) rows of B: each CTA holds 128 rows of A and half
+// of B's (32 or 24 KB a stage) and 128 x BN accumulators, twice, so that one set is drained
+// while the other fills.  The accumulators leave tensor memory every `chunk` stages and are added up in
 // registers, in whatever type the caller's sums need; the matrix unit alone would drop the
 // low bits of long sums (it truncates, it does not round).
 //
@@ -23,16 +23,20 @@ namespace panel {
 
 constexpr int kTileBytes = 16384;             // 128 rows x 64 k x 2 bytes
 constexpr int kTileK = 64;
-constexpr int kStages = 6;
-constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+template <int BN>
+struct Size {
+  static constexpr int kTilesBytes = kTileBytes + BN * 64;      // of one k tile: 128 rows of A, BN / 2 of B
+  static constexpr int kStageBytes = 2 * kTilesBytes;           // a stage is two k tiles
+  static constexpr int kStages = BN == 256 ? 3 : 4;
+  static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+};
 constexpr int kThreads = 384;                 // eight warps drain, one loads, one issues, two are idle
 
 struct Args {
   int ka;                    // tiles along k
-  int tiles_a, tiles_b;      // 256-row tiles of either operand
+  int tiles_a, tiles_b;      // tiles of 256 rows of A and of BN rows of B
   int splits, per_split;     // parts of the sum, k tiles to a part
-  int chunk;                 // stages between two drains
+  int chunk;                 // k tiles between two drains, an even number
 };
 
 // Where a unit of work lies.
@@ -53,32 +57,36 @@ __device__ __forceinline__ Unit unit_at(const Args &g, int u) {
   return r;
 }
 
-// Copies the two operands' part of stage k for this CTA.  DIRECT: B is a matrix in memory.
-template <int DIRECT>
-__device__ __forceinline__ void load_stage(const Args &g, const CUtensorMap *ma, const CUtensorMap *mb, const Unit &w,
+// Copies the two operands' part of k tile k for this CTA.  DIRECT: B is a matrix in memory.  The
+// boxes of B's map are BN / 2 rows of a panel, or 64 by 64 elements of a matrix.
+template <int BN, int DIRECT>
+__device__ __forceinline__ void load_tiles(const Args &g, const CUtensorMap *ma, const CUtensorMap *mb, const Unit &w,
                                            int rank, int k, uint32_t at, uint32_t bar) {
   tc::box_load_pair(at, ma, 0, ((2 * w.ta + rank) * g.ka + k) * 128, bar);
   if constexpr (DIRECT) {
-    const int x = w.tb * 256 + rank * 128;
+    const int x = w.tb * BN + rank * (BN / 2);
     tc::box_load_pair(at + kTileBytes, mb, x, k * kTileK, bar);
-    tc::box_load_pair(at + kTileBytes + 8192, mb, x + 64, k * kTileK, bar);
+    if constexpr (BN == 256) tc::box_load_pair(at + kTileBytes + 8192, mb, x + 64, k * kTileK, bar);
   } else {
-    tc::box_load_pair(at + kTileBytes, mb, 0, ((2 * w.tb + rank) * g.ka + k) * 128, bar);
+    const int block = BN == 256 ? 2 * w.tb + rank : w.tb;
+    tc::box_load_pair(at + kTileBytes, mb, 0, (block * g.ka + k) * 128 + (BN == 256 ? 0 : 64 * rank), bar);
   }
 }
 
 // Ep: `Ep::Sum` is the type of the register sums; add(Sum &, float) takes one accumulator;
 // store(row of A, row of B, 16 sums along B, split) writes 16 outputs.  MN: operands are
 // MN-major; BF16: bfloat16 (else binary16).
-template <class Ep, int MN, int BF16, int DIRECT>
+template <class Ep, int BN, int MN, int BF16, int DIRECT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     panel_kernel(const Args g, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                  const Ep ep) {
+  using S = Size<BN>;
+  constexpr int kStages = S::kStages, kStageBytes = S::kStageBytes, kCols = BN / 2;      // columns a warp drains
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
   const uint32_t full = base + kStages * kStageBytes, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc::warp_number(), lane = threadIdx.x & 31;
   const uint32_t rank = tc::cta_rank();
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1, units = g.tiles_a * g.tiles_b * g.splits;
 
@@ -100,6 +108,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+  tmem = __shfl_sync(0xFFFFFFFFu, tmem, 0);
   bool dead = false;
   grid_go();
   grid_wait();                                // the panels are the work of the kernel before
@@ -109,12 +118,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     for (int u = first; u < units; u += step) {
       const Unit w = unit_at(g, u);
-      for (int k = w.k0; k < w.k1 && !dead; k++, it++) {
-        const uint32_t s = it % kStages;
+      for (int k = w.k0; k < w.k1 && !dead; k += 2, it++) {
+        const uint32_t s = it % kStages, at = base + s * kStageBytes;
+        const bool two = k + 1 < w.k1;
         tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, dead);
         if (dead) break;
-        if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * kStageBytes);
-        load_stage<DIRECT>(g, &ma, &mb, w, rank, k, base + s * kStageBytes, full + 8 * s);
+        if (rank == 0) tc::mbar_expect(full + 8 * s, (two ? 4 : 2) * S::kTilesBytes);
+        load_tiles<BN, DIRECT>(g, &ma, &mb, w, rank, k, at, full + 8 * s);
+        if (two) load_tiles<BN, DIRECT>(g, &ma, &mb, w, rank, k + 1, at + S::kTilesBytes, full + 8 * s);
       }
     }
     if (rank == 0) {                          // both CTAs' copies end before either leaves
@@ -124,49 +135,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::mbar_wait(full + 8 * s, (last / kStages) & 1, late);
       }
     }
-  } else if (warp == 9 && lane == 0 && rank == 0) {   // issues the pair's matrix instructions
-    constexpr uint32_t ins = tc::instruction(256, 256, BF16, MN, MN);
-    uint32_t it = 0, ch = 0;
+  } else if (warp == 9 && rank == 0) {        // issues the pair's matrix instructions
+    constexpr uint32_t ins = tc::instruction(256, BN, BF16, MN, MN);
+    uint32_t s = 0, phase = 0, ch = 0;
     for (int u = first; u < units && !dead; u += step) {
       const Unit w = unit_at(g, u);
       for (int k = w.k0; k < w.k1 && !dead; k += g.chunk, ch++) {
-        const uint32_t set = ch & 1;
-        tc::mbar_wait(acc_empty + 8 * set, ((ch >> 1) & 1) ^ 1, dead);
+        const uint32_t set = ch & 1, d = tmem + set * 256;
+        tc::mbar_wait_warp(acc_empty + 8 * set, ((ch >> 1) & 1) ^ 1, dead);
         tc::fence_after();
         const int n = min(g.chunk, w.k1 - k);
-        for (int i = 0; i < n; i++, it++) {
-          const uint32_t s = it % kStages, at = base + s * kStageBytes, fp = (it / kStages) & 1;
-          tc::mbar_wait(full + 8 * s, fp, dead);
+        bool add = false;
+        for (int i = 0; i < n; i += 2) {
+          const uint32_t at = base + s * kStageBytes;
+          tc::mbar_wait_warp(full + 8 * s, phase, dead);
           if (dead) break;
           tc::fence_after();
-          if constexpr (MN) {
-            // 64 k = eight atoms of eight; atoms of one k lie 8 KB apart along the rows
-            const uint64_t da = tc::operand(at, 8192, 1024), db = tc::operand(at + kTileBytes, 8192, 1024);
 #pragma unroll
-            for (int x = 0; x < 4; x++) tc::mma<2>(tmem + set * 256, da + 128 * x, db + 128 * x, ins, (i | x) != 0);
-          } else {
-            const uint64_t da = tc::operand(at, 16, 1024), db = tc::operand(at + kTileBytes, 16, 1024);
+          for (int h = 0; h < 2; h++) {
+            if (h && i + 1 >= n) break;
+            // 64 k: MN-major eight atoms of eight, atoms of one k 8 KB apart along the rows
+            const uint32_t ta = at + h * S::kTilesBytes, tb = ta + kTileBytes;
+            const uint64_t da = MN ? tc::operand(ta, 8192, 1024) : tc::operand(ta, 16, 1024);
+            const uint64_t db = MN ? tc::operand(tb, 8192, 1024) : tc::operand(tb, 16, 1024);
 #pragma unroll
-            for (int x = 0; x < 4; x++) tc::mma<2>(tmem + set * 256, da + 2 * x, db + 2 * x, ins, (i | x) != 0);
+            for (int x = 0; x < 4; x++) {
+              tc::mma<2>(d, da + (MN ? 128 : 2) * x, db + (MN ? 128 : 2) * x, ins, add);
+              add = true;
+            }
           }
           tc::commit<2>(empty + 8 * s);
+          if (++s == kStages) s = 0, phase ^= 1;
         }
         tc::commit<2>(acc_full + 8 * set);
       }
     }
     bool late = false;                        // everything issued ends before the memory is given back
     tc::commit_here<2>(drain);
-    tc::mbar_wait(drain, 0, late);
+    tc::mbar_wait_warp(drain, 0, late);
   } else if (warp < 8) {
     tc::take_registers();
-    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * 128;
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * kCols;
     uint32_t ch = 0;
     for (int u = first; u < units; u += step) {
       const Unit w = unit_at(g, u);
-      typename Ep::Sum sum[128];
+      typename Ep::Sum sum[kCols];
 #pragma unroll
-      for (int j = 0; j < 128; j++) sum[j] = 0;
-      const int ra = w.ta * 256 + rank * 128 + (warp & 3) * 32 + lane, rb = w.tb * 256 + (warp >> 2) * 128;
+      for (int j = 0; j < kCols; j++) sum[j] = 0;
+      const int ra = w.ta * 256 + rank * 128 + (warp & 3) * 32 + lane, rb = w.tb * BN + (warp >> 2) * kCols;
       for (int k = w.k0; k < w.k1; k += g.chunk, ch++) {
         const uint32_t set = ch & 1;
         tc::mbar_wait(acc_full + 8 * set, (ch >> 1) & 1, dead);
@@ -175,9 +191,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float v[2][16];
         tc::tmem_load16(mine + set * 256, v[0]);
 #pragma unroll
-        for (int j = 0; j < 128; j += 16) {
+        for (int j = 0; j < kCols; j += 16) {
           tc::tmem_wait();
-          if (j + 16 < 128) tc::tmem_load16(mine + set * 256 + j + 16, v[(j >> 4) + 1 & 1]);
+          if (j + 16 < kCols) tc::tmem_load16(mine + set * 256 + j + 16, v[(j >> 4) + 1 & 1]);
 #pragma unroll
           for (int x = 0; x < 16; x++) Ep::add(sum[j + x], v[(j >> 4) & 1][x]);
         }
@@ -187,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // the matrix unit has both sets to go on with meanwhile
 #pragma unroll
-      for (int j = 0; j < 128; j += 16) ep.store(ra, rb + j, &sum[j], w.split);
+      for (int j = 0; j < kCols; j += 16) ep.store(ra, rb + j, &sum[j], w.split);
     }
   }
   __syncwarp();
@@ -199,28 +215,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// Tensor map of a panel of `blocks` 128-row blocks.
-inline int panel_map(CUtensorMap *map, const void *panel, int blocks, int ktiles) {
-  return tc::tensor_map(map, panel, 64, (uint64_t)blocks * ktiles * 128, 64, 128, false);
+// Tensor map of a panel of `blocks` 128-row blocks, in boxes of `box` rows.
+inline int panel_map(CUtensorMap *map, const void *panel, int blocks, int ktiles, int box) {
+  return tc::tensor_map(map, panel, 64, (uint64_t)blocks * ktiles * 128, 64, box, false);
 }
 // What fits a panel: its rows are counted in 32 bits.
 inline bool panel_fits(int64_t blocks, int64_t ktiles) { return blocks * ktiles * 128 <= INT32_MAX; }
 
-template <class Ep, int MN, int BF16, int DIRECT>
-int launch(const Args &g, const CUtensorMap &ma, const CUtensorMap &mb, const Ep &ep, cudaStream_t st) {
+// Rows of B to a tile: 128 where that ends sooner.  A round is every pair's tile; one of 128 rows
+// takes 0.62 of a round of 256 (weight gradient of 8192 x 4096 x 4096: seven rounds 199.5 us, four
+// 185.9; of 1024 x 1024 x 1024, one round either way: 13.9 and 16.7).
+inline int rows_b(int64_t rows_a, int64_t rows, int splits) {
+  const int64_t pairs = sm_count() / 2, ta = (rows_a + 255) / 256;
+  const int64_t wide = (ta * ((rows + 255) / 256) * splits + pairs - 1) / pairs;
+  const int64_t slim = (ta * ((rows + 127) / 128) * splits + pairs - 1) / pairs;
+  return slim * 5 < wide * 8 ? 128 : 256;
+}
+
+template <class Ep, int BN, int MN, int BF16, int DIRECT>
+int launch_tiles(const Args &g, const CUtensorMap &ma, const CUtensorMap &mb, const Ep &ep, cudaStream_t st) {
   static std::atomic<bool> ready[64];
-  const auto kernel = panel_kernel<Ep, MN, BF16, DIRECT>;
+  const auto kernel = panel_kernel<Ep, BN, MN, BF16, DIRECT>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MCEMU_ERR_CUDA;
   if (dev >= 64 || !ready[dev].load()) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Size<BN>::kSmem) != cudaSuccess)
       return MCEMU_ERR_CUDA;
     if (dev < 64) ready[dev].store(true);
   }
   const int64_t units = (int64_t)g.tiles_a * g.tiles_b * g.splits;
   if (units > INT32_MAX / 4) return MCEMU_ERR_UNSUPPORTED;
   const int pairs = (int)(units < sm_count() / 2 ? units : sm_count() / 2);
-  return launch_early(kernel, dim3(2 * pairs), dim3(kThreads), kSmem, st, g, ma, mb, ep);
+  return launch_early(kernel, dim3(2 * pairs), dim3(kThreads), Size<BN>::kSmem, st, g, ma, mb, ep);
+}
+
+// The product of panel a (rows_a rows) and b: a panel, or with `matrix` (MN-major) a matrix of
+// k rows and ld elements between them.
+template <class Ep, int MN, int BF16>
+int launch(const void *a, int rows_a, const void *b, int rows, const void *matrix, int64_t ld, int k, int ktiles,
+           int splits, int per_split, int chunk, const Ep &ep, cudaStream_t st) {
+  const int bn = rows_b(rows_a, rows, splits), blocks_a = (rows_a + 255) / 256 * 2, blocks_b = (rows + 255) / 256 * 2;
+  CUtensorMap ma, mb;
+  int rc = panel_map(&ma, a, blocks_a, ktiles, 128);
+  if (rc == MCEMU_OK)
+    rc = matrix ? tc::tensor_map(&mb, matrix, rows, k, ld, 64, true) : panel_map(&mb, b, blocks_b, ktiles, bn / 2);
+  if (rc != MCEMU_OK) return rc;
+  const Args g{ktiles, blocks_a / 2, (rows + bn - 1) / bn, splits, per_split, chunk};
+  if constexpr (MN) {
+    if (matrix)
+      return bn == 256 ? launch_tiles<Ep, 256, MN, BF16, 1>(g, ma, mb, ep, st)
+                       : launch_tiles<Ep, 128, MN, BF16, 1>(g, ma, mb, ep, st);
+  }
+  return bn == 256 ? launch_tiles<Ep, 256, MN, BF16, 0>(g, ma, mb, ep, st)
+                   : launch_tiles<Ep, 128, MN, BF16, 0>(g, ma, mb, ep, st);
 }
 
 }  // namespace panel

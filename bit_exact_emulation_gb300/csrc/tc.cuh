@@ -150,6 +150,19 @@ __device__ __forceinline__ void box_load_pair(uint32_t to, const CUtensorMap *ma
       : "memory");
 }
 
+// The same by a whole warp, its verdict known to be common to all lanes: what the issuing warp
+// does with it stays in uniform registers, which is what the matrix instruction reads.  (One lane
+// alone in a branch moves every operand there anew: 120 cycles an instruction.)
+__device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, bool &dead) {
+  if (dead) return;
+#pragma unroll 1
+  for (int i = 0; i < 64; i++)
+    if (__any_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return;
+  dead = !__any_sync(0xFFFFFFFFu, mbar_wait_long(bar, parity));
+}
+// The warp's number in its block, known to be uniform.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0); }
+
 // ---- fences ------------------------------------------------------------------
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -198,37 +211,47 @@ __host__ __device__ constexpr uint32_t instruction(int m, int n, int bf16, int a
   return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 |
          (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
+// One matrix instruction, by one elected lane of the calling warp (all lanes call).
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t ins, bool add) {
   if constexpr (CG == 1)
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(ins), "r"((uint32_t)add)
         : "memory");
   else
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(ins), "r"((uint32_t)add)
         : "memory");
 }
-// Arrives on `bar` (of both CTAs for CG 2) once every matrix instruction issued so far is done.
+// Arrives on `bar` (of both CTAs for CG 2) once every matrix instruction issued so far by the
+// elected lane is done (all lanes call).
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (CG == 1)
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+        : "memory");
   else
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
 }
-
 // The same on this CTA's barrier alone.
 template <int CG>
 __device__ __forceinline__ void commit_here(uint32_t bar) {
   if constexpr (CG == 1) commit<1>(bar);
   else
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+        : "memory");
 }
 
 }  // namespace tc
