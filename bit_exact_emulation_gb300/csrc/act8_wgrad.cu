@@ -79,16 +79,15 @@ __device__ __forceinline__ void put(const WgradArgs &a, int64_t at, float v) {
 struct WgradEp {
   using Sum = float;
   WgradArgs a;
-  float *parts;              // [splits][N][K] when the sum is split
+  float *parts;              // of the shared tiles: [slot][BN][256]
+  int bn;
   static __device__ __forceinline__ void add(float &s, float v) { s += v; }
-  __device__ __forceinline__ void store(int k, int n0, const float *sum, int split) const {
-    if (k >= a.K) return;
-    if (parts) {
-      float *p = parts + ((int64_t)split * a.N + n0) * a.K + k;
+  __device__ __forceinline__ void store(const panel::Unit &w, int k, int n0, const float *sum) const {
+    if (w.slot >= 0) {
+      float *p = parts + ((int64_t)w.slot * bn + n0 - w.tb * bn) * 256 + k - w.ta * 256;
 #pragma unroll
-      for (int x = 0; x < 16; x++)
-        if (n0 + x < a.N) p[(int64_t)x * a.K] = sum[x];
-    } else {
+      for (int x = 0; x < 16; x++) p[x * 256] = sum[x];
+    } else if (k < a.K) {
 #pragma unroll
       for (int x = 0; x < 16; x++)
         if (n0 + x < a.N) put(a, (int64_t)(n0 + x) * a.lddw + k, sum[x]);
@@ -96,14 +95,18 @@ struct WgradEp {
   }
 };
 
-// Parts of the sum over the tokens, added in order.
-__global__ void __launch_bounds__(256) join_kernel(const WgradArgs a, const float *__restrict__ parts, int splits) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, size = (int64_t)a.N * a.K;
-  if (i >= size) return;
+// The shared tiles' parts, added in order: a row of a tile to a block.
+__global__ void __launch_bounds__(256) join_kernel(const WgradArgs a, const panel::Args g, int bn,
+                                                   const float *__restrict__ parts) {
+  const int t = blockIdx.x / bn, row = blockIdx.x - t * bn;
+  int ta, tb;
+  panel::tile_at(g, g.full + t, ta, tb);
+  const int n = tb * bn + row, k = ta * 256 + threadIdx.x;
   grid_wait();
-  float s = parts[i];
-  for (int p = 1; p < splits; p++) s += parts[p * size + i];
-  put(a, i / a.K * a.lddw + i % a.K, s);
+  if (n >= a.N || k >= a.K) return;
+  float s = 0.f;
+  for (int p = 0; p < g.parts; p++) s += parts[((int64_t)(p * g.rest + t) * bn + row) * 256 + threadIdx.x];
+  put(a, (int64_t)n * a.lddw + k, s);
 }
 
 // No tokens: a gradient of zeros.
@@ -116,26 +119,20 @@ __global__ void __launch_bounds__(256) zero_kernel(const WgradArgs a) {
 // time: 4 stages 1.2e-7, 273 us; 16 stages 1.8e-7, 225 us; 64 stages 9.5e-7, 217 us.
 constexpr int kChunk = 16;
 
-struct Plan {
-  int ttiles, blocks_k, blocks_n, splits, per_split;
+struct Layout {
+  int ttiles, blocks_k, blocks_n;
+  panel::Plan cut;
   int64_t panel_x, panel_dy, parts;          // bytes
 };
-Plan plan_of(int T, int N, int K, bool direct) {
-  Plan p;
+Layout layout_of(int T, int N, int K, bool direct) {
+  Layout p;
   p.ttiles = (T + 63) / 64;
   p.blocks_k = (K + 255) / 256 * 2;
   p.blocks_n = (N + 255) / 256 * 2;
-  // A product of few tiles is split along the tokens until the pairs of CTAs have work, down to
-  // eight stages a part.
-  const int64_t tiles = (int64_t)(p.blocks_k / 2) * (p.blocks_n / 2), pairs = 76;
-  int64_t s = tiles >= pairs ? 1 : pairs / tiles;
-  if (s > p.ttiles / 8) s = p.ttiles / 8;
-  if (s < 1) s = 1;
-  p.per_split = (int)((p.ttiles + s - 1) / s);
-  p.splits = (p.ttiles + p.per_split - 1) / p.per_split;
+  p.cut = panel::plan_of(K, N, p.ttiles, true);
   p.panel_x = (int64_t)p.blocks_k * p.ttiles * panel::kTileBytes;
   p.panel_dy = direct ? 0 : (int64_t)p.blocks_n * p.ttiles * panel::kTileBytes;
-  p.parts = p.splits > 1 ? (int64_t)p.splits * N * K * 4 : 0;
+  p.parts = (int64_t)p.cut.rest * p.cut.parts * 256 * p.cut.bn * 4;
   return p;
 }
 
@@ -144,7 +141,7 @@ Plan plan_of(int T, int N, int K, bool direct) {
 int act8_wgrad_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_timeouts(st, got); }
 
 size_t act8_wgrad_workspace(int T, int N, int K, bool direct) {
-  const Plan p = plan_of(T, N, K, direct);
+  const Layout p = layout_of(T, N, K, direct);
   return (size_t)(p.panel_x + p.panel_dy + p.parts);
 }
 
@@ -156,17 +153,18 @@ int launch_act8_wgrad(const WgradArgs &a, bool direct, void *ws, void *stream) {
     zero_kernel<<<(unsigned)blocks, 256, 0, st>>>(a);
     return launch_status();
   }
-  const Plan p = plan_of(a.T, a.N, a.K, direct);
+  const Layout p = layout_of(a.T, a.N, a.K, direct);
   if (!panel::panel_fits(p.blocks_k, p.ttiles) || !panel::panel_fits(p.blocks_n, p.ttiles)) return MCEMU_ERR_UNSUPPORTED;
   uint8_t *px = (uint8_t *)ws, *pdy = px + p.panel_x;
-  float *parts = p.splits > 1 ? (float *)(pdy + p.panel_dy) : nullptr;
+  float *parts = (float *)(pdy + p.panel_dy);
   widen_kernel<<<(unsigned)(p.blocks_k * p.ttiles), 256, 0, st>>>(a, p.ttiles, rows16(a.q, a.ldq, 1), px);
   if (!direct) copy_kernel<<<(unsigned)(p.blocks_n * p.ttiles), 256, 0, st>>>(a, p.ttiles, pdy);
-  int rc = panel::launch<WgradEp, 1, 1>(px, a.K, pdy, a.N, direct ? a.dy : nullptr, a.lddy, a.T, p.ttiles, p.splits,
-                                    p.per_split, kChunk, WgradEp{a, parts}, st);
-  if (rc == MCEMU_OK && parts)
-    rc = launch_early(join_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, parts, p.splits);
-  return rc;
+  const int rc = panel::launch<WgradEp, 1, 1>(p.cut, px, a.K, pdy, a.N, direct ? a.dy : nullptr, a.lddy, a.T, p.ttiles,
+                                              kChunk, WgradEp{a, parts, p.cut.bn}, st);
+  if (rc != MCEMU_OK || !p.cut.rest) return rc;
+  const panel::Args g{p.ttiles, p.blocks_k / 2, (a.N + p.cut.bn - 1) / p.cut.bn, p.cut.full, p.cut.rest, p.cut.parts,
+                      p.cut.per_part, kChunk};
+  return launch_early(join_kernel, dim3(p.cut.rest * p.cut.bn), dim3(256), 0, st, a, g, p.cut.bn, (const float *)parts);
 }
 
 }  // namespace mcemu

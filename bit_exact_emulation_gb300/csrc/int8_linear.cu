@@ -106,7 +106,7 @@ struct LinearEp {
   using Sum = int;
   LinearArgs a;
   static __device__ __forceinline__ void add(int &s, float v) { s += __float2int_rn(v); }
-  __device__ __forceinline__ void store(int n, int m0, const int *sum, int) const {
+  __device__ __forceinline__ void store(const panel::Unit &, int n, int m0, const int *sum) const {
     if (n >= a.N) return;
     put16<OUT>(a, m0, n, sum, channel<OUT>(a, n));
   }
@@ -123,8 +123,8 @@ int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
   const int64_t tiles = (int64_t)(x.blocks + w.blocks) * kt;
   if (!panel::panel_fits(x.blocks, kt) || !panel::panel_fits(w.blocks, kt)) return MCEMU_ERR_UNSUPPORTED;
   widen_kernel<<<(unsigned)tiles, 256, 0, st>>>(x, w, a.K, kt, wide);
-  return panel::launch<LinearEp<OUT>, 0, 0>(w.to, a.N, x.to, a.M, nullptr, 0, a.K, kt, 1, kt, 1024 / panel::kTileK,
-                                            LinearEp<OUT>{a}, st);
+  return panel::launch<LinearEp<OUT>, 0, 0>(panel::plan_of(a.N, a.M, kt, false), w.to, a.N, x.to, a.M, nullptr, 0, a.K,
+                                            kt, 1024 / panel::kTileK, LinearEp<OUT>{a}, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -35,25 +35,29 @@ constexpr int kThreads = 384;                 // eight warps drain, one loads, o
 struct Args {
   int ka;                    // tiles along k
   int tiles_a, tiles_b;      // tiles of 256 rows of A and of BN rows of B
-  int splits, per_split;     // parts of the sum, k tiles to a part
+  int full, rest;            // tiles computed by one pair, and tiles whose sum several pairs share
+  int parts, per_part;       // pairs to each of the latter, k tiles to a pair
   int chunk;                 // k tiles between two drains, an even number
 };
 
-// Where a unit of work lies.
+// Where a unit of work lies: a tile, and of a shared one the slot of its part (-1 otherwise).
 struct Unit {
-  int ta, tb, split, k0, k1;
+  int ta, tb, slot, k0, k1;
 };
-__device__ __forceinline__ Unit unit_at(const Args &g, int u) {
-  Unit r;
-  const int tiles = g.tiles_a * g.tiles_b;
-  r.split = u / tiles;
-  const int t = u - r.split * tiles;
+__device__ __forceinline__ void tile_at(const Args &g, int t, int &ta, int &tb) {
   // bands of eight tiles of A, so that the pairs at work share both operands in L2
   const int band = t / (8 * g.tiles_b), rest = t - band * 8 * g.tiles_b, width = min(8, g.tiles_a - band * 8);
-  r.ta = band * 8 + rest % width;
-  r.tb = rest / width;
-  r.k0 = r.split * g.per_split;
-  r.k1 = min(g.ka, r.k0 + g.per_split);
+  ta = band * 8 + rest % width;
+  tb = rest / width;
+}
+__device__ __forceinline__ int units_of(const Args &g) { return g.full + g.rest * g.parts; }
+__device__ __forceinline__ Unit unit_at(const Args &g, int u) {
+  Unit r;
+  r.slot = u - g.full;
+  const int part = r.slot < 0 ? 0 : r.slot / g.rest;
+  tile_at(g, r.slot < 0 ? u : g.full + r.slot - part * g.rest, r.ta, r.tb);
+  r.k0 = part * g.per_part;
+  r.k1 = r.slot < 0 ? g.ka : min(g.ka, r.k0 + g.per_part);
   return r;
 }
 
@@ -74,7 +78,7 @@ __device__ __forceinline__ void load_tiles(const Args &g, const CUtensorMap *ma,
 }
 
 // Ep: `Ep::Sum` is the type of the register sums; add(Sum &, float) takes one accumulator;
-// store(row of A, row of B, 16 sums along B, split) writes 16 outputs.  MN: operands are
+// store(unit, row of A, row of B, 16 sums along B) writes 16 outputs (a shared tile's part).  MN: operands are
 // MN-major; BF16: bfloat16 (else binary16).
 template <class Ep, int BN, int MN, int BF16, int DIRECT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -88,7 +92,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
   const int warp = tc::warp_number(), lane = threadIdx.x & 31;
   const uint32_t rank = tc::cta_rank();
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1, units = g.tiles_a * g.tiles_b * g.splits;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1, units = units_of(g);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; s++) {
@@ -203,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // the matrix unit has both sets to go on with meanwhile
 #pragma unroll
-      for (int j = 0; j < kCols; j += 16) ep.store(ra, rb + j, &sum[j], w.split);
+      for (int j = 0; j < kCols; j += 16) ep.store(w, ra, rb + j, &sum[j]);
     }
   }
   __syncwarp();
@@ -222,14 +226,33 @@ inline int panel_map(CUtensorMap *map, const void *panel, int blocks, int ktiles
 // What fits a panel: its rows are counted in 32 bits.
 inline bool panel_fits(int64_t blocks, int64_t ktiles) { return blocks * ktiles * 128 <= INT32_MAX; }
 
-// Rows of B to a tile: 128 where that ends sooner.  A round is every pair's tile; one of 128 rows
-// takes 0.62 of a round of 256 (weight gradient of 8192 x 4096 x 4096: seven rounds 199.5 us, four
-// 185.9; of 1024 x 1024 x 1024, one round either way: 13.9 and 16.7).
-inline int rows_b(int64_t rows_a, int64_t rows, int splits) {
-  const int64_t pairs = sm_count() / 2, ta = (rows_a + 255) / 256;
-  const int64_t wide = (ta * ((rows + 255) / 256) * splits + pairs - 1) / pairs;
-  const int64_t slim = (ta * ((rows + 127) / 128) * splits + pairs - 1) / pairs;
-  return slim * 5 < wide * 8 ? 128 : 256;
+// How a product is cut.  Every pair takes a tile at a time; what does not fill a last round may
+// be shared (share = true): each of those tiles' sums by as many pairs as there are for it, in
+// parts of at least eight k tiles that a second kernel joins.  Tiles have 128 rows of B in place of
+// 256 where that ends sooner: one takes 0.62 of the time.  (Weight gradient of 8192 x 4096 x 4096:
+// four rounds of 256 185.9 us, seven of 128 199.5, three and a half with the last 28 tiles shared
+// SHARED; of 1024 x 1024 x 1024, one round either way, 16.7 and 13.9.)
+constexpr int kPairs = 76;
+struct Plan {
+  int bn, full, rest, parts, per_part;
+};
+inline Plan plan_of(int rows_a, int rows_b, int ktiles, bool share) {
+  Plan best{};
+  double least = 0;
+  for (int bn = 256; bn >= 128; bn /= 2) {
+    const int64_t tiles = ((int64_t)rows_a + 255) / 256 * (((int64_t)rows_b + bn - 1) / bn), rest = tiles % kPairs;
+    int parts = share && rest ? (int)(kPairs / rest) : 1;
+    if (parts > ktiles / 8) parts = ktiles / 8;
+    if (parts < 2) parts = 1;
+    const int per = (ktiles + parts - 1) / parts;
+    parts = (ktiles + per - 1) / per;
+    const double time = ((double)(tiles / kPairs) + (rest ? 1.0 / parts : 0.0)) * (bn == 256 ? 1.0 : 0.62);
+    if (bn == 256 || time < least) {
+      least = time;
+      best = parts > 1 ? Plan{bn, (int)(tiles - rest), (int)rest, parts, per} : Plan{bn, (int)tiles, 0, 1, ktiles};
+    }
+  }
+  return best;
 }
 
 template <class Ep, int BN, int MN, int BF16, int DIRECT>
@@ -243,24 +266,23 @@ int launch_tiles(const Args &g, const CUtensorMap &ma, const CUtensorMap &mb, co
       return MCEMU_ERR_CUDA;
     if (dev < 64) ready[dev].store(true);
   }
-  const int64_t units = (int64_t)g.tiles_a * g.tiles_b * g.splits;
-  if (units > INT32_MAX / 4) return MCEMU_ERR_UNSUPPORTED;
-  const int pairs = (int)(units < sm_count() / 2 ? units : sm_count() / 2);
+  const int units = g.full + g.rest * g.parts, pairs = units < sm_count() / 2 ? units : sm_count() / 2;
   return launch_early(kernel, dim3(2 * pairs), dim3(kThreads), Size<BN>::kSmem, st, g, ma, mb, ep);
 }
 
 // The product of panel a (rows_a rows) and b: a panel, or with `matrix` (MN-major) a matrix of
 // k rows and ld elements between them.
 template <class Ep, int MN, int BF16>
-int launch(const void *a, int rows_a, const void *b, int rows, const void *matrix, int64_t ld, int k, int ktiles,
-           int splits, int per_split, int chunk, const Ep &ep, cudaStream_t st) {
-  const int bn = rows_b(rows_a, rows, splits), blocks_a = (rows_a + 255) / 256 * 2, blocks_b = (rows + 255) / 256 * 2;
+int launch(const Plan &p, const void *a, int rows_a, const void *b, int rows, const void *matrix, int64_t ld, int k,
+           int ktiles, int chunk, const Ep &ep, cudaStream_t st) {
+  if (((int64_t)rows_a + 255) / 256 * (((int64_t)rows + 127) / 128) > INT32_MAX / 4) return MCEMU_ERR_UNSUPPORTED;
+  const int bn = p.bn, blocks_a = (rows_a + 255) / 256 * 2, blocks_b = (rows + 255) / 256 * 2;
   CUtensorMap ma, mb;
   int rc = panel_map(&ma, a, blocks_a, ktiles, 128);
   if (rc == MCEMU_OK)
     rc = matrix ? tc::tensor_map(&mb, matrix, rows, k, ld, 64, true) : panel_map(&mb, b, blocks_b, ktiles, bn / 2);
   if (rc != MCEMU_OK) return rc;
-  const Args g{ktiles, blocks_a / 2, (rows + bn - 1) / bn, splits, per_split, chunk};
+  const Args g{ktiles, blocks_a / 2, (rows + bn - 1) / bn, p.full, p.rest, p.parts, p.per_part, chunk};
   if constexpr (MN) {
     if (matrix)
       return bn == 256 ? launch_tiles<Ep, 256, MN, BF16, 1>(g, ma, mb, ep, st)
