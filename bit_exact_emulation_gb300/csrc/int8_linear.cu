@@ -2,10 +2,13 @@
 // (include/mcemu_ops.h has the formula).
 //
 // sm_103a has no fast 8-bit integer matrix instruction, so the sums run on the 16-bit floating
-// one, exactly: an 8-bit integer is a binary16 number, a product is below 2^14 + 1, and a sum
-// of 1024 products is an integer of at most 2^24, which fp32 accumulators hold without
-// rounding (every partial sum too, in any order).  Every 1024 products the accumulators are
-// therefore taken out of tensor memory and added to int32 sums in registers.
+// one, exactly: an 8-bit integer is a binary16 number, a product is at most 2^14 in magnitude, and
+// a sum of 1024 products is an integer of at most 2^24, which fp32 accumulators hold without
+// rounding (every partial sum too, in any order, dropped bits or not).  Every 1024 products the
+// accumulators are therefore taken out and added to int32 sums in registers.
+//
+// Three forms, chosen by go() below: few tokens (bound by the weights' bytes), a batch of them
+// (bound by the widening of the weights), many (bound by the matrix unit).
 #include "panel.cuh"
 
 namespace mcemu {
@@ -64,9 +67,11 @@ __device__ __forceinline__ void half4(uint32_t b, uint32_t &lo, uint32_t &hi) {
 }
 
 // ---------------------------------------------------------------------------
-// Large products: both operands are widened to binary16 panels once (3 bytes of traffic an
-// element, against a conversion for every tile that reads it), and pairs of CTAs multiply
-// the panels with nothing but copies and matrix instructions in the loop.
+// Many tokens: both operands are widened to binary16 panels once (3 bytes of traffic an element,
+// against a conversion for every tile that reads it), and pairs of CTAs multiply the panels
+// with nothing but copies and matrix instructions in the loop.  Bound by the matrix unit:
+// 8192 x 8192 x 4096 to bf16 takes 325 us, 35 of them the widening (5.8 TB/s): 1.69 PFLOP/s,
+// 0.88 of the measured bf16 rate.
 // ---------------------------------------------------------------------------
 struct Widen {
   const int8_t *src;
@@ -133,13 +138,11 @@ int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
 // time in turn.  The warp-wide matrix instruction (m16n8k16, 1000 MAC a cycle and SM measured,
 // against 250 for its 8-bit form and for dp4a alike) takes four k of a row from a lane, and
 // which four is free as long as both operands agree: a lane reads 16 consecutive bytes of
-// its rows and feeds them to four instructions.
+// its rows and feeds them to four instructions.  One token by 4096 x 4096 weights: 4.7 us (3.5
+// TB/s of weights, launch included), 16 tokens 5.5, 32 tokens 8.0 (there the matrix instructions
+// and the widening of the tokens, done by every block, weigh as much as the loads).
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
-#ifndef FEW
-#define FEW 32
-#endif
-constexpr int kFew = FEW;                     // most tokens
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -169,13 +172,13 @@ __device__ __forceinline__ void put_any(const LinearArgs &a, int m, int n, int a
 }
 
 template <int NT, bool WIDE>
-__global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a, int blocks_n) {
   constexpr int kAhead = WIDE ? (NT == 1 ? 8 : 4) : 2;       // pieces of 64 k in flight
   constexpr int kOut = 16 * 8 * NT;                          // outputs of a block
   constexpr int kEach = (kOut + 32 * kWarps - 1) / (32 * kWarps);
   __shared__ int part[kWarps][kOut];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 8 * NT;
+  const int mb = blockIdx.x / blocks_n, n0 = (blockIdx.x - mb * blocks_n) * 16, m0 = mb * 8 * NT;
   // this thread's outputs (a channel, every sixteenth token), their factors asked for early
   const int n = n0 + (threadIdx.x & 15);
   const bool scales = a.out_fmt != MCEMU_INT32;
@@ -260,18 +263,21 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a) {
 
 template <int NT>
 int go_few(const LinearArgs &a, bool wide, cudaStream_t st) {
-  const dim3 grid((a.N + 15) / 16, (a.M + 8 * NT - 1) / (8 * NT));
-  if (wide) few_kernel<NT, true><<<grid, 32 * kWarps, 0, st>>>(a);
-  else few_kernel<NT, false><<<grid, 32 * kWarps, 0, st>>>(a);
+  const int64_t blocks_n = ((int64_t)a.N + 15) / 16, blocks = blocks_n * (((int64_t)a.M + 8 * NT - 1) / (8 * NT));
+  if (blocks > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+  if (wide) few_kernel<NT, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, (int)blocks_n);
+  else few_kernel<NT, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, (int)blocks_n);
   return launch_status();
 }
 
 // ---------------------------------------------------------------------------
 // A batch of tokens, too few to pay for panels: a block takes 128 channels by BN tokens and a part
 // of K.  Worker warps read both operands 128 k at a time, kAhead stages ahead, widen them to
-// binary16 and store them in the swizzle; one thread issues the matrix instructions.  The
+// binary16 and store them in the swizzle; one warp issues the matrix instructions.  The
 // blocks of a cluster share K, and each adds up its share of the tile out of the others' shared
-// memory, so that no second launch joins the parts.
+// memory, so that no second launch joins the parts.  128 x 8192 x 4096: 19.4 us (1.7 TB/s of
+// weights).  Bound by the widening: some 60 instructions for 16 elements of a lane, sixteen warps
+// on the four schedulers; the matrix unit is a fifth busy.
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 128;                  // k of a stage: two 128-byte swizzle rows, the first 64 k of all rows first
 constexpr int kChunk = 1024 / kStageK;        // stages between two transfers to int32
@@ -328,32 +334,31 @@ __global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(cons
   for (int j = 0; j < S::kEach; j++) sum[j] = 0;
 
   if (warp == kMma) {
-    {
-      constexpr uint32_t ins = tc::instruction(128, BN, 0, 0, 0);
-      uint32_t it = 0, ch = 0;
-      for (int c = s0; c < s1 && !dead; c += kChunk, ch++) {
-        tc::mbar_wait_warp(acc_empty, (ch & 1) ^ 1, dead);
+    constexpr uint32_t ins = tc::instruction(128, BN, 0, 0, 0);
+    uint32_t it = 0, ch = 0;
+    for (int c = s0; c < s1 && !dead; c += kChunk, ch++) {
+      tc::mbar_wait_warp(acc_empty, (ch & 1) ^ 1, dead);
+      tc::fence_after();
+      const int n = min(kChunk, s1 - c);
+      for (int i = 0; i < n && !dead; i++, it++) {
+        const uint32_t s = it % S::kStages, at = base + s * S::kBytes;
+        tc::mbar_wait_warp(full + 8 * s, (it / S::kStages) & 1, dead);
+        if (dead) break;
         tc::fence_after();
-        const int n = min(kChunk, s1 - c);
-        for (int i = 0; i < n && !dead; i++, it++) {
-          const uint32_t s = it % S::kStages, at = base + s * S::kBytes;
-          tc::mbar_wait_warp(full + 8 * s, (it / S::kStages) & 1, dead);
-          if (dead) break;
-          tc::fence_after();
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const uint64_t da = tc::operand(at + h * S::kHalf, 16, 1024), db = tc::operand(at + h * S::kHalf + 128 * 128, 16, 1024);
+        for (int h = 0; h < 2; h++) {
+          const uint32_t half = at + h * S::kHalf;
+          const uint64_t da = tc::operand(half, 16, 1024), db = tc::operand(half + 128 * 128, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; k++) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, ins, (i | h | k) != 0);
-          }
-          tc::commit<1>(empty + 8 * s);
+          for (int k = 0; k < 4; k++) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, ins, (i | h | k) != 0);
         }
-        tc::commit<1>(acc_full);
+        tc::commit<1>(empty + 8 * s);
       }
-      bool late = false;                       // everything issued ends before the memory is given back
-      tc::commit<1>(drain);
-      tc::mbar_wait_warp(drain, 0, late);
+      tc::commit<1>(acc_full);
     }
+    bool late = false;                       // everything issued ends before the memory is given back
+    tc::commit<1>(drain);
+    tc::mbar_wait_warp(drain, 0, late);
   } else {
     // Pieces of a stage: piece p of a row is k 16p .. 16p + 15.  A warp reads whole 128-byte
     // lines of four rows; eight lanes that store together hold two rows' pieces of one half,
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(cons
     const int rows_w = a.N - n0 - row0, rows_x = a.M - m0 - row0;
     // A thread copies its pieces ahead into places of its own, so that no barrier and no
     // register waits for them (loaded to registers one stage ahead: 128 x 8192 x 4096 in 22 us in
-    // place of BATCHNOW).
+    // place of 20.1).
     const uint32_t place = copies + threadIdx.x * 16;
     const auto copy = [&](int s) {
       const int k = s < s1 ? s * kStageK : a.K;
@@ -481,6 +486,14 @@ __global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(cons
   }
 }
 
+// Parts of K: a power of two of at most eight (a portable cluster), at least two stages each, until
+// the blocks fill the multiprocessors.
+int batch_parts(int64_t tiles, int stages) {
+  int parts = 1;
+  while (parts < 8 && tiles * parts * 2 <= 2 * panel::kPairs && stages >= parts * 4) parts *= 2;
+  return parts;
+}
+
 template <int BN>
 int go_batch(const LinearArgs &a, cudaStream_t st) {
   using S = Batch<BN>;
@@ -495,11 +508,7 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
   }
   const int tiles_n = (a.N + 127) / 128, stages = (a.K + kStageK - 1) / kStageK;
   const int64_t tiles = (int64_t)tiles_n * ((a.M + BN - 1) / BN);
-  // Parts of K: a power of two of at most eight (a portable cluster), at least two stages each,
-  // until the blocks fill the multiprocessors.
-  const int room = sm_count();
-  int parts = 1;
-  while (parts < 8 && tiles * parts * 2 <= room && stages >= parts * 4) parts *= 2;
+  const int parts = batch_parts(tiles, stages);
   if (tiles * parts > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * parts));
@@ -515,10 +524,28 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
   const cudaError_t rc = cudaLaunchKernelEx(&cfg, kernel, a, tiles_n, (stages + parts - 1) / parts);
   return rc == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
 }
-// Products that go through panels: more than one wave of the batch kernel's tiles, or rows that
-// its 16-byte loads do not fit.  WHY
+// Which form.  Up to kFew tokens, and for K = 0, the first: 32 tokens by 4096 x 4096 (8192 x 4096)
+// weights 8.0 us (14.4) against 10.7 (16.6) of the second.  Rows that 16-byte loads do not fit
+// take panels from there on, whose widening reads any rows.  Otherwise what ends sooner by these
+// estimates in microseconds, whose constants are measured:
+//
+//                        batch  panels                           batch  panels
+//   128 x  8192 x 4096    19.4    37.8      1024 x 2048 x 2048    20.9    17.3
+//   256 x  8192 x 4096    32.8    38.3      2048 x 1024 x 1024    14.9    12.4
+//   512 x  1024 x 1024     9.0    11.3      48 x 16384 x 4096     27.7    62.3
+constexpr int kFew = 32;
 bool by_panels(int M, int N, int K, bool wide) {
-  return K > 0 && M > kFew && (!wide || (int64_t)((M + 127) / 128) * ((N + 127) / 128) > sm_count());
+  if (M <= kFew || K == 0) return false;
+  if (!wide) return true;
+  const int bn = M <= 64 ? 64 : 128, stages = (K + kStageK - 1) / kStageK;
+  const int64_t tiles = ((int64_t)N + 127) / 128 * (((int64_t)M + bn - 1) / bn);
+  const int parts = batch_parts(tiles, stages);
+  const double waves = (double)((tiles * parts + 2 * panel::kPairs - 1) / (2 * panel::kPairs));
+  const double batch = 6.0 + waves * ((stages + parts - 1) / parts) * (bn == 64 ? 0.67 : 0.88);
+  const panel::Plan p = panel::plan_of(N, M, ktiles_of(K), false);
+  const double rounds = (double)((p.full + panel::kPairs - 1) / panel::kPairs) * (p.bn == 256 ? 1.0 : 0.62);
+  const double panels = 7.0 + 3.0 * ((double)M + N) * K / 6.2e6 + rounds * ktiles_of(K) * 0.33;
+  return panels < batch;
 }
 
 }  // namespace

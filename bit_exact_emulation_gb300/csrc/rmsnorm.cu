@@ -75,7 +75,7 @@ __device__ __forceinline__ float finish_row(const NormArgs &a, int64_t row, floa
 // A row in the registers of blockDim.x threads, PER vectors of VEC elements each;
 // blockDim.y rows to a block.  h is held in its own type and v = h * w computed twice: the
 // registers of fp32 copies would halve the threads in flight, and with them the bandwidth (98 us
-// in place of NORMNOW for 8192 x 8192 bf16 with a residual).  All of a thread's loads are issued before
+// in place of 72 for 8192 x 8192 bf16 with a residual).  All of a thread's loads are issued before
 // its first store (h may lie on x or res, so the compiler would keep them in order).
 template <class T, int VEC, int PER, bool RES>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a) 
 
 // Rows that no vector fits: one element of every TX to a thread, at distances that the compiler
 // knows (with TX a variable the address of every access is computed anew: 8191 x 5003 bf16 with a
-// residual 149 us in place of SINGLENOW).
+// residual 149 us in place of 86).
 template <class T, int TX, bool RES>
 __global__ void __launch_bounds__(TX < 256 ? 256 : TX) single_kernel(const NormArgs a) {
   __shared__ float2 part[kMaxThreads / 32];

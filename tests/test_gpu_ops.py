@@ -78,7 +78,7 @@ def norm_tol(H):
 
 
 NORM_SHAPES = [(1, 1), (3, 7), (2, 64), (5, 100), (1, 4096), (37, 1000), (700, 128), (650, 1025), (9, 5003),
-               (3, 8192), (400, 4104), (2, 16384), (2, 32768), (2, 33001), (700, 2050)]
+               (3, 8192), (400, 4104), (2, 16384), (2, 32768), (2, 33001), (700, 2050), (310, 16384), (320, 9001)]
 
 
 @pytest.mark.parametrize("T,H", NORM_SHAPES)
@@ -265,7 +265,7 @@ def grad_host(dy, w, rstd, h, dres):
 
 
 GRAD_SHAPES = [(1, 1), (2, 7), (3, 64), (1, 4096), (700, 256), (333, 2050), (65, 5003), (40, 8192), (1300, 136),
-               (3, 16384), (5, 16390), (7, 20000)]
+               (3, 16384), (5, 16390), (7, 20000), (400, 1024), (310, 8200), (160, 16384), (2500, 72)]
 
 
 @pytest.mark.parametrize("T,H", GRAD_SHAPES)
@@ -340,7 +340,7 @@ def test_rmsnorm_backward_strides_and_in_place(O, H, pad, lead):
 # product of 8-bit integers
 # ---------------------------------------------------------------------------
 def linear_host(x, sx, w, sw, bias, out):
-    acc = x.numpy().astype(np.int64) @ w.numpy().astype(np.int64).T
+    acc = x.numpy().astype(np.float64) @ w.numpy().astype(np.float64).T       # integers below 2^53: exact
     assert np.abs(acc).max(initial=0) < 2 ** 31
     if out == "int32":
         return torch.from_numpy(acc.astype(np.int32))
@@ -359,7 +359,8 @@ def int8s(rng, *shape):
 LINEAR_SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1000, 4096), (1, 5, 16391), (2, 130, 77), (3, 256, 512), (5, 129, 1024),
                  (8, 300, 1040), (9, 64, 128), (16, 4096, 256), (17, 100, 333), (33, 257, 2048), (64, 128, 64),
                  (77, 503, 2049), (128, 128, 1024), (129, 255, 1100), (256, 256, 64), (257, 513, 2111), (300, 40, 4096),
-                 (512, 1024, 96), (1000, 264, 520), (31, 1, 100), (2, 3, 0), (700, 700, 15)]
+                 (512, 1024, 96), (1000, 264, 520), (31, 1, 100), (2, 3, 0), (700, 700, 15), (40, 130, 20000),
+                 (130, 700, 16400), (8000, 264, 256), (1300, 1800, 520), (90, 20000, 256), (100, 3, 0)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR_SHAPES)
@@ -426,7 +427,8 @@ def test_int8_linear_matches_the_emulated_unit(O):
 # weight gradient
 # ---------------------------------------------------------------------------
 WGRAD_SHAPES = [(1, 1, 1), (1, 128, 128), (5, 7, 130), (64, 64, 64), (63, 200, 129), (256, 128, 256), (257, 130, 300),
-                (1000, 520, 136), (2049, 40, 1000), (300, 1030, 514), (4100, 256, 264), (128, 1000, 1)]
+                (1000, 520, 136), (2049, 40, 1000), (300, 1030, 514), (4100, 256, 264), (128, 1000, 1), (200, 1300, 1800),
+                (2000, 1304, 1800)]
 
 
 def wgrad_case(rng, T, N, K):
