@@ -109,6 +109,29 @@ __device__ __forceinline__ Vec<int8_t, V> to_int8(const float (&x)[V]) {
   return r;
 }
 
+// Two fp32 operations at once, each rounded as its own (sm_100 and later).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*(unsigned long long *)&d)
+      : "l"(*(unsigned long long *)&a), "l"(*(unsigned long long *)&b), "l"(*(unsigned long long *)&c));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(*(unsigned long long *)&d)
+      : "l"(*(unsigned long long *)&a), "l"(*(unsigned long long *)&b));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*(unsigned long long *)&d)
+      : "l"(*(unsigned long long *)&a), "l"(*(unsigned long long *)&b));
+  return d;
+}
+
 // V signed bytes to fp32, exactly: a byte plus 128 as the last digits of 2^23, less 2^23 + 128.
 template <int V>
 __device__ __forceinline__ void bytes_to_f(const Vec<int8_t, V> &q, float (&f)[V]) {
@@ -119,7 +142,13 @@ __device__ __forceinline__ void bytes_to_f(const Vec<int8_t, V> &q, float (&f)[V
     for (int i = 0; i < V; i += 4) {
       const uint32_t b = *(const uint32_t *)&q.v[i] ^ 0x80808080u;
 #pragma unroll
-      for (int j = 0; j < 4; j++) f[i + j] = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + j)) - 8388736.f;
+      for (int j = 0; j < 4; j += 2) {
+        const float2 u = make_float2(__uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + j)),
+                                     __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7651 + j)));
+        const float2 v = add2(u, make_float2(-8388736.f, -8388736.f));
+        f[i + j] = v.x;
+        f[i + j + 1] = v.y;
+      }
     }
   }
 }
