@@ -4,36 +4,12 @@
 // Bound by HBM: 7 bytes an element for bf16 gradients with a checkpoint and a residual path.
 // Each group of threads walks over rows with its columns' weights and its part of dw in
 // registers; the parts are added in a fixed order by a second, small kernel.
-#include "ops_common.cuh"
+#include "norm_grad.cuh"
 
 namespace mcemu {
 namespace {
 
 constexpr int kThreads = 512;                  // of a block
-
-// Most blocks, each of which keeps a part of dw: one to a multiprocessor, more where a block is
-// one group of threads for a short row.
-int most_blocks(int T, int H) {
-  const int per_sm = H <= 1024 ? 16 : H <= 16384 ? 16384 / H : 1, most = 152 * per_sm;
-  return T < most ? T : most;
-}
-
-// Sum over the TX threads of a row (whole warps), which wait for one another alone.
-template <int TX>
-__device__ __forceinline__ float row_sum(float x, float *part) {
-  x = warp_sum(x);
-  if constexpr (TX > 32) {
-    float *mine = part + threadIdx.y * (TX / 32);
-    const int bar = threadIdx.y + 1;
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TX) : "memory");
-    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = x;
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TX) : "memory");
-    x = 0.f;
-#pragma unroll
-    for (int i = 0; i < TX / 32; i++) x += mine[i];
-  }
-  return x;
-}
 
 // One element of the norm's input, from h or from the checkpoint.
 template <class T, bool CKPT>
@@ -197,69 +173,6 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
   }
 }
 
-// Rows that no vector fits, at any strides: a group of TX threads to a block, one element of every
-// TX to a thread, so that a thread keeps its columns, their weights and its part of dw.
-template <class T, int PER, int TX, bool CKPT>
-__global__ void __launch_bounds__(TX) single_kernel(const NormGradArgs a, float *__restrict__ parts) {
-  __shared__ float sh[32];
-  __shared__ float scales[2][PER * TX / MCEMU_ACT8_BLOCK + 1];      // of this row's blocks of 128 and the next one's
-  const int i0 = threadIdx.x, blocks = (a.H + MCEMU_ACT8_BLOCK - 1) / MCEMU_ACT8_BLOCK;
-  float w[PER], dw[PER];
-  grid_go();
-#pragma unroll
-  for (int p = 0; p < PER; p++) {
-    const int i = i0 + p * TX;
-    dw[p] = w[p] = 0.f;
-    if (i < a.H) w[p] = a.w32 ? ((const float *)a.w)[i] : to_f(((const T *)a.w)[i]);
-  }
-  int64_t row = blockIdx.x;
-  if (CKPT && row < a.T)
-    for (int i = threadIdx.x; i < blocks; i += TX) scales[0][i] = act8_scale(a.e[row * a.lde + i]);
-  __syncthreads();
-  for (int s = 0; row < a.T; row += gridDim.x, s ^= 1) {
-    const T *pdy = (const T *)a.dy + row * a.lddy + i0, *pdr = (const T *)a.dres + row * a.lddr + i0;
-    const T *ph = (const T *)a.h + row * a.ldh + i0;
-    const int8_t *pq = a.q + row * a.ldq + i0;
-    T dy[PER], dr[PER];
-    typename std::conditional<CKPT, int8_t, T>::type in[PER];
-#pragma unroll
-    for (int p = 0; p < PER; p++) {
-      if (i0 + p * TX >= a.H) continue;
-      dy[p] = pdy[p * TX];
-      if constexpr (CKPT) in[p] = pq[p * TX];
-      else in[p] = ph[p * TX];
-      if (a.dres) dr[p] = pdr[p * TX];
-    }
-    const float rstd = a.rstd[row];
-    if (CKPT && row + gridDim.x < a.T)
-      for (int i = threadIdx.x; i < blocks; i += TX)
-        scales[s ^ 1][i] = act8_scale(a.e[(row + gridDim.x) * a.lde + i]);
-    float z[PER], dot = 0.f;
-#pragma unroll
-    for (int p = 0; p < PER; p++) {
-      z[p] = 0.f;
-      if (i0 + p * TX >= a.H) continue;
-      if constexpr (CKPT) z[p] = (float)in[p] * scales[s][(i0 + p * TX) / MCEMU_ACT8_BLOCK] * rstd;
-      else z[p] = to_f(in[p]) * rstd;
-      const float d = to_f(dy[p]);
-      dot = fmaf(d * w[p], z[p], dot);
-      dw[p] = fmaf(d, z[p], dw[p]);
-    }
-    if (TX == 32) __syncwarp();
-    const float k = -(row_sum<TX>(dot, sh) / (float)a.H) * rstd;
-    T *pdx = (T *)a.dx + row * a.lddx + i0;
-#pragma unroll
-    for (int p = 0; p < PER; p++) {
-      if (i0 + p * TX >= a.H) continue;
-      const float g = to_f(dy[p]) * w[p];
-      pdx[p * TX] = from_f<T>(fmaf(z[p], k, a.dres ? fmaf(g, rstd, to_f(dr[p])) : g * rstd));
-    }
-  }
-#pragma unroll
-  for (int p = 0; p < PER; p++)
-    if (i0 + p * TX < a.H) parts[(int64_t)blockIdx.x * a.H + i0 + p * TX] = dw[p];
-}
-
 // dw[j] = sum over the blocks of parts[block][j]: 32 columns and 32 strands of blocks to a block
 // of threads, the strands joined in order.
 __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ parts, int groups, int H, float *dw) {
@@ -336,13 +249,6 @@ int go(const NormGradArgs &a, float *parts, cudaStream_t st) {
   grad_kernel<T, VEC, PER, TX, CKPT><<<blocks, dim3(TX, rows), smem, st>>>(a, parts);
   return blocks;
 }
-template <class T, int TX, bool CKPT>
-int go_single(const NormGradArgs &a, float *parts, cudaStream_t st) {
-  const int blocks = most_blocks(a.T, a.H);
-  single_kernel<T, 16, TX, CKPT><<<blocks, TX, 0, st>>>(a, parts);
-  return blocks;
-}
-
 template <class T, bool CKPT>
 int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T), P = (V == 4 ? 16 : 32) / V;       // 32 columns a thread, 16 of fp32
@@ -357,11 +263,8 @@ int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
     else if (a.H <= 128 * V * P) groups = go<T, V, P, 128, CKPT>(a, ws, st);
     else if (a.H <= 256 * V * P) groups = go<T, V, P, 256, CKPT>(a, ws, st);
     else groups = go<T, V, P, 512, CKPT>(a, ws, st);
-  } else if (a.H <= 16 * 512) {
-    if (a.H <= 16 * 32) groups = go_single<T, 32, CKPT>(a, ws, st);
-    else if (a.H <= 16 * 128) groups = go_single<T, 128, CKPT>(a, ws, st);
-    else if (a.H <= 16 * 256) groups = go_single<T, 256, CKPT>(a, ws, st);
-    else groups = go_single<T, 512, CKPT>(a, ws, st);
+  } else if (a.H <= kMaxSingle) {
+    launch_grad_single<T, CKPT>(a, groups, ws, st);
   } else {
     float *mean = ws + (int64_t)groups * a.H;
     long_mean_kernel<T, CKPT><<<a.T < 152 * 4 ? a.T : 152 * 4, 512, 0, st>>>(a, mean);
