@@ -22,32 +22,38 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *(const uint32_t *)&v;
 }
 
-// Checkpoint to panel, one image (64 tokens by one block of 128) to a block of threads: 16
-// codes a thread, twice.
+// Checkpoint to panel, one image (64 tokens by one block of 128) to a block of threads: 16 codes a
+// thread, twice.
 __global__ void __launch_bounds__(256) widen_kernel(const WgradArgs a, int ttiles, bool wide, uint8_t *__restrict__ to) {
-  const int64_t tile = blockIdx.x;
-  const int block = (int)(tile / ttiles), tt = (int)(tile - (int64_t)block * ttiles);
+  const int block = blockIdx.x / ttiles, tt = blockIdx.x - block * ttiles;
   grid_go();
-  to += tile * panel::kTileBytes;
+  to += (int64_t)blockIdx.x * panel::kTileBytes;
+  const int piece = threadIdx.x & 7, r0 = threadIdx.x >> 3, k = block * 128 + 16 * piece;
+  uint4 v[2];
+  float s[2];
 #pragma unroll
   for (int j = 0; j < 2; j++) {
-    const int piece = threadIdx.x & 7, r = (threadIdx.x >> 3) + 32 * j, t = tt * 64 + r;
-    const int k = block * 128 + 16 * piece;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    float s = 0.f;
+    const int t = tt * 64 + r0 + 32 * j;
+    v[j] = make_uint4(0, 0, 0, 0);
+    s[j] = 0.f;
     if (t < a.T && k < a.K) {
-      v = row16(a.q + (int64_t)t * a.ldq, k, a.K, wide);
-      s = act8_scale(a.e[(int64_t)t * a.lde + block]);
+      v[j] = row16(a.q + (int64_t)t * a.ldq, k, a.K, wide);
+      s[j] = act8_scale(a.e[(int64_t)t * a.lde + block]);
     }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  }
+#pragma unroll
+  for (int j = 0; j < 2; j++) {
+    const int r = r0 + 32 * j;
+    float f[16];
+    Vec<int8_t, 16> q;
+    *(uint4 *)&q = v[j];
+    bytes_to_f<16>(q, f);
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const int b = (int)(w[i >> 1] >> (16 * (i & 1)));
-      o[i] = bf16x2((float)(int8_t)b * s, (float)(int8_t)(b >> 8) * s);
-    }
-    *(uint4 *)(to + image_at(r, 2 * piece)) = make_uint4(o[0], o[1], o[2], o[3]);
-    *(uint4 *)(to + image_at(r, 2 * piece + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int i = 0; i < 8; i++) o[i] = bf16x2(f[2 * i] * s[j], f[2 * i + 1] * s[j]);
+    // the swizzle keeps the 32 bytes in one sector, their halves exchanged in odd rows
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    store32(to + (image_at(r, 2 * piece) & ~31), r & 1 ? hi : lo, r & 1 ? lo : hi);
   }
 }
 

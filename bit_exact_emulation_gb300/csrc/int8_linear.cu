@@ -80,7 +80,8 @@ struct Widen {
   uint8_t *to;
 };
 
-// One tile (128 rows by 64 k) to a block.
+// One tile (128 rows by 64 k) to a block, two pieces of sixteen k to a thread.  A piece becomes 32
+// bytes, which the swizzle keeps in one sector, its halves exchanged in odd rows.
 __global__ void __launch_bounds__(256) widen_kernel(const Widen x, const Widen w, int K, int ktiles, bool wide) {
   int64_t tile = blockIdx.x;
   grid_go();
@@ -89,20 +90,23 @@ __global__ void __launch_bounds__(256) widen_kernel(const Widen x, const Widen w
   if (tile >= mine) tile -= mine;
   const int block = (int)(tile / ktiles), kt = (int)(tile - (int64_t)block * ktiles);
   uint8_t *to = o.to + tile * panel::kTileBytes;
+  const int piece = threadIdx.x & 3, r0 = threadIdx.x >> 2, k = kt * 64 + 16 * piece;
+  uint4 v[2];
 #pragma unroll
   for (int j = 0; j < 2; j++) {
-    const int piece = threadIdx.x & 3, r = (threadIdx.x >> 2) + 64 * j, row = block * 128 + r;
-    const int k = kt * 64 + 16 * piece;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < o.rows && k < K) v = row16(o.src + (int64_t)row * o.ld, k, K, wide);
+    const int row = block * 128 + r0 + 64 * j;
+    v[j] = make_uint4(0, 0, 0, 0);
+    if (row < o.rows && k < K) v[j] = row16(o.src + (int64_t)row * o.ld, k, K, wide);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; j++) {
+    const int r = r0 + 64 * j;
     uint4 lo, hi;
-    half4(v.x, lo.x, lo.y);
-    half4(v.y, lo.z, lo.w);
-    half4(v.z, hi.x, hi.y);
-    half4(v.w, hi.z, hi.w);
-    const int at = r * 128 + (((2 * piece) ^ (r & 7)) << 4);
-    *(uint4 *)(to + at) = lo;
-    *(uint4 *)(to + (at ^ 16)) = hi;
+    half4(v[j].x, lo.x, lo.y);
+    half4(v[j].y, lo.z, lo.w);
+    half4(v[j].z, hi.x, hi.y);
+    half4(v[j].w, hi.z, hi.w);
+    store32(to + r * 128 + ((piece ^ ((r & 7) >> 1)) << 5), r & 1 ? hi : lo, r & 1 ? lo : hi);
   }
 }
 

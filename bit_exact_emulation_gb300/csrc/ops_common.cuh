@@ -171,6 +171,14 @@ __device__ __forceinline__ void load_w(const void *w, int w32, int64_t i, float 
   }
 }
 
+// Thirty-two bytes to a 32-byte boundary at once: a whole sector, where two 16-byte stores each
+// write half of one.
+__device__ __forceinline__ void store32(void *to, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // Asynchronous copies of 4, 8 or 16 bytes to shared memory by the thread that reads them there.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void *to, const void *from) {
