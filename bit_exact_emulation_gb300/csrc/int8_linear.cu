@@ -70,8 +70,8 @@ __device__ __forceinline__ void half4(uint32_t b, uint32_t &lo, uint32_t &hi) {
 // Many tokens: both operands are widened to binary16 panels once (3 bytes of traffic an element,
 // against a conversion for every tile that reads it), and pairs of CTAs multiply the panels
 // with nothing but copies and matrix instructions in the loop.  Bound by the matrix unit:
-// 8192 x 8192 x 4096 to bf16 takes 325 us, 35 of them the widening (5.8 TB/s): 1.69 PFLOP/s,
-// 0.88 of the measured bf16 rate.
+// 8192 x 8192 x 4096 to bf16 takes 319 us, 29 of them the widening (6.9 TB/s, some of it to L2):
+// 1.72 PFLOP/s, 0.90 of the measured bf16 rate; the matrix unit is 84 % busy while it runs.
 // ---------------------------------------------------------------------------
 struct Widen {
   const int8_t *src;
@@ -534,9 +534,9 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
 // estimates in microseconds, whose constants are measured:
 //
 //                        batch  panels                           batch  panels
-//   128 x  8192 x 4096    19.4    37.8      1024 x 2048 x 2048    20.9    17.3
-//   256 x  8192 x 4096    32.8    38.3      2048 x 1024 x 1024    14.9    12.4
-//   512 x  1024 x 1024     9.0    11.3      48 x 16384 x 4096     27.7    62.3
+//   128 x  8192 x 4096    19.4    34.9      1024 x 2048 x 2048    21.1    16.0
+//   256 x  8192 x 4096    32.8    35.9      2048 x 1024 x 1024    15.0    11.9
+//   512 x  1024 x 1024     8.7    11.2      48 x 16384 x 4096     27.9    57.1
 constexpr int kFew = 32;
 bool by_panels(int M, int N, int K, bool wide) {
   if (M <= kFew || K == 0) return false;
@@ -547,8 +547,7 @@ bool by_panels(int M, int N, int K, bool wide) {
   const double waves = (double)((tiles * parts + 2 * panel::kPairs - 1) / (2 * panel::kPairs));
   const double batch = 6.0 + waves * ((stages + parts - 1) / parts) * (bn == 64 ? 0.67 : 0.88);
   const panel::Plan p = panel::plan_of(N, M, ktiles_of(K), false);
-  const double rounds = (double)((p.full + panel::kPairs - 1) / panel::kPairs) * (p.bn == 256 ? 1.0 : 0.62);
-  const double panels = 7.0 + 3.0 * ((double)M + N) * K / 6.2e6 + rounds * ktiles_of(K) * 0.33;
+  const double panels = 7.0 + 3.0 * ((double)M + N) * K / 6.9e6 + p.us;
   return panels < batch;
 }
 

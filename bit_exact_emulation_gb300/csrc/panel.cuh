@@ -229,28 +229,31 @@ inline bool panel_fits(int64_t blocks, int64_t ktiles) { return blocks * ktiles 
 // How a product is cut.  Every pair takes a tile at a time; what does not fill a last round may
 // be shared (share = true): each of those tiles' sums by as many pairs as there are for it, in
 // parts of at least eight k tiles that a second kernel joins.  Tiles have 128 rows of B in place of
-// 256 where that ends sooner: one takes 0.62 of the time.  (Weight gradient of 8192 x 4096 x 4096:
-// four rounds of 256 185.9 us, seven of 128 199.5, three and a half with the last 28 tiles shared
-// 178.8; of 1024 x 1024 x 1024, one round either way, 16.7 and 13.9.)
+// 256 where that ends sooner.  Of the possible cuts the one that an estimate in microseconds
+// prefers: 0.33 a k tile of a round, 0.62 of that with 128 rows, 3 and the traffic of the parts for a
+// join.  Weight gradients, microseconds:
+//
+//                            256 rows   128 rows   shared
+//   8192 x 4096 x 4096          182        196       169      (256 rows; 28 tiles of 256 shared)
+//   1024 x 1024 x 1024          13.6       9.9      11.4      (128 rows)
 constexpr int kPairs = 76;
 struct Plan {
   int bn, full, rest, parts, per_part;
+  double us;
 };
 inline Plan plan_of(int rows_a, int rows_b, int ktiles, bool share) {
   Plan best{};
-  double least = 0;
   for (int bn = 256; bn >= 128; bn /= 2) {
     const int64_t tiles = ((int64_t)rows_a + 255) / 256 * (((int64_t)rows_b + bn - 1) / bn), rest = tiles % kPairs;
+    const double round = ktiles * (bn == 256 ? 0.33 : 0.33 * 0.62), whole = (double)((tiles + kPairs - 1) / kPairs) * round;
+    if (bn == 256 || whole < best.us) best = Plan{bn, (int)tiles, 0, 1, ktiles, whole};
     int parts = share && rest ? (int)(kPairs / rest) : 1;
     if (parts > ktiles / 8) parts = ktiles / 8;
-    if (parts < 2) parts = 1;
+    if (parts < 2) continue;
     const int per = (ktiles + parts - 1) / parts;
     parts = (ktiles + per - 1) / per;
-    const double time = ((double)(tiles / kPairs) + (rest ? 1.0 / parts : 0.0)) * (bn == 256 ? 1.0 : 0.62);
-    if (bn == 256 || time < least) {
-      least = time;
-      best = parts > 1 ? Plan{bn, (int)(tiles - rest), (int)rest, parts, per} : Plan{bn, (int)tiles, 0, 1, ktiles};
-    }
+    const double us = ((double)(tiles / kPairs) + (double)per / ktiles) * round + 3.0 + rest * parts * bn * 2048 / 6e6;
+    if (us < best.us) best = Plan{bn, (int)(tiles - rest), (int)rest, parts, per, us};
   }
   return best;
 }
