@@ -155,16 +155,38 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// Sixteen bytes of a row from k on.  WIDE: rows start on 16-byte boundaries and K is a multiple
-// of 16.
+// Sixteen bytes of a row from k on, asked for at one time and put together at another, so that many
+// can be in flight.  WIDE: rows start on 16-byte boundaries and K is a multiple of 16.  Otherwise
+// five aligned words around them where `inner` says that those lie within the row, for all lanes
+// alike, and lane by lane near its ends.  A choice at each load made each wait for the one before
+// it (1 x 20000 x 5001: 41 us, now 31; 16 x 9000 x 9001: 61, 37; 8 x 9000 x 9001: 29.8, 32.0).
 template <bool WIDE>
-__device__ __forceinline__ uint4 piece16(const int8_t *row, int k, int K, bool have) {
-  if constexpr (WIDE) {
-    return have && k < K ? __ldg((const uint4 *)(row + k)) : make_uint4(0, 0, 0, 0);
-  } else {
-    return have && k < K ? row16(row, k, K, false) : make_uint4(0, 0, 0, 0);
+struct Piece;
+template <>
+struct Piece<true> {
+  uint4 v;
+  __device__ __forceinline__ void ask(const int8_t *row, int k, int K, bool have, bool) {
+    v = have && k < K ? __ldg((const uint4 *)(row + k)) : make_uint4(0, 0, 0, 0);
   }
-}
+  __device__ __forceinline__ uint32_t word(int q, const int8_t *, bool) const { return (&v.x)[q]; }
+};
+template <>
+struct Piece<false> {
+  uint32_t v[5];
+  __device__ __forceinline__ void ask(const int8_t *row, int k, int K, bool have, bool inner) {
+    if (inner) {
+      const uint32_t *p = (const uint32_t *)(row + k - ((uintptr_t)row & 3));
+#pragma unroll
+      for (int i = 0; i < 5; i++) v[i] = have ? __ldg(p + i) : 0;
+    } else {
+      const uint4 x = have && k < K ? row16(row, k, K, false) : make_uint4(0, 0, 0, 0);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = 0;
+    }
+  }
+  __device__ __forceinline__ uint32_t word(int q, const int8_t *row, bool inner) const {
+    return __funnelshift_r(v[q], v[q + 1], inner ? 8 * ((uint32_t)(uintptr_t)row & 3) : 0);
+  }
+};
 
 __device__ __forceinline__ void put_any(const LinearArgs &a, int m, int n, int acc, float sx, float sw, float bias) {
   const int64_t at = (int64_t)m * a.ldy + n;
@@ -177,7 +199,8 @@ __device__ __forceinline__ void put_any(const LinearArgs &a, int m, int n, int a
 
 template <int NT, bool WIDE>
 __global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a, int blocks_n) {
-  constexpr int kAhead = WIDE ? (NT == 1 ? 8 : 4) : 2;       // pieces of 64 k in flight
+  // pieces of 64 k in flight (unaligned rows: four of them measured 9.7 us for 1 x 4096 x 4099, two 8.7)
+  constexpr int kAhead = WIDE ? (NT == 1 ? 8 : 4) : 2;
   constexpr int kOut = 16 * 8 * NT;                          // outputs of a block
   constexpr int kEach = (kOut + 32 * kWarps - 1) / (32 * kWarps);
   __shared__ int part[kWarps][kOut];
@@ -214,27 +237,28 @@ __global__ void __launch_bounds__(32 * kWarps) few_kernel(const LinearArgs a, in
   const int pieces = (a.K + 63) / 64;
   int since = 0;                                             // pieces since the sums were taken out
   for (int p = warp; p < pieces; p += kWarps * kAhead) {
-    uint4 w[kAhead][2], x[kAhead][NT];
+    Piece<WIDE> w[kAhead][2], x[kAhead][NT];
+    bool inner[kAhead];              // whether the words around the piece lie within the rows
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
-      const int k = (p + u * kWarps) * 64 + 16 * t;
+      const int pu = p + u * kWarps, k = pu * 64 + 16 * t;
+      inner[u] = !WIDE && pu > 0 && pu * 64 + 64 + 4 <= a.K;
 #pragma unroll
-      for (int r = 0; r < 2; r++) w[u][r] = piece16<WIDE>(wrow[r], k, a.K, whave[r]);
+      for (int r = 0; r < 2; r++) w[u][r].ask(wrow[r], k, a.K, whave[r], inner[u]);
 #pragma unroll
-      for (int j = 0; j < NT; j++) x[u][j] = piece16<WIDE>(xrow[j], k, a.K, xhave[j]);
+      for (int j = 0; j < NT; j++) x[u][j].ask(xrow[j], k, a.K, xhave[j], inner[u]);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
-      const uint32_t *w0 = &w[u][0].x, *w1 = &w[u][1].x, *xu = &x[u][0].x;
 #pragma unroll
       for (int q = 0; q < 4; q++) {
         uint32_t af[4];
-        half4(w0[q], af[0], af[2]);
-        half4(w1[q], af[1], af[3]);
+        half4(w[u][0].word(q, wrow[0], inner[u]), af[0], af[2]);
+        half4(w[u][1].word(q, wrow[1], inner[u]), af[1], af[3]);
 #pragma unroll
         for (int j = 0; j < NT; j++) {
           uint32_t bf[2];
-          half4(xu[j * 4 + q], bf[0], bf[1]);
+          half4(x[u][j].word(q, xrow[j], inner[u]), bf[0], bf[1]);
           mma16816(acc[j], af, bf);
         }
       }
