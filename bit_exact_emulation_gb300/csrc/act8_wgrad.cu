@@ -3,11 +3,10 @@
 //
 // A product of dY^T (N x T) and the checkpoint (T x K) over the tokens, bound by the matrix unit:
 // 8192 x 4096 x 4096 takes 169 us, 15 of them the widening: 1.63 PFLOP/s, 0.85 of the measured bf16
-// rate.  A code times its
-// power-of-two scale is a bfloat16 number, so the checkpoint is widened once to a bfloat16 panel
-// (3 bytes of traffic an element) and the product is the matrix unit's, with exact operands.
-// Both operands are read with the tokens outermost as they lie in memory (MN-major); dY
-// needs no panel of its own unless its rows miss 16-byte boundaries.
+// rate.  A code times its power-of-two scale is a bfloat16 number, so the checkpoint is widened
+// once to a bfloat16 panel (3 bytes of traffic an element) and the product is the matrix
+// unit's, with exact operands.  Both operands are read with the tokens outermost as they lie in
+// memory (MN-major); dY needs no panel of its own unless its rows miss 16-byte boundaries.
 #include "panel.cuh"
 
 namespace mcemu {

@@ -7,7 +7,7 @@
 // rounding (every partial sum too, in any order, dropped bits or not).  Every 1024 products the
 // accumulators are therefore taken out and added to int32 sums in registers.
 //
-// Three forms, chosen by go() below: few tokens (bound by the weights' bytes), a batch of them
+// Three forms, chosen by form_of() below: few tokens (bound by the weights' bytes), a batch of them
 // (bound by the widening of the weights), many (bound by the matrix unit).
 #include "panel.cuh"
 
@@ -305,12 +305,13 @@ int go_few(const LinearArgs &a, bool wide, cudaStream_t st) {
 // blocks of a cluster share K, and each adds up its share of the tile out of the others' shared
 // memory, so that no second launch joins the parts.  128 x 8192 x 4096: 19.4 us (1.7 TB/s of
 // weights).  Bound by the widening: some 60 instructions for 16 elements of a lane, sixteen warps
-// on the four schedulers; the matrix unit is a fifth busy.
+// on the four schedulers; the matrix unit is a fifth busy.  Rows that 16-byte loads do not fit cost
+// another 15 to shift a piece into place (WIDE: none such; 128 x 8192 x 4097: 26.3 us).
 // ---------------------------------------------------------------------------
 constexpr int kStageK = 128;                  // k of a stage: two 128-byte swizzle rows, the first 64 k of all rows first
 constexpr int kChunk = 1024 / kStageK;        // stages between two transfers to int32
 
-template <int BN>
+template <int BN, bool WIDE>
 struct Batch {
   static constexpr int kWorkers = 512;
   static constexpr int kEach = BN / (kWorkers / 128);           // accumulator columns a worker drains
@@ -319,15 +320,17 @@ struct Batch {
   static constexpr int kStages = 2;
   static constexpr int kPass = kWorkers / 8;                    // rows that the workers load at a time
   static constexpr int kLoads = kRows / kPass;
-  static constexpr int kAhead = BN <= 64 ? 4 : 3;               // stages whose copies are in flight
+  static constexpr int kRowBytes = WIDE ? kStageK : 192;        // of a row's copy
+  static constexpr int kAhead = (BN <= 64 ? 4 : 3) - !WIDE;     // stages whose copies are in flight: what memory holds
   static constexpr int kColumns = BN;                           // tensor memory: a power of two, 32 at least
-  static constexpr int kCopies = kAhead * kLoads * kWorkers * 16;
+  static constexpr int kCopies = kAhead * kRows * kRowBytes;
   static constexpr int kSmem = kStages * kBytes + kCopies + 1024 + 256;     // also holds the tile's 128 * BN sums
 };
 
-template <int BN>
-__global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(const LinearArgs a, int tiles_n, int per) {
-  using S = Batch<BN>;
+template <int BN, bool WIDE>
+__global__ void __launch_bounds__(Batch<BN, WIDE>::kWorkers + 32, 1) batch_kernel(const LinearArgs a, int tiles_n,
+                                                                                  int per) {
+  using S = Batch<BN, WIDE>;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
   const uint32_t copies = base + S::kStages * S::kBytes, full = copies + S::kCopies, empty = full + 8 * S::kStages,
@@ -396,37 +399,96 @@ __global__ void __launch_bounds__(Batch<BN>::kWorkers + 32, 1) batch_kernel(cons
                            (((2 * (piece & 3)) ^ (row0 & 7)) << 4);      // of row0; kPass rows on, 128 bytes each
     const int8_t *pw = a.w + (int64_t)(n0 + row0) * a.ldw + 16 * piece, *px = a.x + (int64_t)(m0 + row0) * a.ldx + 16 * piece;
     const int rows_w = a.N - n0 - row0, rows_x = a.M - m0 - row0;
-    // A thread copies its pieces ahead into places of its own, so that no barrier and no
+    // WIDE: a thread copies its pieces ahead into places of its own, so that no barrier and no
     // register waits for them (loaded to registers one stage ahead: 128 x 8192 x 4096 in 22 us in
     // place of 20.1).
-    const uint32_t place = copies + threadIdx.x * 16;
+    // Otherwise a warp copies the aligned units around its rows, nine to a row and stage, and a
+    // lane takes its piece out of two of them (with copies of single words in place of units
+    // 128 x 8192 x 4097 took 34 us).  Rows lie 192 bytes apart, so that eight lanes that load
+    // together read different banks.  Bytes beyond K are not read but zeros; up to 15 before a
+    // row, in the unit that holds its first, are read and shifted out.
+    const uint32_t place = WIDE ? copies + threadIdx.x * 16 : copies + warp * (4 * S::kLoads * S::kRowBytes);
+    const int rows_mine_w = a.N - n0 - warp * 4, rows_mine_x = a.M - m0 - warp * 4;
+    const auto unit_of = [&](int r, int unit, int &off) {          // of row r after the warp's first
+      const int8_t *p = r < 128 ? a.w + (int64_t)(n0 + warp * 4 + r) * a.ldw : a.x + (int64_t)(m0 + warp * 4 + r - 128) * a.ldx;
+      off = (int)((uintptr_t)p & 15);
+      return p - off + 16 * unit;
+    };
+    // a lane copies unit lane & 7 of row lane / 8 and those 64 rows on, and one row's ninth
+    int off_uw, off_ux, off_ut;
+    const int lane_row = lane >> 3, unit = lane & 7, tail_row = S::kPass * (lane >> 2) + (lane & 3);
+    const int8_t *uw = unit_of(lane_row, unit, off_uw), *ux = unit_of(128 + lane_row, unit, off_ux),
+                 *ut = unit_of(tail_row, 8, off_ut);
+    const bool tail = lane < 4 * S::kLoads;
+    const bool tail_in = tail && (tail_row < 128 ? tail_row < rows_mine_w : tail_row - 128 < rows_mine_x);
+    const auto copy_unit = [&](uint32_t to, const int8_t *from, int left) {        // left: bytes of the row from there on
+      const int bytes = max(0, min(16, left));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                   "l"(bytes ? from : (const int8_t *)((uintptr_t)a.w & ~(uintptr_t)15)), "r"(bytes)
+                   : "memory");
+    };
     const auto copy = [&](int s) {
-      const int k = s < s1 ? s * kStageK : a.K;
-      const bool in = k + 16 * piece < a.K;
-      const uint32_t to = place + (uint32_t)((s - s0) % S::kAhead) * (S::kLoads * S::kWorkers * 16);
+      const uint32_t to = place + (uint32_t)((s - s0) % S::kAhead) * (S::kRows * S::kRowBytes);
+      if constexpr (WIDE) {
+        const int k = s < s1 ? s * kStageK : a.K;
+        const bool in = k + 16 * piece < a.K;
 #pragma unroll
-      for (int j = 0; j < S::kLoads; j++) {
-        const int r = S::kPass * j;                    // rows after row0
-        const bool is_w = r < 128, have = in && (is_w ? r < rows_w : r - 128 < rows_x);
-        const int8_t *from = !have ? a.w : is_w ? pw + r * a.ldw + k : px + (r - 128) * a.ldx + k;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + j * S::kWorkers * 16), "l"(from),
-                     "r"(have ? 16 : 0)
-                     : "memory");
+        for (int j = 0; j < S::kLoads; j++) {
+          const int r = S::kPass * j;                    // rows after row0
+          const bool is_w = r < 128, have = in && (is_w ? r < rows_w : r - 128 < rows_x);
+          const int8_t *from = !have ? a.w : is_w ? pw + r * a.ldw + k : px + (r - 128) * a.ldx + k;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + j * S::kWorkers * 16), "l"(from),
+                       "r"(have ? 16 : 0)
+                       : "memory");
+        }
+      } else if (s < s1) {
+        const int k = s * kStageK;
+#pragma unroll
+        for (int j = 0; j < S::kLoads; j++) {
+          const int r = S::kPass * j;
+          const uint32_t at = to + (4 * j + lane_row) * S::kRowBytes + 16 * unit;
+          if (r < 128) copy_unit(at, uw + r * a.ldw + k, lane_row + r < rows_mine_w ? a.K + off_uw - 16 * unit - k : 0);
+          else
+            copy_unit(at, ux + (r - 128) * a.ldx + k, lane_row + r - 128 < rows_mine_x ? a.K + off_ux - 16 * unit - k : 0);
+        }
+        if (tail) copy_unit(to + lane * S::kRowBytes + 128, ut + k, tail_in ? a.K + off_ut - 128 - k : 0);
       }
       copy_commit();
     };
+    // where a row's first byte lies in its unit: the same for rows 64 apart
+    const int off_w = (int)((uintptr_t)pw & 15), off_x = (int)((uintptr_t)px & 15);
     uint32_t it = 0;
     const auto step = [&](int stage) {
       const uint32_t s = it % S::kStages, at = base + s * S::kBytes;
       copy_wait<S::kAhead - 1>();
       uint4 v[S::kLoads];
-      const uint32_t mine = place + (uint32_t)((stage - s0) % S::kAhead) * (S::kLoads * S::kWorkers * 16);
+      const uint32_t mine = place + (uint32_t)((stage - s0) % S::kAhead) * (S::kRows * S::kRowBytes);
+      if constexpr (!WIDE) __syncwarp();
 #pragma unroll
-      for (int j = 0; j < S::kLoads; j++)
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
-                     : "r"(mine + j * S::kWorkers * 16)
-                     : "memory");
+      for (int j = 0; j < S::kLoads; j++) {
+        if constexpr (WIDE) {
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                       : "r"(mine + j * S::kWorkers * 16)
+                       : "memory");
+        } else {
+          uint32_t u[8];
+          const int off = S::kPass * j < 128 ? off_w : off_x;
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(u[i]), "=r"(u[i + 1]), "=r"(u[i + 2]), "=r"(u[i + 3])
+                         : "r"(mine + (4 * j + ((lane >> 2) & 3)) * S::kRowBytes + 16 * piece + 4 * i)
+                         : "memory");
+#pragma unroll
+          for (int i = 0; i < 6; i++) u[i] = off & 8 ? u[i + 2] : u[i];
+#pragma unroll
+          for (int i = 0; i < 5; i++) u[i] = off & 4 ? u[i + 1] : u[i];
+          const uint32_t shift = 8 * (off & 3);
+          v[j] = make_uint4(__funnelshift_r(u[0], u[1], shift), __funnelshift_r(u[1], u[2], shift),
+                            __funnelshift_r(u[2], u[3], shift), __funnelshift_r(u[3], u[4], shift));
+        }
+      }
       tc::mbar_wait(empty + 8 * s, ((it / S::kStages) & 1) ^ 1, dead);
 #pragma unroll
       for (int j = 0; j < S::kLoads; j++) {
@@ -522,11 +584,11 @@ int batch_parts(int64_t tiles, int stages) {
   return parts;
 }
 
-template <int BN>
+template <int BN, bool WIDE>
 int go_batch(const LinearArgs &a, cudaStream_t st) {
-  using S = Batch<BN>;
+  using S = Batch<BN, WIDE>;
   static std::atomic<bool> ready[64];
-  const auto kernel = batch_kernel<BN>;
+  const auto kernel = batch_kernel<BN, WIDE>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MCEMU_ERR_CUDA;
   if (dev >= 64 || !ready[dev].load()) {
@@ -552,27 +614,33 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
   const cudaError_t rc = cudaLaunchKernelEx(&cfg, kernel, a, tiles_n, (stages + parts - 1) / parts);
   return rc == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
 }
-// Which form.  Up to kFew tokens, and for K = 0, the first: 32 tokens by 4096 x 4096 (8192 x 4096)
-// weights 8.0 us (14.4) against 10.7 (16.6) of the second.  Rows that 16-byte loads do not fit
-// take panels from there on, whose widening reads any rows.  Otherwise what ends sooner by these
-// estimates in microseconds, whose constants are measured:
+// Which form: what ends soonest by these estimates in microseconds, whose constants are measured.
 //
 //                        batch  panels                           batch  panels
 //   128 x  8192 x 4096    19.4    34.9      1024 x 2048 x 2048    21.1    16.0
 //   256 x  8192 x 4096    32.8    35.9      2048 x 1024 x 1024    15.0    11.9
 //   512 x  1024 x 1024     8.7    11.2      48 x 16384 x 4096     27.9    57.1
-constexpr int kFew = 32;
-bool by_panels(int M, int N, int K, bool wide) {
-  if (M <= kFew || K == 0) return false;
-  if (!wide) return true;
+//   128 x  8192 x 4097    26.4    37.5      1024 x 2048 x 2049    28.2    18.2
+//   256 x  8192 x 4097    45.0    38.3      77 x 5003 x 2049      16.9    18.8
+//
+// Few tokens, and K = 0, go the first way: 32 tokens by 4096 x 4096 (8192 x 4096) weights 8.0 us
+// (14.4) against 10.7 (16.6) of the second.  Over rows that 16-byte loads do not fit it is the
+// better up to 16 tokens (4096 x 4099: 12.0, 13.8), and beyond only for little work (32 tokens by
+// 4096 x 4099: 18.0, 13.8; 1000 x 263: 5.5, 8.7).
+enum class Form { few, batch, panels };
+
+Form form_of(int M, int N, int K, bool wide) {
+  if (M <= (wide ? 32 : 16) || K == 0) return Form::few;
   const int bn = M <= 64 ? 64 : 128, stages = (K + kStageK - 1) / kStageK;
   const int64_t tiles = ((int64_t)N + 127) / 128 * (((int64_t)M + bn - 1) / bn);
   const int parts = batch_parts(tiles, stages);
   const double waves = (double)((tiles * parts + 2 * panel::kPairs - 1) / (2 * panel::kPairs));
-  const double batch = 6.0 + waves * ((stages + parts - 1) / parts) * (bn == 64 ? 0.67 : 0.88);
+  const double stage = wide ? (bn == 64 ? 0.67 : 0.88) : (bn == 64 ? 0.90 : 1.20);
+  const double batch = 6.0 + waves * ((stages + parts - 1) / parts) * stage;
+  if (M <= 32 && 4.5 + (double)N * K / 1.4e6 < batch) return Form::few;
   const panel::Plan p = panel::plan_of(N, M, ktiles_of(K), false);
   const double panels = 7.0 + 3.0 * ((double)M + N) * K / 6.9e6 + p.us;
-  return panels < batch;
+  return panels < batch ? Form::panels : Form::batch;
 }
 
 }  // namespace
@@ -580,26 +648,29 @@ bool by_panels(int M, int N, int K, bool wide) {
 int int8_linear_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_timeouts(st, got); }
 
 size_t int8_linear_workspace(int M, int N, int K, bool rows) {
-  if (!by_panels(M, N, K, rows && K % 16 == 0)) return 0;
+  if (form_of(M, N, K, rows && K % 16 == 0) != Form::panels) return 0;
   return (size_t)(blocks128(M) + blocks128(N)) * ktiles_of(K) * panel::kTileBytes;
 }
 
 int launch_int8_linear(const LinearArgs &a, bool rows, void *ws, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   const bool wide = rows && a.K % 16 == 0;
-  if (by_panels(a.M, a.N, a.K, wide)) {
-    switch (a.out_fmt) {
-      case MCEMU_INT32: return go_panels<MCEMU_INT32>(a, rows, ws, st);
-      case MCEMU_FP32: return go_panels<MCEMU_FP32>(a, rows, ws, st);
-      case MCEMU_FP16: return go_panels<MCEMU_FP16>(a, rows, ws, st);
-      default: return go_panels<MCEMU_BF16>(a, rows, ws, st);
-    }
+  switch (form_of(a.M, a.N, a.K, wide)) {
+    case Form::few:
+      if (a.M <= 8) return go_few<1>(a, wide, st);
+      if (a.M <= 16) return go_few<2>(a, wide, st);
+      return go_few<4>(a, wide, st);
+    case Form::batch:
+      if (a.M <= 64) return wide ? go_batch<64, true>(a, st) : go_batch<64, false>(a, st);
+      return wide ? go_batch<128, true>(a, st) : go_batch<128, false>(a, st);
+    default: break;
   }
-  if (a.M <= 8) return go_few<1>(a, wide, st);
-  if (a.M <= 16) return go_few<2>(a, wide, st);
-  if (a.M <= kFew || a.K == 0) return go_few<4>(a, wide, st);
-  if (a.M <= 64) return go_batch<64>(a, st);
-  return go_batch<128>(a, st);
+  switch (a.out_fmt) {
+    case MCEMU_INT32: return go_panels<MCEMU_INT32>(a, rows, ws, st);
+    case MCEMU_FP32: return go_panels<MCEMU_FP32>(a, rows, ws, st);
+    case MCEMU_FP16: return go_panels<MCEMU_FP16>(a, rows, ws, st);
+    default: return go_panels<MCEMU_BF16>(a, rows, ws, st);
+  }
 }
 
 }  // namespace mcemu

@@ -1,9 +1,9 @@
 // rmsnorm.cu -- root-mean-square norm with the residual's addition and an output in 8 bits
-// with a scale for each token, and its gradients (include/mcemu_ops.h has the formulas).
+// with a scale for each token (include/mcemu_ops.h has the formulas).
 //
-// Both directions are bound by HBM: 7 bytes an element for bf16 rows with a residual,
-// against some ten operations.  A row lives in the registers of its threads between the
-// one pass over memory that reads it and the one that writes it.
+// Bound by HBM: 7 bytes an element for bf16 rows with a residual, against some ten operations.
+// A row lives in the registers of its threads between the one pass over memory that reads it
+// and the one that writes it.
 #include "ops_common.cuh"
 
 namespace mcemu {

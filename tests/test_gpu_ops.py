@@ -411,6 +411,18 @@ def test_int8_linear_strides(O, M, pads):
     assert torch.all(back[:, N:] == 7.0)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 50, 1100), (24, 130, 1100), (40, 300, 1100), (140, 300, 1100), (40, 140, 5)])
+def test_int8_linear_every_alignment(O, M, N, K):
+    """Rows that start on every byte of sixteen, in either operand."""
+    rng = np.random.default_rng(M + N)
+    x, w = int8s(rng, M, K), int8s(rng, N, K)
+    want = linear_host(x, None, w, None, None, "int32")
+    for lead in range(16):
+        for px, pw in ((0, 4), (16 - K % 16, 3), (5, 16 - K % 16)):
+            got = O.int8_linear(strided(x, px, lead), None, strided(w, pw, (5 * lead + 3) % 16), None, out="int32")
+            assert same(got, want), (lead, px, pw)
+
+
 def test_int8_linear_matches_the_emulated_unit(O):
     """The sums of the INT8 matrix unit's model, bit for bit."""
     from oracle.presets import block_models
