@@ -158,7 +158,7 @@ int act8_wgrad_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_ti
 
 size_t act8_wgrad_workspace(int T, int N, int K, bool direct) {
   const Layout p = layout_of(T, N, K, direct);
-  return (size_t)(p.panel_x + p.panel_dy + p.parts);
+  return (size_t)(p.panel_x + p.panel_dy + p.parts) + kPanelPad;
 }
 
 int launch_act8_wgrad(const WgradArgs &a, bool direct, void *ws, void *stream) {
@@ -171,7 +171,7 @@ int launch_act8_wgrad(const WgradArgs &a, bool direct, void *ws, void *stream) {
   }
   const Layout p = layout_of(a.T, a.N, a.K, direct);
   if (!panel::panel_fits(p.blocks_k, p.ttiles) || !panel::panel_fits(p.blocks_n, p.ttiles)) return MCEMU_ERR_UNSUPPORTED;
-  uint8_t *px = (uint8_t *)ws, *pdy = px + p.panel_x;
+  uint8_t *px = panels_in(ws), *pdy = px + p.panel_x;
   float *parts = (float *)(pdy + p.panel_dy);
   widen_kernel<<<(unsigned)(p.blocks_k * p.ttiles), 256, 0, st>>>(a, p.ttiles, rows16(a.q, a.ldq, 1), px);
   if (!direct) copy_kernel<<<(unsigned)(p.blocks_n * p.ttiles), 256, 0, st>>>(a, p.ttiles, pdy);

@@ -127,7 +127,7 @@ int ktiles_of(int K) { return (K + 63) / 64; }
 template <int OUT>
 int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
   const int kt = ktiles_of(a.K);
-  Widen x{a.x, a.ldx, a.M, blocks128(a.M), (uint8_t *)ws};
+  Widen x{a.x, a.ldx, a.M, blocks128(a.M), panels_in(ws)};
   Widen w{a.w, a.ldw, a.N, blocks128(a.N), x.to + (int64_t)x.blocks * kt * panel::kTileBytes};
   const int64_t tiles = (int64_t)(x.blocks + w.blocks) * kt;
   if (!panel::panel_fits(x.blocks, kt) || !panel::panel_fits(w.blocks, kt)) return MCEMU_ERR_UNSUPPORTED;
@@ -649,7 +649,7 @@ int int8_linear_timeouts(cudaStream_t st, unsigned int *got) { return tc::take_t
 
 size_t int8_linear_workspace(int M, int N, int K, bool rows) {
   if (form_of(M, N, K, rows && K % 16 == 0) != Form::panels) return 0;
-  return (size_t)(blocks128(M) + blocks128(N)) * ktiles_of(K) * panel::kTileBytes;
+  return (size_t)(blocks128(M) + blocks128(N)) * ktiles_of(K) * panel::kTileBytes + kPanelPad;
 }
 
 int launch_int8_linear(const LinearArgs &a, bool rows, void *ws, void *stream) {

@@ -268,6 +268,11 @@ int launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaS
 
 inline int launch_status() { return cudaGetLastError() == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA; }
 
+// A caller's workspace is aligned to 16 bytes, panels that store32 writes to 32: where they begin in
+// one that is kPanelPad bytes longer.
+constexpr size_t kPanelPad = 16;
+inline uint8_t *panels_in(void *ws) { return (uint8_t *)(((uintptr_t)ws + 31) & ~(uintptr_t)31); }
+
 // Whether a row-major operand's rows all start on 16-byte boundaries (an absent one does).
 inline bool rows16(const void *p, int64_t ld, int elem_bytes) {
   return !p || (((uintptr_t)p & 15) == 0 && (ld * elem_bytes) % 16 == 0);

@@ -606,6 +606,36 @@ def test_capture_in_a_graph(O):
         assert all(same(a, b) for a, b in zip(got, want))
 
 
+def inside(need):
+    """`need` bytes on a 16-byte boundary that is no 32-byte one, and what lies around them."""
+    buf = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert buf.data_ptr() % 32 == 0
+    return buf[16:16 + need], (buf[:16], buf[16 + need:])
+
+
+@pytest.mark.parametrize("M,N,K", [(1300, 1800, 520), (1100, 1030, 1024)])
+def test_workspace_of_the_product(O, M, N, K):
+    """Any 16-byte boundary will do, and nothing outside the workspace is written."""
+    rng = np.random.default_rng(K)
+    x, w = int8s(rng, M, K), int8s(rng, N, K)
+    need = O.lib().mcemu_int8_linear_workspace(M, N, K, K % 16 == 0)
+    assert need > 0
+    ws, around = inside(need)
+    got = O.int8_linear(x.cuda(), None, w.cuda(), None, out="int32", workspace=ws)
+    assert same(got, linear_host(x, None, w, None, None, "int32"))
+    assert all(torch.all(b == 0xA5) for b in around)
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 264, 200), (700, 257, 130), (5000, 520, 1000)])
+def test_workspace_of_the_weight_gradient(O, T, N, K):
+    g = torch.Generator("cuda").manual_seed(T)
+    dy = torch.randn(T, N, device="cuda", generator=g).bfloat16()
+    q, e = O.act8_compress(torch.randn(T, K, device="cuda", generator=g))
+    ws, around = inside(O.lib().mcemu_act8_wgrad_workspace(T, N, K, int(N % 8 == 0)))
+    assert same(O.act8_wgrad(dy, q, e, workspace=ws), O.act8_wgrad(dy, q, e))
+    assert all(torch.all(b == 0xA5) for b in around)
+
+
 def test_python_refusals(O):
     E = O.McemuError
     bf, f, i8 = torch.bfloat16, torch.float32, torch.int8
