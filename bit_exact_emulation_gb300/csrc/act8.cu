@@ -49,6 +49,14 @@ __device__ __forceinline__ float amax_of(const Vec<T, V> &x) {
   }
 }
 
+// Blocks along the columns: the grid's second axis, which ends at 65535, and its third.  (One axis
+// and a division in place of three: 70 us for 16384 x 8192 bf16 in place of 64.)
+__device__ __forceinline__ int across() { return blockIdx.y + blockIdx.z * gridDim.y; }
+dim3 grid_of(int high, int wide) {
+  const int y = wide < 65535 ? wide : 65535;
+  return dim3(high, y, (wide + y - 1) / y);
+}
+
 // blockDim.x * VEC columns by blockDim.y * kRows rows to a block of 256 threads, kRows rows to a
 // thread so that as many loads are in flight; 128 / VEC neighbouring lanes share a block of 128.
 constexpr int kRows = 4;
@@ -57,7 +65,7 @@ template <class T, int VEC>
 __global__ void __launch_bounds__(256) compress_kernel(int T_, int H, const T *__restrict__ x, int64_t ldx,
                                                        int8_t *__restrict__ q, int64_t ldq, int8_t *__restrict__ e,
                                                        int64_t lde) {
-  const int i = ((int)(blockIdx.y * blockDim.x) + threadIdx.x) * VEC;
+  const int i = (across() * (int)blockDim.x + threadIdx.x) * VEC;
   const int64_t row0 = (int64_t)blockIdx.x * (blockDim.y * kRows) + threadIdx.y;
   Vec<T, VEC> v[kRows];
   bool in[kRows];
@@ -104,7 +112,7 @@ template <class T>
 __global__ void __launch_bounds__(256) compress_any_kernel(int T_, int H, const T *__restrict__ x, int64_t ldx,
                                                            int8_t *__restrict__ q, int64_t ldq, int8_t *__restrict__ e,
                                                            int64_t lde) {
-  const int lane = threadIdx.x & 31, b = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, b = across() * 8 + (threadIdx.x >> 5);
   const int64_t row0 = (int64_t)blockIdx.x * kRows;
   if (b * kBlock >= H) return;
   T v[kRows][4];
@@ -160,12 +168,12 @@ int compress_typed(int T_, int H, const void *x, int64_t ldx, int8_t *q, int64_t
     const int items = H / V;
     int tx = 32;
     while (tx < 256 && tx < items) tx *= 2;
-    const dim3 block(tx, 256 / tx), grid((T_ + block.y * kRows - 1) / (block.y * kRows), (items + tx - 1) / tx);
-    if (grid.y > 65535) return MCEMU_ERR_UNSUPPORTED;
+    const dim3 block(tx, 256 / tx);
+    const int rows = 256 / tx * kRows;
+    const dim3 grid = grid_of((T_ + rows - 1) / rows, (items + tx - 1) / tx);
     compress_kernel<T, V><<<grid, block, 0, st>>>(T_, H, (const T *)x, ldx, q, ldq, e, lde);
   } else {
-    const dim3 grid((T_ + kRows - 1) / kRows, (H + 8 * kBlock - 1) / (8 * kBlock));
-    if (grid.y > 65535) return MCEMU_ERR_UNSUPPORTED;
+    const dim3 grid = grid_of((T_ + kRows - 1) / kRows, (H + 8 * kBlock - 1) / (8 * kBlock));
     compress_any_kernel<T><<<grid, 256, 0, st>>>(T_, H, (const T *)x, ldx, q, ldq, e, lde);
   }
   return launch_status();
@@ -178,6 +186,7 @@ int expand_typed(int T_, int H, const int8_t *q, int64_t ldq, const int8_t *e, i
   const bool wide = H % V == 0 && rows16(x, ldx, sizeof(T)) && rows_on(q, ldq, 1, V);
   const int per_row = wide ? H / V : H;
   const int64_t tasks = (int64_t)T_ * per_row;
+  if ((tasks + 255) / 256 > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
   if (wide) expand_kernel<T, V><<<blocks_for(tasks), 256, 0, st>>>(tasks, per_row, q, ldq, e, lde, (T *)x, ldx);
   else expand_kernel<T, 1><<<blocks_for(tasks), 256, 0, st>>>(tasks, per_row, q, ldq, e, lde, (T *)x, ldx);
   return launch_status();

@@ -15,6 +15,9 @@ int bytes_of(int fmt) {
 }
 bool float_fmt(int fmt) { return fmt == MCEMU_FP16 || fmt == MCEMU_BF16 || fmt == MCEMU_FP32; }
 bool known_fmt(int fmt) { return fmt >= MCEMU_FP16 && fmt <= MCEMU_INT32; }
+// Sizes and what they are rounded up to are counted in 32 bits.
+constexpr int kMost = INT32_MAX - 65535;
+bool too_large(int a, int b, int c = 0) { return a > kMost || b > kMost || c > kMost; }
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 int blocks_of(int h) { return h / MCEMU_ACT8_BLOCK + (h % MCEMU_ACT8_BLOCK != 0); }
 
@@ -36,6 +39,7 @@ extern "C" int mcemu_rmsnorm(int fmt, int wfmt, int out_fmt, int T, int H, const
   if (!float_fmt(fmt) || (wfmt != fmt && wfmt != MCEMU_FP32) || (!narrow && out_fmt != fmt))
     return MCEMU_ERR_UNSUPPORTED;
   if (T < 0 || H < 1 || !(eps >= 0.f) || std::isinf(eps)) return MCEMU_ERR_INVALID_ARG;
+  if (too_large(T, H)) return MCEMU_ERR_UNSUPPORTED;
   if (T == 0) return MCEMU_OK;
   if (!x || !w || !y || (narrow && !scale) || !res != !h) return MCEMU_ERR_INVALID_ARG;
   if (ldx < H || ldy < H || (res && (ldr < H || ldh < H))) return MCEMU_ERR_INVALID_ARG;
@@ -48,7 +52,7 @@ extern "C" int mcemu_rmsnorm(int fmt, int wfmt, int out_fmt, int T, int H, const
 }
 
 extern "C" size_t mcemu_rmsnorm_backward_workspace(int T, int H) {
-  return T < 1 || H < 1 ? 0 : rmsnorm_backward_workspace(T, H);
+  return T < 1 || H < 1 || too_large(T, H) ? 0 : rmsnorm_backward_workspace(T, H);
 }
 
 extern "C" int mcemu_rmsnorm_backward(int fmt, int wfmt, int T, int H, const void *dy, int64_t lddy,
@@ -59,6 +63,7 @@ extern "C" int mcemu_rmsnorm_backward(int fmt, int wfmt, int T, int H, const voi
   if (!known_fmt(fmt) || !known_fmt(wfmt)) return MCEMU_ERR_INVALID_ARG;
   if (!float_fmt(fmt) || (wfmt != fmt && wfmt != MCEMU_FP32)) return MCEMU_ERR_UNSUPPORTED;
   if (T < 0 || H < 1 || !dw) return MCEMU_ERR_INVALID_ARG;
+  if (too_large(T, H)) return MCEMU_ERR_UNSUPPORTED;
   if (!aligned(dw, 4)) return MCEMU_ERR_ALIGNMENT;
   if (T == 0)
     return cudaMemsetAsync(dw, 0, (size_t)H * 4, (cudaStream_t)stream) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
@@ -80,6 +85,7 @@ extern "C" int mcemu_act8_compress(int fmt, int T, int H, const void *x, int64_t
   if (!known_fmt(fmt)) return MCEMU_ERR_INVALID_ARG;
   if (!float_fmt(fmt)) return MCEMU_ERR_UNSUPPORTED;
   if (T < 0 || H < 1) return MCEMU_ERR_INVALID_ARG;
+  if (too_large(T, H)) return MCEMU_ERR_UNSUPPORTED;
   if (T == 0) return MCEMU_OK;
   if (!x || !q || !e || ldx < H || ldq < H || lde < blocks_of(H)) return MCEMU_ERR_INVALID_ARG;
   if (!aligned(x, bytes_of(fmt))) return MCEMU_ERR_ALIGNMENT;
@@ -91,6 +97,7 @@ extern "C" int mcemu_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t
   if (!known_fmt(fmt)) return MCEMU_ERR_INVALID_ARG;
   if (!float_fmt(fmt)) return MCEMU_ERR_UNSUPPORTED;
   if (T < 0 || H < 1) return MCEMU_ERR_INVALID_ARG;
+  if (too_large(T, H)) return MCEMU_ERR_UNSUPPORTED;
   if (T == 0) return MCEMU_OK;
   if (!x || !q || !e || ldx < H || ldq < H || lde < blocks_of(H)) return MCEMU_ERR_INVALID_ARG;
   if (!aligned(x, bytes_of(fmt))) return MCEMU_ERR_ALIGNMENT;
@@ -98,7 +105,7 @@ extern "C" int mcemu_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t
 }
 
 extern "C" size_t mcemu_int8_linear_workspace(int M, int N, int K, int rows_aligned) {
-  return M < 1 || N < 1 || K < 1 || K > 131071 ? 0 : int8_linear_workspace(M, N, K, rows_aligned != 0);
+  return M < 1 || N < 1 || K < 1 || K > 131071 || too_large(M, N) ? 0 : int8_linear_workspace(M, N, K, rows_aligned != 0);
 }
 
 extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t ldx, const float *sx,
@@ -107,7 +114,7 @@ extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t l
   if (!known_fmt(out_fmt)) return MCEMU_ERR_INVALID_ARG;
   if (!float_fmt(out_fmt) && out_fmt != MCEMU_INT32) return MCEMU_ERR_UNSUPPORTED;
   if (M < 0 || N < 0 || K < 0) return MCEMU_ERR_INVALID_ARG;
-  if (K > 131071) return MCEMU_ERR_UNSUPPORTED;
+  if (K > 131071 || too_large(M, N)) return MCEMU_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MCEMU_OK;
   if ((K > 0 && (!x || !w)) || !y) return MCEMU_ERR_INVALID_ARG;
   if (out_fmt == MCEMU_INT32 ? (sx || sw || bias) : (!sx || !sw)) return MCEMU_ERR_INVALID_ARG;
@@ -122,7 +129,7 @@ extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t l
 }
 
 extern "C" size_t mcemu_act8_wgrad_workspace(int T, int N, int K, int dy_rows_aligned) {
-  return T < 1 || N < 1 || K < 1 ? 0 : act8_wgrad_workspace(T, N, K, dy_rows_aligned != 0);
+  return T < 1 || N < 1 || K < 1 || too_large(T, N, K) ? 0 : act8_wgrad_workspace(T, N, K, dy_rows_aligned != 0);
 }
 
 extern "C" int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t lddy, const int8_t *q, int64_t ldq,
@@ -132,6 +139,7 @@ extern "C" int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t
   if ((out_fmt != MCEMU_FP32 && out_fmt != MCEMU_BF16) || (accumulate && out_fmt != MCEMU_FP32))
     return MCEMU_ERR_UNSUPPORTED;
   if (T < 0 || N < 0 || K < 0) return MCEMU_ERR_INVALID_ARG;
+  if (too_large(T, N, K)) return MCEMU_ERR_UNSUPPORTED;
   if (N == 0 || K == 0) return MCEMU_OK;
   if ((T > 0 && (!dy || !q || !e)) || !dW) return MCEMU_ERR_INVALID_ARG;
   if (lddy < N || ldq < K || lde < blocks_of(K) || lddw < K) return MCEMU_ERR_INVALID_ARG;

@@ -29,8 +29,9 @@ __device__ __forceinline__ int padded(int k) { return k + (k >> 3); }
 // row into shared memory while it works on the present one, so that loads are in flight
 // throughout without a register for them.  TX is known to the compiler, so that the vectors
 // of a row lie at fixed distances; 32 elements a thread, where the row is long enough, keep what a
-// row costs on top of its elements small.  8192 x 4096 bf16 with a residual path: 45.8 us (the joining kernel included);
-// rows loaded to registers when their turn comes 71; 8 elements a thread and TX a variable 86.
+// row costs on top of its elements small.  8192 x 4096 bf16 with a residual path: 45.8 us (the
+// joining kernel included); rows loaded to registers when their turn comes 71; 8 elements a
+// thread and TX a variable 86.
 template <class T, int VEC, int PER, bool CKPT>
 struct Stage {                                  // of kThreads threads
   Vec<T, VEC> dy[PER][kThreads], dr[PER][kThreads];
@@ -212,11 +213,11 @@ __global__ void __launch_bounds__(512) long_mean_kernel(const NormGradArgs a, fl
 template <class T, bool CKPT>
 __global__ void __launch_bounds__(256) long_grad_kernel(const NormGradArgs a, const float *__restrict__ mean,
                                                         float *__restrict__ parts) {
-  const int i = blockIdx.y * blockDim.x + threadIdx.x;
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= a.H) return;
   float w[1], dw = 0.f;
   load_w<T, 1>(a.w, a.w32, i, w);
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+  for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
     const float rstd = a.rstd[row], d = to_f(((const T *)a.dy)[row * a.lddy + i]);
     float z[1];
     z[0] = input_at<T, CKPT>(a, row, i) * rstd;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(256) long_grad_kernel(const NormGradArgs a, co
     if (a.dres) x += to_f(((const T *)a.dres)[row * a.lddr + i]);
     ((T *)a.dx)[row * a.lddx + i] = from_f<T>(x);
   }
-  parts[(int64_t)blockIdx.x * a.H + i] = dw;
+  parts[(int64_t)blockIdx.y * a.H + i] = dw;
 }
 
 template <class K>
@@ -268,7 +269,7 @@ int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
   } else {
     float *mean = ws + (int64_t)groups * a.H;
     long_mean_kernel<T, CKPT><<<a.T < 152 * 4 ? a.T : 152 * 4, 512, 0, st>>>(a, mean);
-    long_grad_kernel<T, CKPT><<<dim3(groups, (a.H + 255) / 256), 256, 0, st>>>(a, mean, ws);
+    long_grad_kernel<T, CKPT><<<dim3((a.H + 255) / 256, groups), 256, 0, st>>>(a, mean, ws);
   }
   if (groups < 0) return MCEMU_ERR_CUDA;
   if (cudaGetLastError() != cudaSuccess) return MCEMU_ERR_CUDA;

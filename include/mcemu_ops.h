@@ -19,8 +19,10 @@
  * with leading dimensions in elements, at least the row length; elements of a
  * row are contiguous.  Element pointers must be aligned to their element
  * (MCEMU_ERR_ALIGNMENT); rows that start on 16-byte boundaries take the widest
- * loads.  Buffers do not overlap unless a function says so.  No result depends
- * on the order in which blocks run: the same call gives the same bits.
+ * loads.  Buffers do not overlap unless a function says so.  Sizes are at most
+ * 2^31 - 65536, and the product's operands what 32 bits count in rows of 64
+ * (MCEMU_ERR_UNSUPPORTED).  No result depends on the order in which blocks
+ * run: the same call gives the same bits.
  */
 #ifndef MCEMU_OPS_H
 #define MCEMU_OPS_H
@@ -47,7 +49,8 @@ enum { MCEMU_INT32 = 8 };
  * depends on no summation order: v, A, P / A and the product are single fp32
  * operations (round to nearest, ties to even, as is the rounding to 8 bits).
  * The norm acts on h as it is stored.  A row that holds a NaN or an infinity
- * (or meets one in w) gets a scale that is not finite, or NaN in y.
+ * (or meets one in w) gets a scale that is not finite, or NaN in y; so does a
+ * row of zeros with eps = 0, whose rstd is infinite.
  * fmt: FP16, BF16 or FP32 (x, res, h); wfmt: fmt or FP32; out_fmt: fmt, INT8,
  * E4M3 or E5M2 (the OCP encodings).  res and h are given together or not at
  * all; h may be x or res (same leading dimension).  scale [T] is required for

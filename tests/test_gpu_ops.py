@@ -606,6 +606,30 @@ def test_capture_in_a_graph(O):
         assert all(same(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("H", [135_000_008, 68_000_001])
+def test_act8_very_long_rows(O, H):
+    """A row of more blocks than a grid's second axis has: the same codes as its parts."""
+    g = torch.Generator("cuda").manual_seed(H)
+    x = torch.randn(1, H, device="cuda", generator=g).bfloat16()
+    q, e = O.act8_compress(x)
+    for a, b in ((0, 1 << 20), (64 << 20, 67_500_000), ((H - 100_000) // 128 * 128, H)):
+        qa, ea = O.act8_compress(x[:, a:b].contiguous())
+        assert same(q[:, a:b], qa) and same(e[:, a // 128:-(-b // 128)], ea)
+
+
+def test_rmsnorm_backward_very_long_rows(O):
+    """Against 64 bits, with the bounds of shorter rows."""
+    T, H = 2, 17_000_001
+    rng = np.random.default_rng(1)
+    h, dy, w = (rows(rng, n, H, torch.bfloat16) for n in (T, T, 1))
+    rstd = torch.rsqrt(h.double().square().mean(1) + EPS).float()
+    dx, dw = O.rmsnorm_backward(dy.cuda(), w[0].cuda(), rstd.cuda(), h=h.cuda())
+    dx0, dw0, mag, wmag = grad_host(dy, w[0], rstd, h, None)
+    chain = H / 512 + 1 + 21 + 10
+    assert torch.all((dx.cpu().double() - dx0).abs() <= chain * U32 * mag + UNIT["bf16"] * dx0.abs() * 1.01 + 2.0 ** -25)
+    assert torch.all((dw.cpu().double() - dw0).abs() <= (T + 4) * U32 * wmag + 1e-30)
+
+
 def inside(need):
     """`need` bytes on a 16-byte boundary that is no 32-byte one, and what lies around them."""
     buf = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")

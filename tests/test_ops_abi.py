@@ -122,6 +122,23 @@ def test_act8_wgrad_refusals(L, kw, status):
     assert wgrad(L, **kw) == status
 
 
+def test_sizes_beyond_32_bits_are_refused(L):
+    """Sizes so near 2^31 that what they are rounded up to would not fit."""
+    n = 2 ** 31 - 65535
+    big = dict(ldx=n, ldy=n, lddy=n, lddx=n, ldh=n, ldq=n, lde=n, lddw=n)
+    some = lambda *names: {k: big[k] for k in names}
+    assert norm(L, H=n, **some("ldx", "ldy")) == UNSUPPORTED and norm(L, T=n) == UNSUPPORTED
+    assert grad(L, H=n, **some("lddy", "lddx", "ldh")) == UNSUPPORTED and grad(L, T=n) == UNSUPPORTED
+    assert linear(L, M=n) == UNSUPPORTED and linear(L, N=n, ldy=n) == UNSUPPORTED
+    for f in ("mcemu_act8_compress", "mcemu_act8_expand"):
+        assert act(L, f, H=n, **some("ldx", "ldq", "lde")) == UNSUPPORTED and act(L, f, T=n) == UNSUPPORTED
+    assert wgrad(L, T=n) == UNSUPPORTED and wgrad(L, N=n, lddy=n) == UNSUPPORTED
+    assert wgrad(L, K=n, **some("ldq", "lde", "lddw")) == UNSUPPORTED
+    for need in (L.mcemu_rmsnorm_backward_workspace(n, 5), L.mcemu_int8_linear_workspace(n, 5, 5, 1),
+                 L.mcemu_act8_wgrad_workspace(5, n, 5, 1)):
+        assert need == 0
+
+
 def test_workspaces(L):
     """Sizes come without a device, are 0 for empty problems and do not wrap for large ones."""
     assert L.mcemu_rmsnorm_backward_workspace(0, 10) == 0
