@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(Batch<BN, WIDE>::kWorkers + 32, 1) batch_kerne
   tc::cluster_sync();
   if (warp < kMma) {
     // four channels of every kMma-th token to a thread; all blocks' parts asked for at once
-    const int r = lane * 4, n = n0 + r, share = BN / parts, end = min(a.M - m0, (int)(rank + 1) * share);
+    const int r = lane * 4, n = n0 + r, share = (BN + parts - 1) / parts;
+    const int end = min(a.M - m0, min(BN, (int)(rank + 1) * share));
     const bool scales = a.out_fmt != MCEMU_INT32;
     float sw[4], bias[4];
 #pragma unroll
@@ -576,12 +577,25 @@ __global__ void __launch_bounds__(Batch<BN, WIDE>::kWorkers + 32, 1) batch_kerne
   }
 }
 
-// Parts of K: a power of two of at most eight (a portable cluster), at least two stages each, until
-// the blocks fill the multiprocessors.
-int batch_parts(int64_t tiles, int stages) {
-  int parts = 1;
-  while (parts < 8 && tiles * parts * 2 <= 2 * panel::kPairs && stages >= parts * 4) parts *= 2;
-  return parts;
+// Parts of K, one to a block of a cluster (eight at most, the portable limit; two stages each at
+// least), so that the stages that blocks go through one after another are fewest, with four more for
+// each round of clusters after the first.  The clusters that run at a time are what the device
+// reports for blocks that take a multiprocessor each: the larger, the fewer fit.  200 x 1024 x
+// 4096 in six parts 11.5 us, in eight (two rounds) 18.3; 77 x 5003 x 2049 in three 12.8, in two 17.0;
+// 128 x 12288 x 4096 in one 32.8, in four (three rounds) 36.2.
+struct Split {
+  int parts;
+  int64_t steps;             // stages in a row and what rounds add
+};
+Split split_of(int64_t tiles, int stages) {
+  constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+  Split best{1, 0};
+  for (int parts = 1; parts <= 8 && (parts == 1 || stages >= 2 * parts); parts++) {
+    const int64_t rounds = (tiles + kClusters[parts] - 1) / kClusters[parts];
+    const int64_t steps = rounds * ((stages + parts - 1) / parts + 4) - 4;
+    if (parts == 1 || steps < best.steps) best = Split{parts, steps};
+  }
+  return best;
 }
 
 template <int BN, bool WIDE>
@@ -598,7 +612,7 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
   }
   const int tiles_n = (a.N + 127) / 128, stages = (a.K + kStageK - 1) / kStageK;
   const int64_t tiles = (int64_t)tiles_n * ((a.M + BN - 1) / BN);
-  const int parts = batch_parts(tiles, stages);
+  const int parts = split_of(tiles, stages).parts;
   if (tiles * parts > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * parts));
@@ -621,7 +635,7 @@ int go_batch(const LinearArgs &a, cudaStream_t st) {
 //   256 x  8192 x 4096    32.8    35.9      2048 x 1024 x 1024    15.0    11.9
 //   512 x  1024 x 1024     8.7    11.2      48 x 16384 x 4096     27.9    57.1
 //   128 x  8192 x 4097    26.4    37.5      1024 x 2048 x 2049    28.2    18.2
-//   256 x  8192 x 4097    45.0    38.3      77 x 5003 x 2049      16.9    18.8
+//   256 x  8192 x 4097    45.0    38.3      77 x 5003 x 2049      12.7    18.8
 //
 // Few tokens, and K = 0, go the first way: 32 tokens by 4096 x 4096 (8192 x 4096) weights 8.0 us
 // (14.4) against 10.7 (16.6) of the second.  Over rows that 16-byte loads do not fit it is the
@@ -633,10 +647,8 @@ Form form_of(int M, int N, int K, bool wide) {
   if (M <= (wide ? 32 : 16) || K == 0) return Form::few;
   const int bn = M <= 64 ? 64 : 128, stages = (K + kStageK - 1) / kStageK;
   const int64_t tiles = ((int64_t)N + 127) / 128 * (((int64_t)M + bn - 1) / bn);
-  const int parts = batch_parts(tiles, stages);
-  const double waves = (double)((tiles * parts + 2 * panel::kPairs - 1) / (2 * panel::kPairs));
   const double stage = wide ? (bn == 64 ? 0.67 : 0.88) : (bn == 64 ? 0.90 : 1.20);
-  const double batch = 6.0 + waves * ((stages + parts - 1) / parts) * stage;
+  const double batch = 6.0 + split_of(tiles, stages).steps * stage;
   if (M <= 32 && 4.5 + (double)N * K / 1.4e6 < batch) return Form::few;
   const panel::Plan p = panel::plan_of(N, M, ktiles_of(K), false);
   const double panels = 7.0 + 3.0 * ((double)M + N) * K / 6.9e6 + p.us;

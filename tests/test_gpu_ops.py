@@ -423,6 +423,15 @@ def test_int8_linear_every_alignment(O, M, N, K):
             assert same(got, want), (lead, px, pw)
 
 
+@pytest.mark.parametrize("M,N,K", [(40, 76 * 128 - 3, 520), (40, 46 * 128 - 5, 900), (100, 36 * 128, 1536),
+                                   (40, 28 * 128 - 1, 2000), (77, 23 * 128 - 100, 1999), (128, 15 * 128, 1792), (65, 300, 4096)])
+def test_int8_linear_parts_of_k(O, M, N, K):
+    """K shared by two to eight blocks, the tokens of a tile dealt out evenly or not."""
+    rng = np.random.default_rng(N)
+    x, w = int8s(rng, M, K), int8s(rng, N, K)
+    assert same(O.int8_linear(x.cuda(), None, w.cuda(), None, out="int32"), linear_host(x, None, w, None, None, "int32"))
+
+
 def test_int8_linear_matches_the_emulated_unit(O):
     """The sums of the INT8 matrix unit's model, bit for bit."""
     from oracle.presets import block_models
