@@ -30,9 +30,9 @@ __device__ __forceinline__ float row_sum(float x, float *part) {
 }
 
 // Rows of at most kMaxSingle elements at any strides, on `blocks` blocks that leave their parts of
-// dw in `parts`.
+// dw in `parts`.  Their number, -1 after an error.
 constexpr int kMaxSingle = 8192;
 template <class T, bool CKPT>
-void launch_grad_single(const NormGradArgs &a, int blocks, float *parts, cudaStream_t st);
+int launch_grad_single(const NormGradArgs &a, int blocks, float *parts, cudaStream_t st);
 
 }  // namespace mcemu

@@ -265,7 +265,7 @@ int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
     else if (a.H <= 256 * V * P) groups = go<T, V, P, 256, CKPT>(a, ws, st);
     else groups = go<T, V, P, 512, CKPT>(a, ws, st);
   } else if (a.H <= kMaxSingle) {
-    launch_grad_single<T, CKPT>(a, groups, ws, st);
+    groups = launch_grad_single<T, CKPT>(a, groups, ws, st);
   } else {
     float *mean = ws + (int64_t)groups * a.H;
     long_mean_kernel<T, CKPT><<<a.T < 152 * 4 ? a.T : 152 * 4, 512, 0, st>>>(a, mean);
