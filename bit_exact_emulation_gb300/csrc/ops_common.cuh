@@ -246,6 +246,18 @@ inline int sm_count() {
   return n;
 }
 
+// Lets a kernel have its dynamic shared memory, always the same; asked for once per device.
+template <auto KERNEL>
+bool allow_smem(int bytes) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && ready[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
 // A kernel that begins while the one before it on the stream still runs (programmatic dependent
 // launch): its set-up overlaps, and grid_wait() in it waits for that kernel's end and results.
 // The one before says with grid_go() that it may begin.

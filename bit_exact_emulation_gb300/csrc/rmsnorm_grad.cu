@@ -229,12 +229,6 @@ __global__ void __launch_bounds__(256) long_grad_kernel(const NormGradArgs a, co
   parts[(int64_t)blockIdx.y * a.H + i] = dw;
 }
 
-template <class K>
-bool allow_smem(K kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ||
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-}
-
 // Blocks launched, -1 after an error.
 template <class T, int VEC, int PER, int TX, bool CKPT>
 int go(const NormGradArgs &a, float *parts, cudaStream_t st) {
@@ -246,7 +240,7 @@ int go(const NormGradArgs &a, float *parts, cudaStream_t st) {
   const size_t smem = 2 * sizeof(Stage<T, VEC, PER, CKPT>);
   static_assert(2 * sizeof(Stage<T, VEC, PER, CKPT>) >= kThreads / TX * (TX * PER * VEC * 9 / 8 + 2) * sizeof(float),
                 "the parts of dw fit the copies' memory");
-  if (!allow_smem(grad_kernel<T, VEC, PER, TX, CKPT>, smem)) return -1;
+  if (!allow_smem<grad_kernel<T, VEC, PER, TX, CKPT>>((int)smem)) return -1;
   grad_kernel<T, VEC, PER, TX, CKPT><<<blocks, dim3(TX, rows), smem, st>>>(a, parts);
   return blocks;
 }

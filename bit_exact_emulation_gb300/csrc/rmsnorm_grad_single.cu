@@ -1,50 +1,22 @@
 // rmsnorm_grad_single.cu -- gradients of the root-mean-square norm for rows that no vector fits
 // (include/mcemu_ops.h has the formulas).
 #include "norm_grad.cuh"
+#include "norm_rows.cuh"
 
 namespace mcemu {
 namespace {
 
 constexpr int kPer = 8;                        // elements a thread
 
-// One operand's rows, every `step` bytes, copied a row at a time to shared memory in aligned 16-byte
-// units: a row's first byte then lies `off` behind the copy's.  Places beyond the row are
-// zeros; up to 15 bytes before it are read with its first unit.
-template <int TX, int BYTES>                   // of an element
-struct Rows {
-  static constexpr int kPitch = kPer * TX * BYTES + 16, kUnits = (kPer * BYTES + 15) / 16;
-  const uint8_t *row;
-  int64_t step;
-  int bytes, off;
-  __device__ __forceinline__ Rows(const void *p, int64_t ld, int H)
-      : row((const uint8_t *)p + blockIdx.x * ld * BYTES), step(gridDim.x * ld * BYTES), bytes(H * BYTES), off(0) {}
-  __device__ __forceinline__ void unit(uint8_t *to, int u, int end) const {
-    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to + u);
-    const int n = max(0, min(16, end - u));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(row - off + (n ? u : 0)), "r"(n)
-                 : "memory");
-  }
-  // Copies the next row.
-  __device__ __forceinline__ void fetch(uint8_t *to) {
-    off = (int)((uintptr_t)row & 15);
-    const int end = off + bytes;
-#pragma unroll
-    for (int j = 0; j < kUnits; j++)
-      if (j * TX * 16 + (int)threadIdx.x * 16 < kPitch) unit(to, (j * TX + (int)threadIdx.x) * 16, end);
-    if (kPitch - 16 == kUnits * TX * 16 && threadIdx.x == 0) unit(to, kPitch - 16, end);
-    row += step;
-  }
-};
-
 // Rows that no vector fits, at any strides: a group of TX threads to a block, one element of every
 // TX to a thread, so that a thread keeps its columns, their weights and its part of dw.  The
 // next row is copied to shared memory meanwhile, whole units at a time; columns beyond a row are
-// zeros there and need no questions until they are stored.  8191 x 4099 with a residual path: bf16 90
+// zeros there and need no questions until they are stored.  8191 x 4099 with a residual path: bf16 87
 // us, fp32 88 (elements loaded one by one from memory 121, 134); bound by instruction issue.
 template <class T, int TX, bool CKPT>
 struct Single {
-  using Dy = Rows<TX, sizeof(T)>;
-  using In = Rows<TX, CKPT ? 1 : (int)sizeof(T)>;
+  using Dy = Rows<TX, kPer, sizeof(T)>;
+  using In = Rows<TX, kPer, CKPT ? 1 : (int)sizeof(T)>;
   static constexpr int kStage = 2 * Dy::kPitch + In::kPitch;
 };
 template <class T, int TX, bool CKPT>
@@ -144,17 +116,15 @@ __global__ void __launch_bounds__(TX) single_kernel(const NormGradArgs a, float 
 template <class T, int TX, bool CKPT>
 bool go(const NormGradArgs &a, int blocks, float *parts, cudaStream_t st) {
   constexpr int kSmem = 2 * Single<T, TX, CKPT>::kStage;
-  if (kSmem > 40 * 1024 && cudaFuncSetAttribute(single_kernel<T, TX, CKPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                kSmem) != cudaSuccess)
-    return false;
+  if (!allow_smem<single_kernel<T, TX, CKPT>>(kSmem)) return false;
   single_kernel<T, TX, CKPT><<<blocks, TX, kSmem, st>>>(a, parts);
   return true;
 }
 
 }  // namespace
 
-// Threads to a row: several steps between powers of two, since elements beyond the row are skipped
-// one by one.
+// Threads to a row: several steps between powers of two, since columns beyond the row are computed
+// too (16384 x 1025 bf16 by 256 threads 64 us, by 160 48).
 template <class T, bool CKPT>
 int launch_grad_single(const NormGradArgs &a, int blocks, float *parts, cudaStream_t st) {
   const int threads = (a.H + kPer - 1) / kPer;
@@ -162,9 +132,12 @@ int launch_grad_single(const NormGradArgs &a, int blocks, float *parts, cudaStre
   if (threads <= 32) ok = go<T, 32, CKPT>(a, blocks, parts, st);
   else if (threads <= 64) ok = go<T, 64, CKPT>(a, blocks, parts, st);
   else if (threads <= 128) ok = go<T, 128, CKPT>(a, blocks, parts, st);
+  else if (threads <= 160) ok = go<T, 160, CKPT>(a, blocks, parts, st);
   else if (threads <= 256) ok = go<T, 256, CKPT>(a, blocks, parts, st);
+  else if (threads <= 320) ok = go<T, 320, CKPT>(a, blocks, parts, st);
   else if (threads <= 384) ok = go<T, 384, CKPT>(a, blocks, parts, st);
   else if (threads <= 512) ok = go<T, 512, CKPT>(a, blocks, parts, st);
+  else if (threads <= 576) ok = go<T, 576, CKPT>(a, blocks, parts, st);
   else if (threads <= 640) ok = go<T, 640, CKPT>(a, blocks, parts, st);
   else if (threads <= 768) ok = go<T, 768, CKPT>(a, blocks, parts, st);
   else ok = go<T, 1024, CKPT>(a, blocks, parts, st);

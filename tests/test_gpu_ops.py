@@ -107,6 +107,29 @@ def test_rmsnorm(O, T, H, fmt, out):
         assert torch.all((scale.cpu().double() - scale0).abs() <= (tol + 2 * U32) * scale0)
 
 
+@pytest.mark.parametrize("H", [3, 201, 500, 1001, 1201, 2001, 2501, 3001, 4001, 4503, 5003, 6001, 8191])
+@pytest.mark.parametrize("fmt,out", [("bf16", "int8"), ("fp16", "own"), ("fp32", "e4m3")])
+def test_rmsnorm_many_odd_rows(O, H, fmt, out):
+    """Many rows that no vector fits, at every number of threads to a row."""
+    for T in (305, 700):
+        test_rmsnorm(O, T, H, fmt, out)
+
+
+@pytest.mark.parametrize("H", [201, 1001, 5003])
+@pytest.mark.parametrize("pad,lead", [(0, 0), (3, 1), (8, 5)])
+def test_rmsnorm_many_odd_rows_strides_and_in_place(O, H, pad, lead):
+    rng = np.random.default_rng(H + pad)
+    x, r = rows(rng, 500, H, torch.bfloat16), rows(rng, 500, H, torch.bfloat16)
+    w = rows(rng, 1, H, torch.bfloat16)[0]
+    h, q = norm_host(x, w, r, "int8")[:2]
+    for into in (0, 1):
+        gx, gr = strided(x, pad, lead), strided(r, pad, lead)
+        y, scale, rstd, got = O.rmsnorm(gx, w.cuda(), EPS, residual=gr, h=(gx, gr)[into])
+        assert same(got, h) and same(y, q)
+    fresh = O.rmsnorm(x.cuda(), w.cuda(), EPS, residual=r.cuda())
+    assert same(fresh[0], q) and same(fresh[1], scale) and same(fresh[2], rstd)
+
+
 @pytest.mark.parametrize("pads", [(8, 8, 16, 16, 0), (1, 3, 5, 7, 1), (8, 8, 8, 3, 0), (0, 0, 0, 0, 1)])
 @pytest.mark.parametrize("H", [512, 1001])
 def test_rmsnorm_strides(O, pads, H):
@@ -294,6 +317,13 @@ def test_rmsnorm_backward(O, T, H, fmt, ckpt):
     assert torch.all((dw.cpu().double() - dw0).abs() <= (T + 4) * U32 * wmag + 1e-30)
     again = O.rmsnorm_backward(dy.cuda(), w.cuda(), rstd.cuda(), **kw)
     assert same(dx, again[0]) and same(dw, again[1])
+
+
+@pytest.mark.parametrize("H", [3, 201, 500, 1001, 1201, 2001, 2501, 3001, 4001, 4503, 5003, 6001, 8191])
+@pytest.mark.parametrize("fmt,ckpt", [("bf16", True), ("fp16", False), ("fp32", True), ("fp32", False)])
+def test_rmsnorm_backward_odd_rows(O, H, fmt, ckpt):
+    """Rows that no vector fits, at every number of threads to a row."""
+    test_rmsnorm_backward(O, 330, H, fmt, ckpt)
 
 
 def test_rmsnorm_backward_against_differences(O):
