@@ -12,7 +12,8 @@ constexpr int kPer = 8;                        // elements a thread
 // TX to a thread, so that a thread keeps its columns, their weights and its part of dw.  The
 // next row is copied to shared memory meanwhile, whole units at a time; columns beyond a row are
 // zeros there and need no questions until they are stored.  8191 x 4099 with a residual path: bf16 87
-// us, fp32 88 (elements loaded one by one from memory 121, 134); bound by instruction issue.
+// us, fp32 88 (elements loaded one by one from memory 121, 134); between instruction issue (59 %) and
+// latency.
 template <class T, int TX, bool CKPT>
 struct Single {
   using Dy = Rows<TX, kPer, sizeof(T)>;
