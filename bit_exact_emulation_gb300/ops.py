@@ -22,6 +22,7 @@ from .binding import FMT, McemuError
 ACT8_BLOCK = 128                 # MCEMU_ACT8_BLOCK: elements of a row that share an exponent
 ACT8_NAN = -128                  # MCEMU_ACT8_NAN: exponent of a block that is not finite
 INT32 = 8                        # MCEMU_INT32
+_MOST = 2 ** 31 - 65536          # of any size; ctypes would take a larger one modulo 2^32
 
 _V, _I, _L, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 SYMBOLS = {
@@ -90,6 +91,8 @@ def _matrix(where, name, t, dtypes, dev, shape=None):
     if shape is not None and size != shape:
         _bad(where, f"{name} must have the shape {tuple(shape)}")
     rows, cols = size
+    if rows > _MOST or cols > _MOST:
+        raise McemuError(2, f"{where}: {name} has more than {_MOST} rows or columns")
     ld, one = t.stride()
     if rows <= 1:
         ld = cols
