@@ -174,8 +174,13 @@ int launch_act8_wgrad(const WgradArgs &a, bool direct, void *ws, void *stream) {
   uint8_t *px = panels_in(ws), *pdy = px + p.panel_x;
   float *parts = (float *)(pdy + p.panel_dy);
   widen_kernel<<<(unsigned)(p.blocks_k * p.ttiles), 256, 0, st>>>(a, p.ttiles, rows16(a.q, a.ldq, 1), px);
-  if (!direct) copy_kernel<<<(unsigned)(p.blocks_n * p.ttiles), 256, 0, st>>>(a, p.ttiles, pdy);
-  const int rc = panel::launch<WgradEp, 1, 1>(p.cut, px, a.K, pdy, a.N, direct ? a.dy : nullptr, a.lddy, a.T, p.ttiles,
+  int rc = launch_status();
+  if (rc == MCEMU_OK && !direct) {
+    copy_kernel<<<(unsigned)(p.blocks_n * p.ttiles), 256, 0, st>>>(a, p.ttiles, pdy);
+    rc = launch_status();
+  }
+  if (rc != MCEMU_OK) return rc;              // the panels would be whatever the workspace held
+  rc = panel::launch<WgradEp, 1, 1>(p.cut, px, a.K, pdy, a.N, direct ? a.dy : nullptr, a.lddy, a.T, p.ttiles,
                                               kChunk, WgradEp{a, parts, p.cut.bn}, st);
   if (rc != MCEMU_OK || !p.cut.rest) return rc;
   const panel::Args g{p.ttiles, p.blocks_k / 2, (a.N + p.cut.bn - 1) / p.cut.bn, p.cut.full, p.cut.rest, p.cut.parts,

@@ -132,6 +132,8 @@ int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
   const int64_t tiles = (int64_t)(x.blocks + w.blocks) * kt;
   if (!panel::panel_fits(x.blocks, kt) || !panel::panel_fits(w.blocks, kt)) return MCEMU_ERR_UNSUPPORTED;
   widen_kernel<<<(unsigned)tiles, 256, 0, st>>>(x, w, a.K, kt, wide);
+  const int rc = launch_status();
+  if (rc != MCEMU_OK) return rc;              // the panels would be whatever the workspace held
   return panel::launch<LinearEp<OUT>, 0, 0>(panel::plan_of(a.N, a.M, kt, false), w.to, a.N, x.to, a.M, nullptr, 0, a.K,
                                             kt, 1024 / panel::kTileK, LinearEp<OUT>{a}, st);
 }

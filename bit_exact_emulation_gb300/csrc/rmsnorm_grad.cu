@@ -263,6 +263,8 @@ int grad_typed(const NormGradArgs &a, float *ws, cudaStream_t st) {
   } else {
     float *mean = ws + (int64_t)groups * a.H;
     long_mean_kernel<T, CKPT><<<a.T < 152 * 4 ? a.T : 152 * 4, 512, 0, st>>>(a, mean);
+    const int rc = launch_status();
+    if (rc != MCEMU_OK) return rc;
     long_grad_kernel<T, CKPT><<<dim3((a.H + 255) / 256, groups), 256, 0, st>>>(a, mean, ws);
   }
   if (groups < 0) return MCEMU_ERR_CUDA;
