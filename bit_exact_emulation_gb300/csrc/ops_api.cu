@@ -29,6 +29,13 @@ int check_ws(const void *ws, size_t have, size_t need) {
   return aligned(ws, 16) ? MCEMU_OK : MCEMU_ERR_ALIGNMENT;
 }
 
+// A call's status; a CUDA error that it reports is taken from the runtime, where the next call's
+// question after its own launches would find it.
+int collected(int st) {
+  if (st == MCEMU_ERR_CUDA) cudaGetLastError();
+  return st;
+}
+
 }  // namespace
 
 extern "C" int mcemu_rmsnorm(int fmt, int wfmt, int out_fmt, int T, int H, const void *x, int64_t ldx,
@@ -48,7 +55,7 @@ extern "C" int mcemu_rmsnorm(int fmt, int wfmt, int out_fmt, int T, int H, const
       !aligned(y, bytes_of(out_fmt)) || !aligned(scale, 4) || !aligned(rstd, 4))
     return MCEMU_ERR_ALIGNMENT;
   NormArgs a{T, H, x, res, w, h, y, ldx, ldr, ldh, ldy, scale, rstd, eps, wfmt == MCEMU_FP32, out_fmt};
-  return launch_rmsnorm(fmt, a, stream);
+  return collected(launch_rmsnorm(fmt, a, stream));
 }
 
 extern "C" size_t mcemu_rmsnorm_backward_workspace(int T, int H) {
@@ -66,7 +73,7 @@ extern "C" int mcemu_rmsnorm_backward(int fmt, int wfmt, int T, int H, const voi
   if (too_large(T, H)) return MCEMU_ERR_UNSUPPORTED;
   if (!aligned(dw, 4)) return MCEMU_ERR_ALIGNMENT;
   if (T == 0)
-    return cudaMemsetAsync(dw, 0, (size_t)H * 4, (cudaStream_t)stream) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
+    return collected(cudaMemsetAsync(dw, 0, (size_t)H * 4, (cudaStream_t)stream) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA);
   if (!dy || !w || !dx || !rstd || !q != !e || !h == !q) return MCEMU_ERR_INVALID_ARG;
   if (lddy < H || lddx < H || (dres && lddr < H) || (h && ldh < H) || (q && (ldq < H || lde < blocks_of(H))))
     return MCEMU_ERR_INVALID_ARG;
@@ -77,7 +84,7 @@ extern "C" int mcemu_rmsnorm_backward(int fmt, int wfmt, int T, int H, const voi
   const int st = check_ws(workspace, ws_bytes, rmsnorm_backward_workspace(T, H));
   if (st != MCEMU_OK) return st;
   NormGradArgs a{T, H, dy, dres, h, w, q, e, rstd, dx, dw, lddy, lddr, ldh, ldq, lde, lddx, wfmt == MCEMU_FP32};
-  return launch_rmsnorm_backward(fmt, a, workspace, stream);
+  return collected(launch_rmsnorm_backward(fmt, a, workspace, stream));
 }
 
 extern "C" int mcemu_act8_compress(int fmt, int T, int H, const void *x, int64_t ldx, int8_t *q, int64_t ldq,
@@ -89,7 +96,7 @@ extern "C" int mcemu_act8_compress(int fmt, int T, int H, const void *x, int64_t
   if (T == 0) return MCEMU_OK;
   if (!x || !q || !e || ldx < H || ldq < H || lde < blocks_of(H)) return MCEMU_ERR_INVALID_ARG;
   if (!aligned(x, bytes_of(fmt))) return MCEMU_ERR_ALIGNMENT;
-  return launch_act8_compress(fmt, T, H, x, ldx, q, ldq, e, lde, stream);
+  return collected(launch_act8_compress(fmt, T, H, x, ldx, q, ldq, e, lde, stream));
 }
 
 extern "C" int mcemu_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t ldq, const int8_t *e, int64_t lde,
@@ -101,7 +108,7 @@ extern "C" int mcemu_act8_expand(int fmt, int T, int H, const int8_t *q, int64_t
   if (T == 0) return MCEMU_OK;
   if (!x || !q || !e || ldx < H || ldq < H || lde < blocks_of(H)) return MCEMU_ERR_INVALID_ARG;
   if (!aligned(x, bytes_of(fmt))) return MCEMU_ERR_ALIGNMENT;
-  return launch_act8_expand(fmt, T, H, q, ldq, e, lde, x, ldx, stream);
+  return collected(launch_act8_expand(fmt, T, H, q, ldq, e, lde, x, ldx, stream));
 }
 
 extern "C" size_t mcemu_int8_linear_workspace(int M, int N, int K, int rows_aligned) {
@@ -125,7 +132,7 @@ extern "C" int mcemu_int8_linear(int M, int N, int K, const int8_t *x, int64_t l
   const int st = check_ws(workspace, ws_bytes, mcemu_int8_linear_workspace(M, N, K, rows));
   if (st != MCEMU_OK) return st;
   LinearArgs a{M, N, K, x, w, ldx, ldw, ldy, sx, sw, bias, y, out_fmt};
-  return launch_int8_linear(a, rows, workspace, stream);
+  return collected(launch_int8_linear(a, rows, workspace, stream));
 }
 
 extern "C" size_t mcemu_act8_wgrad_workspace(int T, int N, int K, int dy_rows_aligned) {
@@ -148,13 +155,13 @@ extern "C" int mcemu_act8_wgrad(int T, int N, int K, const uint16_t *dy, int64_t
   const int st = check_ws(workspace, ws_bytes, mcemu_act8_wgrad_workspace(T, N, K, direct));
   if (st != MCEMU_OK) return st;
   WgradArgs a{T, N, K, dy, q, e, lddy, ldq, lde, lddw, dW, out_fmt, accumulate};
-  return launch_act8_wgrad(a, direct, workspace, stream);
+  return collected(launch_act8_wgrad(a, direct, workspace, stream));
 }
 
 extern "C" int mcemu_ops_check(void *stream) {
   unsigned int linear = 0, wgrad = 0;
   if (int8_linear_timeouts((cudaStream_t)stream, &linear) != MCEMU_OK ||
       act8_wgrad_timeouts((cudaStream_t)stream, &wgrad) != MCEMU_OK)
-    return MCEMU_ERR_CUDA;
+    return collected(MCEMU_ERR_CUDA);
   return linear || wgrad ? MCEMU_ERR_TIMEOUT : MCEMU_OK;
 }

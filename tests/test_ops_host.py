@@ -61,7 +61,8 @@ LAUNCHES = {"norm gradients": 2, "norm gradients of odd rows": 2, "norm gradient
 
 @pytest.mark.parametrize("name", CALLS)
 def test_a_launch_that_fails_is_reported(F, name):
-    """Whichever launch of a call fails, that call says so and launches nothing on top of it."""
+    """Whichever launch of a call fails, that call says so, launches nothing on top of it and leaves no
+    error to the calls after it."""
     F.fake_reset(-1)
     assert CALLS[name](F) == OK
     n = F.fake_launches()
@@ -70,3 +71,4 @@ def test_a_launch_that_fails_is_reported(F, name):
         F.fake_reset(k)
         assert CALLS[name](F) == CUDA_ERROR, (k, F.fake_name(k))
         assert F.fake_launches() == k + 1
+        assert F.cudaGetLastError() == 0
