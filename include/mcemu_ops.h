@@ -50,7 +50,11 @@ enum { MCEMU_INT32 = 8 };
  * operations (round to nearest, ties to even, as is the rounding to 8 bits).
  * The norm acts on h as it is stored.  A row that holds a NaN or an infinity
  * (or meets one in w) gets a scale that is not finite, or NaN in y; so does a
- * row of zeros with eps = 0, whose rstd is infinite.
+ * row of zeros with eps = 0, whose rstd is infinite.  Every other row has its
+ * rstd: where the squares or their sum leave fp32's range they are added up
+ * in fp64.  What is left are results that fp32 does not hold: an rstd above
+ * 2^128 is infinite, and so is a v beyond fp32; and 8-bit values of a row
+ * whose v lie below 2^-100 lose digits, to zeros at last.
  * fmt: FP16, BF16 or FP32 (x, res, h); wfmt: fmt or FP32; out_fmt: fmt, INT8,
  * E4M3 or E5M2 (the OCP encodings).  res and h are given together or not at
  * all; h may be x or res (same leading dimension).  scale [T] is required for
