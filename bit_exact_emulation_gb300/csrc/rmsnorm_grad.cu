@@ -125,12 +125,16 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
       get(p, f);
       unpack<T, VEC>(cur.dy[p][t], d);
       weights(p, i, w);
-      // rstd * (g - z * mean) + dres, the factors of f gathered
-      const float k = -(scale[p] * mean * rstd);
+      // rstd * (g - z * mean) + dres, the factors of f in z * mean gathered (with rstd's among them they
+      // would hold its square, which leaves fp32 for rows beyond 10^19 or below 10^-19)
+      const float k = -(scale[p] * mean);
       const float2 k2 = make_float2(k, k), r2 = make_float2(rstd, rstd);
       float2 g[VEC / 2];
 #pragma unroll
-      for (int j = 0; j < VEC; j += 2) g[j / 2] = mul2(make_float2(d[j], d[j + 1]), make_float2(w[j], w[j + 1]));
+      for (int j = 0; j < VEC; j += 2) {
+        g[j / 2] = mul2(make_float2(d[j], d[j + 1]), make_float2(w[j], w[j + 1]));
+        g[j / 2] = fma2(make_float2(f[j], f[j + 1]), k2, g[j / 2]);
+      }
       if (a.dres) {
         unpack<T, VEC>(cur.dr[p][t], d);
 #pragma unroll
@@ -140,11 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
         for (int j = 0; j < VEC; j += 2) g[j / 2] = mul2(g[j / 2], r2);
       }
 #pragma unroll
-      for (int j = 0; j < VEC; j += 2) {
-        const float2 x = fma2(make_float2(f[j], f[j + 1]), k2, g[j / 2]);
-        f[j] = x.x;
-        f[j + 1] = x.y;
-      }
+      for (int j = 0; j < VEC; j += 2) f[j] = g[j / 2].x, f[j + 1] = g[j / 2].y;
       store_vec((T *)a.dx + row * a.lddx + i, pack<T, VEC>(f));
     }
   }

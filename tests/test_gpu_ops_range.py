@@ -1,8 +1,8 @@
-"""The norm over the whole range of their types, against 64 bits."""
+"""The norm and its gradients over the whole range of their types, against 64 bits."""
 import numpy as np
 import pytest
 
-from test_gpu_ops import DT, FP8, O, TOP, U32, UNIT, norm_tol, rows, same  # noqa: F401
+from test_gpu_ops import DT, FP8, O, TOP, U32, UNIT, grad_host, norm_tol, rows, same  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -60,3 +60,27 @@ def test_rmsnorm_rows_beyond_repair(O, H):
     back = (y.cpu().float() * scale.cpu()[:, None])
     assert not torch.isfinite(back[[1, 3, 5]]).any() and torch.isinf(rstd[5]).item()
     assert torch.all((back[[0, 2, 4, 6, 7]] - 1).abs() <= 1e-5)
+
+
+@pytest.mark.parametrize("H", [512, 501, 9001])
+@pytest.mark.parametrize("fmt", ["bf16", "fp32"])
+@pytest.mark.parametrize("ckpt", [True, False])
+@pytest.mark.parametrize("scales", [(1e19, 1e25, 1e30), (1e-20, 1e-25, 1e-28)])
+def test_rmsnorm_backward_of_very_large_and_small_rows(O, H, fmt, ckpt, scales):
+    """No intermediate of dx leaves the range that rstd and dx themselves keep to."""
+    T = 330
+    h = spread(T, H, DT[fmt], scales, H)
+    dy = rows(np.random.default_rng(H), T, H, DT[fmt], 0.1)
+    w = torch.from_numpy((1 + 0.2 * np.random.default_rng(1).standard_normal(H)).astype(np.float32)).to(DT[fmt])
+    if ckpt:
+        q, e = O.act8_compress(h.cuda())
+        h = O.act8_expand(q, e, out="fp32").cpu()
+        kw = {"ckpt": (q, e)}
+    else:
+        kw = {"h": h.cuda()}
+    rstd = (1 / torch.sqrt(h.double().square().mean(1))).float()
+    dx, dw = O.rmsnorm_backward(dy.cuda(), w.cuda(), rstd.cuda(), **kw)
+    dx0, dw0, mag, wmag = grad_host(dy, w, rstd, h, None)
+    chain = max(32, H / 512 + 1) + 21 + 10
+    assert torch.all((dx.cpu().double() - dx0).abs() <= chain * U32 * mag + UNIT[fmt] * dx0.abs() * 1.01 + DENORMAL)
+    assert torch.all((dw.cpu().double() - dw0).abs() <= (T + 4) * U32 * wmag + 1e-30)
