@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(TX) walk_kernel(const NormArgs a) {
   }
 }
 
-// Longer rows: a block to a row, h read a second time.
+// Longer rows: a block of 1024 threads to a row, h read a second time.  A vector's squares are added up
+// on their own, so that no thread adds more than H / 1024 numbers in a row.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_long_kernel(const NormArgs a) {
   __shared__ float2 part[kMaxThreads / 32];
@@ -313,14 +314,15 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_long_kernel(const NormArg
       x = add_vec<T, VEC>(x, load_vec<T, VEC>((const T *)a.res + row * a.ldr + i));
       store_vec((T *)a.h + row * a.ldh + i, x);
     }
-    float w[VEC];
+    float w[VEC], some = 0.f;
     load_w<T, VEC>(a.w, a.w32, i, w);
 #pragma unroll
     for (int j = 0; j < VEC; j++) {
       const float h = to_f(x.v[j]);
-      sum = fmaf(h, h, sum);
+      some = fmaf(h, h, some);
       mx = max_nan(mx, fabsf(h * w[j]));
     }
+    sum += some;
   }
   row_reduce(sum, mx, part);
   const float mul = finish_row<T>(a, row, sum, mx);
@@ -424,8 +426,8 @@ int norm_typed(const NormArgs &a, cudaStream_t st) {
     if (!go_walks<T>(a, st)) return MCEMU_ERR_CUDA;
   }
   else if (a.H <= kMaxThreads * kSingles) go_singles<T>(a, st);
-  else if (wide) rmsnorm_long_kernel<T, V><<<a.T, 512, 0, st>>>(a);
-  else rmsnorm_long_kernel<T, 1><<<a.T, 512, 0, st>>>(a);
+  else if (wide) rmsnorm_long_kernel<T, V><<<a.T, kMaxThreads, 0, st>>>(a);
+  else rmsnorm_long_kernel<T, 1><<<a.T, kMaxThreads, 0, st>>>(a);
   return launch_status();
 }
 
