@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const NormGradArgs a,
 }
 
 // dw[j] = sum over the blocks of parts[block][j]: 32 columns and 32 strands of blocks to a block
-// of threads, the strands joined in order.
+// of threads, the strands joined in a tree of five additions (one after another they cost 31 roundings).
 __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ parts, int groups, int H, float *dw) {
   __shared__ float sh[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
@@ -187,9 +187,14 @@ __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ pa
   sh[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && col < H) {
+    float v[32];
 #pragma unroll
-    for (int i = 1; i < 32; i++) s += sh[i][threadIdx.x];
-    dw[col] = s;
+    for (int i = 0; i < 32; i++) v[i] = sh[i][threadIdx.x];
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < o; i++) v[i] += v[i + o];
+    dw[col] = v[0];
   }
 }
 
