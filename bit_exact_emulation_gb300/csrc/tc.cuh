@@ -7,22 +7,32 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "../../include/mcemu_ops.h"
 
 namespace mcemu {
 namespace tc {
 
-// Set when a wait gave up (one to a translation unit; mcemu_ops_check reads and clears them).
+// Waits that gave up (one count to a translation unit, as is all that touches it: hence static).
 static __device__ unsigned int g_timeouts = 0;
 
-// The flag's value once `st` is done, and 0 in its place.
-inline int take_timeouts(cudaStream_t st, unsigned int *got) {
-  const unsigned int zero = 0;
-  if (cudaMemcpyFromSymbolAsync(got, g_timeouts, sizeof *got, 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-      cudaMemcpyToSymbolAsync(g_timeouts, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
+// How many gave up on the current device, as of the end of `st`, since the last question.  The count
+// only grows, so that one that gives up on another stream meanwhile is there for the next question.
+static inline int take_timeouts(cudaStream_t st, unsigned int *got) {
+  static std::mutex alone;
+  static unsigned int known[64];
+  unsigned int now = 0, none = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) return MCEMU_ERR_CUDA;
+  const std::lock_guard<std::mutex> lock(alone);
+  if (cudaMemcpyFromSymbolAsync(&now, g_timeouts, sizeof now, 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return MCEMU_ERR_CUDA;
-  return cudaStreamSynchronize(st) == cudaSuccess ? MCEMU_OK : MCEMU_ERR_CUDA;
+  unsigned int &last = dev < 64 ? known[dev] : none;
+  *got = now < last ? now : now - last;       // less than before: the device was reset
+  last = now;
+  return MCEMU_OK;
 }
 
 // Tensor map of a row-major matrix of 16-bit elements: `cols` x `rows`, `ld` elements between
@@ -114,23 +124,23 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of `parity` to end.  Gives up after two seconds: `dead` is then set, the
-// flag too, and later waits return at once, so that the kernel runs to its end on what it has.
+// Waits for the phase of `parity` to end.  Gives up after two seconds: `dead` is then set, it is
+// counted, and later waits return at once, so that the kernel runs to its end on what it has.
 __device__ __forceinline__ uint64_t now_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
+static __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = now_ns();
   for (int i = 0; i < 1 << 26; i++) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 63) == 63 && now_ns() - t0 > 2000000000ull) break;
   }
-  atomicExch(&g_timeouts, 1u);
+  atomicAdd(&g_timeouts, 1u);
   return false;
 }
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool &dead) {
+static __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, bool &dead) {
   if (dead) return;
 #pragma unroll 1
   for (int i = 0; i < 64; i++)
@@ -153,7 +163,7 @@ __device__ __forceinline__ void box_load_pair(uint32_t to, const CUtensorMap *ma
 // The same by a whole warp, its verdict known to be common to all lanes: what the issuing warp
 // does with it stays in uniform registers, which is what the matrix instruction reads.  (One lane
 // alone in a branch moves every operand there anew: 120 cycles an instruction.)
-__device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, bool &dead) {
+static __device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, bool &dead) {
   if (dead) return;
 #pragma unroll 1
   for (int i = 0; i < 64; i++)

@@ -11,6 +11,8 @@
 namespace {
 std::map<const void *, std::string> names;
 std::map<const void *, size_t> sizes;
+std::vector<unsigned *> words;                 // symbols of four bytes
+int raise_after = -1;                          // the one that grows by one after the next copy from a symbol
 std::vector<std::string> launched;
 int fail_at = -1, pending = 0;                 // number of the launch that fails; the error not yet collected
 struct Config {
@@ -31,6 +33,11 @@ extern "C" {
 void fake_reset(int fail) { launched.clear(), fail_at = fail, pending = 0; }
 int fake_launches() { return (int)launched.size(); }
 const char *fake_name(int i) { return launched[i].c_str(); }
+int fake_words() { return (int)words.size(); }
+void fake_raise(int i, int after) {
+  if (after) raise_after = i;
+  else ++*words[i];
+}
 
 void **__cudaRegisterFatBinary(void *) { return nullptr; }
 void __cudaRegisterFatBinaryEnd(void **) {}
@@ -38,7 +45,10 @@ void __cudaUnregisterFatBinary(void **) {}
 void __cudaRegisterFunction(void **, const char *host, char *, const char *name, int, uint3 *, uint3 *, dim3 *, dim3 *, int *) {
   names[host] = name;
 }
-void __cudaRegisterVar(void **, char *host, char *, const char *, int, size_t size, int, int) { sizes[host] = size; }
+void __cudaRegisterVar(void **, char *host, char *, const char *, int, size_t size, int, int) {
+  sizes[host] = size;
+  if (size == 4) words.push_back((unsigned *)host);
+}
 unsigned __cudaPushCallConfiguration(dim3 g, dim3 b, size_t smem, cudaStream_t st) {
   config = Config{g, b, smem, st};
   return 0;
@@ -74,6 +84,7 @@ cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
 cudaError_t cudaMemcpyFromSymbolAsync(void *to, const void *sym, size_t n, size_t off, cudaMemcpyKind, cudaStream_t) {
   if (off + n > sizes[sym]) return cudaErrorInvalidValue;
   memcpy(to, (const char *)sym + off, n);
+  if (raise_after >= 0) ++*words[raise_after], raise_after = -1;
   return cudaSuccess;
 }
 cudaError_t cudaMemcpyToSymbolAsync(const void *sym, const void *from, size_t n, size_t off, cudaMemcpyKind, cudaStream_t) {

@@ -12,8 +12,16 @@ from bit_exact_emulation_gb300 import ops
 HERE = os.path.dirname(os.path.abspath(__file__))
 OBJECTS = ["ops_api", "rmsnorm", "rmsnorm_grad", "rmsnorm_grad_single", "act8", "int8_linear", "act8_wgrad"]
 FP16, BF16, XF32, FP32, E4M3, E5M2, INT8, UINT8, INT32 = range(9)
-OK, CUDA_ERROR = 0, 5
+OK, CUDA_ERROR, TIMEOUT = 0, 5, 6
 P = 0x10000                                        # a pointer that is never followed
+
+
+def on_stand_in(objects, folder):
+    so = str(folder / "libfake.so")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B._nvcc()))), "include")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-I", cuda, os.path.join(HERE, "fake_cudart.cpp"),
+                    *objects, "-o", so], check=True)
+    return ctypes.CDLL(so)
 
 
 @pytest.fixture(scope="module")
@@ -21,11 +29,7 @@ def F(tmp_path_factory):
     """The operators' objects as they were built, on the stand-in."""
     objects = [os.path.join(B.HERE, "_build", f + ".o") for f in OBJECTS]
     B.build(force=not all(map(os.path.exists, objects)))
-    so = str(tmp_path_factory.mktemp("fake") / "libfake.so")
-    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B._nvcc()))), "include")
-    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-I", cuda, os.path.join(HERE, "fake_cudart.cpp"),
-                    *objects, "-o", so], check=True)
-    L = ctypes.CDLL(so)
+    L = on_stand_in(objects, tmp_path_factory.mktemp("fake"))
     for name, (res, args) in ops.SYMBOLS.items():
         f = getattr(L, name)
         f.restype, f.argtypes = res, args
@@ -72,3 +76,39 @@ def test_a_launch_that_fails_is_reported(F, name):
         assert CALLS[name](F) == CUDA_ERROR, (k, F.fake_name(k))
         assert F.fake_launches() == k + 1
         assert F.cudaGetLastError() == 0
+
+
+def test_check_reports_each_wait_that_gave_up_once(F):
+    """Of either product's file; also one that gives up on another stream while the call reads."""
+    assert F.fake_words() == 2 and F.mcemu_ops_check(None) == OK
+    for i in (0, 1):
+        F.fake_raise(i, 0)
+        assert F.mcemu_ops_check(None) == TIMEOUT
+        assert F.mcemu_ops_check(None) == OK
+        F.fake_raise(i, 1)                         # grows after the first copy
+        assert TIMEOUT in (F.mcemu_ops_check(None), F.mcemu_ops_check(None))
+        assert F.mcemu_ops_check(None) == OK
+
+
+def test_each_file_has_a_flag_of_its_own(tmp_path):
+    """Without inlining too, where one copy of a function of two files would serve both."""
+    objects = []
+    for name in "ab":
+        src, obj = tmp_path / f"{name}.cu", tmp_path / f"{name}.o"
+        src.write_text(f'#include "{B.CSRC}/tc.cuh"\n'
+                       f'extern "C" int take_{name}(unsigned *got) {{ return mcemu::tc::take_timeouts(nullptr, got); }}\n'
+                       "static __global__ void user(uint32_t bar, bool dead) { mcemu::tc::mbar_wait(bar, 0, dead); }\n")
+        subprocess.run([B._nvcc(), *B.ARCH, "-O0", "-std=c++17", "-Xcompiler", "-fPIC", "-c", str(src), "-o", str(obj)], check=True)
+        objects.append(str(obj))
+    L = on_stand_in(objects, tmp_path)
+    got = ctypes.c_uint()
+
+    def take(f):
+        assert f(ctypes.byref(got)) == OK
+        return got.value
+
+    assert L.fake_words() == 2
+    L.fake_raise(0, 0)
+    seen = [take(L.take_a), take(L.take_b)]
+    L.fake_raise(1, 0)
+    assert [seen, [take(L.take_a), take(L.take_b)]] in ([[1, 0], [0, 1]], [[0, 1], [1, 0]])
