@@ -7,8 +7,9 @@ tensors: argument checks and marshalling only.
 ``rmsnorm_backward`` compute gradients from it.  Matrices are two-dimensional with contiguous
 rows (any row stride).  Calls run on torch's current CUDA stream and return before the work
 finishes.  An argument that does not fit raises ``McemuError`` and nothing runs.  Results and
-workspaces that are not passed in are allocated by torch.  There is no fallback when the
-library is missing.
+workspaces that are not passed in are allocated by torch.  Nothing is recorded for autograd:
+gradients are calls of their own, and a tensor that requires one is refused while torch
+records.  There is no fallback when the library is missing.
 """
 from __future__ import annotations
 
@@ -83,6 +84,13 @@ if hasattr(torch._C, "_cuda_getCurrentRawStream"):       # the same number, 3 us
     _stream = torch._C._cuda_getCurrentRawStream
 
 
+def _recorded(where, name):
+    """What autograd would lose: called for a tensor that requires a gradient."""
+    if torch.is_grad_enabled():
+        _bad(where, f"{name} requires a gradient, which this call does not record: detach it, or call under torch.no_grad() "
+                    f"or from an autograd.Function")
+
+
 def _matrix(where, name, t, dtypes, dev, shape=None):
     """Data pointer and row stride of a matrix on the current device whose rows are contiguous."""
     size = t.shape
@@ -90,6 +98,8 @@ def _matrix(where, name, t, dtypes, dev, shape=None):
         _bad(where, f"{name} must be a 2-D tensor of {' or '.join(map(str, dtypes))} on the current device (cuda:{dev})")
     if shape is not None and size != shape:
         _bad(where, f"{name} must have the shape {tuple(shape)}")
+    if t.requires_grad:
+        _recorded(where, name)
     rows, cols = size
     if rows > _MOST or cols > _MOST:
         raise McemuError(2, f"{where}: {name} has more than {_MOST} rows or columns")
@@ -105,6 +115,8 @@ def _vector(where, name, t, dtypes, dev, n):
     if t.shape != (n,) or t.dtype not in dtypes or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
         _bad(where, f"{name} must be a contiguous vector of {n} {' or '.join(map(str, dtypes))} on the current device "
                     f"(cuda:{dev})")
+    if t.requires_grad:
+        _recorded(where, name)
     return t.data_ptr()
 
 

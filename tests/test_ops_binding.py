@@ -45,3 +45,26 @@ def test_sizes_beyond_32_bits_raise(O, n):
         with pytest.raises(ops.McemuError) as e:
             call()
         assert e.value.status == UNSUPPORTED, i
+
+
+def test_a_gradient_is_not_dropped_silently(O):
+    """The operators record nothing for autograd: a tensor that requires a gradient is refused where one
+    would be recorded, and taken where it would not."""
+    def g(*size, dt=BF16):
+        return z(*size, dt=dt).requires_grad_()
+
+    f = lambda *s: z(*s, dt=F32)
+    i = lambda *s: z(*s, dt=I8)
+    calls = (lambda: O.rmsnorm(g(4, 8), z(8), 1e-5), lambda: O.rmsnorm(z(4, 8), g(8), 1e-5),
+             lambda: O.rmsnorm(z(4, 8), z(8), 1e-5, residual=g(4, 8)), lambda: O.rmsnorm(z(4, 8), z(8), 1e-5, out="own", y=g(4, 8)),
+             lambda: O.rmsnorm_backward(g(4, 8), z(8), f(4), h=z(4, 8)), lambda: O.rmsnorm_backward(z(4, 8), g(8), f(4), h=z(4, 8)),
+             lambda: O.rmsnorm_backward(z(4, 8), z(8), g(4, dt=F32), h=z(4, 8)), lambda: O.rmsnorm_backward(z(4, 8), z(8), f(4), h=g(4, 8)),
+             lambda: O.rmsnorm_backward(z(4, 8), z(8), f(4), h=z(4, 8), dres=g(4, 8)),
+             lambda: O.int8_linear(i(4, 8), g(4, dt=F32), i(5, 8), f(5)), lambda: O.int8_linear(i(4, 8), f(4), i(5, 8), g(5, dt=F32)),
+             lambda: O.int8_linear(i(4, 8), f(4), i(5, 8), f(5), bias=g(5, dt=F32)), lambda: O.act8_compress(g(4, 8)),
+             lambda: O.act8_wgrad(g(4, 8), i(4, 9), i(4, 1)))
+    for n, call in enumerate(calls):
+        with pytest.raises(ops.McemuError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(pytest.fail.Exception, match="was called"):
+            call()
