@@ -7,8 +7,8 @@
 // rounding (every partial sum too, in any order, dropped bits or not).  Every 1024 products the
 // accumulators are therefore taken out and added to int32 sums in registers.
 //
-// Three forms, chosen by form_of() below: few tokens (bound by the weights' bytes), a batch of them
-// (bound by the widening of the weights), many (bound by the matrix unit).
+// Three forms, chosen by form_of() below: few tokens (the weights' bytes are most of the work), a batch
+// of them (bound by the widening of the weights), many (bound by the matrix unit).
 #include "panel.cuh"
 
 namespace mcemu {
@@ -146,7 +146,9 @@ int go_panels(const LinearArgs &a, bool wide, void *ws, cudaStream_t st) {
 // which four is free as long as both operands agree: a lane reads 16 consecutive bytes of
 // its rows and feeds them to four instructions.  One token by 4096 x 4096 weights: 4.7 us (3.5
 // TB/s of weights, launch included), 16 tokens 5.5, 32 tokens 8.0 (there the matrix instructions
-// and the widening of the tokens, done by every block, weigh as much as the loads).
+// and the widening of the tokens, done by every block, weigh as much as the loads).  Weights
+// larger than L2 are no faster, half the memory's rate (16384 x 4096 19.2 us under the profiler): at K =
+// 4096 a warp's share is one round of loads, and a block has none in flight while it works.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
 
@@ -581,8 +583,9 @@ __global__ void __launch_bounds__(Batch<BN, WIDE>::kWorkers + 32, 1) batch_kerne
 
 // Parts of K, one to a block of a cluster (eight at most, the portable limit; two stages each at
 // least), so that the stages that blocks go through one after another are fewest, with four more for
-// each round of clusters after the first.  The clusters that run at a time are what the device
-// reports for blocks that take a multiprocessor each: the larger, the fewer fit.  200 x 1024 x
+// each round of clusters after the first.  The clusters that run at a time are what a GB300
+// of 152 multiprocessors reports for blocks that take one each: the larger, the fewer fit.  (A
+// table, since the form, and with it the workspace's size, is known without a device.)  200 x 1024 x
 // 4096 in six parts 11.5 us, in eight (two rounds) 18.3; 77 x 5003 x 2049 in three 12.8, in two 17.0;
 // 128 x 12288 x 4096 in one 32.8, in four (three rounds) 36.2.
 struct Split {

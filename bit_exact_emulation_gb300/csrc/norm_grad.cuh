@@ -5,8 +5,9 @@
 
 namespace mcemu {
 
-// Most blocks, each of which keeps a part of dw: one to a multiprocessor, more where a block is
-// one group of threads for a short row.
+// Most blocks, each of which keeps a part of dw: one to a multiprocessor of a GB300's 152 (the
+// workspace's size goes by them and is known without a device), more where a block is one group
+// of threads for a short row.
 inline int most_blocks(int T, int H) {
   const int per_sm = H <= 1024 ? 16 : H <= 16384 ? 16384 / H : 1, most = 152 * per_sm;
   return T < most ? T : most;

@@ -236,6 +236,9 @@ inline bool panel_fits(int64_t blocks, int64_t ktiles) { return blocks * ktiles 
 //                            256 rows   128 rows   shared
 //   8192 x 4096 x 4096          182        196       169      (256 rows; 28 tiles of 256 shared)
 //   1024 x 1024 x 1024          13.6       9.9      11.4      (128 rows)
+//
+// The pairs are those of a GB300's 152 multiprocessors: the workspace's size goes by the cut and is
+// known without a device.  A launch has as many as there are.
 constexpr int kPairs = 76;
 struct Plan {
   int bn, full, rest, parts, per_part;

@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(TX < 256 ? 256 : TX) single_kernel(const NormA
 // The same for many rows (two to a multiprocessor at least; fewer are as fast the other way, 300 x 777
 // fp32 2.7 us against 2.9): a block walks over rows, its columns' weights in registers, and copies
 // the next row to shared memory meanwhile in whole units.  Columns beyond a row are zeros there.
-// bf16 with a residual to int8, against one row to a block: 8191 x 5003 75 us, 85; 8191 x 4099 66,
-// 80; 16384 x 1025 39, 49.
+// bf16 with a residual to int8, against one row to a block: 8191 x 5003 71 us, 84; 8191 x 4099 63,
+// 79; 16384 x 1025 34, 47.
 constexpr int kWalk = 8;                      // elements a thread holds
 
 template <class T, int TX, bool RES>
@@ -385,7 +385,8 @@ void go_singles(const NormArgs &a, cudaStream_t st) {
 }
 
 // Steps between powers of two, since columns beyond the row are computed too (16384 x 1025 by 256
-// threads 53 us, by 160 39).
+// threads 49 us, by 160 34).  Others than these were not measured; rows just above 512 and 1280 elements
+// compute the most columns that they do not have (97 and 60 %).
 template <class T, int TX, bool RES>
 bool go_walk(const NormArgs &a, cudaStream_t st) {
   constexpr int kSmem = 2 * (RES ? 2 : 1) * Rows<TX, kWalk, (int)sizeof(T)>::kPitch;

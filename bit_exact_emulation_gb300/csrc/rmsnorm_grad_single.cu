@@ -125,7 +125,8 @@ bool go(const NormGradArgs &a, int blocks, float *parts, cudaStream_t st) {
 }  // namespace
 
 // Threads to a row: several steps between powers of two, since columns beyond the row are computed
-// too (16384 x 1025 bf16 by 256 threads 64 us, by 160 48).
+// too (16384 x 1025 bf16 by 256 threads 64 us, by 160 48).  Others than these were not measured; rows just
+// above 512 and 1280 elements compute the most columns that they do not have (97 and 60 %).
 template <class T, bool CKPT>
 int launch_grad_single(const NormGradArgs &a, int blocks, float *parts, cudaStream_t st) {
   const int threads = (a.H + kPer - 1) / kPer;

@@ -19,7 +19,9 @@
  * with leading dimensions in elements, at least the row length; elements of a
  * row are contiguous.  Element pointers must be aligned to their element
  * (MCEMU_ERR_ALIGNMENT); rows that start on 16-byte boundaries take the widest
- * loads.  Buffers do not overlap unless a function says so.  Sizes are at most
+ * loads, others are read in the aligned units of 16 bytes that hold them, so
+ * that up to 15 bytes before a buffer may be read (and are not used: they lie in
+ * the same allocation).  Buffers do not overlap unless a function says so.  Sizes are at most
  * 2^31 - 65536, and the product's operands what 32 bits count in rows of 64
  * (MCEMU_ERR_UNSUPPORTED).  No result depends on the order in which blocks
  * run: the same call gives the same bits.
