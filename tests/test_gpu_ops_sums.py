@@ -86,3 +86,15 @@ def test_act8_wgrad_of_whole_and_shared_tiles(O, T, N, K, out):
         dW = base.cuda()
         O.act8_wgrad(dy.cuda(), q, e, dW=dW, accumulate=True)
         wgrad_check(dW, dy, xq, out, base)
+
+
+def test_rmsnorm_backward_joins_many_blocks(O):
+    """dw from 2432 rows, a block's each: what a strand of 76 blocks would drop from 1 is kept by four
+    shorter ones.  19 additions in a row, two and five joins, four roundings of a row's part."""
+    T, H = 2432, 263
+    dy = torch.zeros(T, H)
+    dy[::32] = 0.99 * U32
+    dy[0] = 1
+    _, dw = O.rmsnorm_backward(dy.cuda(), torch.ones(H).cuda(), torch.ones(T).cuda(), h=torch.ones(T, H, device="cuda"))
+    want = dy.double().sum(0)
+    assert torch.all((dw.cpu().double() - want).abs() <= 30 * U32 * want)
