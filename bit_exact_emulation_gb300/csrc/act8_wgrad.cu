@@ -2,7 +2,7 @@
 // (include/mcemu_ops.h has the formula).
 //
 // A product of dY^T (N x T) and the checkpoint (T x K) over the tokens, bound by the matrix unit:
-// 8192 x 4096 x 4096 takes 169 us, 15 of them the widening: 1.63 PFLOP/s, 0.85 of the measured bf16
+// 8192 x 4096 x 4096 takes 171 us, 15 of them the widening: 1.61 PFLOP/s, 0.84 of the measured bf16
 // rate.  A code times its power-of-two scale is a bfloat16 number, so the checkpoint is widened
 // once to a bfloat16 panel (3 bytes of traffic an element) and the product is the matrix
 // unit's, with exact operands.  Both operands are read with the tokens outermost as they lie in
@@ -131,10 +131,10 @@ __global__ void __launch_bounds__(256) zero_kernel(const WgradArgs a) {
 }
 
 // 64-token tiles between two drains.  Relative error of 8192 x 4096 x 4096 against 64 bits, for activations
-// with a few large channels (and for normal ones), and time: 4 tiles 1.4e-7 (1.2e-7), 177 us; 16 tiles
-// 4.3e-7 (1.8e-7), 167 us; 64 tiles 2.3e-6 (9.5e-7), 166 us.  A library's fp32 product of the same
-// numbers: 5.1e-7 (2.9e-7).
-constexpr int kChunk = 16;
+// with a few large channels (and for normal ones), and time: 4 tiles 1.4e-7 (1.2e-7), 178 us; 8 tiles
+// 2.0e-7 (1.2e-7), 171 us; 16 tiles 4.3e-7 (1.8e-7), 169 us; 64 tiles 2.3e-6 (9.5e-7), 168 us.  A
+// library's fp32 product of the same numbers: 5.1e-7 (2.9e-7).
+constexpr int kChunk = 8;
 
 struct Layout {
   int ttiles, blocks_k, blocks_n;

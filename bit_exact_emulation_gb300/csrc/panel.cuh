@@ -231,7 +231,7 @@ inline bool panel_fits(int64_t blocks, int64_t ktiles) { return blocks * ktiles 
 // parts of at least eight k tiles that a second kernel joins.  Tiles have 128 rows of B in place of
 // 256 where that ends sooner.  Of the possible cuts the one that an estimate in microseconds
 // prefers: 0.33 a k tile of a round, 0.62 of that with 128 rows, 3 and the traffic of the parts for a
-// join.  Weight gradients, microseconds:
+// join.  Weight gradients (accumulators taken out every 16 tiles), microseconds:
 //
 //                            256 rows   128 rows   shared
 //   8192 x 4096 x 4096          182        196       169      (256 rows; 28 tiles of 256 shared)

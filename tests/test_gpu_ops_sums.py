@@ -98,3 +98,14 @@ def test_rmsnorm_backward_joins_many_blocks(O):
     _, dw = O.rmsnorm_backward(dy.cuda(), torch.ones(H).cuda(), torch.ones(T).cuda(), h=torch.ones(T, H, device="cuda"))
     want = dy.double().sum(0)
     assert torch.all((dw.cpu().double() - want).abs() <= 30 * U32 * want)
+
+
+@pytest.mark.parametrize("N,K", [(64, 128), (300, 200)])
+def test_act8_wgrad_takes_the_accumulators_out(O, N, K):
+    """One product of 2^24 and 1023 of 1/16, sixteen of which the matrix unit's accumulators drop beside it:
+    at most the other 511 tokens' of its 512 are lost, and a step of the result."""
+    T = 1024
+    dy, x = torch.full((T, N), 1 / 16), torch.ones(T, K)
+    dy[0], x[0] = 4096, 4096
+    got = O.act8_wgrad(dy.bfloat16().cuda(), *O.act8_compress(x.cuda()))
+    assert torch.all((got.cpu().double() - (2.0 ** 24 + 1023 / 16)).abs() <= 511 / 16 + 2)
