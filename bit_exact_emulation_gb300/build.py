@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libmcemu.so")
 SOURCES = ["api.cu", "stream.cu", "stream_fp8.cu", "gemm.cu", "gemm_fast.cu", "gemm_fast_sw.cu", "gemm_exact.cu", "sparse.cu", "multiword.cu",
-           "ops_api.cu", "rmsnorm.cu", "rmsnorm_grad.cu", "rmsnorm_grad_single.cu", "act8.cu", "int8_linear.cu", "act8_wgrad.cu"]
+           "ops_api.cu", "rmsnorm.cu", "rmsnorm_grad.cu", "rmsnorm_grad_single.cu", "act8.cu", "int8_linear.cu", "act8_wgrad.cu",
+           "fp8_api.cu", "fp8_quant.cu", "fp8_product.cu", "fp8_pair.cu", "fp8_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(HERE, "..", "include")]
@@ -26,7 +27,7 @@ def _nvcc():
 
 
 def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(HERE, "..", "include", f) for f in ("mcemu.h", "mcemu_ops.h")]
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(HERE, "..", "include", f) for f in ("mcemu.h", "mcemu_ops.h", "mcemu_fp8.h")]
 
 
 def up_to_date() -> bool:

@@ -1,0 +1,231 @@
+// fp8_tc.cuh -- what the FP8 products' kernels share: sm_103a's block-scaled matrix instruction
+// and its operands, exponents on their way to tensor memory, the groups' place in the work.
+//
+// Operands lie in shared memory as rows of 128 codes (one block of a row) in the 128-byte swizzle,
+// 1024 bytes to eight rows, as the copy engine makes them.  The matrix unit multiplies 32 codes of a
+// row at a time and scales the products by two exponents of eight bits (2^(byte - 127), 255: NaN; the
+// stored exponent plus 127) out of tensor memory.  There a 32-bit word holds four bytes of
+// one row, and a column of 32 lanes 32 rows: here the four bytes are four blocks of 128 along k, a
+// chunk, and each matrix instruction names the byte that it takes.  A chunk's exponents of 128 rows lie
+// in shared memory as 32 rows of 16 bytes: word i of row l belongs to the operand's row l + 32 i.
+#pragma once
+#include "fp8.h"
+#include "ops_common.cuh"
+#include "tc.cuh"
+
+namespace mcemu {
+namespace fp8 {
+
+constexpr int kBlock = MCEMU_FP8_BLOCK;
+constexpr int kTileBytes = 128 * kBlock;      // 128 rows of a block
+// Blocks along k between two drains of the accumulators: the matrix unit truncates what it adds up.
+constexpr int kChunk = 4;
+constexpr int kScaleBytes = 512;              // a chunk's exponents of 128 rows
+
+// Tensor map of E row-major matrices of bytes, boxes of 128 columns by `box` rows in the 128-byte swizzle.
+inline int tensor_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t matrices,
+                      uint64_t stride, uint32_t box) {
+  using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<void *> known{nullptr};
+  void *f = known.load();
+  if (!f) {
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess || !f)
+      return MCEMU_ERR_CUDA;
+    known.store(f);
+  }
+  const cuuint64_t dims[3] = {cols, rows, matrices}, strides[2] = {ld, matrices > 1 ? stride : ld};
+  const cuuint32_t boxes[3] = {kBlock, box, 1}, ones[3] = {1, 1, 1};
+  return ((Encode)f)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, boxes, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MCEMU_OK
+             : MCEMU_ERR_CUDA;
+}
+
+// ---- copies and barriers -------------------------------------------------------
+// A box from (x, y, z) on into this CTA's shared memory, its bytes counted on this CTA's barrier.
+__device__ __forceinline__ void box_load(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// The same, counted on the barrier at the same offset in CTA 0 of the pair.
+__device__ __forceinline__ void box_load_pair(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .b32 b;\nmapa.shared::cluster.u32 b, %5, 0;\n"
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [b];\n}" ::"r"(to),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// Arrives on the barrier at the same offset in CTA `rank` of the cluster; what this thread has written is
+// visible to who waits there at cluster scope.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\n"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar),
+      "r"(rank)
+      : "memory");
+}
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// tc::mbar_wait_warp, at cluster scope: a bounded wait by a whole warp.
+static __device__ __forceinline__ void mbar_wait_warp_cluster(uint32_t bar, uint32_t parity, bool &dead) {
+  tc::mbar_wait_warp(bar, parity, dead);
+  if (!dead) (void)mbar_try_cluster(bar, parity);        // the phase is over: this one only orders
+}
+
+// ---- matrix instruction -----------------------------------------------------------
+// Instruction word of kind::mxf8f6f4: fp32 accumulators, E4M3 (0) or E5M2 (1) operands, both K-major,
+// exponents in UE8M0, their bytes 0 of each word.
+__host__ __device__ constexpr uint32_t instruction(int m, int n, int fmt_a, int fmt_b) {
+  return (uint32_t)(fmt_a == MCEMU_E5M2) << 7 | (uint32_t)(fmt_b == MCEMU_E5M2) << 10 | (uint32_t)(n >> 3) << 17 |
+         1u << 23 | (uint32_t)(m >> 4) << 24;
+}
+constexpr uint32_t kNextByte = 1u << 29 | 1u << 4;        // the same with the next byte of both words
+
+// One matrix instruction over 32 of k, by one elected lane of the calling warp (all lanes call).
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t ins, uint32_t scale_a,
+                                    uint32_t scale_b, bool add) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(ins), "r"((uint32_t)add), "r"(scale_a), "r"(scale_b)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|q, 0xFFFFFFFF;\n"
+        "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(ins), "r"((uint32_t)add), "r"(scale_a), "r"(scale_b)
+        : "memory");
+}
+// A chunk's exponents of 128 rows from shared memory to four columns of tensor memory, in both CTAs for
+// CG 2; ordered before the matrix instructions that the same thread issues after it.
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t to, uint32_t from) {
+  // rows of 16 bytes, eight of them 128 bytes from the next eight, no swizzle
+  const uint64_t desc = (uint64_t)((from & 0x3FFFF) >> 4) | 8ull << 16 | 8ull << 32 | 1ull << 46;
+  if constexpr (CG == 1)
+    asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(to),
+                 "l"(desc)
+                 : "memory");
+  else
+    asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(to),
+                 "l"(desc)
+                 : "memory");
+}
+
+// ---- exponents -----------------------------------------------------------------
+// The exponents of blocks kb .. kb + 3 of a row as the matrix unit takes them; 2^0 for rows that the
+// operand has not and blocks from `end` on, whose codes are zeros or whose sums nobody stores.
+__device__ __forceinline__ uint32_t scale_word(const Fp8Operand &o, int matrix, int row, int kb, int end) {
+  if (row >= o.rows) return 0x7F7F7F7Fu;
+  const int8_t *p = o.e + matrix * o.stride_e + (int64_t)(row >> o.tile) * o.lde + kb;
+  uint32_t w = 0;
+  if (((uintptr_t)p & 3) == 0 && kb + 4 <= end) {
+    w = __ldg((const uint32_t *)p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if (kb + j < end) w |= (uint32_t)(uint8_t)__ldg(p + j) << (8 * j);
+  }
+  return __vadd4(w, 0x7F7F7F7Fu);
+}
+// Those of 128 rows from `row` on, by a warp, to shared memory.
+__device__ __forceinline__ void load_scales(const Fp8Operand &o, int matrix, int row, int kb, int end, uint32_t (&w)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; i++) w[i] = scale_word(o, matrix, row + lane + 32 * i, kb, end);
+}
+__device__ __forceinline__ void store_scales(uint32_t to, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (threadIdx.x & 31) * 16), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3])
+               : "memory");
+}
+
+// ---- groups ---------------------------------------------------------------------
+// Where each group's rows (blocks) begin and how many tiles of `tile` rows come before it; by one warp.
+// at[g] .. at[g + 1] are group g's rows, or with by_k its blocks of 128 along k; before[] as many entries.
+// Offsets count as at most T and as no less than the one before.
+__device__ __forceinline__ void place_groups(const Fp8Product &p, int tile, int *at, int *before) {
+  const int lane = threadIdx.x & 31;
+  if (!p.offsets) {
+    if (lane == 0) at[0] = 0, at[1] = p.T, before[0] = 0, before[1] = (p.T + tile - 1) / tile;
+    return;
+  }
+  int most = 0, blocks = 0, tiles = 0;        // of the groups before these 32
+  for (int g0 = 0; g0 <= p.E; g0 += 32) {
+    const int g = g0 + lane;
+    int o = g <= p.E ? min(max(__ldg(p.offsets + g), 0), p.T) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int other = __shfl_up_sync(0xFFFFFFFFu, o, d);
+      if (lane >= d) o = max(o, other);
+    }
+    o = max(o, most);
+    int last = __shfl_up_sync(0xFFFFFFFFu, o, 1);
+    if (lane == 0) last = g0 ? most : o;
+    // what ends at this offset: the group before it
+    int b = g <= p.E ? (o - last + kBlock - 1) / kBlock : 0, t = g <= p.E ? (o - last + tile - 1) / tile : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int ob = __shfl_up_sync(0xFFFFFFFFu, b, d), ot = __shfl_up_sync(0xFFFFFFFFu, t, d);
+      if (lane >= d) b += ob, t += ot;
+    }
+    if (g <= p.E) at[g] = p.by_k ? min(blocks + b, p.T / kBlock) : o, before[g] = tiles + t;
+    most = __shfl_sync(0xFFFFFFFFu, o, 31);
+    blocks += __shfl_sync(0xFFFFFFFFu, b, 31);
+    tiles += __shfl_sync(0xFFFFFFFFu, t, 31);
+  }
+}
+
+// ---- results ---------------------------------------------------------------------
+template <class T>
+__device__ __forceinline__ void put(T *y, float v, int accumulate) {
+  if constexpr (sizeof(T) == 4) *y = accumulate ? *y + v : v;
+  else *y = from_f<T>(v);
+}
+// Sixteen sums along a row of y; `left` columns from there on are in the matrix.
+template <class T>
+__device__ __forceinline__ void put16(T *y, const float *sum, int left, int accumulate) {
+  if (left >= 16 && ((uintptr_t)y & 31) == 0) {
+    uint32_t o[sizeof(T) * 4];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; i++) o[i] = __float_as_uint(accumulate ? y[i] + sum[i] : sum[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float f[2] = {sum[i], sum[i + 1]};
+        const Vec<T, 2> v = pack<T, 2>(f);
+        o[i / 2] = *(const uint32_t *)&v;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) * 4; i += 8)
+      store32((uint32_t *)y + i, make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]),
+              make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+      if (i < left) put(y + i, sum[i], accumulate);
+  }
+}
+
+}  // namespace fp8
+}  // namespace mcemu
