@@ -43,6 +43,33 @@ __device__ __forceinline__ void push(uint32_t to, float v, uint32_t bar) {
                : "memory");
 }
 
+// A warp's way through the units, bringing a chunk's exponents of R * 32 rows of a or b to each slot.
+template <int R, int BT>
+__device__ __forceinline__ void few_scales(const Fp8Product &p, const int *at, const int *before, int tiles_b, int first, int step,
+                                           int units, int k0, int k1, bool of_a, uint32_t scales, uint32_t sf_full,
+                                           uint32_t sf_empty, bool &dead) {
+  using S = Few<BT>;
+  Scales<R> v;
+  uint32_t ch = 0;
+  int g = 0;
+  for (int u = first; u < units && !dead; u += step) {
+    const FewUnit r = few_unit_at(at, before, tiles_b, BT, u, g);
+    if (of_a) v.rows(p.a, 0, r.a);
+    else v.rows(p.b, r.g, r.b);
+    for (int k = k0; k < k1; k += kChunk, ch++) {
+      const uint32_t sf = ch % S::kScaleSlots;
+      uint32_t x[1][4];
+      v.load(0, k, k1, x);
+      tc::mbar_wait_warp(sf_empty + 8 * sf, ((ch / S::kScaleSlots) & 1) ^ 1, dead);
+      if (dead) return;
+      store_scales(scales + sf * S::kSlotBytes, x[0]);
+      tc::fence_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) tc::mbar_arrive(sf_full + 8 * sf);
+    }
+  }
+}
+
 template <class T, int BT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_kernel(const __grid_constant__ Fp8Product p, const __grid_constant__ CUtensorMap ma,
@@ -147,27 +174,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     bool late = false;                        // everything issued ends before the memory is given back
     tc::commit<1>(drain);
     tc::mbar_wait_warp(drain, 0, late);
-  } else if (warp >= 6) {                     // exponents of b's rows, or of a's
-    uint32_t ch = 0;
-    for (int u = first; u < units && !dead; u += step) {
-      const FewUnit r = few_unit_at(at, before, tiles_b, BT, u, g);
-      for (int k = k0; k < k1 && !dead; k += kChunk, ch++) {
-        const uint32_t sf = ch % kSlots, to = scales + sf * S::kSlotBytes;
-        uint32_t v[4] = {0, 0, 0, 0};
-        if (warp == 6) {
-          load_scales(p.b, r.g, r.b, k, k1, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < (BT + 31) / 32; i++) v[i] = scale_word(p.a, 0, r.a + lane + 32 * i, k, k1);
-        }
-        tc::mbar_wait_warp(sf_empty + 8 * sf, ((ch / kSlots) & 1) ^ 1, dead);
-        if (dead) break;
-        store_scales(to + (warp == 6 ? 0 : kScaleBytes), v);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sf_full + 8 * sf);
-      }
-    }
+  } else if (warp == 6) {                     // exponents of b's rows
+    few_scales<4, BT>(p, at, before, tiles_b, first, step, units, k0, k1, false, scales, sf_full, sf_empty, dead);
+  } else if (warp == 7) {                     // of a's
+    few_scales<(BT + 31) / 32, BT>(p, at, before, tiles_b, first, step, units, k0, k1, true, scales + kScaleBytes, sf_full, sf_empty, dead);
   } else {
     const uint32_t mine = tmem + ((uint32_t)warp << 21);
     const int row = warp * 32 + lane;

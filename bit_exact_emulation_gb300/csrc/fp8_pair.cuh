@@ -2,21 +2,30 @@
 //
 // A pair computes tiles of 256 rows of a by BN rows of b: each CTA holds 128 rows of a and half of
 // b's, and 128 x BN accumulators, twice, so that one set is drained into registers while the other fills.
-// The exponents of a chunk (four blocks along k) go to tensor memory with the chunk: for a those of
-// the CTA's own rows, for b those of all BN, in both CTAs.  Tensor memory has 512 columns: two sets of
-// accumulators and two of exponents (4 + 8 columns) leave BN at most 224.
+// The exponents go to tensor memory eight blocks at a time: for a those of the CTA's own rows, for b those
+// of all BN, in both CTAs.  (Four at a time the warps that bring them were the slowest: passing them on to
+// the issuing CTA takes a release at cluster scope, 0.95 us.)  Tensor memory has 512 columns: two sets of accumulators and two
+// of exponents (8 + 16 columns) leave BN at most 224.
 #pragma once
 #include "fp8_tc.cuh"
 
 namespace mcemu {
 namespace fp8 {
 
-constexpr int kPairThreads = 384;             // eight warps drain, then: copies, matrix instructions, exponents of a, of b
+// Eight warps drain; then come one for copies, two that issue matrix instructions, one for the exponents of
+// a, one for each 128 rows of b's, and idle ones.
+constexpr int kPairThreads = 512;
+constexpr int kPairChunk = 8;                 // blocks along k between two drains
+// Registers of the warps that hold sums, and of the others: as many as 128 a thread at launch.
+__device__ __forceinline__ void pair_take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+__device__ __forceinline__ void pair_give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 template <int BN>
 struct Pair {
-  static constexpr int kStageBytes = kTileBytes + BN / 2 * kBlock;
-  static constexpr int kStages = BN > 192 ? 7 : BN > 128 ? 7 : 8;
-  static constexpr int kScaleSlots = 4, kSlotBytes = 3 * kScaleBytes;
+  static constexpr int kBlockBytes = kTileBytes + BN / 2 * kBlock;      // of one block along k
+  static constexpr int kStageBytes = 2 * kBlockBytes;                   // a stage is two
+  static constexpr int kStages = BN > 128 ? 3 : 4;
+  static constexpr int kRowTiles = 1 + (BN + 127) / 128;        // 128 rows of a and of b, whose exponents a CTA holds
+  static constexpr int kScaleSlots = 3, kSlotBytes = 2 * kRowTiles * kScaleBytes;
   static constexpr int kSmem = kStages * kStageBytes + kScaleSlots * kSlotBytes + 1024 + 512 + 2 * 4 * (MCEMU_FP8_MAX_GROUPS + 1);
 };
 
@@ -54,6 +63,98 @@ __device__ __forceinline__ PairUnit unit_at(const Fp8Product &p, const PairGroup
   return r;
 }
 
+// A warp's way through the units, bringing eight blocks' exponents of 128 rows to each slot: of the tile's rows
+// of a, or of b, from `skip` on.
+template <int BN>
+__device__ __forceinline__ void feed_scales(const Fp8Product &p, const PairGroups &w, int first, int step, int units, bool of_a,
+                                            int skip, uint32_t scales, uint32_t sf_full, uint32_t sf_empty, bool &dead) {
+  using S = Pair<BN>;
+  Scales<4> v;
+  uint32_t turn = 0;
+  int g = 0;
+  for (int u = first; u < units && !dead; u += step) {
+    const PairUnit r = unit_at(p, w, BN, u, g);
+    if (of_a) v.rows(p.a, 0, r.a + skip);
+    else v.rows(p.b, p.by_k ? 0 : r.g, r.b + skip);
+    for (int k = r.k0; k < r.k1; k += kPairChunk, turn++) {
+      const uint32_t sf = turn % S::kScaleSlots, to = scales + sf * S::kSlotBytes;
+      uint32_t x[2][4];
+      v.load(0, k, r.k1, x);
+      tc::mbar_wait_warp(sf_empty + 8 * sf, ((turn / S::kScaleSlots) & 1) ^ 1, dead);
+      if (dead) return;
+      store_scales(to, x[0]);
+      store_scales(to + kScaleBytes, x[1]);
+      tc::fence_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive_at(sf_full + 8 * sf, 0);
+    }
+  }
+}
+
+// The units' chunks of `set`'s turn (every other one): waits for their operands and exponents and issues their
+// matrix instructions into that set of accumulators.  By two warps, one to a set: waiting, passing on and issuing
+// cost a warp some 2700 cycles for four blocks, and the matrix unit takes 1800 for them.
+// A stage's barrier tells one use from the next by parity alone, so that a stage may be waited for only when its
+// use before is known to be over: the warps pass a token (`pass`) when the last stage of a chunk has come.
+template <int BN>
+__device__ __forceinline__ void issue(const Fp8Product &p, const PairGroups &w, int first, int step, int units, uint32_t set,
+                                      uint32_t tmem, uint32_t base, uint32_t scales, uint32_t full, uint32_t empty,
+                                      uint32_t sf_full, uint32_t sf_empty, uint32_t acc_full, uint32_t acc_empty,
+                                      uint32_t drain, uint32_t pass, bool &dead) {
+  using S = Pair<BN>;
+  constexpr int kB = S::kRowTiles - 1;
+  const uint32_t ins = instruction(256, BN, p.a.fmt, p.b.fmt), d = tmem + set * 256, sa = d + BN, sb = sa + 8;
+  uint32_t s = 0, phase = 0, ch = 0, parity = 1;
+  int g = 0;
+  for (int u = first; u < units && !dead; u += step) {
+    const PairUnit r = unit_at(p, w, BN, u, g);
+    for (int k = r.k0; k < r.k1 && !dead; k += kPairChunk, ch++) {
+      const int n = min(kPairChunk, r.k1 - k);
+      if ((ch & 1) != set) {
+        for (int i = 0; i < n; i += 2)
+          if (++s == S::kStages) s = 0, phase ^= 1;
+        continue;
+      }
+      const uint32_t sf = ch % S::kScaleSlots, from = scales + sf * S::kSlotBytes;
+      tc::mbar_wait_warp(acc_empty, parity, dead);
+      mbar_wait_warp_cluster(sf_full + 8 * sf, (ch / S::kScaleSlots) & 1, dead);
+      if (dead) break;
+      tc::fence_after();
+      // into the columns of this set's chunk before, whose accumulators have been drained
+#pragma unroll
+      for (int t = 0; t < 2; t++) copy_scales<2>(sa + 4 * t, from + t * kScaleBytes);
+#pragma unroll
+      for (int t = 0; t < 2 * kB; t++)        // b's first four blocks of all its rows, then the other four
+        copy_scales<2>(sb + 4 * ((t & 1) * kB + (t >> 1)), from + (2 + t) * kScaleBytes);
+      tc::commit<2>(sf_empty + 8 * sf);
+      tc::mbar_wait_warp(pass + 8 * set, parity ^ set, dead);     // set 0 begins
+      parity ^= 1;
+      for (int i = 0; i < n; i += 2) {
+        tc::mbar_wait_warp(full + 8 * s, phase, dead);
+        if (dead) break;
+        if (i + 2 >= n && (threadIdx.x & 31) == 0) tc::mbar_arrive(pass + 8 * (set ^ 1));
+        __syncwarp();
+        tc::fence_after();
+        const uint32_t half = i >> 2, fa = sa + 4 * half, fb = sb + 4 * kB * half, word = ins + (i & 3) * kNextByte;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          if (h && i + 1 >= n) break;
+          const uint32_t ta = base + s * S::kStageBytes + h * S::kBlockBytes;
+          const uint64_t da = tc::operand(ta, 16, 1024), db = tc::operand(ta + kTileBytes, 16, 1024);
+#pragma unroll
+          for (int x = 0; x < 4; x++) mma<2>(d, da + 2 * x, db + 2 * x, word + h * kNextByte, fa, fb, (i | h | x) != 0);
+        }
+        tc::commit<2>(empty + 8 * s);
+        if (++s == S::kStages) s = 0, phase ^= 1;
+      }
+      if (!dead) tc::commit<2>(acc_full);
+    }
+  }
+  bool late = false;                          // everything issued ends before the memory is given back
+  tc::commit_here<2>(drain);
+  tc::mbar_wait_warp(drain, 0, late);
+}
+
 template <class T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ Fp8Product p, const __grid_constant__ CUtensorMap ma,
@@ -64,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
   const uint32_t scales = base + kStages * kStageBytes, full = scales + kSlots * S::kSlotBytes, empty = full + 8 * kStages,
                  sf_full = empty + 8 * kStages, sf_empty = sf_full + 8 * kSlots, acc_full = sf_empty + 8 * kSlots,
-                 acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
+                 acc_empty = acc_full + 16, drain = acc_empty + 16, pass = drain + 16, slot = pass + 16;
   int *at = (int *)(raw + (slot + 16 - tc::smem_addr(raw))), *before = at + MCEMU_FP8_MAX_GROUPS + 1;
   const int warp = tc::warp_number(), lane = threadIdx.x & 31;
   const uint32_t rank = tc::cta_rank();
@@ -75,14 +176,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc::mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < kSlots; s++) {
-      tc::mbar_init(sf_full + 8 * s, 4);      // two warps of each CTA, on CTA 0's
+      tc::mbar_init(sf_full + 8 * s, 2 * S::kRowTiles);         // a warp of each CTA for each 128 rows, on CTA 0's
       tc::mbar_init(sf_empty + 8 * s, 1);
     }
     for (int s = 0; s < 2; s++) {
       tc::mbar_init(acc_full + 8 * s, 1);
       tc::mbar_init(acc_empty + 8 * s, 16);
+      tc::mbar_init(drain + 8 * s, 1);
+      tc::mbar_init(pass + 8 * s, 1);
     }
-    tc::mbar_init(drain, 1);
     tc::mbar_init_fence();
   }
   if (warp == 8) tc::tmem_alloc<2>(slot, 512);
@@ -100,19 +202,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1, units = units_of(p, w);
   int g = 0;
 
-  if (warp >= 8) tc::give_registers();
+  if (warp >= 8) pair_give_registers();
   if (warp == 8 && lane == 0) {               // copies this CTA's half of both operands
     uint32_t it = 0;
     for (int u = first; u < units && !dead; u += step) {
       const PairUnit r = unit_at(p, w, BN, u, g);
       const int y = r.a + (int)rank * 128, yb = r.b + (int)rank * (BN / 2), z = p.by_k ? 0 : r.g;
-      for (int k = r.k0; k < r.k1; k++, it++) {
+      for (int k = r.k0; k < r.k1; k += 2, it++) {
         const uint32_t s = it % kStages, to = base + s * kStageBytes;
+        const bool two = k + 1 < r.k1;
         tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, dead);
         if (dead) break;
-        if (rank == 0) tc::mbar_expect(full + 8 * s, 2 * kStageBytes);
+        if (rank == 0) tc::mbar_expect(full + 8 * s, (two ? 4 : 2) * S::kBlockBytes);
         box_load_pair(to, &ma, k * kBlock, y, 0, full + 8 * s);
         box_load_pair(to + kTileBytes, &mb, k * kBlock, yb, z, full + 8 * s);
+        if (two) {
+          box_load_pair(to + S::kBlockBytes, &ma, (k + 1) * kBlock, y, 0, full + 8 * s);
+          box_load_pair(to + S::kBlockBytes + kTileBytes, &mb, (k + 1) * kBlock, yb, z, full + 8 * s);
+        }
       }
     }
     if (rank == 0) {                          // both CTAs' copies end before either leaves
@@ -122,67 +229,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tc::mbar_wait(full + 8 * s, (last / kStages) & 1, late);
       }
     }
-  } else if (warp == 9 && rank == 0) {        // issues the pair's matrix instructions
-    const uint32_t ins = instruction(256, BN, p.a.fmt, p.b.fmt);
-    uint32_t s = 0, phase = 0, ch = 0;
-    for (int u = first; u < units && !dead; u += step) {
-      const PairUnit r = unit_at(p, w, BN, u, g);
-      for (int k = r.k0; k < r.k1 && !dead; k += kChunk, ch++) {
-        const uint32_t set = ch & 1, d = tmem + set * 256, sa = d + BN, sb = sa + 4, sf = ch % kSlots;
-        const uint32_t from = scales + sf * S::kSlotBytes;
-        tc::mbar_wait_warp(acc_empty + 8 * set, ((ch >> 1) & 1) ^ 1, dead);
-        mbar_wait_warp_cluster(sf_full + 8 * sf, (ch / kSlots) & 1, dead);
-        if (dead) break;
-        tc::fence_after();
-        // Into the columns that the chunk before the last used: its accumulators have been drained.
-        copy_scales<2>(sa, from);
-        copy_scales<2>(sb, from + kScaleBytes);
-        if (BN > 128) copy_scales<2>(sb + 4, from + 2 * kScaleBytes);
-        tc::commit<2>(sf_empty + 8 * sf);
-        const int n = min(kChunk, r.k1 - k);
-        uint32_t word = ins;
-        for (int i = 0; i < n; i++, word += kNextByte) {
-          tc::mbar_wait_warp(full + 8 * s, phase, dead);
-          if (dead) break;
-          tc::fence_after();
-          const uint32_t ta = base + s * kStageBytes;
-          const uint64_t da = tc::operand(ta, 16, 1024), db = tc::operand(ta + kTileBytes, 16, 1024);
-#pragma unroll
-          for (int x = 0; x < 4; x++) mma<2>(d, da + 2 * x, db + 2 * x, word, sa, sb, (i | x) != 0);
-          tc::commit<2>(empty + 8 * s);
-          if (++s == kStages) s = 0, phase ^= 1;
-        }
-        tc::commit<2>(acc_full + 8 * set);
-      }
-    }
-    bool late = false;                        // everything issued ends before the memory is given back
-    tc::commit_here<2>(drain);
-    tc::mbar_wait_warp(drain, 0, late);
-  } else if (warp >= 10) {                    // exponents of this CTA's rows of a, or of b's
-    uint32_t ch = 0;
-    for (int u = first; u < units && !dead; u += step) {
-      const PairUnit r = unit_at(p, w, BN, u, g);
-      const int z = p.by_k ? 0 : r.g;
-      for (int k = r.k0; k < r.k1 && !dead; k += kChunk, ch++) {
-        const uint32_t sf = ch % kSlots, to = scales + sf * S::kSlotBytes;
-        uint32_t v[2][4];
-        if (warp == 10) {
-          load_scales(p.a, 0, r.a + (int)rank * 128, k, r.k1, v[0]);
-        } else {
-          load_scales(p.b, z, r.b, k, r.k1, v[0]);
-          if (BN > 128) load_scales(p.b, z, r.b + 128, k, r.k1, v[1]);
-        }
-        tc::mbar_wait_warp(sf_empty + 8 * sf, ((ch / kSlots) & 1) ^ 1, dead);
-        if (dead) break;
-        store_scales(to + (warp == 10 ? 0 : kScaleBytes), v[0]);
-        if (BN > 128 && warp == 11) store_scales(to + 2 * kScaleBytes, v[1]);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(sf_full + 8 * sf, 0);
-      }
-    }
+  } else if (warp == 9 || warp == 10) {
+    const uint32_t set = warp - 9;
+    if (rank == 0)
+      issue<BN>(p, w, first, step, units, set, tmem, base, scales, full, empty, sf_full, sf_empty, acc_full + 8 * set,
+                acc_empty + 8 * set, drain + 8 * set, pass, dead);
+  } else if (warp == 11) {
+    feed_scales<BN>(p, w, first, step, units, true, (int)rank * 128, scales, sf_full, sf_empty, dead);
+  } else if (warp > 11 && warp < 11 + S::kRowTiles) {
+    feed_scales<BN>(p, w, first, step, units, false, (warp - 12) * 128, scales + (warp - 11) * 2 * kScaleBytes, sf_full, sf_empty, dead);
   } else if (warp < 8) {
-    tc::take_registers();
+    pair_take_registers();
     const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * kCols;
     uint32_t ch = 0;
     for (int u = first; u < units; u += step) {
@@ -190,7 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       float sum[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; j++) sum[j] = 0.f;
-      for (int k = r.k0; k < r.k1; k += kChunk, ch++) {
+      for (int k = r.k0; k < r.k1; k += kPairChunk, ch++) {
         const uint32_t set = ch & 1;
         tc::mbar_wait(acc_full + 8 * set, (ch >> 1) & 1, dead);
         __syncwarp();

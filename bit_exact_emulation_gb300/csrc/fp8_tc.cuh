@@ -5,9 +5,9 @@
 // 1024 bytes to eight rows, as the copy engine makes them.  The matrix unit multiplies 32 codes of a
 // row at a time and scales the products by two exponents of eight bits (2^(byte - 127), 255: NaN; the
 // stored exponent plus 127) out of tensor memory.  There a 32-bit word holds four bytes of
-// one row, and a column of 32 lanes 32 rows: here the four bytes are four blocks of 128 along k, a
-// chunk, and each matrix instruction names the byte that it takes.  A chunk's exponents of 128 rows lie
-// in shared memory as 32 rows of 16 bytes: word i of row l belongs to the operand's row l + 32 i.
+// one row, and a column of 32 lanes 32 rows: here the four bytes are four blocks of 128 along k, and
+// each matrix instruction names the byte that it takes.  Four blocks' exponents of 128 rows lie in shared
+// memory as 32 rows of 16 bytes: word i of row l belongs to the operand's row l + 32 i.
 #pragma once
 #include "fp8.h"
 #include "ops_common.cuh"
@@ -20,7 +20,7 @@ constexpr int kBlock = MCEMU_FP8_BLOCK;
 constexpr int kTileBytes = 128 * kBlock;      // 128 rows of a block
 // Blocks along k between two drains of the accumulators: the matrix unit truncates what it adds up.
 constexpr int kChunk = 4;
-constexpr int kScaleBytes = 512;              // a chunk's exponents of 128 rows
+constexpr int kScaleBytes = 512;              // four blocks' exponents of 128 rows
 
 // Tensor map of E row-major matrices of bytes, boxes of 128 columns by `box` rows in the 128-byte swizzle.
 inline int tensor_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t matrices,
@@ -114,7 +114,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         "l"(a), "l"(b), "r"(ins), "r"((uint32_t)add), "r"(scale_a), "r"(scale_b)
         : "memory");
 }
-// A chunk's exponents of 128 rows from shared memory to four columns of tensor memory, in both CTAs for
+// Four blocks' exponents of 128 rows from shared memory to four columns of tensor memory, in both CTAs for
 // CG 2; ordered before the matrix instructions that the same thread issues after it.
 template <int CG>
 __device__ __forceinline__ void copy_scales(uint32_t to, uint32_t from) {
@@ -131,27 +131,49 @@ __device__ __forceinline__ void copy_scales(uint32_t to, uint32_t from) {
 }
 
 // ---- exponents -----------------------------------------------------------------
-// The exponents of blocks kb .. kb + 3 of a row as the matrix unit takes them; 2^0 for rows that the
-// operand has not and blocks from `end` on, whose codes are zeros or whose sums nobody stores.
-__device__ __forceinline__ uint32_t scale_word(const Fp8Operand &o, int matrix, int row, int kb, int end) {
-  if (row >= o.rows) return 0x7F7F7F7Fu;
-  const int8_t *p = o.e + matrix * o.stride_e + (int64_t)(row >> o.tile) * o.lde + kb;
-  uint32_t w = 0;
-  if (((uintptr_t)p & 3) == 0 && kb + 4 <= end) {
-    w = __ldg((const uint32_t *)p);
-  } else {
+// The exponents of rows `first` + lane + 32 i of an operand, on their way from memory to shared memory by a
+// warp.
+template <int R>
+struct Scales {
+  const int8_t *row[R];                       // null: the operand has no such row
+
+  __device__ __forceinline__ void rows(const Fp8Operand &o, int matrix, int first) {
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-      if (kb + j < end) w |= (uint32_t)(uint8_t)__ldg(p + j) << (8 * j);
+    for (int i = 0; i < R; i++) {
+      const int r = first + (int)(threadIdx.x & 31) + 32 * i;
+      row[i] = r < o.rows ? o.e + matrix * o.stride_e + (int64_t)(r >> o.tile) * o.lde : nullptr;
+    }
   }
-  return __vadd4(w, 0x7F7F7F7Fu);
-}
-// Those of 128 rows from `row` on, by a warp, to shared memory.
-__device__ __forceinline__ void load_scales(const Fp8Operand &o, int matrix, int row, int kb, int end, uint32_t (&w)[4]) {
-  const int lane = threadIdx.x & 31;
+  // Those of blocks kb .. kb + 4 W - 1 of rows i0 .. i0 + 3, of which the ones before `end` count, as the matrix
+  // unit takes them: 2^0 for rows that there are not and blocks from `end` on, whose codes are zeros or whose
+  // sums nobody stores.  Read in aligned words, so that up to three bytes beside a row are read and not used.
+  template <int W>
+  __device__ __forceinline__ void load(int i0, int kb, int end, uint32_t (&w)[W][4]) const {
+    uint32_t raw[4][W + 1];
 #pragma unroll
-  for (int i = 0; i < 4; i++) w[i] = scale_word(o, matrix, row + lane + 32 * i, kb, end);
-}
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j <= W; j++) {
+        raw[i][j] = 0;
+        if (i0 + i >= R) continue;
+        const uintptr_t p = (uintptr_t)(row[i0 + i] + kb);
+        if (row[i0 + i] && kb + 4 * j - (int)(p & 3) < end && (j < W || (p & 3)))
+          raw[i][j] = __ldg((const uint32_t *)(p & ~(uintptr_t)3) + j);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < W; j++) {
+        w[j][i] = 0x7F7F7F7Fu;
+        if (i0 + i >= R) continue;
+        uint32_t v = __funnelshift_r(raw[i][j], raw[i][j + 1], 8 * (int)((uintptr_t)(row[i0 + i] + kb) & 3));
+        const int left = end - kb - 4 * j;    // blocks from here on
+        if (left < 4) v = left <= 0 ? 0u : v & 0xFFFFFFFFu >> (32 - 8 * left);
+        if (row[i0 + i]) w[j][i] = __vadd4(v, 0x7F7F7F7Fu);
+      }
+  }
+};
+// Words of rows l, l + 32, l + 64, l + 96 of 128, by lane l, to shared memory.
 __device__ __forceinline__ void store_scales(uint32_t to, const uint32_t (&w)[4]) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (threadIdx.x & 31) * 16), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3])

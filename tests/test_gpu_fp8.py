@@ -263,7 +263,7 @@ def test_quantize_weight(F, shape, fmt, out, pad):
 # ---------------------------------------------------------------------------
 SHAPES = [(1, 1, 1), (1, 128, 128), (2, 5, 33), (3, 17, 130), (16, 4096, 512), (17, 300, 1000), (33, 129, 257), (64, 1000, 2048),
           (77, 5003, 2049), (128, 512, 4096), (129, 513, 640), (300, 500, 1111), (700, 230, 96), (1, 4096, 16384), (513, 1025, 513),
-          (2048, 1000, 300), (1000, 2, 200), (1, 200, 128 * 67), (256, 224, 512), (257, 225, 513)]
+          (2048, 1000, 300), (1000, 2, 200), (1, 200, 128 * 67), (256, 224, 512), (257, 225, 513), (4000, 5000, 2700), (3000, 9000, 1024), (2304, 20000, 130)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -289,7 +289,7 @@ def counts_of(offsets, T):
 
 GROUPED = [(300, [0, 0, 5, 5, 135, 263, 300]), (300, [7, 8, 8, 200, 290]), (5, [0, 1, 2, 2, 5]), (1, [0, 1]), (1000, [0, 1000]),
            (700, [0, 256, 512, 700]), (300, [300, 300, 300]), (300, [20, 10, 400, -5, 290]), (64, list(range(0, 65))),
-           (1500, [0, 3, 1400, 1400, 1500])]
+           (1500, [0, 3, 1400, 1400, 1500]), (9000, [0, 3000, 3001, 6500, 9000])]
 
 
 @pytest.mark.parametrize("T,offsets", GROUPED, ids=str)
