@@ -20,8 +20,8 @@ int go(const Fp8Product &p, const Fp8Plan &plan, const CUtensorMap &ma, const CU
 
 int launch_fp8_few(const Fp8Product &p, const Fp8Plan &plan, void *stream) {
   CUtensorMap ma, mb;
-  int rc = fp8::tensor_map(&ma, p.a.q, p.K, p.a.rows, p.a.ld, 1, 0, plan.width);
-  if (rc == MCEMU_OK) rc = fp8::tensor_map(&mb, p.b.q, p.K, p.b.rows, p.b.ld, p.E, p.b.stride, 128);
+  int rc = fp8::tensor_map(&ma, -1, p.a.q, p.K, p.a.rows, p.a.ld, 1, 0, 128, plan.width);
+  if (rc == MCEMU_OK) rc = fp8::tensor_map(&mb, -1, p.b.q, p.K, p.b.rows, p.b.ld, p.E, p.b.stride, 128, 128);
   if (rc != MCEMU_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
   return p.out_fmt == MCEMU_FP32   ? go<float>(p, plan, ma, mb, st)

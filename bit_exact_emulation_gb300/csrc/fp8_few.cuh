@@ -31,12 +31,7 @@ __device__ __forceinline__ FewUnit few_unit_at(const int *at, const int *before,
   return FewUnit{g, a, min(bt, at[g + 1] - a), t / tiles_a * 128};      // one tile of channels for all tokens, then the next
 }
 
-// Four bytes to this thread's address `addr` in CTA `rank`, counted on the barrier at `bar` there.
-__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
+// Four bytes to `to`, counted on the barrier `bar` there (addresses in the cluster, of the same CTA).
 __device__ __forceinline__ void push(uint32_t to, float v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
                "r"(__float_as_uint(v)), "r"(bar)

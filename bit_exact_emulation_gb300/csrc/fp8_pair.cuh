@@ -12,8 +12,8 @@
 namespace mcemu {
 namespace fp8 {
 
-// Eight warps drain; then come one for copies, two that issue matrix instructions, one for the exponents of
-// a, one for each 128 rows of b's, and idle ones.
+// Eight warps drain; then come one for the copies of a, two that issue matrix instructions, one for the exponents
+// of a, one for each 128 rows of b's, (13 + ...) and the last for the copies of b.
 constexpr int kPairThreads = 512;
 constexpr int kPairChunk = 8;                 // blocks along k between two drains
 // Registers of the warps that hold sums, and of the others: as many as 128 a thread at launch.
@@ -21,12 +21,18 @@ __device__ __forceinline__ void pair_take_registers() { asm volatile("setmaxnreg
 __device__ __forceinline__ void pair_give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
 template <int BN>
 struct Pair {
-  static constexpr int kBlockBytes = kTileBytes + BN / 2 * kBlock;      // of one block along k
-  static constexpr int kStageBytes = 2 * kBlockBytes;                   // a stage is two
-  static constexpr int kStages = BN > 128 ? 3 : 4;
+  // A block along k has a slot, which is free again when its matrix instructions are done; the blocks are passed
+  // on two at a time (a stage), since each wait costs the issuing warp 300 cycles.
+  static constexpr int kBlockBytes = kTileBytes + BN / 2 * kBlock;
+  static constexpr int kStages = BN > 128 ? 3 : 4, kBlocks = 2 * kStages;
   static constexpr int kRowTiles = 1 + (BN + 127) / 128;        // 128 rows of a and of b, whose exponents a CTA holds
   static constexpr int kScaleSlots = 3, kSlotBytes = 2 * kRowTiles * kScaleBytes;
-  static constexpr int kSmem = kStages * kStageBytes + kScaleSlots * kSlotBytes + 1024 + 512 + 2 * 4 * (MCEMU_FP8_MAX_GROUPS + 1);
+  // A warp's place for results on their way out: 32 rows of 112 bytes (64), two pieces of its columns in 16 bits,
+  // four in fp32.  Sixteen-byte stores of a row to a lane meet no bank twice at 112.
+  static constexpr int kPieceBytes = BN == 224 ? 112 : 64, kOutBytes = 8 * 32 * kPieceBytes;
+  static constexpr int kSmem =
+      kBlocks * kBlockBytes + kScaleSlots * kSlotBytes + kOutBytes + 1024 + 512 + 2 * 4 * (MCEMU_FP8_MAX_GROUPS + 1);
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct PairUnit {
@@ -138,13 +144,14 @@ __device__ __forceinline__ void issue(const Fp8Product &p, const PairGroups &w, 
         const uint32_t half = i >> 2, fa = sa + 4 * half, fb = sb + 4 * kB * half, word = ins + (i & 3) * kNextByte;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          if (h && i + 1 >= n) break;
-          const uint32_t ta = base + s * S::kStageBytes + h * S::kBlockBytes;
+          const uint32_t ta = base + (2 * s + h) * S::kBlockBytes;
           const uint64_t da = tc::operand(ta, 16, 1024), db = tc::operand(ta + kTileBytes, 16, 1024);
+          if (i + h < n) {
 #pragma unroll
-          for (int x = 0; x < 4; x++) mma<2>(d, da + 2 * x, db + 2 * x, word + h * kNextByte, fa, fb, (i | h | x) != 0);
+            for (int x = 0; x < 4; x++) mma<2>(d, da + 2 * x, db + 2 * x, word + h * kNextByte, fa, fb, (i | h | x) != 0);
+          }
+          tc::commit<2>(empty + 8 * (2 * s + h));
         }
-        tc::commit<2>(empty + 8 * s);
         if (++s == S::kStages) s = 0, phase ^= 1;
       }
       if (!dead) tc::commit<2>(acc_full);
@@ -158,23 +165,21 @@ __device__ __forceinline__ void issue(const Fp8Product &p, const PairGroups &w, 
 template <class T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ Fp8Product p, const __grid_constant__ CUtensorMap ma,
-                const __grid_constant__ CUtensorMap mb) {
+                const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap my, bool boxes) {
   using S = Pair<BN>;
-  constexpr int kStages = S::kStages, kStageBytes = S::kStageBytes, kSlots = S::kScaleSlots, kCols = BN / 2;
+  constexpr int kStages = S::kStages, kBlocks = S::kBlocks, kSlots = S::kScaleSlots, kCols = BN / 2;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t scales = base + kStages * kStageBytes, full = scales + kSlots * S::kSlotBytes, empty = full + 8 * kStages,
-                 sf_full = empty + 8 * kStages, sf_empty = sf_full + 8 * kSlots, acc_full = sf_empty + 8 * kSlots,
+  const uint32_t scales = base + kBlocks * S::kBlockBytes, out = scales + kSlots * S::kSlotBytes, full = out + S::kOutBytes, empty = full + 8 * kStages,
+                 sf_full = empty + 8 * kBlocks, sf_empty = sf_full + 8 * kSlots, acc_full = sf_empty + 8 * kSlots,
                  acc_empty = acc_full + 16, drain = acc_empty + 16, pass = drain + 16, slot = pass + 16;
   int *at = (int *)(raw + (slot + 16 - tc::smem_addr(raw))), *before = at + MCEMU_FP8_MAX_GROUPS + 1;
   const int warp = tc::warp_number(), lane = threadIdx.x & 31;
   const uint32_t rank = tc::cta_rank();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; s++) {
-      tc::mbar_init(full + 8 * s, 1);
-      tc::mbar_init(empty + 8 * s, 1);
-    }
+    for (int s = 0; s < kStages; s++) tc::mbar_init(full + 8 * s, 1);
+    for (int s = 0; s < kBlocks; s++) tc::mbar_init(empty + 8 * s, 1);
     for (int s = 0; s < kSlots; s++) {
       tc::mbar_init(sf_full + 8 * s, 2 * S::kRowTiles);         // a warp of each CTA for each 128 rows, on CTA 0's
       tc::mbar_init(sf_empty + 8 * s, 1);
@@ -203,30 +208,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   int g = 0;
 
   if (warp >= 8) pair_give_registers();
-  if (warp == 8 && lane == 0) {               // copies this CTA's half of both operands
-    uint32_t it = 0;
+  if (warp == 8 || warp == 15) {              // copies this CTA's half of a, or of b
+    const bool of_a = warp == 8;
+    const CUtensorMap *map = of_a ? &ma : &mb;
+    const uint32_t lead = at_rank(full, 0);
+    uint32_t s = 0, stage = 0, phase = 1, it = 0;
     for (int u = first; u < units && !dead; u += step) {
       const PairUnit r = unit_at(p, w, BN, u, g);
-      const int y = r.a + (int)rank * 128, yb = r.b + (int)rank * (BN / 2), z = p.by_k ? 0 : r.g;
-      for (int k = r.k0; k < r.k1; k += 2, it++) {
-        const uint32_t s = it % kStages, to = base + s * kStageBytes;
-        const bool two = k + 1 < r.k1;
-        tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, dead);
-        if (dead) break;
-        if (rank == 0) tc::mbar_expect(full + 8 * s, (two ? 4 : 2) * S::kBlockBytes);
-        box_load_pair(to, &ma, k * kBlock, y, 0, full + 8 * s);
-        box_load_pair(to + kTileBytes, &mb, k * kBlock, yb, z, full + 8 * s);
-        if (two) {
-          box_load_pair(to + S::kBlockBytes, &ma, (k + 1) * kBlock, y, 0, full + 8 * s);
-          box_load_pair(to + S::kBlockBytes + kTileBytes, &mb, (k + 1) * kBlock, yb, z, full + 8 * s);
+      const int y = of_a ? r.a + (int)rank * 128 : r.b + (int)rank * (BN / 2), z = of_a || p.by_k ? 0 : r.g;
+      for (int k = r.k0; k < r.k1 && !dead; k += 2, it++) {
+        const int n = min(2, r.k1 - k);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          tc::mbar_wait_warp(empty + 8 * (s + h), phase, dead);  // of a block that there is not, too: see issue()
+          if (dead) break;
+          if (h == 0 && of_a && rank == 0 && lane == 0) tc::mbar_expect(full + 8 * stage, n * 2 * S::kBlockBytes);
+          __syncwarp();
+          if (h < n)
+            box_load_pair(base + (s + h) * S::kBlockBytes + (of_a ? 0 : kTileBytes), map, (k + h) * kBlock, y, z, lead + 8 * stage);
         }
+        s += 2;
+        if (++stage == kStages) s = 0, stage = 0, phase ^= 1;
       }
     }
-    if (rank == 0) {                          // both CTAs' copies end before either leaves
+    if (of_a && rank == 0) {                  // all copies end before either CTA leaves
       bool late = false;
-      for (uint32_t s = 0; s < kStages && s < it; s++) {
-        const uint32_t last = it - 1 - (it - 1 - s) % kStages;      // the last use of slot s
-        tc::mbar_wait(full + 8 * s, (last / kStages) & 1, late);
+      for (uint32_t q = 0; q < kStages && q < it; q++) {
+        const uint32_t last = it - 1 - (it - 1 - q) % kStages;        // the last use of stage q
+        tc::mbar_wait_warp(full + 8 * q, (last / kStages) & 1, late);
       }
     }
   } else if (warp == 9 || warp == 10) {
@@ -265,18 +274,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_lead(acc_empty + 8 * set);
       }
-      // the matrix unit has both sets to go on with meanwhile
-      const int row = r.a + (int)rank * 128 + (warp & 3) * 32 + lane, col = r.b + (warp >> 2) * kCols;
-      T *y = (T *)p.y + (p.by_k ? r.g * p.stride_y : 0) + (int64_t)row * p.ldy + col;
+      // Out through shared memory, where the copy engine takes over: the matrix unit has both sets to go on with
+      // for two chunks, and stores by the threads themselves, 32 rows at a time, held them for longer (4300 cycles
+      // a tile, since all CTAs write at once).  What the copy engine cannot write (rows that end a group
+      // amid the warp's, other alignments) leaves by rows.
+      constexpr int kPiece = S::kPieceBytes / sizeof(T), kVec = 16 / sizeof(T);
+      const int row0 = r.a + (int)rank * 128 + (warp & 3) * 32, col0 = r.b + (warp >> 2) * kCols, z = p.by_k ? r.g : 0;
+      const uint32_t place = out + warp * 32 * S::kPieceBytes;
+      const bool whole = boxes && (row0 + 32 <= r.end || r.end == p.a.rows);
       if (p.bias) {
+        if (((uintptr_t)p.bias & 15) == 0 && col0 + kCols <= p.b.rows) {
 #pragma unroll
-        for (int j = 0; j < kCols; j++) sum[j] += col + j < p.b.rows ? __ldg(p.bias + col + j) : 0.f;
+          for (int j = 0; j < kCols; j += 4) {
+            const float4 b = __ldg((const float4 *)(p.bias + col0 + j));
+            sum[j] += b.x, sum[j + 1] += b.y, sum[j + 2] += b.z, sum[j + 3] += b.w;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; j++) sum[j] += col0 + j < p.b.rows ? __ldg(p.bias + col0 + j) : 0.f;
+        }
       }
-      if (row < r.end && !dead) {
+      if (row0 >= r.end || dead) continue;
 #pragma unroll
-        for (int j = 0; j < kCols; j += 16) put16(y + j, &sum[j], p.b.rows - col - j, p.accumulate);
+      for (int j = 0; j < kCols; j += kPiece) {
+        if (col0 + j >= p.b.rows) break;
+        if (lane == 0) boxes_left();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPiece; i += kVec) {
+          const uint4 v = pack16<T>(&sum[j + i]);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place + lane * S::kPieceBytes + i * (int)sizeof(T)), "r"(v.x),
+                       "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        if (whole) {
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) box_store(&my, place, col0 + j, row0, z, p.accumulate);
+        } else {
+          __syncwarp();
+          const T *from = (const T *)(raw + (place - tc::smem_addr(raw)));
+          T *y = (T *)p.y + z * p.stride_y + (int64_t)row0 * p.ldy + col0 + j;
+          const int rows = min(32, r.end - row0), cols = min(kPiece, p.b.rows - col0 - j);
+          if (boxes && cols == kPiece && !p.accumulate) {
+#pragma unroll
+            for (int t = lane; t < kPiece / kVec * 32; t += 32) {
+              const int i = t / (kPiece / kVec), c = t % (kPiece / kVec) * kVec;
+              if (i < rows) *(uint4 *)(y + i * p.ldy + c) = *(const uint4 *)(from + i * kPiece + c);
+            }
+          } else {
+#pragma unroll 8
+            for (int i = 0; i < rows; i++)
+#pragma unroll
+              for (int c = lane; c < kPiece; c += 32)
+                if (c < cols) put_as(y + i * p.ldy + c, from[i * kPiece + c], p.accumulate);
+          }
+        }
       }
     }
+    if (lane == 0) boxes_written();
   }
   __syncwarp();
   tc::fence_before();
@@ -289,9 +345,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 template <class T, int BN>
 int launch_pair(const Fp8Product &p, const CUtensorMap &ma, const CUtensorMap &mb, int64_t units, cudaStream_t st) {
+  constexpr int kSize = sizeof(T);
+  const bool boxes = rows16(p.y, p.ldy, kSize) && (!p.by_k || p.E == 1 || p.stride_y * kSize % 16 == 0);
+  CUtensorMap my = ma;
+  if (boxes) {
+    const int rc = tensor_map(&my, p.out_fmt, p.y, p.b.rows, p.a.rows, p.ldy, p.by_k ? p.E : 1, p.stride_y,
+                              Pair<BN>::kPieceBytes / kSize, 32);
+    if (rc != MCEMU_OK) return rc;
+  }
   if (!allow_smem<pair_kernel<T, BN>>(Pair<BN>::kSmem)) return MCEMU_ERR_CUDA;
   const int pairs = units < sm_count() / 2 ? (int)units : sm_count() / 2;
-  return launch_early(pair_kernel<T, BN>, dim3(2 * pairs), dim3(kPairThreads), Pair<BN>::kSmem, st, p, ma, mb);
+  return launch_early(pair_kernel<T, BN>, dim3(2 * pairs), dim3(kPairThreads), Pair<BN>::kSmem, st, p, ma, mb, my, boxes);
 }
 
 }  // namespace fp8

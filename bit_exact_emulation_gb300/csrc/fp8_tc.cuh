@@ -22,9 +22,10 @@ constexpr int kTileBytes = 128 * kBlock;      // 128 rows of a block
 constexpr int kChunk = 4;
 constexpr int kScaleBytes = 512;              // four blocks' exponents of 128 rows
 
-// Tensor map of E row-major matrices of bytes, boxes of 128 columns by `box` rows in the 128-byte swizzle.
-inline int tensor_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t matrices,
-                      uint64_t stride, uint32_t box) {
+// Tensor map of row-major matrices, boxes of `wide` columns by `high` rows; of codes (fmt < 0) in the 128-byte
+// swizzle, of results plainly.
+inline int tensor_map(CUtensorMap *map, int fmt, const void *base, uint64_t cols, uint64_t rows, uint64_t ld,
+                      uint64_t matrices, uint64_t stride, uint32_t wide, uint32_t high) {
   using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -37,10 +38,15 @@ inline int tensor_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_
       return MCEMU_ERR_CUDA;
     known.store(f);
   }
-  const cuuint64_t dims[3] = {cols, rows, matrices}, strides[2] = {ld, matrices > 1 ? stride : ld};
-  const cuuint32_t boxes[3] = {kBlock, box, 1}, ones[3] = {1, 1, 1};
-  return ((Encode)f)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, boxes, ones,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const int size = fmt < 0 ? 1 : fmt == MCEMU_FP32 ? 4 : 2;
+  const CUtensorMapDataType type = fmt < 0             ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : fmt == MCEMU_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : fmt == MCEMU_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t dims[3] = {cols, rows, matrices}, strides[2] = {ld * size, (matrices > 1 ? stride : ld) * size};
+  const cuuint32_t boxes[3] = {wide, high, 1}, ones[3] = {1, 1, 1};
+  return ((Encode)f)(map, type, 3, const_cast<void *>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     fmt < 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? MCEMU_OK
              : MCEMU_ERR_CUDA;
@@ -54,15 +60,38 @@ __device__ __forceinline__ void box_load(uint32_t to, const CUtensorMap *map, in
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// The same, counted on the barrier at the same offset in CTA 0 of the pair.
+// The same by one elected lane of the calling warp (all lanes call), for an instruction that spans a pair of
+// CTAs: counted on `bar`, an address in the cluster (at_rank).  A lane alone in a branch takes twice as long, 130 cycles.
 __device__ __forceinline__ void box_load_pair(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "{\n.reg .b32 b;\nmapa.shared::cluster.u32 b, %5, 0;\n"
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-      "%4}], [b];\n}" ::"r"(to),
+      "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];\n}" ::"r"(to),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// This CTA's shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+// A box of shared memory to global memory, or added to what is there (fp32); by one thread, which also counts
+// them in groups.  What lies outside the tensor is not written.
+__device__ __forceinline__ void box_store(const CUtensorMap *map, uint32_t from, int x, int y, int z, bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(z), "r"(from)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(from)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until all of the calling thread's boxes have left shared memory, or are written.
+__device__ __forceinline__ void boxes_left() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void boxes_written() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Arrives on the barrier at the same offset in CTA `rank` of the cluster; what this thread has written is
 // visible to who waits there at cluster scope.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank) {
@@ -222,31 +251,28 @@ __device__ __forceinline__ void put(T *y, float v, int accumulate) {
   if constexpr (sizeof(T) == 4) *y = accumulate ? *y + v : v;
   else *y = from_f<T>(v);
 }
-// Sixteen sums along a row of y; `left` columns from there on are in the matrix.
+// The same for a result that has its type already.
 template <class T>
-__device__ __forceinline__ void put16(T *y, const float *sum, int left, int accumulate) {
-  if (left >= 16 && ((uintptr_t)y & 31) == 0) {
-    uint32_t o[sizeof(T) * 4];
-    if constexpr (sizeof(T) == 4) {
+__device__ __forceinline__ void put_as(T *y, T v, int accumulate) {
+  if constexpr (sizeof(T) == 4) *y = accumulate ? *y + v : v;
+  else *y = v;
+}
+// Eight sums, or four of fp32, as they lie in memory.
+template <class T>
+__device__ __forceinline__ uint4 pack16(const float *sum) {
+  uint32_t o[4];
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 16; i++) o[i] = __float_as_uint(accumulate ? y[i] + sum[i] : sum[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float f[2] = {sum[i], sum[i + 1]};
-        const Vec<T, 2> v = pack<T, 2>(f);
-        o[i / 2] = *(const uint32_t *)&v;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) * 4; i += 8)
-      store32((uint32_t *)y + i, make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]),
-              make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]));
+    for (int i = 0; i < 4; i++) o[i] = __float_as_uint(sum[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; i++)
-      if (i < left) put(y + i, sum[i], accumulate);
+    for (int i = 0; i < 4; i++) {
+      const float f[2] = {sum[2 * i], sum[2 * i + 1]};
+      const Vec<T, 2> v = pack<T, 2>(f);
+      o[i] = *(const uint32_t *)&v;
+    }
   }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace fp8
