@@ -41,34 +41,69 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return codes2<F>(a, b) | codes2<F>(c, d) << 16;
 }
 
-// Largest magnitude, a NaN kept.
-template <class T, int V>
-__device__ __forceinline__ float amax_of(const Vec<T, V> &x) {
-  float f[V];
-  unpack<T, V>(x, f);
-  float m = fabsf(f[0]);
-#pragma unroll
-  for (int i = 1; i < V; i++) m = max_nan(m, fabsf(f[i]));
+// ---- eight elements of a row --------------------------------------------------------
+// Magnitudes are compared as whole numbers, which orders them as numbers, a NaN above all; 16-bit types two at a
+// time.  A `Peak` is the largest magnitude so far: two halves of a register, or fp32's bits.
+template <class T>
+__device__ __forceinline__ uint32_t peak_of(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 2) return __vmaxu2(a, b);
+  else return max(a, b);
+}
+template <class T, int I>
+__device__ __forceinline__ uint32_t magnitudes(const Vec<T, 8> &x) {           // of word I
+  return ((const uint32_t *)&x)[I] & (sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+}
+template <class T>
+__device__ __forceinline__ uint32_t row_peak(const Vec<T, 8> &x) {
+  uint32_t m = peak_of<T>(peak_of<T>(magnitudes<T, 0>(x), magnitudes<T, 1>(x)), peak_of<T>(magnitudes<T, 2>(x), magnitudes<T, 3>(x)));
+  if constexpr (sizeof(T) == 4)
+    m = max(m, max(max(magnitudes<T, 4>(x), magnitudes<T, 5>(x)), max(magnitudes<T, 6>(x), magnitudes<T, 7>(x))));
   return m;
 }
-
-// V elements of a row from column c on, zeros beyond H.
-template <class T, int V>
-__device__ __forceinline__ Vec<T, V> some(const T *row, int c, int H, bool wide) {
-  Vec<T, V> r;
-  constexpr int kEach = 16 / sizeof(T);
-  if (wide && c + V <= H) {
-#pragma unroll
-    for (int i = 0; i < V; i += kEach) *(uint4 *)&r.v[i] = __ldg((const uint4 *)(row + c + i));
+// A magnitude in the low half (or all) of a word.
+template <class T>
+__device__ __forceinline__ float magnitude(uint32_t m) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(m);
+  else if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)m));
+  else return __uint_as_float(m << 16);
+}
+template <class T>
+__device__ __forceinline__ float whole_peak(uint32_t m) {
+  if constexpr (sizeof(T) == 2) m = max(m & 0xFFFFu, m >> 16);
+  return magnitude<T>(m);
+}
+// Element i.
+template <class T, int I>
+__device__ __forceinline__ float element(const Vec<T, 8> &x) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const uint32_t w = ((const uint32_t *)&x)[I / 2];
+    return __uint_as_float(I & 1 ? w & 0xFFFF0000u : w << 16);
   } else {
-#pragma unroll
-    for (int i = 0; i < V; i++) r.v[i] = c + i < H ? row[c + i] : from_f<T>(0.f);
+    return to_f(x.v[I]);
   }
+}
+// Codes of the eight elements, all scaled by s.
+template <class T, class F>
+__device__ __forceinline__ uint2 row_codes(const Vec<T, 8> &x, float s) {
+  const float2 ss = make_float2(s, s);
+  float f[8];
+  unpack<T, 8>(x, f);
+  const float2 a = mul2(make_float2(f[0], f[1]), ss), b = mul2(make_float2(f[2], f[3]), ss);
+  const float2 c = mul2(make_float2(f[4], f[5]), ss), d = mul2(make_float2(f[6], f[7]), ss);
+  return make_uint2(codes4<F>(a.x, a.y, b.x, b.y), codes4<F>(c.x, c.y, d.x, d.y));
+}
+
+// Eight elements of a row from column c on, zeros beyond H, at any alignment.
+template <class T>
+__device__ __forceinline__ Vec<T, 8> load8_any(const T *row, int c, int H) {
+  Vec<T, 8> r;
+#pragma unroll
+  for (int i = 0; i < 8; i++) r.v[i] = c + i < H ? row[c + i] : from_f<T>(0.f);
   return r;
 }
 // Eight bytes of a row from column c on, `left` of them in it.
-__device__ __forceinline__ void put8(uint8_t *row, int c, int left, uint2 v, bool wide) {
-  if (wide && left >= 8) {
+__device__ __forceinline__ void put8_any(uint8_t *row, int c, int left, uint2 v) {
+  if (left >= 8 && ((uintptr_t)(row + c) & 7) == 0) {
     *(uint2 *)(row + c) = v;
   } else {
 #pragma unroll
@@ -77,81 +112,127 @@ __device__ __forceinline__ void put8(uint8_t *row, int c, int left, uint2 v, boo
   }
 }
 
+// A kernel's WIDE form takes rows of whole vectors, on 16-byte boundaries in x, 8 in q and 16 in qt; the
+// other one any.
+template <class T, bool WIDE>
+__device__ __forceinline__ Vec<T, 8> load8(const T *row, int c, int H) {
+  if constexpr (!WIDE) return load8_any<T>(row, c, H);
+  Vec<T, 8> r = {};
+  if (c < H) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 16 / (int)sizeof(T)) *(uint4 *)&r.v[i] = __ldg((const uint4 *)(row + c + i));
+  }
+  return r;
+}
+template <bool WIDE>
+__device__ __forceinline__ void put8(uint8_t *row, int c, int left, uint2 v) {
+  if constexpr (WIDE) {
+    if (left > 0) *(uint2 *)(row + c) = v;
+  } else {
+    put8_any(row, c, left, v);
+  }
+}
+
 // ---- rows alone -------------------------------------------------------------------
-// Sixteen lanes to a block of a row, eight elements each; kRows rows a thread.
-constexpr int kRows = 2;
-template <class T, class F>
-__global__ void __launch_bounds__(256) rows_kernel(const QuantArgs a, int64_t tasks, int blocks, bool wide_in, bool wide_out) {
+// Sixteen lanes to a block of a row, eight elements each, kRows rows a thread; a block of threads takes `wide`
+// (1 to 16) blocks of 16 / wide * kRows rows.
+constexpr int kRows = 4;
+template <class T, class F, bool WIDE>
+__global__ void __launch_bounds__(256) rows_kernel(const QuantArgs a, int blocks, int wide) {
   grid_go();
-  const int lane = threadIdx.x & 15;
-  const int64_t task0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * kRows;
+  const int lane = threadIdx.x & 15, at = threadIdx.x >> 4, high = 16 / wide;
+  const int block = (int)((blockIdx.y + blockIdx.z * gridDim.y) * wide) + at % wide, c = block * kBlock + 8 * lane;
+  const int64_t row0 = (int64_t)blockIdx.x * (high * kRows) + at / wide;
+  const T *x = (const T *)a.x + row0 * a.ldx;
   Vec<T, 8> v[kRows];
+  uint32_t m[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; i++) {
-    const int64_t task = task0 + i;
-    if (task >= tasks) continue;
-    const int64_t row = task / blocks;
-    v[i] = some<T, 8>((const T *)a.x + row * a.ldx, (int)(task - row * blocks) * kBlock + 8 * lane, a.H, wide_in);
+    if (row0 + i * high < a.T && block < blocks) {
+      v[i] = load8<T, WIDE>(x + i * high * a.ldx, c, a.H);
+    } else {
+      v[i] = Vec<T, 8>{};
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kRows; i++) {
-    const int64_t task = task0 + i;
-    const int64_t row = task / blocks;
-    const int block = (int)(task - row * blocks), c = block * kBlock + 8 * lane;
-    float amax = task < tasks ? amax_of<T, 8>(v[i]) : 0.f;
+  for (int i = 0; i < kRows; i++) m[i] = row_peak<T>(v[i]);
+  if constexpr (sizeof(T) == 2) {             // two rows to a word
 #pragma unroll
-    for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if (task >= tasks) continue;
-    const int e = exponent_of<F::kTop>(amax);
-    const float s = inverse_of(e);
-    float f[8];
-    unpack<T, 8>(v[i], f);
-    put8(a.q + row * a.ldq, c, a.H - c,
-         make_uint2(codes4<F>(f[0] * s, f[1] * s, f[2] * s, f[3] * s), codes4<F>(f[4] * s, f[5] * s, f[6] * s, f[7] * s)), wide_out);
-    if (lane == 0) a.e[row * a.lde + block] = (int8_t)e;
+    for (int i = 0; i < kRows; i += 2) {
+      uint32_t w = __vmaxu2(__byte_perm(m[i], m[i + 1], 0x5410), __byte_perm(m[i], m[i + 1], 0x7632));
+#pragma unroll
+      for (int o = 8; o; o >>= 1) w = __vmaxu2(w, __shfl_xor_sync(0xFFFFFFFFu, w, o));
+      m[i] = w & 0xFFFFu, m[i + 1] = w >> 16;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; i++)
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m[i] = max(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+  }
+  uint8_t *q = a.q + row0 * a.ldq;
+  int8_t *e = a.e + row0 * a.lde + block;
+#pragma unroll
+  for (int i = 0; i < kRows; i++) {
+    if (row0 + i * high >= a.T || block >= blocks) break;
+    const int ex = exponent_of<F::kTop>(magnitude<T>(m[i]));
+    put8<WIDE>(q + i * high * a.ldq, c, a.H - c, row_codes<T, F>(v[i], inverse_of(ex)));
+    if (lane == 0) e[i * high * a.lde] = (int8_t)ex;
   }
 }
 
 // ---- tiles of 128 x 128 -------------------------------------------------------------
 // A tile in the registers of 256 threads: thread (tx, ty) = (t & 15, t >> 4) holds columns 8 tx .. + 7 of
 // rows 8 ty .. + 7, so that its codes of a column are eight bytes of the transposed matrix.  They go
-// through shared memory, 128 bytes a column, units of eight exchanged so that neither side
-// meets a bank twice.
-template <class T>
-__device__ __forceinline__ void load_tile(Vec<T, 8> (&v)[8], const T *x, int64_t ld, int rows, int c, int H, bool wide) {
-  const int ty = threadIdx.x >> 4;
+// through shared memory, 128 bytes a column, eight-byte units exchanged by the column so that neither side meets a bank twice.
+template <class T, bool WIDE>
+__device__ __forceinline__ void load_tile(Vec<T, 8> (&v)[8], const T *x, int64_t ld, int rows, int c, int H) {
+  const int r0 = 8 * (threadIdx.x >> 4);
+  x += r0 * ld;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const int r = 8 * ty + i;
-    if (r < rows) {
-      v[i] = some<T, 8>(x + r * ld, c, H, wide);
+    if (r0 + i < rows) {
+      v[i] = load8<T, WIDE>(x + i * ld, c, H);
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; j++) v[i].v[j] = from_f<T>(0.f);
+      v[i] = Vec<T, 8>{};
     }
   }
 }
-// The codes of a thread's eight columns, column j scaled by s[j], to shared memory.
+// Column j's codes of the thread's eight rows, scaled by s.
+template <class T, class F, int J>
+__device__ __forceinline__ void turn_column(const Vec<T, 8> (&v)[8], float s, uint2 *turned) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float2 ss = make_float2(s, s);
+  const float2 a = mul2(make_float2(element<T, J>(v[0]), element<T, J>(v[1])), ss), b = mul2(make_float2(element<T, J>(v[2]), element<T, J>(v[3])), ss);
+  const float2 c = mul2(make_float2(element<T, J>(v[4]), element<T, J>(v[5])), ss), d = mul2(make_float2(element<T, J>(v[6]), element<T, J>(v[7])), ss);
+  turned[(8 * tx + J) * 16 + (ty ^ ((tx & 7) << 1) ^ (tx >> 3))] = make_uint2(codes4<F>(a.x, a.y, b.x, b.y), codes4<F>(c.x, c.y, d.x, d.y));
+}
 template <class T, class F>
 __device__ __forceinline__ void turn_tile(const Vec<T, 8> (&v)[8], const float (&s)[8], uint2 *turned) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float f[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; i++) unpack<T, 8>(v[i], f[i]);
-#pragma unroll
-  for (int j = 0; j < 8; j++)
-    turned[(8 * tx + j) * 16 + (ty ^ tx)] =
-        make_uint2(codes4<F>(f[0][j] * s[j], f[1][j] * s[j], f[2][j] * s[j], f[3][j] * s[j]),
-                   codes4<F>(f[4][j] * s[j], f[5][j] * s[j], f[6][j] * s[j], f[7][j] * s[j]));
+  turn_column<T, F, 0>(v, s[0], turned), turn_column<T, F, 1>(v, s[1], turned);
+  turn_column<T, F, 2>(v, s[2], turned), turn_column<T, F, 3>(v, s[3], turned);
+  turn_column<T, F, 4>(v, s[4], turned), turn_column<T, F, 5>(v, s[5], turned);
+  turn_column<T, F, 6>(v, s[6], turned), turn_column<T, F, 7>(v, s[7], turned);
 }
-// And from there to `columns` rows of the transposed matrix, `left` bytes each at most.
-__device__ __forceinline__ void put_turned(const uint2 *turned, uint8_t *to, int64_t ld, int columns, int left, bool wide) {
-  const int unit = threadIdx.x & 15;
+// And from there to `columns` rows of the transposed matrix, `left` bytes each at most: sixteen a thread, four times.
+template <bool WIDE>
+__device__ __forceinline__ void put_turned(const uint2 *turned, uint8_t *to, int64_t ld, int columns, int left) {
+  const int unit = threadIdx.x & 7, c0 = threadIdx.x >> 3;
+  to += c0 * ld + 16 * unit;
+  left -= 16 * unit;
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const int c = (threadIdx.x >> 4) + 16 * i;
-    if (c < columns && 8 * unit < left)
-      put8(to + c * ld, 8 * unit, left - 8 * unit, turned[c * 16 + (unit ^ (c >> 3))], wide);
+  for (int i = 0; i < 4; i++) {
+    const int c = c0 + 32 * i, tx = c >> 3;
+    if (c >= columns || left <= 0) break;
+    const uint4 w = *(const uint4 *)(turned + c * 16 + 2 * (unit ^ (tx & 7)));
+    const uint4 v = tx & 8 ? make_uint4(w.z, w.w, w.x, w.y) : w;
+    uint8_t *p = to + 32 * i * ld;
+    if (left >= 16 && (WIDE || ((uintptr_t)p & 15) == 0)) {
+      *(uint4 *)p = v;
+    } else {
+      put8_any(p, 0, left, make_uint2(v.x, v.y));
+      put8_any(p, 8, left - 8, make_uint2(v.z, v.w));
+    }
   }
 }
 
@@ -203,155 +284,180 @@ __device__ __forceinline__ Place place_of(const QuantArgs &a, int block) {
   return r;
 }
 
-// Codes and exponents of the rows that a tile's threads hold.
-template <class T, class F>
-__device__ __forceinline__ void put_rows(const QuantArgs &a, const Vec<T, 8> (&v)[8], int row, int rows, int block, bool wide) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c = block * kBlock + 8 * tx;
+// Codes and exponents of the rows that a tile's threads hold: sixteen lanes have eight rows, and lane i makes the
+// i-th one's exponent for all.
+template <class T, class F, bool WIDE>
+__device__ __forceinline__ void put_rows(const QuantArgs &a, const Vec<T, 8> (&v)[8], int row, int rows, int block) {
+  const int tx = threadIdx.x & 15, r0 = 8 * (threadIdx.x >> 4), c = block * kBlock + 8 * tx;
+  uint32_t m[8], mine;
+#pragma unroll
+  for (int i = 0; i < 8; i++) m[i] = row_peak<T>(v[i]);
+  if constexpr (sizeof(T) == 2) {             // two rows to a word
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      m[i] = __vmaxu2(__byte_perm(m[i], m[i + 1], 0x5410), __byte_perm(m[i], m[i + 1], 0x7632));
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m[i] = __vmaxu2(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+    }
+    mine = tx & 4 ? (tx & 2 ? m[6] : m[4]) : (tx & 2 ? m[2] : m[0]);
+    mine = tx & 1 ? mine >> 16 : mine & 0xFFFFu;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m[i] = max(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+    mine = tx & 4 ? (tx & 2 ? (tx & 1 ? m[7] : m[6]) : (tx & 1 ? m[5] : m[4])) : (tx & 2 ? (tx & 1 ? m[3] : m[2]) : (tx & 1 ? m[1] : m[0]));
+  }
+  const int ex = exponent_of<F::kTop>(magnitude<T>(mine));
+  const float inverse = inverse_of(ex);
+  if (tx < 8 && r0 + tx < rows) a.e[(int64_t)(row + r0 + tx) * a.lde + block] = (int8_t)ex;
+  uint8_t *q = a.q + (int64_t)(row + r0) * a.ldq;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    float amax = amax_of<T, 8>(v[i]);
-#pragma unroll
-    for (int o = 8; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if (8 * ty + i >= rows) continue;
-    const int64_t r = row + 8 * ty + i;
-    const int e = exponent_of<F::kTop>(amax);
-    const float s = inverse_of(e);
-    float f[8];
-    unpack<T, 8>(v[i], f);
-    put8(a.q + r * a.ldq, c, a.H - c,
-         make_uint2(codes4<F>(f[0] * s, f[1] * s, f[2] * s, f[3] * s), codes4<F>(f[4] * s, f[5] * s, f[6] * s, f[7] * s)), wide);
-    if (tx == 0) a.e[r * a.lde + block] = (int8_t)e;
+    const float s = __shfl_sync(0xFFFFFFFFu, inverse, (threadIdx.x & 16) + i);
+    if (r0 + i < rows) put8<WIDE>(q + i * a.ldq, c, a.H - c, row_codes<T, F>(v[i], s));
   }
+}
+
+// The largest magnitudes of word W's columns over a thread's rows, and with the other thread of its warp.
+template <class T, int W>
+__device__ __forceinline__ uint32_t column_peak(const Vec<T, 8> (&v)[8]) {
+  uint32_t m = magnitudes<T, W>(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; i++) m = peak_of<T>(m, magnitudes<T, W>(v[i]));
+  return peak_of<T>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
 }
 
 // Columns, and with a.q rows: a block of threads takes one block of 128 places and every gridDim.y-th block
 // of columns; rows outside all groups (rarely any) are dealt out over the blocks for their row codes.
-template <class T, class F>
-__global__ void __launch_bounds__(256) columns_kernel(const QuantArgs a, int places, bool wide_in, bool wide_q, bool wide_t) {
-  __shared__ uint2 turned[128 * 16];
-  __shared__ float peak[8][128];
+template <class T, class F, bool WIDE>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) columns_kernel(const QuantArgs a, int places) {
+  constexpr int kWords = 2 * sizeof(T);       // of a thread's eight columns
+  __shared__ __align__(16) uint2 turned[128 * 16];
+  __shared__ __align__(16) uint32_t peak[8][16 * kWords];
+  __shared__ __align__(16) float scale[kBlock];
   grid_go();
   const int tx = threadIdx.x & 15, warp = threadIdx.x >> 5, blocks = (a.H + kBlock - 1) / kBlock;
   const Place at = place_of(a, blockIdx.x);
   Vec<T, 8> v[8];
   for (int block = blockIdx.y; block < blocks; block += gridDim.y) {
     const int c = block * kBlock + 8 * tx;
-    load_tile<T>(v, (const T *)a.x + (int64_t)at.row * a.ldx, a.ldx, at.rows, c, a.H, wide_in);
-    if (a.q) put_rows<T, F>(a, v, at.row, at.rows, block, wide_q);
-    // each column's largest magnitude: a thread's eight rows, the warp's two threads, the eight warps
-    float m[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) m[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      float f[8];
-      unpack<T, 8>(v[i], f);
-#pragma unroll
-      for (int j = 0; j < 8; j++) m[j] = max_nan(m[j], fabsf(f[j]));
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) m[j] = max_nan(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+    load_tile<T, WIDE>(v, (const T *)a.x + (int64_t)at.row * a.ldx, a.ldx, at.rows, c, a.H);
+    uint32_t m[kWords];
+    m[0] = column_peak<T, 0>(v), m[1] = column_peak<T, 1>(v), m[2] = column_peak<T, 2>(v), m[3] = column_peak<T, 3>(v);
+    if constexpr (sizeof(T) == 4)
+      m[4] = column_peak<T, 4>(v), m[5] = column_peak<T, 5>(v), m[6] = column_peak<T, 6>(v), m[7] = column_peak<T, 7>(v);
     __syncthreads();                          // the tile before has left shared memory
     if ((threadIdx.x & 16) == 0) {
 #pragma unroll
-      for (int j = 0; j < 8; j++) peak[warp][8 * tx + j] = m[j];
+      for (int i = 0; i < kWords; i += 4) *(uint4 *)&peak[warp][tx * kWords + i] = make_uint4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+    }
+    if (a.q) put_rows<T, F, WIDE>(a, v, at.row, at.rows, block);
+    __syncthreads();
+    if (threadIdx.x < 16 * kWords) {          // a word's column, or two
+      uint32_t all = peak[0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < 8; w++) all = peak_of<T>(all, peak[w][threadIdx.x]);
+      constexpr int kEach = 4 / sizeof(T);
+#pragma unroll
+      for (int j = 0; j < kEach; j++) {
+        const int at_column = kEach * threadIdx.x + j, e = exponent_of<F::kTop>(magnitude<T>(kEach == 1 ? all : j ? all >> 16 : all & 0xFFFFu));
+        scale[at_column] = inverse_of(e);
+        if (block * kBlock + at_column < a.H) a.et[(int64_t)(block * kBlock + at_column) * a.ldet + blockIdx.x] = (int8_t)e;
+      }
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-#pragma unroll
-      for (int q = 0; q < 8; q++) m[j] = max_nan(m[j], peak[q][8 * tx + j]);
     float s[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const int e = exponent_of<F::kTop>(m[j]);
-      s[j] = inverse_of(e);
-      if (threadIdx.x < 16 && c + j < a.H) a.et[(int64_t)(c + j) * a.ldet + blockIdx.x] = (int8_t)e;
-    }
+    *(float4 *)&s[0] = *(const float4 *)&scale[8 * tx];
+    *(float4 *)&s[4] = *(const float4 *)&scale[8 * tx + 4];
     turn_tile<T, F>(v, s, turned);
     __syncthreads();
-    put_turned(turned, a.qt + (int64_t)block * kBlock * a.ldqt + (int64_t)blockIdx.x * kBlock, a.ldqt, a.H - block * kBlock, kBlock,
-               wide_t);
+    put_turned<WIDE>(turned, a.qt + (int64_t)block * kBlock * a.ldqt + (int64_t)blockIdx.x * kBlock, a.ldqt, a.H - block * kBlock, kBlock);
   }
   const int lead = (at.first + kBlock - 1) / kBlock, tail = (a.T - at.last + kBlock - 1) / kBlock;
   if (a.q)
     for (int o = blockIdx.x; o < lead + tail; o += places) {
       const int row = o < lead ? o * kBlock : at.last + (o - lead) * kBlock, rows = min(kBlock, (o < lead ? at.first : a.T) - row);
       for (int block = blockIdx.y; block < blocks; block += gridDim.y) {
-        load_tile<T>(v, (const T *)a.x + (int64_t)row * a.ldx, a.ldx, rows, block * kBlock + 8 * tx, a.H, wide_in);
-        put_rows<T, F>(a, v, row, rows, block, wide_q);
+        load_tile<T, WIDE>(v, (const T *)a.x + (int64_t)row * a.ldx, a.ldx, rows, block * kBlock + 8 * tx, a.H);
+        put_rows<T, F, WIDE>(a, v, row, rows, block);
       }
     }
 }
 
 // Weights: one exponent to a tile.
-template <class T, class F>
-__global__ void __launch_bounds__(256) weight_kernel(const QuantWeightArgs a, int high, int wide, bool wide_in, bool wide_q,
-                                                     bool wide_t) {
-  __shared__ uint2 turned[128 * 16];
-  __shared__ float peak[8];
+template <class T, class F, bool WIDE>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) weight_kernel(const QuantWeightArgs a, int high, int wide) {
+  __shared__ __align__(16) uint2 turned[128 * 16];
+  __shared__ uint32_t peak[8];
   grid_go();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t tile = blockIdx.x, matrix = tile / ((int64_t)high * wide), t = tile - matrix * high * wide;
-  const int down = (int)(t / wide), across = (int)(t - (int64_t)down * wide), n0 = down * kBlock, k0 = across * kBlock;
-  const int c = k0 + 8 * tx, rows = min(kBlock, a.N - n0);
+  const int tx = threadIdx.x & 15, r0 = 8 * (threadIdx.x >> 4), tile = blockIdx.x, per = high * wide;
+  const int matrix = tile / per, t = tile - matrix * per, down = t / wide, across = t - down * wide;
+  const int n0 = down * kBlock, k0 = across * kBlock, c = k0 + 8 * tx, rows = min(kBlock, a.N - n0);
   Vec<T, 8> v[8];
-  load_tile<T>(v, (const T *)a.w + matrix * a.w_stride + (int64_t)n0 * a.ldw, a.ldw, rows, c, a.K, wide_in);
-  float m = 0.f;
+  load_tile<T, WIDE>(v, (const T *)a.w + matrix * a.w_stride + (int64_t)n0 * a.ldw, a.ldw, rows, c, a.K);
+  uint32_t m = row_peak<T>(v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; i++) m = max_nan(m, amax_of<T, 8>(v[i]));
-  m = warp_max(m);
+  for (int i = 1; i < 8; i++) m = peak_of<T>(m, row_peak<T>(v[i]));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = peak_of<T>(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   if ((threadIdx.x & 31) == 0) peak[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; i++) m = max_nan(m, peak[i]);
-  const int e = exponent_of<F::kTop>(m);
+  for (int i = 0; i < 8; i++) m = peak_of<T>(m, peak[i]);
+  const int e = exponent_of<F::kTop>(whole_peak<T>(m));
   const float s = inverse_of(e);
   if (threadIdx.x == 0) {
     a.e[tile] = (int8_t)e;
-    if (a.qt) a.et[(matrix * wide + across) * high + down] = (int8_t)e;
+    if (a.qt) a.et[(int64_t)matrix * per + across * high + down] = (int8_t)e;
   }
+  uint8_t *q = a.q + matrix * a.q_stride + (int64_t)(n0 + r0) * a.ldq;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    if (8 * ty + i >= rows) break;
-    float f[8];
-    unpack<T, 8>(v[i], f);
-    put8(a.q + matrix * a.q_stride + (int64_t)(n0 + 8 * ty + i) * a.ldq, c, a.K - c,
-         make_uint2(codes4<F>(f[0] * s, f[1] * s, f[2] * s, f[3] * s), codes4<F>(f[4] * s, f[5] * s, f[6] * s, f[7] * s)), wide_q);
+    if (r0 + i >= rows) break;
+    put8<WIDE>(q + i * a.ldq, c, a.K - c, row_codes<T, F>(v[i], s));
   }
   if (!a.qt) return;
   const float all[8] = {s, s, s, s, s, s, s, s};
   turn_tile<T, F>(v, all, turned);
   __syncthreads();
-  put_turned(turned, a.qt + matrix * a.qt_stride + (int64_t)k0 * a.ldqt + n0, a.ldqt, a.K - k0, rows, wide_t);
+  put_turned<WIDE>(turned, a.qt + matrix * a.qt_stride + (int64_t)k0 * a.ldqt + n0, a.ldqt, a.K - k0, rows);
 }
 
 template <class T, class F>
 int quantize_typed(const QuantArgs &a, cudaStream_t st) {
   const int blocks = (a.H + kBlock - 1) / kBlock;
-  const bool wide_in = rows16(a.x, a.ldx, sizeof(T)), wide_q = rows_on(a.q, a.ldq, 1, 8);
+  const bool whole = a.H % 8 == 0 && rows16(a.x, a.ldx, sizeof(T)) && rows_on(a.q, a.ldq, 1, 8);
   if (!a.qt) {
-    const int64_t tasks = (int64_t)a.T * blocks, grid = (tasks + 16 * kRows - 1) / (16 * kRows);
-    if (grid > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
-    rows_kernel<T, F><<<(unsigned)grid, 256, 0, st>>>(a, tasks, blocks, wide_in, wide_q);
+    int wide = 1;
+    while (wide < 16 && wide < blocks) wide *= 2;
+    const int high = 16 / wide * kRows, across = (blocks + wide - 1) / wide, y = across < 65535 ? across : 65535;
+    const dim3 grid((a.T + high - 1) / high, y, (across + y - 1) / y);
+    if (whole) rows_kernel<T, F, true><<<grid, 256, 0, st>>>(a, blocks, wide);
+    else rows_kernel<T, F, false><<<grid, 256, 0, st>>>(a, blocks, wide);
     return launch_status();
   }
   const int places = (int)(mcemu_fp8_columns(a.T, a.E) / kBlock);
   int across = 16 * sm_count() / places + 1;
   across = across < blocks ? across : blocks;
-  columns_kernel<T, F><<<dim3(places, across < 65535 ? across : 65535), 256, 0, st>>>(a, places, wide_in, wide_q, rows_on(a.qt, a.ldqt, 1, 8));
+  const dim3 grid(places, across < 65535 ? across : 65535);
+  if (whole && rows_on(a.qt, a.ldqt, 1, 16)) columns_kernel<T, F, true><<<grid, 256, 0, st>>>(a, places);
+  else columns_kernel<T, F, false><<<grid, 256, 0, st>>>(a, places);
   return launch_status();
 }
 template <class T, class F>
 int weight_typed(const QuantWeightArgs &a, cudaStream_t st) {
   const int high = (a.N + kBlock - 1) / kBlock, wide = (a.K + kBlock - 1) / kBlock;
   const int64_t tiles = (int64_t)high * wide * a.E;
-  if ((int64_t)high * wide > INT32_MAX || tiles > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+  if (tiles > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
   const auto on = [&](const void *p, int64_t ld, int64_t stride, int size, int n) {
     return rows_on(p, ld, size, n) && (a.E == 1 || stride * size % n == 0);
   };
-  weight_kernel<T, F><<<(unsigned)tiles, 256, 0, st>>>(a, high, wide, on(a.w, a.ldw, a.w_stride, sizeof(T), 16),
-                                                       on(a.q, a.ldq, a.q_stride, 1, 8), on(a.qt, a.ldqt, a.qt_stride, 1, 8));
+  const dim3 grid((unsigned)tiles);
+  if (a.K % 8 == 0 && on(a.w, a.ldw, a.w_stride, sizeof(T), 16) && on(a.q, a.ldq, a.q_stride, 1, 8) && on(a.qt, a.ldqt, a.qt_stride, 1, 16))
+    weight_kernel<T, F, true><<<grid, 256, 0, st>>>(a, high, wide);
+  else
+    weight_kernel<T, F, false><<<grid, 256, 0, st>>>(a, high, wide);
   return launch_status();
 }
 
