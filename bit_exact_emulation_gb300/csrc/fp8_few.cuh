@@ -2,24 +2,33 @@
 //
 // The roles change: 128 channels are the matrix instruction's rows and BT tokens its columns, so that the
 // weights stream through once at whatever rate memory gives.  The CTAs of a cluster share K; each has
-// its own copies in flight (a ring of stages in shared memory), and pushes its sums of each token into the shared
-// memory of the CTA that adds up that token's parts, in the order of the parts.  Clusters walk over the
-// units of work, the next one's copies on their way while a unit is joined.
+// its own copies in flight (a ring of stages in shared memory), and sends its sums of each token into the shared
+// memory of the CTA that adds up that token's parts, in the order of the parts.  (By the copy engine, a token's
+// 128 sums in 512 bytes: threads that stored into the other CTAs took 330 cycles a store, 6600 for 77 tokens.)
+// Clusters walk over the units of work, the next one's copies on their way while a unit is joined; with more
+// than 32 tokens a cluster that shares K has one unit, whose sums leave through the stages' memory.
 #pragma once
 #include "fp8_tc.cuh"
 
 namespace mcemu {
 namespace fp8 {
 
-constexpr int kFewThreads = 256;              // four warps drain, then: copies, matrix instructions, exponents of b, of a
+// Four warps drain; then come one for the copies of b, one that issues matrix instructions, one for the exponents
+// of b, one for a's, one for the copies of a.
+constexpr int kFewThreads = 288;
+// CTAs that share K at most: eight, the portable limit of a cluster.
+constexpr int kMostParts = 8;
+
 template <int BT>
 struct Few {
   static constexpr int kStageBytes = kTileBytes + BT * kBlock;
-  static constexpr int kStages = BT <= 16 ? 10 : BT <= 32 ? 8 : BT <= 64 ? 6 : 4;
+  static constexpr int kStages = BT <= 16 ? 9 : BT <= 32 ? 8 : BT <= 64 ? 6 : 4;
   static constexpr int kScaleSlots = 4, kSlotBytes = 2 * kScaleBytes;
-  static constexpr int kJoinBytes = (BT + 8) * 512;
-  static constexpr int kSmem = kStages * kStageBytes + kScaleSlots * kSlotBytes + kJoinBytes + 1024 + 512 +
+  static constexpr int kSendBytes = BT <= 32 ? BT * 512 : 0;   // sums on their way out; with more tokens: the stages
+  static constexpr int kJoinBytes = (BT + kMostParts - 1 + 3) * 512;    // three places to read over
+  static constexpr int kSmem = kStages * kStageBytes + kScaleSlots * kSlotBytes + kSendBytes + kJoinBytes + 1024 + 512 +
                                2 * 4 * (MCEMU_FP8_MAX_GROUPS + 1);
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 struct FewUnit {
@@ -29,13 +38,6 @@ __device__ __forceinline__ FewUnit few_unit_at(const int *at, const int *before,
   while (u >= before[g + 1] * tiles_b) g++;
   const int t = u - before[g] * tiles_b, tiles_a = before[g + 1] - before[g], a = at[g] + t % tiles_a * bt;
   return FewUnit{g, a, min(bt, at[g + 1] - a), t / tiles_a * 128};      // one tile of channels for all tokens, then the next
-}
-
-// Four bytes to `to`, counted on the barrier `bar` there (addresses in the cluster, of the same CTA).
-__device__ __forceinline__ void push(uint32_t to, float v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
-               "r"(__float_as_uint(v)), "r"(bar)
-               : "memory");
 }
 
 // A warp's way through the units, bringing a chunk's exponents of R * 32 rows of a or b to each slot.
@@ -67,13 +69,14 @@ __device__ __forceinline__ void few_scales(const Fp8Product &p, const int *at, c
 
 template <class T, int BT>
 __global__ void __launch_bounds__(kFewThreads, 1)
-    few_kernel(const __grid_constant__ Fp8Product p, const __grid_constant__ CUtensorMap ma,
+    few_kernel(const Fp8Product p, const __grid_constant__ CUtensorMap ma,
                const __grid_constant__ CUtensorMap mb, int per) {
   using S = Few<BT>;
   constexpr int kStages = S::kStages, kStageBytes = S::kStageBytes, kSlots = S::kScaleSlots;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t scales = base + kStages * kStageBytes, join = scales + kSlots * S::kSlotBytes, full = join + S::kJoinBytes,
+  const uint32_t scales = base + kStages * kStageBytes, send = S::kSendBytes ? scales + kSlots * S::kSlotBytes : base,
+                 join = scales + kSlots * S::kSlotBytes + S::kSendBytes, full = join + S::kJoinBytes,
                  empty = full + 8 * kStages, sf_full = empty + 8 * kStages, sf_empty = sf_full + 8 * kSlots,
                  acc_full = sf_empty + 8 * kSlots, acc_empty = acc_full + 16, drain = acc_empty + 16, join_full = drain + 8,
                  join_empty = join_full + 8, slot = join_empty + 8;
@@ -81,9 +84,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int warp = tc::warp_number(), lane = threadIdx.x & 31;
   const uint32_t parts = tc::cluster_size(), rank = tc::cta_rank();
 
+  if (threadIdx.x == 128) prefetch_map(&mb);
+  if (threadIdx.x == 256) prefetch_map(&ma);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; s++) {
-      tc::mbar_init(full + 8 * s, 1);
+      tc::mbar_init(full + 8 * s, 2);         // both copying warps
       tc::mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < kSlots; s++) {
@@ -115,25 +120,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int k0 = (int)rank * per, k1 = min(blocks, k0 + per);
   int g = 0;
 
-  if (warp == 4) {
-    if (lane == 0) {                          // copies both operands' parts
-      uint32_t it = 0;
-      for (int u = first; u < units && !dead; u += step) {
-        const FewUnit r = few_unit_at(at, before, tiles_b, BT, u, g);
-        for (int k = k0; k < k1; k++, it++) {
-          const uint32_t s = it % kStages, to = base + s * kStageBytes;
-          tc::mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, dead);
-          if (dead) break;
-          tc::mbar_expect(full + 8 * s, kStageBytes);
-          box_load(to, &mb, k * kBlock, r.b, r.g, full + 8 * s);
-          box_load(to + kTileBytes, &ma, k * kBlock, r.a, 0, full + 8 * s);
-        }
+  if (warp == 4 || warp == 8) {               // copies b's part, or a's
+    const bool of_b = warp == 4;
+    const CUtensorMap *map = of_b ? &mb : &ma;
+    uint32_t s = 0, phase = 1, it = 0;
+    for (int u = first; u < units && !dead; u += step) {
+      const FewUnit r = few_unit_at(at, before, tiles_b, BT, u, g);
+      for (int k = k0; k < k1; k++, it++) {
+        if (it >= kStages) tc::mbar_wait_warp(empty + 8 * s, phase, dead);
+        if (dead) break;
+        if (lane == 0) tc::mbar_expect(full + 8 * s, of_b ? kTileBytes : BT * kBlock);
+        __syncwarp();
+        box_load(base + s * kStageBytes + (of_b ? 0 : kTileBytes), map, k * kBlock, of_b ? r.b : r.a, of_b ? r.g : 0, full + 8 * s);
+        if (++s == kStages) s = 0, phase ^= 1;
       }
-      bool late = false;                      // the copies end before the CTA leaves
-      for (uint32_t s = 0; s < kStages && s < it; s++) {
-        const uint32_t last = it - 1 - (it - 1 - s) % kStages;
-        tc::mbar_wait(full + 8 * s, (last / kStages) & 1, late);
-      }
+    }
+    bool late = false;                        // the copies end before the CTA leaves
+    for (uint32_t q = 0; q < kStages && q < it; q++) {
+      const uint32_t last = it - 1 - (it - 1 - q) % kStages;
+      tc::mbar_wait_warp(full + 8 * q, (last / kStages) & 1, late);
     }
   } else if (warp == 5) {                     // issues the matrix instructions
     const uint32_t ins = instruction(128, BT, p.b.fmt, p.a.fmt);
@@ -212,39 +217,48 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         continue;
       }
-      // tokens share * o to share * (o + 1) - 1 are joined by CTA o: part q's sums of its token c lie in
-      // slot q * share + c
+      // tokens share * o to share * (o + 1) - 1 are joined by CTA o, where part q's lie in places q * share and on;
+      // a place has a token's 128 sums
       const int share = (r.n + (int)parts - 1) / (int)parts, mine_n = max(0, min(share, r.n - (int)rank * share));
+      if (turn && threadIdx.x < parts) boxes_left();             // what was sent last
       if (threadIdx.x == 0) tc::mbar_expect(join_full, mine_n * parts * 512);
-      tc::mbar_wait(join_empty, (turn & 1) ^ 1, dead);           // what was pushed last has been taken
-      const uint32_t place = join + (rank * share * 128 + row) * 4;
-      uint32_t to = at_rank(place, 0), bar = at_rank(join_full, 0);
-      int o = 0, c = 0;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-      for (int j = 0; j < BT; j++) {
-        if (j < r.n && !dead) {
-          push(to + c * 512, sum[j], bar);
-          if (++c == share && j + 1 < r.n) {
-            c = 0, o++;
-            to = at_rank(place, o), bar = at_rank(join_full, o);
-          }
-        }
+      for (int j = 0; j < BT; j++)
+        if (j < r.n) asm volatile("st.shared.f32 [%0], %1;" ::"r"(send + j * 512 + row * 4), "f"(sum[j]) : "memory");
+      tc::fence_async_smem();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (threadIdx.x < parts) {
+        const int o = threadIdx.x, n_o = min(share, r.n - o * share);
+        tc::mbar_wait(join_empty, (turn & 1) ^ 1, dead);         // what was sent last has been taken
+        if (n_o > 0 && !dead)
+          bulk_push(at_rank(join + rank * share * 512, o), send + o * share * 512, n_o * 512, at_rank(join_full, o));
       }
+      __syncwarp();
       tc::mbar_wait(join_full, turn & 1, dead);
       if (!dead) (void)mbar_try_cluster(join_full, turn & 1);
-      for (int i = 0; i < mine_n && !dead; i++) {
-        float total = 0.f;
-        for (uint32_t q = 0; q < parts; q++) {
-          float v;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(join + ((q * share + i) * 128 + row) * 4) : "memory");
-          total += v;
+      y += (int64_t)rank * share * p.ldy;
+      const float *from = (const float *)(raw + (join - tc::smem_addr(raw))) + row;
+      // few instructions: what runs once in a launch waits for its code (unrolled: twice as long)
+#pragma unroll 1
+      for (int i = 0; i < mine_n; i += 4) {
+        float total[4] = {0.f, 0.f, 0.f, 0.f};
+        const float *at_q = from + i * 128;   // places behind the last are read and not used
+#pragma unroll 1
+        for (int q = 0; q < (int)parts; q++, at_q += share * 128) {
+#pragma unroll
+          for (int x = 0; x < 4; x++) total[x] += at_q[x * 128];
         }
-        if (in) put(y + (int64_t)(rank * share + i) * p.ldy, total + bias, p.accumulate);
+        const int n = in && !dead ? min(4, mine_n - i) : 0;
+#pragma unroll
+        for (int x = 0; x < 4; x++, y += p.ldy)
+          if (x < n) put(y, total[x] + bias, p.accumulate);
       }
       __syncwarp();
       if (lane < (int)parts) mbar_arrive_at(join_empty, lane);
     }
   }
+  if (warp == 0) boxes_left();                // lanes that sent
   __syncwarp();
   tc::fence_before();
   tc::cluster_sync();                         // no CTA leaves while another pushes into it
@@ -259,6 +273,7 @@ int launch_few(const Fp8Product &p, const CUtensorMap &ma, const CUtensorMap &mb
                int64_t clusters, cudaStream_t st) {
   if (!allow_smem<few_kernel<T, BT>>(Few<BT>::kSmem)) return MCEMU_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
+  if (BT > 32 && parts > 1 && units * parts > sm_count()) parts = 1, per = (p.K + kBlock - 1) / kBlock;      // one unit to a cluster
   const int64_t fit = sm_count() / parts, most = clusters < fit ? clusters : fit > 0 ? fit : 1;
   cfg.gridDim = dim3((unsigned)((units < most ? units : most) * parts));
   cfg.blockDim = dim3(kFewThreads);

@@ -164,7 +164,7 @@ __device__ __forceinline__ void issue(const Fp8Product &p, const PairGroups &w, 
 
 template <class T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    pair_kernel(const __grid_constant__ Fp8Product p, const __grid_constant__ CUtensorMap ma,
+    pair_kernel(const Fp8Product p, const __grid_constant__ CUtensorMap ma,
                 const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap my, bool boxes) {
   using S = Pair<BN>;
   constexpr int kStages = S::kStages, kBlocks = S::kBlocks, kSlots = S::kScaleSlots, kCols = BN / 2;

@@ -8,26 +8,25 @@ namespace {
 
 constexpr int kBlock = MCEMU_FP8_BLOCK;
 
-// Rows at any address to rows on 16-byte boundaries, sixteen bytes a thread.
-__global__ void __launch_bounds__(256) align_kernel(const uint8_t *__restrict__ from, int64_t ld, int64_t stride, int rows,
-                                                    int64_t tasks, int K, int ldto, uint8_t *__restrict__ to) {
+// Rows at any address to rows on 16-byte boundaries, sixteen bytes a thread; both operands by one kernel.
+struct Copy {
+  const uint8_t *from;
+  int64_t ld, stride, tasks;
+  int rows;
+  uint8_t *to;
+};
+__global__ void __launch_bounds__(256) align_kernel(const Copy a, const Copy b, int K, int units) {
   grid_go();
-  const int64_t task = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (task >= tasks) return;
-  const int units = ldto / 16;
-  const int64_t row = task / units;
+  int64_t task = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool second = task >= a.tasks;
+  if (second) task -= a.tasks;
+  const Copy &c = second ? b : a;
+  if (task >= c.tasks) return;
+  const int64_t row = task / units, matrix = row / c.rows;
   const int k = (int)(task - row * units) * 16;
-  const int64_t matrix = row / rows;
-  *(uint4 *)(to + task * 16) = row16((const int8_t *)from + matrix * stride + (row - matrix * rows) * ld, k, K, false);
+  *(uint4 *)(c.to + task * 16) = row16((const int8_t *)c.from + matrix * c.stride + (row - matrix * c.rows) * c.ld, k, K, false);
 }
 
-int align(const Fp8Operand &o, int matrices, int K, uint8_t *to, cudaStream_t st) {
-  const int ldto = (K + 15) & ~15;
-  const int64_t tasks = (int64_t)o.rows * matrices * (ldto / 16), blocks = (tasks + 255) / 256;
-  if (blocks > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
-  align_kernel<<<(unsigned)blocks, 256, 0, st>>>(o.q, o.ld, o.stride, o.rows, tasks, K, ldto, to);
-  return launch_status();
-}
 int64_t aligned_bytes(int64_t rows, int matrices, int K) { return rows * matrices * ((K + 15) & ~15); }
 
 // A product without blocks along k: bias, or zeros, in every row that belongs to a group.
@@ -63,38 +62,78 @@ int launch_empty(const Fp8Product &p, cudaStream_t st) {
                                    : launch_early(empty_kernel<__nv_bfloat16>, grid, block, 0, st, p, tasks);
 }
 
-// Parts of K (a cluster's CTAs) and blocks of 128 to each: what takes the fewest blocks in a row, with two
-// more for each unit's joining.  How many clusters run at a time is what a GB300 of 152 multiprocessors reports.
-Fp8Plan few_plan(int64_t busy, int64_t units, int width, int blocks) {
+// Which form, and how it is cut: what ends soonest by these estimates in microseconds, whose constants are fitted
+// to the following (bf16 results, operands in L2; `few` with the parts of K that it prefers):
+//
+//   M x N x K            few   pairs, 224   pairs, 128
+//   16 x 1024 x 1024     4.5       7.2          6.2
+//   512 x 1024 x 1024   10.2       8.6          7.2
+//   16 x 4096 x 4096     5.5      13.0         13.4
+//   128 x 4096 x 4096   12.5      14.2         11.4
+//   512 x 4096 x 4096   12.8      14.8         12.9
+//   1024 x 4096 x 4096  20.9      16.7         20.1
+//   64 x 16384 x 4096    9.1      15.6         17.9
+//   256 x 16384 x 4096  22.3      16.7         20.0
+//   256 x 1024 x 8192   12.3      21.3         16.2
+//   64 x 8192 x 8192    16.1      24.5         17.9
+//   256 x 8192 x 8192   22.3      22.1         19.6
+//   1024 x 8192 x 8192  72.1      42.8         61.9
+//
+// `busy` tiles are expected and `most` possible (a group's rows are known on the device alone).
+constexpr int kPairs = 76;
+struct Choice {
+  Fp8Plan plan;
+  double us;
+};
+Choice pair_choice(int width, double busy, int64_t most, int blocks) {
+  const double full = busy < kPairs ? busy / kPairs : 1.0, rounds = (double)(int64_t)((busy + kPairs - 1) / kPairs);
+  const double block = width == 224 ? 0.22 + 0.06 * full : 0.147 + 0.08 * full;
+  return {Fp8Plan{false, width, most, 1, blocks, 0}, (width == 224 ? 6.7 : 5.4) + rounds * (blocks * block + 0.4)};
+}
+// Parts of K (a cluster's CTAs): how many clusters run at a time is what a GB300 of 152 multiprocessors reports.
+Choice few_choice(int width, double busy, int64_t most, int blocks) {
   constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-  Fp8Plan best{true, width, units, 1, blocks, kClusters[1]};
-  int64_t least = 0;
+  const double block = width == 16 ? 0.115 : width == 32 ? 0.12 : width == 64 ? 0.15 : 0.24;
+  const double join = width == 16 ? 0.5 : width == 32 ? 0.9 : width == 64 ? 3.0 : 4.5, start = width == 128 ? 5.4 : 4.3;
+  Choice best{};
   for (int parts = 1; parts <= 8 && parts <= blocks; parts++) {
     const int per = (blocks + parts - 1) / parts;
     if (per * (parts - 1) >= blocks) continue;                  // a part would be empty
-    const int64_t rounds = (busy + kClusters[parts] - 1) / kClusters[parts], steps = rounds * (per + (parts > 1 ? 2 : 1));
-    if (parts == 1 || steps < least) {
-      best = Fp8Plan{true, width, units, parts, per, kClusters[parts]};
-      least = steps;
-    }
+    if (parts > 1 && width > 32 && most > kClusters[parts]) continue;          // see fp8_few.cuh
+    const double rounds = (double)(int64_t)((busy + kClusters[parts] - 1) / kClusters[parts]);
+    const double us = start + rounds * (per * block + (parts > 1 ? join : 0.2));
+    if (parts == 1 || us < best.us) best = {Fp8Plan{true, width, most, parts, per, kClusters[parts]}, us};
   }
   return best;
 }
 
 Fp8Plan plan_of(const Fp8Product &p) {
   const int blocks = (p.K + kBlock - 1) / kBlock;
-  const int64_t groups = p.by_k ? 1 : p.E, rows = ((int64_t)p.a.rows + groups - 1) / groups;
-  if (!p.by_k && rows <= 128) {
-    // a group's rows differ: tiles that hold half as many again, so that few weights are read twice
-    const int64_t fit = p.offsets ? rows + rows / 2 : rows;
-    const int width = fit <= 16 ? 16 : fit <= 32 ? 32 : fit <= 64 ? 64 : 128;
-    const int64_t tiles_b = ((int64_t)p.b.rows + 127) / 128, filled = p.a.rows < groups ? p.a.rows : groups;
-    return few_plan(filled * tiles_b, ((int64_t)p.a.rows / width + filled) * tiles_b, width, blocks);
+  // sums over groups of blocks: a group's share of them is one unit's work
+  const int64_t groups = p.E, filled = p.by_k || p.a.rows > groups ? groups : p.a.rows;
+  const int each = p.by_k ? (int)((blocks + groups - 1) / groups) : blocks;
+  const auto tiles = [](int64_t rows, int tile) { return (rows + tile - 1) / tile; };
+  Choice best{};
+  for (int width : {224, 128}) {
+    const int64_t across = tiles(p.b.rows, width);
+    // a group's last tile is half empty on average
+    const double high = p.by_k ? (double)groups * tiles(p.a.rows, 256)
+                        : p.offsets ? p.a.rows / 256.0 + filled * 0.5
+                                    : (double)tiles(p.a.rows, 256);
+    const int64_t most = (p.by_k ? groups * tiles(p.a.rows, 256) : p.offsets ? p.a.rows / 256 + groups : tiles(p.a.rows, 256)) * across;
+    const Choice c = pair_choice(width, high * across, most, each);
+    if (width == 224 || c.us < best.us) best = c;
   }
-  const int width = 224;
-  const int64_t tiles_b = ((int64_t)p.b.rows + width - 1) / width;
-  const int64_t tiles_a = p.by_k ? ((int64_t)p.a.rows + 255) / 256 * p.E : (int64_t)p.a.rows / 256 + groups;
-  return Fp8Plan{false, width, tiles_a * tiles_b, 1, blocks, 0};
+  if (p.by_k) return best.plan;
+  const int64_t across = tiles(p.b.rows, 128), mean = tiles(p.a.rows, (int)filled);
+  for (int width : {16, 32, 64, 128}) {
+    if (width < 128 && width < (p.offsets ? mean + mean / 2 : mean)) continue;       // would read most weights twice
+    const double high = p.offsets ? p.a.rows / (double)width + filled * 0.5 : (double)tiles(p.a.rows, width);
+    const int64_t most = (p.offsets ? p.a.rows / width + filled : tiles(p.a.rows, width)) * across;
+    const Choice c = few_choice(width, (high > filled ? high : (double)filled) * across, most, blocks);
+    if (c.us < best.us) best = c;
+  }
+  return best.plan;
 }
 
 }  // namespace
@@ -109,18 +148,18 @@ int launch_fp8_product(const Fp8Product &given, bool a_rows, bool b_rows, void *
   if (p.K == 0) return launch_empty(p, st);
   const Fp8Plan plan = plan_of(p);
   if (plan.units > INT32_MAX / 2) return MCEMU_ERR_UNSUPPORTED;
-  const int ld = (p.K + 15) & ~15, matrices = p.by_k ? 1 : p.E;
-  uint8_t *to = (uint8_t *)ws;
-  if (!a_rows) {
-    const int rc = align(p.a, 1, p.K, to, st);
-    if (rc != MCEMU_OK) return rc;                              // the operand would be whatever the workspace held
-    p.a.q = to, p.a.ld = ld;
-    to += aligned_bytes(p.a.rows, 1, p.K);
-  }
-  if (!b_rows) {
-    const int rc = align(p.b, matrices, p.K, to, st);
-    if (rc != MCEMU_OK) return rc;
-    p.b.q = to, p.b.ld = ld, p.b.stride = (int64_t)p.b.rows * ld;
+  if (!a_rows || !b_rows) {
+    const int ld = (p.K + 15) & ~15, matrices = p.by_k ? 1 : p.E;
+    uint8_t *to_a = (uint8_t *)ws, *to_b = to_a + (a_rows ? 0 : aligned_bytes(p.a.rows, 1, p.K));
+    const Copy a{p.a.q, p.a.ld, 0, a_rows ? 0 : (int64_t)p.a.rows * (ld / 16), p.a.rows, to_a};
+    const Copy b{p.b.q, p.b.ld, p.b.stride, b_rows ? 0 : (int64_t)p.b.rows * matrices * (ld / 16), p.b.rows, to_b};
+    const int64_t blocks = (a.tasks + b.tasks + 255) / 256;
+    if (blocks > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+    align_kernel<<<(unsigned)blocks, 256, 0, st>>>(a, b, p.K, ld / 16);
+    const int rc = launch_status();
+    if (rc != MCEMU_OK) return rc;                              // the operands would be whatever the workspace held
+    if (!a_rows) p.a.q = to_a, p.a.ld = ld;
+    if (!b_rows) p.b.q = to_b, p.b.ld = ld, p.b.stride = (int64_t)p.b.rows * ld;
   }
   return plan.few ? launch_fp8_few(p, plan, stream) : launch_fp8_pair(p, plan, stream);
 }

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) columns_kernel(co
 
 // Weights: one exponent to a tile.
 template <class T, class F, bool WIDE>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) weight_kernel(const QuantWeightArgs a, int high, int wide) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) weight_kernel(const QuantWeightArgs a, int high, int wide) {
   __shared__ __align__(16) uint2 turned[128 * 16];
   __shared__ uint32_t peak[8];
   grid_go();

@@ -53,15 +53,17 @@ inline int tensor_map(CUtensorMap *map, int fmt, const void *base, uint64_t cols
 }
 
 // ---- copies and barriers -------------------------------------------------------
-// A box from (x, y, z) on into this CTA's shared memory, its bytes counted on this CTA's barrier.
+// A box from (x, y, z) on into this CTA's shared memory, its bytes counted on this CTA's barrier; by one elected
+// lane of the calling warp (all lanes call): alone in a branch it takes two to four times as long, 130 cycles and more.
 __device__ __forceinline__ void box_load(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+      "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
+      "@q cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(to),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// The same by one elected lane of the calling warp (all lanes call), for an instruction that spans a pair of
-// CTAs: counted on `bar`, an address in the cluster (at_rank).  A lane alone in a branch takes twice as long, 130 cycles.
+// The same for a pair of CTAs that issue matrix instructions as one: counted on `bar`, an address in the
+// cluster (at_rank).
 __device__ __forceinline__ void box_load_pair(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\n"
@@ -89,7 +91,19 @@ __device__ __forceinline__ void box_store(const CUtensorMap *map, uint32_t from,
                  : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// Until all of the calling thread's boxes have left shared memory, or are written.
+// Fetches a tensor map ahead of its first use, which waits 600 cycles for it otherwise.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// `bytes` of this CTA's shared memory to the address `to` in the cluster, counted on the barrier `bar` of the
+// same CTA; by one thread.
+__device__ __forceinline__ void bulk_push(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "r"(from),
+               "r"(bytes), "r"(bar)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until all of the calling thread's boxes and pushes have left shared memory, or are written.
 __device__ __forceinline__ void boxes_left() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void boxes_written() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Arrives on the barrier at the same offset in CTA `rank` of the cluster; what this thread has written is
@@ -246,17 +260,18 @@ __device__ __forceinline__ void place_groups(const Fp8Product &p, int tile, int 
 }
 
 // ---- results ---------------------------------------------------------------------
-template <class T>
-__device__ __forceinline__ void put(T *y, float v, int accumulate) {
-  if constexpr (sizeof(T) == 4) *y = accumulate ? *y + v : v;
-  else *y = from_f<T>(v);
-}
-// The same for a result that has its type already.
+// One result, added to what is there when fp32 and `accumulate`.  Volatile, since the compiler reads what it may
+// read without harm and every store would wait for memory (130 cycles a token).
 template <class T>
 __device__ __forceinline__ void put_as(T *y, T v, int accumulate) {
-  if constexpr (sizeof(T) == 4) *y = accumulate ? *y + v : v;
-  else *y = v;
+  if constexpr (sizeof(T) == 4) {
+    if (accumulate) v += *(volatile const T *)y;
+  }
+  *y = v;
 }
+template <class T>
+__device__ __forceinline__ void put(T *y, float v, int accumulate) { put_as(y, from_f<T>(v), accumulate); }
+
 // Eight sums, or four of fp32, as they lie in memory.
 template <class T>
 __device__ __forceinline__ uint4 pack16(const float *sum) {
