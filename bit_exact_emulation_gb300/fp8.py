@@ -76,11 +76,14 @@ def _blocks(n):
 
 
 def _codes(shape, dtype, dev):
-    """New codes whose rows start on 16-byte boundaries."""
+    """(new codes whose rows start on 16-byte boundaries, their pointer and row stride)."""
     cols = shape[-1]
     if cols % 16 == 0:
-        return ops._empty(shape, dtype=dtype, device=dev)
-    return ops._empty((*shape[:-1], (cols + 15) // 16 * 16), dtype=dtype, device=dev)[..., :cols]
+        t = ops._empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr(), cols
+    ld = (cols + 15) // 16 * 16
+    t = ops._empty((*shape[:-1], ld), dtype=dtype, device=dev)
+    return t.narrow(-1, 0, cols), t.data_ptr(), ld
 
 
 def _matrices(where, name, t, dtypes, dev, shape=None):
@@ -148,8 +151,9 @@ def quantize(x, out: str = "e4m3", rows: bool = True, columns: bool = False, off
         po, E = _offsets(w, offsets, dev)
     if rows:
         if q is None:
-            q = _codes((T, H), code, dev)
-        pq, ldq = _matrix(w, "q", q, (code,), dev, (T, H))
+            q, pq, ldq = _codes((T, H), code, dev)
+        else:
+            pq, ldq = _matrix(w, "q", q, (code,), dev, (T, H))
         if e is None:
             lde = _blocks(H)
             e = ops._empty((T, lde), dtype=torch.int8, device=dev)
@@ -199,21 +203,29 @@ def quantize_weight(weight, out: str = "e4m3", transposed: bool = False, q=None,
         _bad(w, "out must be 'e4m3' or 'e5m2'")
     code = _CODE[out]
     if q is None:
-        q = _codes((E, N, K), code, dev)
-    pq, ldq, sq = _matrices(w, "q", q, (code,), dev, (E, N, K))
+        q, pq, ldq = _codes((E, N, K), code, dev)
+        sq = N * ldq
+    else:
+        pq, ldq, sq = _matrices(w, "q", q, (code,), dev, (E, N, K))
     shape = E, _blocks(N), _blocks(K)
     if e is None:
         e = ops._empty(shape, dtype=torch.int8, device=dev)
-    pe = _dense(w, "e", e, shape, dev)
+        pe = e.data_ptr()
+    else:
+        pe = _dense(w, "e", e, shape, dev)
     pqt = ldqt = sqt = pet = 0
     if transposed:
         if qt is None:
-            qt = _codes((E, K, N), code, dev)
-        pqt, ldqt, sqt = _matrices(w, "qt", qt, (code,), dev, (E, K, N))
+            qt, pqt, ldqt = _codes((E, K, N), code, dev)
+            sqt = K * ldqt
+        else:
+            pqt, ldqt, sqt = _matrices(w, "qt", qt, (code,), dev, (E, K, N))
         shape = E, _blocks(K), _blocks(N)
         if et is None:
             et = ops._empty(shape, dtype=torch.int8, device=dev)
-        pet = _dense(w, "et", et, shape, dev)
+            pet = et.data_ptr()
+        else:
+            pet = _dense(w, "et", et, shape, dev)
     elif qt is not None or et is not None:
         _bad(w, "qt and et are written only when transposed")
     if N == 0 or K == 0:
