@@ -198,6 +198,30 @@ __device__ __forceinline__ void load_tile(Vec<T, 8> (&v)[8], const T *x, int64_t
     }
   }
 }
+// The same of 16-bit elements by copies into places of the thread's own, which are under way while it works on
+// the tile before (loaded when they are needed, 8192 x 8192 took 53.1 us in place of 49.8).
+template <class T>
+__device__ __forceinline__ void ask_tile(uint4 *places, const T *x, int64_t ld, int rows, int c, int H) {
+  const int r0 = 8 * (threadIdx.x >> 4);
+  x += r0 * ld + c;
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (r0 + i < rows && c < H) copy_async<16>(places + 256 * i + threadIdx.x, x + i * ld);
+  copy_commit();
+}
+template <class T>
+__device__ __forceinline__ void take_tile(Vec<T, 8> (&v)[8], const uint4 *places, int rows, int c, int H) {
+  const int r0 = 8 * (threadIdx.x >> 4);
+  copy_wait<0>();
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    if (r0 + i < rows && c < H) {
+      *(uint4 *)&v[i] = places[256 * i + threadIdx.x];
+    } else {
+      v[i] = Vec<T, 8>{};
+    }
+  }
+}
 // Column j's codes of the thread's eight rows, scaled by s.
 template <class T, class F, int J>
 __device__ __forceinline__ void turn_column(const Vec<T, 8> (&v)[8], float s, uint2 *turned) {
@@ -336,13 +360,22 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) columns_kernel(co
   __shared__ __align__(16) uint2 turned[128 * 16];
   __shared__ __align__(16) uint32_t peak[8][16 * kWords];
   __shared__ __align__(16) float scale[kBlock];
+  extern __shared__ __align__(16) uint4 places_ahead[];        // AHEAD: 2048
+  constexpr bool AHEAD = WIDE && sizeof(T) == 2;
   grid_go();
   const int tx = threadIdx.x & 15, warp = threadIdx.x >> 5, blocks = (a.H + kBlock - 1) / kBlock;
   const Place at = place_of(a, blockIdx.x);
   Vec<T, 8> v[8];
+  const T *x = (const T *)a.x + (int64_t)at.row * a.ldx;
+  if constexpr (AHEAD) ask_tile<T>(places_ahead, x, a.ldx, at.rows, blockIdx.y * kBlock + 8 * tx, a.H);
   for (int block = blockIdx.y; block < blocks; block += gridDim.y) {
     const int c = block * kBlock + 8 * tx;
-    load_tile<T, WIDE>(v, (const T *)a.x + (int64_t)at.row * a.ldx, a.ldx, at.rows, c, a.H);
+    if constexpr (AHEAD) {
+      take_tile<T>(v, places_ahead, at.rows, c, a.H);
+      ask_tile<T>(places_ahead, x, a.ldx, at.rows, c + (int)gridDim.y * kBlock, a.H);
+    } else {
+      load_tile<T, WIDE>(v, x, a.ldx, at.rows, c, a.H);
+    }
     uint32_t m[kWords];
     m[0] = column_peak<T, 0>(v), m[1] = column_peak<T, 1>(v), m[2] = column_peak<T, 2>(v), m[3] = column_peak<T, 3>(v);
     if constexpr (sizeof(T) == 4)
@@ -438,11 +471,19 @@ int quantize_typed(const QuantArgs &a, cudaStream_t st) {
     return launch_status();
   }
   const int places = (int)(mcemu_fp8_columns(a.T, a.E) / kBlock);
-  int across = 16 * sm_count() / places + 1;
-  across = across < blocks ? across : blocks;
+  // two rounds of the blocks of threads that run at a time, with so many tiles each, one's copies under way while
+  // the one before is worked on.  8192 x 8192: tiles each and microseconds 2 49.7, 4 49.8, 5 49.3, 8 55.2, 10 60.1.
+  int64_t turns = (int64_t)places * blocks / (6 * sm_count());
+  turns = turns < 1 ? 1 : turns < blocks ? turns : blocks;
+  const int64_t across = (blocks + turns - 1) / turns;
   const dim3 grid(places, across < 65535 ? across : 65535);
-  if (whole && rows_on(a.qt, a.ldqt, 1, 16)) columns_kernel<T, F, true><<<grid, 256, 0, st>>>(a, places);
-  else columns_kernel<T, F, false><<<grid, 256, 0, st>>>(a, places);
+  if (whole && rows_on(a.qt, a.ldqt, 1, 16)) {
+    constexpr int kAhead = sizeof(T) == 2 ? 32768 : 0;
+    if (!allow_smem<columns_kernel<T, F, true>>(kAhead)) return MCEMU_ERR_CUDA;
+    columns_kernel<T, F, true><<<grid, 256, kAhead, st>>>(a, places);
+  } else {
+    columns_kernel<T, F, false><<<grid, 256, 0, st>>>(a, places);
+  }
   return launch_status();
 }
 template <class T, class F>
