@@ -2,10 +2,16 @@
 //
 // A pair computes tiles of 256 rows of a by BN rows of b: each CTA holds 128 rows of a and half of
 // b's, and 128 x BN accumulators, twice, so that one set is drained into registers while the other fills.
+// The accumulators leave tensor memory every 1024 of k: the matrix unit truncates what it adds up.
 // The exponents go to tensor memory eight blocks at a time: for a those of the CTA's own rows, for b those
 // of all BN, in both CTAs.  (Four at a time the warps that bring them were the slowest: passing them on to
 // the issuing CTA takes a release at cluster scope, 0.95 us.)  Tensor memory has 512 columns: two sets of accumulators and two
 // of exponents (8 + 16 columns) leave BN at most 224.
+//
+// Bound by power where there is much work: 8192 x 8192 x 4096 takes 165 us in a burst (3.3 PFLOP/s), 177 to 193
+// under the 1.4 kW limit, at 1.5 GHz.  Of 177, copies without a use would take away 18, results without a
+// place 20, both 28; two warps that issue in place of one took away 40, copies by two whole warps in place of a
+// lane 15.  A library's product with a scale for each 32 of k, measured beside it: 172.
 #pragma once
 #include "fp8_tc.cuh"
 
@@ -274,10 +280,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_lead(acc_empty + 8 * set);
       }
-      // Out through shared memory, where the copy engine takes over: the matrix unit has both sets to go on with
-      // for two chunks, and stores by the threads themselves, 32 rows at a time, held them for longer (4300 cycles
-      // a tile, since all CTAs write at once).  What the copy engine cannot write (rows that end a group
-      // amid the warp's, other alignments) leaves by rows.
+      // Out through shared memory, where the copy engine takes over while the matrix unit goes on with both sets
+      // (weight gradients of 8 experts, 2048 x 4096 x 2048 each in fp32, 127 us; by the threads themselves 16 bytes of 32 rows at
+      // a time for every other piece 157, by rows 132; with larger pieces and fewer slots 130).  What the copy
+      // engine cannot write (rows that end a group amid the warp's, other alignments) leaves by rows.
       constexpr int kPiece = S::kPieceBytes / sizeof(T), kVec = 16 / sizeof(T);
       const int row0 = r.a + (int)rank * 128 + (warp & 3) * 32, col0 = r.b + (warp >> 2) * kCols, z = p.by_k ? r.g : 0;
       const uint32_t place = out + warp * 32 * S::kPieceBytes;

@@ -91,18 +91,23 @@ Choice pair_choice(int width, double busy, int64_t most, int blocks) {
   return {Fp8Plan{false, width, most, 1, blocks, 0}, (width == 224 ? 6.7 : 5.4) + rounds * (blocks * block + 0.4)};
 }
 // Parts of K (a cluster's CTAs): how many clusters run at a time is what a GB300 of 152 multiprocessors reports.
-Choice few_choice(int width, double busy, int64_t most, int blocks) {
+// A join's time goes by the tokens of a tile; by 4096 x 4096, one part and four: 16 tokens 7.6 and 5.4 us, 64
+// tokens 8.6 and 7.4, 80 tokens 11.2 and 9.2, 128 tokens 11.2 and 11.6.
+Choice few_choice(int width, int64_t tokens, double busy, int64_t most, int blocks) {
   constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-  const double block = width == 16 ? 0.115 : width == 32 ? 0.12 : width == 64 ? 0.15 : 0.24;
-  const double join = width == 16 ? 0.5 : width == 32 ? 0.9 : width == 64 ? 3.0 : 4.5, start = width == 128 ? 5.4 : 4.3;
+  const double n = (double)(tokens < width ? tokens : width), join = 0.3 + n * n / 3400;
+  const double start = width == 128 ? 5.2 : 4.1 + width * 0.005;
   Choice best{};
   for (int parts = 1; parts <= 8 && parts <= blocks; parts++) {
     const int per = (blocks + parts - 1) / parts;
     if (per * (parts - 1) >= blocks) continue;                  // a part would be empty
     if (parts > 1 && width > 32 && most > kClusters[parts]) continue;          // see fp8_few.cuh
+    const double full = busy * parts < 152 ? busy * parts / 152 : 1.0;
+    const double block = width == 128 ? 0.17 + 0.07 * full : width == 64 ? 0.12 + 0.03 * full : 0.11;
     const double rounds = (double)(int64_t)((busy + kClusters[parts] - 1) / kClusters[parts]);
     const double us = start + rounds * (per * block + (parts > 1 ? join : 0.2));
-    if (parts == 1 || us < best.us) best = {Fp8Plan{true, width, most, parts, per, kClusters[parts]}, us};
+    // fewer parts where that costs nothing (128 rows of 32 experts of 2048 x 4096: one 43.6 us, two 47.5)
+    if (parts == 1 || us < 0.97 * best.us) best = {Fp8Plan{true, width, most, parts, per, kClusters[parts]}, us};
   }
   return best;
 }
@@ -130,7 +135,7 @@ Fp8Plan plan_of(const Fp8Product &p) {
     if (width < 128 && width < (p.offsets ? mean + mean / 2 : mean)) continue;       // would read most weights twice
     const double high = p.offsets ? p.a.rows / (double)width + filled * 0.5 : (double)tiles(p.a.rows, width);
     const int64_t most = (p.offsets ? p.a.rows / width + filled : tiles(p.a.rows, width)) * across;
-    const Choice c = few_choice(width, (high > filled ? high : (double)filled) * across, most, blocks);
+    const Choice c = few_choice(width, mean, (high > filled ? high : (double)filled) * across, most, blocks);
     if (c.us < best.us) best = c;
   }
   return best.plan;

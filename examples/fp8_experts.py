@@ -4,8 +4,8 @@
      each block of 128, products of ragged groups, gradients of the input and of the weights from the
      same codes.  Errors against the unquantised layer, and against the quantised operands themselves
      in 64 bits: what is left there is the GPU's arithmetic.
-  2. The same operands through the emulated FP8 unit: the product's sums within 512 of k are
-     those of the emulated B200 unit, bit for bit.
+  2. The same operands through the emulated FP8 unit: the product's sums within a block are those of
+     the emulated B200 unit, bit for bit.
 
 Run on a GPU: python examples/fp8_experts.py
 """
@@ -73,8 +73,8 @@ def serve(x, W):
     w, ew, _, _ = fp8.quantize_weight(W)
     q, e, _, _ = fp8.quantize(x)
     y, one = fp8.linear(q, e, w, ew), fp8.linear(q[:1], e[:1], w, ew)
-    M, N, K = min(64, len(x)), min(64, len(W)), min(512, x.shape[1] // 32 * 32)
-    zero = lambda rows: torch.zeros(rows, -(-K // fp8.BLOCK), dtype=torch.int8, device=x.device)
+    M, N, K = min(64, len(x)), min(64, len(W)), fp8.BLOCK
+    zero = lambda rows: torch.zeros(rows, 1, dtype=torch.int8, device=x.device)
     sums = fp8.linear(q[:M, :K], zero(M), w[:N, :K], zero(N), out="fp32")
     unit = binding.Model(binding.preset_desc("b200_fp8"))
     emulated = binding.tile_gemm(unit, binding.tile(0, 16, 16, 32, 8), q[:M, :K], w[:N, :K],
