@@ -168,6 +168,16 @@ __device__ __forceinline__ void issue(const Fp8Product &p, const PairGroups &w, 
   tc::mbar_wait_warp(drain, 0, late);
 }
 
+// Rows of N results from shared memory, by a warp, as vectors of type V.
+template <class T, class V, int N>
+__device__ __forceinline__ void copy_rows(T *y, int64_t ld, const T *from, int rows) {
+  constexpr int kEach = sizeof(V) / sizeof(T), kRow = N / kEach;
+#pragma unroll 4
+  for (int t = threadIdx.x & 31; t < kRow * rows; t += 32) {
+    const int i = t / kRow, c = t % kRow * kEach;
+    *(V *)(y + i * ld + c) = *(const V *)(from + i * N + c);
+  }
+}
 template <class T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const Fp8Product p, const __grid_constant__ CUtensorMap ma,
@@ -322,18 +332,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const T *from = (const T *)(raw + (place - tc::smem_addr(raw)));
           T *y = (T *)p.y + z * p.stride_y + (int64_t)row0 * p.ldy + col0 + j;
           const int rows = min(32, r.end - row0), cols = min(kPiece, p.b.rows - col0 - j);
-          if (boxes && cols == kPiece && !p.accumulate) {
-#pragma unroll
-            for (int t = lane; t < kPiece / kVec * 32; t += 32) {
-              const int i = t / (kPiece / kVec), c = t % (kPiece / kVec) * kVec;
-              if (i < rows) *(uint4 *)(y + i * p.ldy + c) = *(const uint4 *)(from + i * kPiece + c);
-            }
-          } else {
+          const uint32_t where = (uint32_t)((uintptr_t)y | (uintptr_t)(p.ldy * (int64_t)sizeof(T)));
+          if (cols < kPiece || p.accumulate || where % (sizeof(T) == 2 ? 4 : 8)) {
 #pragma unroll 8
             for (int i = 0; i < rows; i++)
 #pragma unroll
               for (int c = lane; c < kPiece; c += 32)
                 if (c < cols) put_as(y + i * p.ldy + c, from[i * kPiece + c], p.accumulate);
+          } else if (where % 16 == 0) {
+            copy_rows<T, uint4, kPiece>(y, p.ldy, from, rows);
+          } else if (where % 8 == 0) {
+            copy_rows<T, uint2, kPiece>(y, p.ldy, from, rows);
+          } else {
+            copy_rows<T, typename std::conditional<sizeof(T) == 2, uint32_t, uint2>::type, kPiece>(y, p.ldy, from, rows);
           }
         }
       }

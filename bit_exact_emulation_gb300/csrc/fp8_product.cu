@@ -8,23 +8,60 @@ namespace {
 
 constexpr int kBlock = MCEMU_FP8_BLOCK;
 
-// Rows at any address to rows on 16-byte boundaries, sixteen bytes a thread; both operands by one kernel.
+// Sixteen bytes of a row of K from k on, zeros beyond its end, at any alignment: out of the four or five words that hold
+// them (of which three bytes may lie beside the row).  Without a branch, so that several are under way at once.
+__device__ __forceinline__ uint4 bytes16(const uint8_t *row, int k, int K) {
+  const uintptr_t p = (uintptr_t)(row + k);
+  const uint32_t *from = (const uint32_t *)(p & ~(uintptr_t)3);
+  const int off = (int)(p & 3), left = K - k;
+  uint32_t w[5], v[4];
+#pragma unroll
+  for (int i = 0; i < 5; i++) w[i] = 4 * i - off < left && left > 0 && (i < 4 || off) ? __ldg(from + i) : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    v[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
+    const int n = left - 4 * i;               // bytes that count
+    if (n < 4) v[i] = n <= 0 ? 0u : v[i] & 0xFFFFFFFFu >> (32 - 8 * n);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Rows at any address to rows on 16-byte boundaries, sixteen bytes a thread, kCopies times; both operands by one
+// kernel.  Of matrices for groups only those whose group has rows (or may have: an offset above the one before).
+constexpr int kCopies = 4, kBlockTasks = 256 * kCopies;
 struct Copy {
   const uint8_t *from;
-  int64_t ld, stride, tasks;
-  int rows;
+  int64_t ld, stride;
+  int rows, blocks;          // of one matrix: rows, and blocks of threads (0: no copy)
   uint8_t *to;
 };
-__global__ void __launch_bounds__(256) align_kernel(const Copy a, const Copy b, int K, int units) {
+__global__ void __launch_bounds__(256) align_kernel(const Copy a, const Copy b, int K, int units, const int32_t *offsets, int T) {
   grid_go();
-  int64_t task = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const bool second = task >= a.tasks;
-  if (second) task -= a.tasks;
-  const Copy &c = second ? b : a;
-  if (task >= c.tasks) return;
-  const int64_t row = task / units, matrix = row / c.rows;
-  const int k = (int)(task - row * units) * 16;
-  *(uint4 *)(c.to + task * 16) = row16((const int8_t *)c.from + matrix * c.stride + (row - matrix * c.rows) * c.ld, k, K, false);
+  int block = blockIdx.x, matrix = 0;
+  const bool second = block >= a.blocks;
+  if (second) {
+    matrix = (block - a.blocks) / b.blocks;
+    block = block - a.blocks - matrix * b.blocks;
+    if (offsets && min(__ldg(offsets + matrix + 1), T) <= max(__ldg(offsets + matrix), 0)) return;
+  }
+  const int rows = second ? b.rows : a.rows;
+  const int64_t ld = second ? b.ld : a.ld;
+  const uint8_t *from = second ? b.from + matrix * b.stride : a.from;
+  uint8_t *to = second ? b.to + (int64_t)matrix * rows * units * 16 : a.to;
+  const int64_t first = (int64_t)block * kBlockTasks, row0 = first / units;
+  const int skip = (int)(first - row0 * units);
+  uint4 v[kCopies];
+  int64_t place[kCopies];
+#pragma unroll
+  for (int n = 0; n < kCopies; n++) {
+    const int at = skip + n * 256 + (int)threadIdx.x, down = at / units, unit = at - down * units;
+    const int64_t row = row0 + down;
+    place[n] = row < rows ? row * units + unit : -1;
+    v[n] = bytes16(from + (row < rows ? row : 0) * ld, unit * 16, row < rows ? K : 0);
+  }
+#pragma unroll
+  for (int n = 0; n < kCopies; n++)
+    if (place[n] >= 0) *(uint4 *)(to + place[n] * 16) = v[n];
 }
 
 int64_t aligned_bytes(int64_t rows, int matrices, int K) { return rows * matrices * ((K + 15) & ~15); }
@@ -156,11 +193,12 @@ int launch_fp8_product(const Fp8Product &given, bool a_rows, bool b_rows, void *
   if (!a_rows || !b_rows) {
     const int ld = (p.K + 15) & ~15, matrices = p.by_k ? 1 : p.E;
     uint8_t *to_a = (uint8_t *)ws, *to_b = to_a + (a_rows ? 0 : aligned_bytes(p.a.rows, 1, p.K));
-    const Copy a{p.a.q, p.a.ld, 0, a_rows ? 0 : (int64_t)p.a.rows * (ld / 16), p.a.rows, to_a};
-    const Copy b{p.b.q, p.b.ld, p.b.stride, b_rows ? 0 : (int64_t)p.b.rows * matrices * (ld / 16), p.b.rows, to_b};
-    const int64_t blocks = (a.tasks + b.tasks + 255) / 256;
-    if (blocks > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
-    align_kernel<<<(unsigned)blocks, 256, 0, st>>>(a, b, p.K, ld / 16);
+    const auto blocks = [&](int rows) { return ((int64_t)rows * (ld / 16) + kBlockTasks - 1) / kBlockTasks; };
+    const int64_t blocks_a = a_rows ? 0 : blocks(p.a.rows), blocks_b = b_rows ? 0 : blocks(p.b.rows);
+    const int64_t all = blocks_a + blocks_b * matrices;
+    if (blocks_a > INT32_MAX || blocks_b > INT32_MAX || all > INT32_MAX) return MCEMU_ERR_UNSUPPORTED;
+    const Copy a{p.a.q, p.a.ld, 0, p.a.rows, (int)blocks_a, to_a}, b{p.b.q, p.b.ld, p.b.stride, p.b.rows, (int)blocks_b, to_b};
+    align_kernel<<<(unsigned)all, 256, 0, st>>>(a, b, p.K, ld / 16, p.by_k ? nullptr : p.offsets, p.T);
     const int rc = launch_status();
     if (rc != MCEMU_OK) return rc;                              // the operands would be whatever the workspace held
     if (!a_rows) p.a.q = to_a, p.a.ld = ld;

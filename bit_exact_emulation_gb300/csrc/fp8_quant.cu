@@ -94,12 +94,28 @@ __device__ __forceinline__ uint2 row_codes(const Vec<T, 8> &x, float s) {
   return make_uint2(codes4<F>(a.x, a.y, b.x, b.y), codes4<F>(c.x, c.y, d.x, d.y));
 }
 
-// Eight elements of a row from column c on, zeros beyond H, at any alignment.
+// Eight elements of a row from column c on, zeros beyond H, at any alignment: 16-bit ones out of the four or five
+// words that hold them (of which two bytes may lie beside the row).  Without a branch, so that the loads of
+// many rows are under way at once.
 template <class T>
 __device__ __forceinline__ Vec<T, 8> load8_any(const T *row, int c, int H) {
   Vec<T, 8> r;
+  if constexpr (sizeof(T) == 2) {
+    const uintptr_t p = (uintptr_t)(row + c);
+    const uint32_t *from = (const uint32_t *)(p & ~(uintptr_t)3);
+    const int odd = (int)(p >> 1) & 1, left = H - c;
+    uint32_t w[5];
 #pragma unroll
-  for (int i = 0; i < 8; i++) r.v[i] = c + i < H ? row[c + i] : from_f<T>(0.f);
+    for (int i = 0; i < 5; i++) w[i] = 2 * i - odd < left && left > 0 && (i < 4 || odd) ? __ldg(from + i) : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t v = __funnelshift_r(w[i], w[i + 1], 16 * odd);
+      ((uint32_t *)&r)[i] = 2 * i + 1 < left ? v : 2 * i < left ? v & 0xFFFFu : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) r.v[i] = c + i < H ? row[c + i] : from_f<T>(0.f);
+  }
   return r;
 }
 // Eight bytes of a row from column c on, `left` of them in it.
@@ -149,7 +165,9 @@ __global__ void __launch_bounds__(256) rows_kernel(const QuantArgs a, int blocks
   uint32_t m[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; i++) {
-    if (row0 + i * high < a.T && block < blocks) {
+    if constexpr (!WIDE) {
+      v[i] = load8_any<T>(x + i * high * a.ldx, c, row0 + i * high < a.T ? a.H : 0);
+    } else if (row0 + i * high < a.T && block < blocks) {
       v[i] = load8<T, WIDE>(x + i * high * a.ldx, c, a.H);
     } else {
       v[i] = Vec<T, 8>{};
@@ -192,7 +210,9 @@ __device__ __forceinline__ void load_tile(Vec<T, 8> (&v)[8], const T *x, int64_t
   x += r0 * ld;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    if (r0 + i < rows) {
+    if constexpr (!WIDE) {
+      v[i] = load8_any<T>(x + i * ld, c, r0 + i < rows ? H : 0);
+    } else if (r0 + i < rows) {
       v[i] = load8<T, WIDE>(x + i * ld, c, H);
     } else {
       v[i] = Vec<T, 8>{};
