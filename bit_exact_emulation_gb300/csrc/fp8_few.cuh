@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int j = 0; j < BT; j++) sum[j] = 0.f;
       for (int k = k0; k < k1; k += kChunk, ch++) {
         const uint32_t set = ch & 1;
-        tc::mbar_wait(acc_full + 8 * set, (ch >> 1) & 1, dead);
+        tc::mbar_wait_warp(acc_full + 8 * set, (ch >> 1) & 1, dead);       // a whole warp's verdict: what follows is one's
         __syncwarp();
         tc::fence_after();
         float v[2][16];
@@ -232,18 +232,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (j < r.n) asm volatile("st.shared.f32 [%0], %1;" ::"r"(send + j * 512 + row * 4), "f"(sum[j]) : "memory");
       tc::fence_async_smem();
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (threadIdx.x < parts) {
-        const int o = threadIdx.x, n_o = min(share, r.n - o * share);
-        tc::mbar_wait(join_empty, (turn & 1) ^ 1, dead);         // what was sent last has been taken
-        if (n_o > 0 && !dead)
+      if (warp == 0) {
+        tc::mbar_wait_warp(join_empty, (turn & 1) ^ 1, dead);    // what was sent last has been taken
+        const int o = lane, n_o = min(share, r.n - o * share);
+        if (o < (int)parts && n_o > 0 && !dead)
           bulk_push(at_rank(join + rank * share * 512, o), send + o * share * 512, n_o * 512, at_rank(join_full, o));
+        __syncwarp();
       }
-      __syncwarp();
-      tc::mbar_wait(join_full, turn & 1, dead);
+      tc::mbar_wait_warp(join_full, turn & 1, dead);
       if (!dead) (void)mbar_try_cluster(join_full, turn & 1);
       y += (int64_t)rank * share * p.ldy;
       const float *from = (const float *)(raw + (join - tc::smem_addr(raw))) + row;
-      // few instructions: what runs once in a launch waits for its code (unrolled: twice as long)
 #pragma unroll 1
       for (int i = 0; i < mine_n; i += 4) {
         float total[4] = {0.f, 0.f, 0.f, 0.f};

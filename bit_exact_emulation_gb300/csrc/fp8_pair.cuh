@@ -19,7 +19,7 @@ namespace mcemu {
 namespace fp8 {
 
 // Eight warps drain; then come one for the copies of a, two that issue matrix instructions, one for the exponents
-// of a, one for each 128 rows of b's, (13 + ...) and the last for the copies of b.
+// of a, one for each 128 rows of b's, and as the last one for the copies of b.
 constexpr int kPairThreads = 512;
 constexpr int kPairChunk = 8;                 // blocks along k between two drains
 // Registers of the warps that hold sums, and of the others: as many as 128 a thread at launch.
@@ -178,6 +178,7 @@ __device__ __forceinline__ void copy_rows(T *y, int64_t ld, const T *from, int r
     *(V *)(y + i * ld + c) = *(const V *)(from + i * N + c);
   }
 }
+
 template <class T, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const Fp8Product p, const __grid_constant__ CUtensorMap ma,
@@ -186,8 +187,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   constexpr int kStages = S::kStages, kBlocks = S::kBlocks, kSlots = S::kScaleSlots, kCols = BN / 2;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tc::smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t scales = base + kBlocks * S::kBlockBytes, out = scales + kSlots * S::kSlotBytes, full = out + S::kOutBytes, empty = full + 8 * kStages,
-                 sf_full = empty + 8 * kBlocks, sf_empty = sf_full + 8 * kSlots, acc_full = sf_empty + 8 * kSlots,
+  const uint32_t scales = base + kBlocks * S::kBlockBytes, out = scales + kSlots * S::kSlotBytes, full = out + S::kOutBytes,
+                 empty = full + 8 * kStages, sf_full = empty + 8 * kBlocks, sf_empty = sf_full + 8 * kSlots, acc_full = sf_empty + 8 * kSlots,
                  acc_empty = acc_full + 16, drain = acc_empty + 16, pass = drain + 16, slot = pass + 16;
   int *at = (int *)(raw + (slot + 16 - tc::smem_addr(raw))), *before = at + MCEMU_FP8_MAX_GROUPS + 1;
   const int warp = tc::warp_number(), lane = threadIdx.x & 31;
@@ -274,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int j = 0; j < kCols; j++) sum[j] = 0.f;
       for (int k = r.k0; k < r.k1; k += kPairChunk, ch++) {
         const uint32_t set = ch & 1;
-        tc::mbar_wait(acc_full + 8 * set, (ch >> 1) & 1, dead);
+        tc::mbar_wait_warp(acc_full + 8 * set, (ch >> 1) & 1, dead);       // a whole warp's verdict: what follows is one's
         __syncwarp();
         tc::fence_after();
         float v[2][16];

@@ -18,7 +18,7 @@ namespace fp8 {
 
 constexpr int kBlock = MCEMU_FP8_BLOCK;
 constexpr int kTileBytes = 128 * kBlock;      // 128 rows of a block
-// Blocks along k between two drains of the accumulators: the matrix unit truncates what it adds up.
+// Blocks along k between two drains of few rows' accumulators: the matrix unit truncates what it adds up.
 constexpr int kChunk = 4;
 constexpr int kScaleBytes = 512;              // four blocks' exponents of 128 rows
 
@@ -260,8 +260,7 @@ __device__ __forceinline__ void place_groups(const Fp8Product &p, int tile, int 
 }
 
 // ---- results ---------------------------------------------------------------------
-// One result, added to what is there when fp32 and `accumulate`.  Volatile, since the compiler reads what it may
-// read without harm and every store would wait for memory (130 cycles a token).
+// One result, added to what is there when fp32 and `accumulate`.  Volatile, so that nothing is read otherwise.
 template <class T>
 __device__ __forceinline__ void put_as(T *y, T v, int accumulate) {
   if constexpr (sizeof(T) == 4) {
