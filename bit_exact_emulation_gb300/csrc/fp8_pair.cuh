@@ -2,7 +2,9 @@
 //
 // A pair computes tiles of 256 rows of a by BN rows of b: each CTA holds 128 rows of a and half of
 // b's, and 128 x BN accumulators, twice, so that one set is drained into registers while the other fills.
-// The accumulators leave tensor memory every 1024 of k: the matrix unit truncates what it adds up.
+// The accumulators leave tensor memory every 1024 of k: the matrix unit truncates what it adds up.  Relative errors
+// of 2048 x 4096 x 16384 against 64 bits, for normal values, with large channels and for positive ones: 9.7e-8, 1.2e-7
+// and 1.9e-7; of a library's fp32 product of the same numbers 1.9e-7, 2.5e-7 and 8.4e-7.
 // The exponents go to tensor memory eight blocks at a time: for a those of the CTA's own rows, for b those
 // of all BN, in both CTAs.  (Four at a time the warps that bring them were the slowest: passing them on to
 // the issuing CTA takes a release at cluster scope, 0.95 us.)  Tensor memory has 512 columns: two sets of accumulators and two

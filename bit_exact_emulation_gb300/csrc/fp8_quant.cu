@@ -152,7 +152,7 @@ __device__ __forceinline__ void put8(uint8_t *row, int c, int left, uint2 v) {
 
 // ---- rows alone -------------------------------------------------------------------
 // Sixteen lanes to a block of a row, eight elements each, kRows rows a thread; a block of threads takes `wide`
-// (1 to 16) blocks of 16 / wide * kRows rows.
+// (1 to 16) blocks of 16 / wide * kRows rows.  8192 x 8192 bf16 with two rows a thread 34.7 us, four 32.5, eight 43.2.
 constexpr int kRows = 4;
 template <class T, class F, bool WIDE>
 __global__ void __launch_bounds__(256) rows_kernel(const QuantArgs a, int blocks, int wide) {

@@ -75,6 +75,9 @@ def _blocks(n):
     return (n + BLOCK - 1) // BLOCK
 
 
+_strided = torch.empty_strided
+
+
 def _codes(shape, dtype, dev):
     """(new codes whose rows start on 16-byte boundaries, their pointer and row stride)."""
     cols = shape[-1]
@@ -82,8 +85,8 @@ def _codes(shape, dtype, dev):
         t = ops._empty(shape, dtype=dtype, device=dev)
         return t, t.data_ptr(), cols
     ld = (cols + 15) // 16 * 16
-    t = ops._empty((*shape[:-1], ld), dtype=dtype, device=dev)
-    return t.narrow(-1, 0, cols), t.data_ptr(), ld
+    t = _strided(shape, (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1), dtype=dtype, device=dev)
+    return t, t.data_ptr(), ld
 
 
 def _matrices(where, name, t, dtypes, dev, shape=None):

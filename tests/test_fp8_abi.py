@@ -154,6 +154,7 @@ def F(monkeypatch):
     monkeypatch.setattr(ops, "_device", lambda where, t: -1)
     monkeypatch.setattr(ops, "_stream", lambda dev: 0)
     monkeypatch.setattr(ops, "_empty", lambda *s, dtype, device: z(*s, dt=dtype))
+    monkeypatch.setattr(fp8, "_strided", lambda s, st, dtype, device: torch.empty_strided(s, st, dtype=dtype, device="meta"))
     return fp8
 
 
