@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) columns_kernel(co
     const int c = block * kBlock + 8 * tx;
     if constexpr (AHEAD) {
       take_tile<T>(v, places_ahead, at.rows, c, a.H);
-      ask_tile<T>(places_ahead, x, a.ldx, at.rows, c + (int)gridDim.y * kBlock, a.H);
+      if (block + (int)gridDim.y < blocks)    // a column beyond that may be more than 32 bits count
+        ask_tile<T>(places_ahead, x, a.ldx, at.rows, c + (int)gridDim.y * kBlock, a.H);
     } else {
       load_tile<T, WIDE>(v, x, a.ldx, at.rows, c, a.H);
     }
