@@ -17,6 +17,8 @@ constexpr int kMost = INT32_MAX - 65535;
 bool too_large(int a, int b, int c = 0) { return a > kMost || b > kMost || c > kMost; }
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 bool rows_of(const void *p, int64_t ld, int64_t stride = 0) { return aligned(p, 16) && ld % 16 == 0 && stride % 16 == 0; }
+// A single row has no next one, and the pitch that the copy engine wants.
+int64_t pitch_of(int rows, int K, int64_t ld) { return rows == 1 ? ((int64_t)K + 15) & ~(int64_t)15 : ld; }
 int blocks_of(int n) { return n / MCEMU_FP8_BLOCK + (n % MCEMU_FP8_BLOCK != 0); }
 bool bad_groups(int E) { return E < 1 || E > MCEMU_FP8_MAX_GROUPS; }
 
@@ -95,6 +97,8 @@ extern "C" int mcemu_fp8_linear(int M, int N, int K, int x_fmt, const uint8_t *x
   if ((K > 0 && (!x || !w || !ex || !ew)) || !y) return MCEMU_ERR_INVALID_ARG;
   if (ldx < K || ldw < K || ldy < N || ldex < blocks_of(K) || ldew < blocks_of(K)) return MCEMU_ERR_INVALID_ARG;
   if (!aligned(y, bytes_of(out_fmt)) || !aligned(bias, 4)) return MCEMU_ERR_ALIGNMENT;
+  ldx = pitch_of(M, K, ldx);
+  ldw = pitch_of(N, K, ldw);
   const bool xr = rows_of(x, ldx), wr = rows_of(w, ldw);
   const int st = check_ws(workspace, ws_bytes, mcemu_fp8_linear_workspace(M, N, K, xr, wr));
   if (st != MCEMU_OK) return st;
@@ -121,6 +125,8 @@ extern "C" int mcemu_fp8_grouped_linear(int T, int E, int N, int K, int x_fmt, c
   if ((K > 0 && (!x || !w || !ex || !ew)) || !y || !offsets) return MCEMU_ERR_INVALID_ARG;
   if (ldx < K || ldw < K || ldy < N || ldex < blocks_of(K) || (E > 1 && w_stride < (N - 1) * ldw + K)) return MCEMU_ERR_INVALID_ARG;
   if (!aligned(y, bytes_of(out_fmt)) || !aligned(offsets, 4)) return MCEMU_ERR_ALIGNMENT;
+  ldx = pitch_of(T, K, ldx);
+  ldw = pitch_of(N, K, ldw);
   const bool xr = rows_of(x, ldx), wr = rows_of(w, ldw, E > 1 ? w_stride : 0);
   const int st = check_ws(workspace, ws_bytes, mcemu_fp8_grouped_linear_workspace(T, E, N, K, xr, wr));
   if (st != MCEMU_OK) return st;

@@ -266,7 +266,7 @@ def linear(x, ex, weight, ew, bias=None, out: str = "bf16", y=None, accumulate: 
     else:
         py, ldy = _matrix(w, "y", y, (_OUT[out],), dev, (M, N))
     L = _lib or lib()
-    xr, wr = (px | ldx) % 16 == 0, (pw | ldw) % 16 == 0
+    xr, wr = (px | (ldx if M != 1 else 0)) % 16 == 0, (pw | (ldw if N != 1 else 0)) % 16 == 0
     ws, pws, nws = (None, None, 0) if xr and wr else _workspace(w, L.mcemu_fp8_linear_workspace(M, N, K, xr, wr), dev, workspace)
     st = L.mcemu_fp8_linear(M, N, K, _CODE_FMT[x.dtype], px, ldx, pex, ldex, _CODE_FMT[weight.dtype], pw, ldw, pew, ldew, tiles, pb,
                             FMT[out], accumulate, py, ldy, pws, nws, ops._stream(dev))
@@ -300,7 +300,7 @@ def grouped_linear(x, ex, weight, ew, offsets, out: str = "bf16", y=None, worksp
     else:
         py, ldy = _matrix(w, "y", y, (_OUT[out],), dev, (T, N))
     L = _lib or lib()
-    xr, wr = (px | ldx) % 16 == 0, (pw | ldw | (sw if E > 1 else 0)) % 16 == 0
+    xr, wr = (px | (ldx if T != 1 else 0)) % 16 == 0, (pw | (ldw if N != 1 else 0) | (sw if E > 1 else 0)) % 16 == 0
     ws, pws, nws = (None, None, 0) if xr and wr else _workspace(w, L.mcemu_fp8_grouped_linear_workspace(T, E, N, K, xr, wr), dev, workspace)
     st = L.mcemu_fp8_grouped_linear(T, E, N, K, _CODE_FMT[x.dtype], px, ldx, pex, ldex, _CODE_FMT[weight.dtype], pw, ldw, sw, pew, po,
                                     FMT[out], py, ldy, pws, nws, ops._stream(dev))

@@ -87,7 +87,8 @@ int mcemu_fp8_quantize_weight(int fmt, int out_fmt, int E, int N, int K, const v
  *   weight's gradient  x = dY's columns, w = the activations' columns, w_tiles = 0
  * workspace: mcemu_fp8_linear_workspace(M, N, K, x_rows, w_rows) bytes, 16-byte
  * aligned; may be NULL where that is 0.  x_rows, w_rows: 1 when every row of the
- * operand starts on a 16-byte boundary; an operand of other rows is copied there. */
+ * operand starts on a 16-byte boundary (of a single row the pointer decides); an operand
+ * of other rows is copied there. */
 int mcemu_fp8_linear(int M, int N, int K, int x_fmt, const uint8_t *x, int64_t ldx, const int8_t *ex, int64_t ldex,
                      int w_fmt, const uint8_t *w, int64_t ldw, const int8_t *ew, int64_t ldew, int w_tiles,
                      const float *bias, int out_fmt, int accumulate, void *y, int64_t ldy, void *workspace,

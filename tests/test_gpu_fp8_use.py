@@ -425,3 +425,20 @@ def test_fp8_experts_example(F):
     assert got["output_error"] < 0.08 and got["served_error"] < 0.08 and got["one_token_error"] < 0.08
     assert got["input_gradient_error"] < 0.12 and got["weight_gradient_error"] < 0.12
     assert got["error_of_the_arithmetic"] < 1e-5
+
+
+@pytest.mark.parametrize("K", [1, 33, 2049])
+@pytest.mark.parametrize("M,N", [(1, 300), (1, 1), (40, 1)])
+def test_a_single_row_of_any_length_is_read_in_place(F, monkeypatch, M, N, K):
+    """Only where it begins counts, so that no workspace is needed."""
+    monkeypatch.setattr(F, "_workspace", lambda *a: pytest.fail("a workspace was asked for"))
+    g = gen(M + N + K)
+    x, w = whole(g, (M, K), "e4m3"), whole(g, (N, K), "e5m2")
+    ex, ew = exps(g, M, blocks(K)), exps(g, 1, blocks(N), blocks(K))
+    x, w = (t if len(t) == 1 else strided(t, -K % 16) for t in (x, w))
+    want = of_rows(x, ex) @ of_tiles(w, ew[0]).T
+    assert same(F.linear(x, ex, w, ew[0], out="fp32"), rounded(want, "fp32"))
+    if M == 1:
+        offsets = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        assert same(F.grouped_linear(x, ex, w[None], ew, offsets, out="fp32"), rounded(want, "fp32"))
+    F.check()
