@@ -53,6 +53,7 @@ struct Fp8Product {
   void *y;
   int64_t ldy, stride_y;
   int out_fmt, accumulate;
+  bool turned;               // a and b have changed places: y = b a^T, and the groups and `T` are b's
 };
 // a_rows, b_rows: every row of the operand starts on a 16-byte boundary (no copy of it is needed).
 size_t fp8_product_workspace(int rows_a, int rows_b, int matrices_b, int K, bool a_rows, bool b_rows);

@@ -10,6 +10,11 @@
 // the issuing CTA takes a release at cluster scope, 0.95 us.)  Tensor memory has 512 columns: two sets of accumulators and two
 // of exponents (8 + 16 columns) leave BN at most 224.
 //
+// TURNED: the operands have changed places, so that a lane's row is a column of y. A piece of results then leaves as rows of 32
+// neighbours, 128 bytes in fp32, from any row on: groups that begin amid a tile of tokens need no other way out, and
+// only the pieces at their ends go by lanes.  Turned and not, microseconds: 16384 rows of 16 experts of 4096 x 2048 106 and 120,
+// weight gradients of 8 experts, 4096 x 2048 each in fp32, 120 and 131, 8192 x 8192 x 4096 183 and 190 under the power limit.
+//
 // Bound by power where there is much work: 8192 x 8192 x 4096 takes 165 us in a burst (3.3 PFLOP/s), 177 to 193
 // under the 1.4 kW limit, at 1.5 GHz.  Of 177, copies without a use would take away 18, results without a
 // place 20, both 28; two warps that issue in place of one took away 40, copies by two whole warps in place of a
@@ -44,34 +49,38 @@ struct Pair {
 };
 
 struct PairUnit {
-  int g, a, end, b, k0, k1;  // group, first row of a and where a's rows end, first row of b, blocks along k
+  int g, a, b, end, k0, k1;  // group, first rows, where the rows of the one with groups end, blocks along k
 };
 struct PairGroups {
   const int *at, *before;
-  int tiles_a, tiles_b, blocks;      // tiles of a (by_k), of b; blocks along k (not by_k)
+  int tiles_a, tiles_b, blocks;      // tiles of all rows of a, of b; blocks along k (not by_k)
 };
+template <bool TURNED>
 __device__ __forceinline__ int units_of(const Fp8Product &p, const PairGroups &w) {
-  return (p.by_k ? p.E * w.tiles_a : w.before[p.E]) * w.tiles_b;
+  return p.by_k ? p.E * w.tiles_a * w.tiles_b : w.before[p.E] * (TURNED ? w.tiles_a : w.tiles_b);
 }
-// The u-th unit; g is the group of an earlier one.  Bands of eight tiles of a, so that the pairs at work
+// The u-th unit; g is the group of an earlier one.  Groups are of a's rows, TURNED of b's.  Bands of eight tiles of a, so that the pairs at work
 // share both operands in L2.
-__device__ __forceinline__ PairUnit unit_at(const Fp8Product &p, const PairGroups &w, int bn, int u, int &g) {
+template <int BN, bool TURNED>
+__device__ __forceinline__ PairUnit unit_at(const Fp8Product &p, const PairGroups &w, int u, int &g) {
   PairUnit r;
-  int t, tiles_a = w.tiles_a;
+  int t, tiles_a = w.tiles_a, tiles_b = w.tiles_b;
   if (p.by_k) {
-    const int each = tiles_a * w.tiles_b;
+    const int each = tiles_a * tiles_b;
     g = u / each;
     t = u - g * each;
   } else {
-    while (u >= w.before[g + 1] * w.tiles_b) g++;
-    t = u - w.before[g] * w.tiles_b;
-    tiles_a = w.before[g + 1] - w.before[g];
+    const int others = TURNED ? tiles_a : tiles_b;
+    while (u >= w.before[g + 1] * others) g++;
+    t = u - w.before[g] * others;
+    (TURNED ? tiles_b : tiles_a) = w.before[g + 1] - w.before[g];
   }
-  const int band = t / (8 * w.tiles_b), rest = t - band * 8 * w.tiles_b, width = min(8, tiles_a - band * 8);
+  const int band = t / (8 * tiles_b), rest = t - band * 8 * tiles_b, width = min(8, tiles_a - band * 8);
   r.g = g;
-  r.a = (p.by_k ? 0 : w.at[g]) + (band * 8 + rest % width) * 256;
-  r.end = p.by_k ? p.a.rows : w.at[g + 1];
-  r.b = rest / width * bn;
+  const int begin = p.by_k ? 0 : w.at[g];
+  r.a = (TURNED ? 0 : begin) + (band * 8 + rest % width) * 256;
+  r.b = (TURNED ? begin : 0) + rest / width * BN;
+  r.end = p.by_k ? (TURNED ? p.b : p.a).rows : w.at[g + 1];
   r.k0 = p.by_k ? w.at[g] : 0;
   r.k1 = p.by_k ? w.at[g + 1] : w.blocks;
   return r;
@@ -79,7 +88,7 @@ __device__ __forceinline__ PairUnit unit_at(const Fp8Product &p, const PairGroup
 
 // A warp's way through the units, bringing eight blocks' exponents of 128 rows to each slot: of the tile's rows
 // of a, or of b, from `skip` on.
-template <int BN>
+template <int BN, bool TURNED>
 __device__ __forceinline__ void feed_scales(const Fp8Product &p, const PairGroups &w, int first, int step, int units, bool of_a,
                                             int skip, uint32_t scales, uint32_t sf_full, uint32_t sf_empty, bool &dead) {
   using S = Pair<BN>;
@@ -87,9 +96,10 @@ __device__ __forceinline__ void feed_scales(const Fp8Product &p, const PairGroup
   uint32_t turn = 0;
   int g = 0;
   for (int u = first; u < units && !dead; u += step) {
-    const PairUnit r = unit_at(p, w, BN, u, g);
-    if (of_a) v.rows(p.a, 0, r.a + skip);
-    else v.rows(p.b, p.by_k ? 0 : r.g, r.b + skip);
+    const PairUnit r = unit_at<BN, TURNED>(p, w, u, g);
+    const int matrix = of_a != TURNED || p.by_k ? 0 : r.g;
+    if (of_a) v.rows(p.a, matrix, r.a + skip);
+    else v.rows(p.b, matrix, r.b + skip);
     for (int k = r.k0; k < r.k1; k += kPairChunk, turn++) {
       const uint32_t sf = turn % S::kScaleSlots, to = scales + sf * S::kSlotBytes;
       uint32_t x[2][4];
@@ -110,7 +120,7 @@ __device__ __forceinline__ void feed_scales(const Fp8Product &p, const PairGroup
 // cost a warp some 2700 cycles for four blocks, and the matrix unit takes 1800 for them.
 // A stage's barrier tells one use from the next by parity alone, so that a stage may be waited for only when its
 // use before is known to be over: the warps pass a token (`pass`) when the last stage of a chunk has come.
-template <int BN>
+template <int BN, bool TURNED>
 __device__ __forceinline__ void issue(const Fp8Product &p, const PairGroups &w, int first, int step, int units, uint32_t set,
                                       uint32_t tmem, uint32_t base, uint32_t scales, uint32_t full, uint32_t empty,
                                       uint32_t sf_full, uint32_t sf_empty, uint32_t acc_full, uint32_t acc_empty,
@@ -121,7 +131,7 @@ __device__ __forceinline__ void issue(const Fp8Product &p, const PairGroups &w, 
   uint32_t s = 0, phase = 0, ch = 0, parity = 1;
   int g = 0;
   for (int u = first; u < units && !dead; u += step) {
-    const PairUnit r = unit_at(p, w, BN, u, g);
+    const PairUnit r = unit_at<BN, TURNED>(p, w, u, g);
     for (int k = r.k0; k < r.k1 && !dead; k += kPairChunk, ch++) {
       const int n = min(kPairChunk, r.k1 - k);
       if ((ch & 1) != set) {
@@ -181,7 +191,7 @@ __device__ __forceinline__ void copy_rows(T *y, int64_t ld, const T *from, int r
   }
 }
 
-template <class T, int BN>
+template <class T, int BN, bool TURNED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const Fp8Product p, const __grid_constant__ CUtensorMap ma,
                 const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap my, bool boxes) {
@@ -214,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 8) tc::tmem_alloc<2>(slot, 512);
   grid_go();
   grid_wait();                                // operands and offsets may be the work of the kernel before
-  if (warp == 0) place_groups(p, 256, at, before);
+  if (warp == 0) place_groups(p, TURNED ? BN : 256, at, before);
   tc::fence_before();
   tc::cluster_sync();
   tc::fence_after();
@@ -223,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tmem = __shfl_sync(0xFFFFFFFFu, tmem, 0);
   bool dead = false;
   const PairGroups w{at, before, (p.a.rows + 255) / 256, (p.b.rows + BN - 1) / BN, (p.K + kBlock - 1) / kBlock};
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1, units = units_of(p, w);
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1, units = units_of<TURNED>(p, w);
   int g = 0;
 
   if (warp >= 8) pair_give_registers();
@@ -233,8 +243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t lead = at_rank(full, 0);
     uint32_t s = 0, stage = 0, phase = 1, it = 0;
     for (int u = first; u < units && !dead; u += step) {
-      const PairUnit r = unit_at(p, w, BN, u, g);
-      const int y = of_a ? r.a + (int)rank * 128 : r.b + (int)rank * (BN / 2), z = of_a || p.by_k ? 0 : r.g;
+      const PairUnit r = unit_at<BN, TURNED>(p, w, u, g);
+      const int y = of_a ? r.a + (int)rank * 128 : r.b + (int)rank * (BN / 2), z = of_a != TURNED || p.by_k ? 0 : r.g;
       for (int k = r.k0; k < r.k1 && !dead; k += 2, it++) {
         const int n = min(2, r.k1 - k);
 #pragma unroll
@@ -260,18 +270,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 9 || warp == 10) {
     const uint32_t set = warp - 9;
     if (rank == 0)
-      issue<BN>(p, w, first, step, units, set, tmem, base, scales, full, empty, sf_full, sf_empty, acc_full + 8 * set,
+      issue<BN, TURNED>(p, w, first, step, units, set, tmem, base, scales, full, empty, sf_full, sf_empty, acc_full + 8 * set,
                 acc_empty + 8 * set, drain + 8 * set, pass, dead);
   } else if (warp == 11) {
-    feed_scales<BN>(p, w, first, step, units, true, (int)rank * 128, scales, sf_full, sf_empty, dead);
+    feed_scales<BN, TURNED>(p, w, first, step, units, true, (int)rank * 128, scales, sf_full, sf_empty, dead);
   } else if (warp > 11 && warp < 11 + S::kRowTiles) {
-    feed_scales<BN>(p, w, first, step, units, false, (warp - 12) * 128, scales + (warp - 11) * 2 * kScaleBytes, sf_full, sf_empty, dead);
+    feed_scales<BN, TURNED>(p, w, first, step, units, false, (warp - 12) * 128, scales + (warp - 11) * 2 * kScaleBytes, sf_full, sf_empty, dead);
   } else if (warp < 8) {
     pair_take_registers();
     const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + (warp >> 2) * kCols;
     uint32_t ch = 0;
     for (int u = first; u < units; u += step) {
-      const PairUnit r = unit_at(p, w, BN, u, g);
+      const PairUnit r = unit_at<BN, TURNED>(p, w, u, g);
       float sum[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; j++) sum[j] = 0.f;
@@ -301,7 +311,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int row0 = r.a + (int)rank * 128 + (warp & 3) * 32, col0 = r.b + (warp >> 2) * kCols, z = p.by_k ? r.g : 0;
       const uint32_t place = out + warp * 32 * S::kPieceBytes;
       const bool whole = boxes && (row0 + 32 <= r.end || r.end == p.a.rows);
-      if (p.bias) {
+      if constexpr (TURNED) {                 // a lane's row of a is a column of y
+        if (p.bias) {
+          const float b = row0 + lane < p.a.rows ? __ldg(p.bias + row0 + lane) : 0.f;
+#pragma unroll
+          for (int j = 0; j < kCols; j++) sum[j] += b;
+        }
+      } else if (p.bias) {
         if (((uintptr_t)p.bias & 15) == 0 && col0 + kCols <= p.b.rows) {
 #pragma unroll
           for (int j = 0; j < kCols; j += 4) {
@@ -313,7 +329,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           for (int j = 0; j < kCols; j++) sum[j] += col0 + j < p.b.rows ? __ldg(p.bias + col0 + j) : 0.f;
         }
       }
-      if (row0 >= r.end || dead) continue;
+      if (row0 >= (TURNED ? p.a.rows : r.end) || dead) continue;
+      if constexpr (TURNED) {
+        T *y = (T *)p.y + z * p.stride_y + (int64_t)col0 * p.ldy + row0 + lane;
+#pragma unroll
+        for (int j = 0; j < kCols; j += kPiece) {
+          if (col0 + j >= r.end) break;
+          if (boxes && (col0 + j + kPiece <= r.end || r.end == p.b.rows)) {
+            if (lane == 0) boxes_left();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kPiece; i++) put_shared<T>(place + (i * 32 + lane) * (int)sizeof(T), sum[j + i]);
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) box_store(&my, place, row0, col0 + j, z, p.accumulate);
+          } else if (row0 + lane < p.a.rows) {
+#pragma unroll
+            for (int i = 0; i < kPiece; i++)
+              if (col0 + j + i < r.end) put(y + (j + i) * p.ldy, sum[j + i], p.accumulate);
+          }
+        }
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < kCols; j += kPiece) {
         if (col0 + j >= p.b.rows) break;
@@ -363,19 +400,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 }
 
-template <class T, int BN>
+template <class T, int BN, bool TURNED>
 int launch_pair(const Fp8Product &p, const CUtensorMap &ma, const CUtensorMap &mb, int64_t units, cudaStream_t st) {
   constexpr int kSize = sizeof(T);
   const bool boxes = rows16(p.y, p.ldy, kSize) && (!p.by_k || p.E == 1 || p.stride_y * kSize % 16 == 0);
   CUtensorMap my = ma;
   if (boxes) {
-    const int rc = tensor_map(&my, p.out_fmt, p.y, p.b.rows, p.a.rows, p.ldy, p.by_k ? p.E : 1, p.stride_y,
-                              Pair<BN>::kPieceBytes / kSize, 32);
+    constexpr int kPiece = Pair<BN>::kPieceBytes / kSize;
+    const int rc = TURNED ? tensor_map(&my, p.out_fmt, p.y, p.a.rows, p.b.rows, p.ldy, p.by_k ? p.E : 1, p.stride_y, 32, kPiece)
+                          : tensor_map(&my, p.out_fmt, p.y, p.b.rows, p.a.rows, p.ldy, p.by_k ? p.E : 1, p.stride_y, kPiece, 32);
     if (rc != MCEMU_OK) return rc;
   }
-  if (!allow_smem<pair_kernel<T, BN>>(Pair<BN>::kSmem)) return MCEMU_ERR_CUDA;
+  if (!allow_smem<pair_kernel<T, BN, TURNED>>(Pair<BN>::kSmem)) return MCEMU_ERR_CUDA;
   const int pairs = units < sm_count() / 2 ? (int)units : sm_count() / 2;
-  return launch_early(pair_kernel<T, BN>, dim3(2 * pairs), dim3(kPairThreads), Pair<BN>::kSmem, st, p, ma, mb, my, boxes);
+  return launch_early(pair_kernel<T, BN, TURNED>, dim3(2 * pairs), dim3(kPairThreads), Pair<BN>::kSmem, st, p, ma, mb, my, boxes);
 }
 
 }  // namespace fp8

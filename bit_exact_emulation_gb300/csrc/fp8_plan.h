@@ -10,6 +10,7 @@ struct Fp8Plan {
   int64_t units;             // tiles at most (a group's rows are known on the device alone)
   int parts, per;            // few: CTAs that share K, blocks of 128 to each
   int64_t clusters;          // and how many such clusters run at a time
+  bool turned;               // pair: with the operands exchanged
 };
 int launch_fp8_pair(const Fp8Product &p, const Fp8Plan &plan, void *stream);
 int launch_fp8_few(const Fp8Product &p, const Fp8Plan &plan, void *stream);

@@ -1,5 +1,7 @@
 // fp8_product.cu -- FP8 products: which form a call takes, operands whose rows the copy engine
 // cannot read, and sums of nothing.
+#include <utility>
+
 #include "fp8_plan.h"
 #include "ops_common.cuh"
 
@@ -116,16 +118,18 @@ int launch_empty(const Fp8Product &p, cudaStream_t st) {
 //   256 x 8192 x 8192   22.3      22.1         19.6
 //   1024 x 8192 x 8192  72.1      42.8         61.9
 //
-// `busy` tiles are expected and `most` possible (a group's rows are known on the device alone).
+// `busy` tiles are expected and `most` possible (a group's rows are known on the device alone).  `out` is what a tile
+// costs beside its blocks: turned (fp8_pair.cuh) 0.4, else in 16 bits 0.55 and in fp32 1.1 (weight gradients of 8
+// experts, 2048 x 4096 each: 16 rounds of tiles 123 us, turned 17 rounds 119).
 constexpr int kPairs = 76;
 struct Choice {
   Fp8Plan plan;
   double us;
 };
-Choice pair_choice(int width, double busy, int64_t most, int blocks) {
+Choice pair_choice(int width, double busy, int64_t most, int blocks, double out) {
   const double full = busy < kPairs ? busy / kPairs : 1.0, rounds = (double)(int64_t)((busy + kPairs - 1) / kPairs);
   const double block = width == 224 ? 0.22 + 0.06 * full : 0.147 + 0.08 * full;
-  return {Fp8Plan{false, width, most, 1, blocks, 0}, (width == 224 ? 6.7 : 5.4) + rounds * (blocks * block + 0.4)};
+  return {Fp8Plan{false, width, most, 1, blocks, 0}, (width == 224 ? 6.7 : 5.4) + rounds * (blocks * block + out)};
 }
 // Parts of K (a cluster's CTAs): how many clusters run at a time is what a GB300 of 152 multiprocessors reports.
 // A join's time goes by the tokens of a tile; by 4096 x 4096, one part and four: 16 tokens 7.6 and 5.4 us, 64
@@ -156,16 +160,19 @@ Fp8Plan plan_of(const Fp8Product &p) {
   const int each = p.by_k ? (int)((blocks + groups - 1) / groups) : blocks;
   const auto tiles = [](int64_t rows, int tile) { return (rows + tile - 1) / tile; };
   Choice best{};
-  for (int width : {224, 128}) {
-    const int64_t across = tiles(p.b.rows, width);
-    // a group's last tile is half empty on average
-    const double high = p.by_k ? (double)groups * tiles(p.a.rows, 256)
-                        : p.offsets ? p.a.rows / 256.0 + filled * 0.5
-                                    : (double)tiles(p.a.rows, 256);
-    const int64_t most = (p.by_k ? groups * tiles(p.a.rows, 256) : p.offsets ? p.a.rows / 256 + groups : tiles(p.a.rows, 256)) * across;
-    const Choice c = pair_choice(width, high * across, most, each);
-    if (width == 224 || c.us < best.us) best = c;
-  }
+  for (const bool turned : {false, true})
+    for (int width : {224, 128}) {
+      const int tile_a = turned ? width : 256;
+      const int64_t across = tiles(p.b.rows, turned ? 256 : width);
+      // a group's last tile is half empty on average
+      const double high = p.by_k ? (double)groups * tiles(p.a.rows, tile_a)
+                          : p.offsets ? p.a.rows / (double)tile_a + filled * 0.5
+                                      : (double)tiles(p.a.rows, tile_a);
+      const int64_t most = (p.by_k ? groups * tiles(p.a.rows, tile_a) : p.offsets ? p.a.rows / tile_a + groups : tiles(p.a.rows, tile_a)) * across;
+      Choice c = pair_choice(width, high * across, most, each, turned ? 0.4 : p.out_fmt == MCEMU_FP32 ? 1.1 : 0.55);
+      c.plan.turned = turned;
+      if (best.us == 0 || c.us < best.us) best = c;
+    }
   if (p.by_k) return best.plan;
   const int64_t across = tiles(p.b.rows, 128), mean = tiles(p.a.rows, (int)filled);
   for (int width : {16, 32, 64, 128}) {
@@ -203,6 +210,10 @@ int launch_fp8_product(const Fp8Product &given, bool a_rows, bool b_rows, void *
     if (rc != MCEMU_OK) return rc;                              // the operands would be whatever the workspace held
     if (!a_rows) p.a.q = to_a, p.a.ld = ld;
     if (!b_rows) p.b.q = to_b, p.b.ld = ld, p.b.stride = (int64_t)p.b.rows * ld;
+  }
+  if (plan.turned) {
+    std::swap(p.a, p.b);
+    p.turned = true;
   }
   return plan.few ? launch_fp8_few(p, plan, stream) : launch_fp8_pair(p, plan, stream);
 }

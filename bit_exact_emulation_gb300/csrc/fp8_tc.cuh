@@ -271,6 +271,13 @@ __device__ __forceinline__ void put_as(T *y, T v, int accumulate) {
 template <class T>
 __device__ __forceinline__ void put(T *y, float v, int accumulate) { put_as(y, from_f<T>(v), accumulate); }
 
+// One result to shared memory.
+template <class T>
+__device__ __forceinline__ void put_shared(uint32_t to, float sum) {
+  const T v = from_f<T>(sum);
+  if constexpr (sizeof(T) == 4) asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+  else asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(*(const uint16_t *)&v) : "memory");
+}
 // Eight sums, or four of fp32, as they lie in memory.
 template <class T>
 __device__ __forceinline__ uint4 pack16(const float *sum) {

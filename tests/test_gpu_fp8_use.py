@@ -442,3 +442,59 @@ def test_a_single_row_of_any_length_is_read_in_place(F, monkeypatch, M, N, K):
         offsets = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
         assert same(F.grouped_linear(x, ex, w[None], ew, offsets, out="fp32"), rounded(want, "fp32"))
     F.check()
+
+
+# Results leave in either of two directions, by whichever has fewer rounds of tiles: sizes of both, with whole
+# tiles and odd ones, in rows that the copy engine can write and in others.
+@pytest.mark.parametrize("M,N,K", [(4096, 4099, 300), (4099, 4096, 300), (1030, 8200, 200), (8200, 1030, 200), (2300, 2100, 1200)])
+@pytest.mark.parametrize("out,pad,lead", [("bf16", 0, 0), ("fp32", 5, 3), ("fp16", 16, 8), ("fp32", 8, 4)])
+def test_many_rows_in_both_directions(F, M, N, K, out, pad, lead):
+    g = gen(M + N + pad)
+    x, w = whole(g, (M, K), "e4m3"), whole(g, (N, K), "e5m2")
+    ex, ew = exps(g, M, blocks(K)), exps(g, blocks(N), blocks(K))
+    bias = torch.randint(-8, 9, (N + 1,), generator=g, device="cuda").float()[lead % 2:][:N]
+    y = strided(torch.full((M, N), 5.0, dtype=DT[out], device="cuda"), pad, lead)
+    product = of_rows(x, ex) @ of_tiles(w, ew).T
+    F.linear(x, ex, w, ew, bias=bias, out=out, y=y)
+    assert same(y.clone(), rounded(product + bias.double(), out))
+    if out == "fp32":
+        y.fill_(-3.0)
+        F.linear(x, ex, w, ew, out=out, y=y, accumulate=True)
+        assert same(y.clone(), rounded(product - 3, out))
+    F.check()
+
+
+@pytest.mark.parametrize("N,K", [(1000, 300), (2064, 200), (4099, 136)])
+@pytest.mark.parametrize("out,pad,lead", [("bf16", 0, 0), ("fp32", 5, 3), ("fp16", 16, 8), ("fp32", 0, 0)])
+def test_groups_of_many_rows_in_both_directions(F, N, K, out, pad, lead):
+    """Groups that end amid a tile, a piece or a row of one; what lies outside stays."""
+    T, offsets = 9000, [3, 1000, 1001, 1001, 3303, 5000, 8991]
+    E, g = len(offsets) - 1, gen(N + pad)
+    x, w = whole(g, (T, K), "e4m3"), whole(g, (E, N, K), "e4m3")
+    ex, ew = exps(g, T, blocks(K)), exps(g, E, blocks(N), blocks(K))
+    want = torch.full((T, N), 123.0, dtype=DT[out], device="cuda")
+    y = strided(want, pad, lead)
+    F.grouped_linear(x, ex, w, ew, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=out, y=y)
+    xv, wv = of_rows(x, ex), of_tiles(w, ew)
+    for i, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        want[a:b] = rounded(xv[a:b] @ wv[i].T, out)
+    assert same(y.clone(), want)
+    F.check()
+
+
+@pytest.mark.parametrize("N,K", [(2048, 1030), (1030, 2048), (515, 2300), (2300, 515)])
+@pytest.mark.parametrize("out,pad", [("fp32", 0), ("fp32", 3), ("bf16", 8), ("fp16", 1)])
+def test_weight_gradients_in_both_directions(F, N, K, out, pad):
+    T, offsets = 2000, [0, 700, 700, 701, 1500, 1990]
+    E, g = len(offsets) - 1, gen(N + K + pad)
+    o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    dy, x = (torch.randint(-2, 3, (T, n), generator=g, device="cuda").to(torch.bfloat16) for n in (N, K))
+    (_, _, dyt, edyt), (_, _, xt, ext) = (F.quantize(t, rows=False, columns=True, offsets=o) for t in (dy, x))
+    dW = strided(torch.full((E, N, K), 7.0, dtype=DT[out], device="cuda"), pad)
+    want = torch.stack([dy[a:b].double().T @ x[a:b].double() for a, b in zip(offsets, offsets[1:])])
+    F.grouped_wgrad(dyt, edyt, xt, ext, o, out=out, dW=dW)
+    assert same(dW.clone(), rounded(want, out))
+    if out == "fp32":
+        F.grouped_wgrad(dyt, edyt, xt, ext, o, dW=dW, accumulate=True)
+        assert same(dW.clone(), rounded(2 * want, out))
+    F.check()
