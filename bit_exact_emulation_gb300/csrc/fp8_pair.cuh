@@ -10,10 +10,11 @@
 // the issuing CTA takes a release at cluster scope, 0.95 us.)  Tensor memory has 512 columns: two sets of accumulators and two
 // of exponents (8 + 16 columns) leave BN at most 224.
 //
-// TURNED: the operands have changed places, so that a lane's row is a column of y. A piece of results then leaves as rows of 32
-// neighbours, 128 bytes in fp32, from any row on: groups that begin amid a tile of tokens need no other way out, and
-// only the pieces at their ends go by lanes.  Turned and not, microseconds: 16384 rows of 16 experts of 4096 x 2048 106 and 120,
-// weight gradients of 8 experts, 4096 x 2048 each in fp32, 120 and 131, 8192 x 8192 x 4096 183 and 190 under the power limit.
+// TURNED: the operands have changed places, so that a lane's row is a column of y.  A piece of results then leaves as
+// rows of 32 neighbours, 128 bytes in fp32, from any row on: groups that begin amid a tile of tokens need no other
+// way out, and only the pieces at their ends go by lanes.  Turned and not, us: 16384 rows of 16 experts of 4096 x 2048
+// 106 and 120, weight gradients of 8 experts, 4096 x 2048 each in fp32, 120 and 131, 8192 x 8192 x 4096 183 and 190,
+// all under the power limit.
 //
 // Bound by power where there is much work: 8192 x 8192 x 4096 takes 165 us in a burst (3.3 PFLOP/s), 177 to 193
 // under the 1.4 kW limit, at 1.5 GHz.  Of 177, copies without a use would take away 18, results without a
@@ -303,10 +304,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_lead(acc_empty + 8 * set);
       }
-      // Out through shared memory, where the copy engine takes over while the matrix unit goes on with both sets
-      // (weight gradients of 8 experts, 2048 x 4096 x 2048 each in fp32, 127 us; by the threads themselves 16 bytes of 32 rows at
-      // a time for every other piece 157, by rows 132; with larger pieces and fewer slots 130).  What the copy
-      // engine cannot write (rows that end a group amid the warp's, other alignments) leaves by rows.
+      // Out through shared memory, where the copy engine takes over while the matrix unit goes on with both sets (weight
+      // gradients of 8 experts, 2048 x 4096 x 2048 each in fp32, not TURNED, 127 us; by the threads themselves 16 bytes of 32
+      // rows at a time for every other piece 157, by rows 132; with larger pieces and fewer slots 130.  TURNED 114, by
+      // the threads themselves 119).  What the copy engine cannot write (rows that end a group amid the warp's, or TURNED
+      // amid a piece; other alignments) leaves by rows.
       constexpr int kPiece = S::kPieceBytes / sizeof(T), kVec = 16 / sizeof(T);
       const int row0 = r.a + (int)rank * 128 + (warp & 3) * 32, col0 = r.b + (warp >> 2) * kCols, z = p.by_k ? r.g : 0;
       const uint32_t place = out + warp * 32 * S::kPieceBytes;
