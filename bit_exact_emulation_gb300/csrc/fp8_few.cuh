@@ -224,8 +224,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // tokens share * o to share * (o + 1) - 1 are joined by CTA o, where part q's lie in places q * share and on;
       // a place has a token's 128 sums
       const int share = (r.n + (int)parts - 1) / (int)parts, mine_n = max(0, min(share, r.n - (int)rank * share));
-      if (turn && threadIdx.x < parts) boxes_left();             // what was sent last
-      if (threadIdx.x == 0) tc::mbar_expect(join_full, mine_n * parts * 512);
+      // Every CTA has taken what was sent last before anything is written over it (a push tells its arrival alone, to
+      // the CTA that it goes to), and before the barrier is told of the next: one that joins nothing would
+      // otherwise end two phases while a warp still waits for the first, and look as if it had ended none.
+      if (warp == 0) {
+        mbar_wait_warp_cluster(join_empty, (turn & 1) ^ 1, dead);
+        if (lane == 0) tc::mbar_expect(join_full, mine_n * parts * 512);
+      }
       asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
       for (int j = 0; j < BT; j++)
@@ -233,7 +238,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       tc::fence_async_smem();
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (warp == 0) {
-        tc::mbar_wait_warp(join_empty, (turn & 1) ^ 1, dead);    // what was sent last has been taken
         const int o = lane, n_o = min(share, r.n - o * share);
         if (o < (int)parts && n_o > 0 && !dead)
           bulk_push(at_rank(join + rank * share * 512, o), send + o * share * 512, n_o * 512, at_rank(join_full, o));
@@ -261,10 +265,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (lane < (int)parts) mbar_arrive_at(join_empty, lane);
     }
   }
-  if (warp == 0) boxes_left();                // lanes that sent
   __syncwarp();
   tc::fence_before();
-  tc::cluster_sync();                         // no CTA leaves while another pushes into it
+  tc::cluster_sync();                         // no CTA leaves before all have what was pushed
   if (warp == 5) {
     tc::fence_after();
     tc::tmem_free<1>(tmem, 512);

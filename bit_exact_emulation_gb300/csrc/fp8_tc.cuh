@@ -96,14 +96,14 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 // `bytes` of this CTA's shared memory to the address `to` in the cluster, counted on the barrier `bar` of the
-// same CTA; by one thread.
+// same CTA; by one thread.  That count is all that tells when the bytes have been read: the sender's own groups
+// (boxes_left) hold only copies without a barrier.
 __device__ __forceinline__ void bulk_push(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "r"(from),
                "r"(bytes), "r"(bar)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// Until all of the calling thread's boxes and pushes have left shared memory, or are written.
+// Until all of the calling thread's boxes have left shared memory, or are written.
 __device__ __forceinline__ void boxes_left() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void boxes_written() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Arrives on the barrier at the same offset in CTA `rank` of the cluster; what this thread has written is

@@ -14,6 +14,7 @@ std::map<const void *, size_t> sizes;
 std::vector<unsigned *> words;                 // symbols of four bytes
 int raise_after = -1;                          // the one that grows by one after the next copy from a symbol
 std::vector<std::string> launched;
+std::vector<std::pair<int, int>> shapes;       // of each launch: blocks along x, and to a cluster
 int fail_at = -1, pending = 0;                 // number of the launch that fails; the error not yet collected
 struct Config {
   dim3 grid, block;
@@ -21,8 +22,9 @@ struct Config {
   cudaStream_t st;
 } config;
 
-cudaError_t launch(const void *f) {
+cudaError_t launch(const void *f, unsigned blocks, unsigned cluster = 1) {
   launched.push_back(names[f]);
+  shapes.push_back({(int)blocks, (int)cluster});
   if ((int)launched.size() - 1 != fail_at) return cudaSuccess;
   return (cudaError_t)(pending = cudaErrorMemoryAllocation);
 }
@@ -30,9 +32,11 @@ CUresult encode(...) { return CUDA_SUCCESS; }
 }  // namespace
 
 extern "C" {
-void fake_reset(int fail) { launched.clear(), fail_at = fail, pending = 0; }
+void fake_reset(int fail) { launched.clear(), shapes.clear(), fail_at = fail, pending = 0; }
 int fake_launches() { return (int)launched.size(); }
 const char *fake_name(int i) { return launched[i].c_str(); }
+int fake_blocks(int i) { return shapes[i].first; }
+int fake_cluster(int i) { return shapes[i].second; }
 int fake_words() { return (int)words.size(); }
 void fake_raise(int i, int after) {
   if (after) raise_after = i;
@@ -61,9 +65,14 @@ cudaError_t __cudaGetKernel(cudaKernel_t *k, const void *f) {
   *k = (cudaKernel_t)f;
   return cudaSuccess;
 }
-cudaError_t __cudaLaunchKernel(cudaKernel_t k, dim3, dim3, void **, size_t, cudaStream_t) { return launch((const void *)k); }
-cudaError_t cudaLaunchKernel(const void *f, dim3, dim3, void **, size_t, cudaStream_t) { return launch(f); }
-cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *, const void *f, void **) { return launch(f); }
+cudaError_t __cudaLaunchKernel(cudaKernel_t k, dim3 g, dim3, void **, size_t, cudaStream_t) { return launch((const void *)k, g.x); }
+cudaError_t cudaLaunchKernel(const void *f, dim3 g, dim3, void **, size_t, cudaStream_t) { return launch(f, g.x); }
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const void *f, void **) {
+  unsigned cluster = 1;
+  for (unsigned i = 0; i < c->numAttrs; i++)
+    if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = c->attrs[i].val.clusterDim.x;
+  return launch(f, c->gridDim.x, cluster);
+}
 cudaError_t cudaGetLastError() {
   const int e = pending;
   pending = 0;

@@ -1,0 +1,32 @@
+"""The FP8 products on the GPU in each form that they take, at sizes that take it (tests/test_fp8_forms.py holds them to
+that), against plain implementations in 64 bits."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from test_fp8_forms import JOINS  # noqa: E402
+from test_gpu_fp8 import DT, F, blocks, exps, gen, of_rows, of_tiles, rounded, same, strided, whole  # noqa: E402,F401
+
+
+def offsets_of(counts):
+    return torch.tensor([0, *counts], device="cuda").cumsum(0).int()
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,N,K,tile,parts", JOINS, ids=str)
+def test_joins_of_several_units_to_a_cluster(F, rows, N, K, tile, parts, out):
+    """Every sum is different from its neighbours', and the same call gives the same bits."""
+    counts = [rows] if isinstance(rows, int) else rows
+    T, E, g = sum(counts), len(counts), gen(N + K)
+    x, w = (strided(whole(g, shape, "e4m3"), -K % 16) for shape in ((T, K), (E, N, K)))
+    ex, ew = exps(g, T, blocks(K)), exps(g, E, blocks(N), blocks(K))
+    o = offsets_of(counts)
+    call = ((lambda: F.linear(x, ex, w[0], ew[0], out=out)) if isinstance(rows, int) else
+            (lambda: F.grouped_linear(x, ex, w, ew, o, out=out)))
+    got = [call() for _ in range(6)]
+    xv, at = of_rows(x, ex), o.tolist()
+    want = torch.cat([rounded(xv[a:b] @ of_tiles(w[i], ew[i]).T, out) for i, (a, b) in enumerate(zip(at, at[1:]))])
+    for y in got:
+        assert same(y, want)
+    F.check()
