@@ -159,6 +159,8 @@ extern "C" int mcemu_fp8_grouped_wgrad(int P, int E, int N, int K, int dy_fmt, c
   if (lddyt < P || ldxt < P || ldedyt < blocks || ldext < blocks || lddw < K || (E > 1 && dw_stride < (N - 1) * lddw + K))
     return MCEMU_ERR_INVALID_ARG;
   if (!aligned(dW, bytes_of(out_fmt)) || !aligned(offsets, 4)) return MCEMU_ERR_ALIGNMENT;
+  lddyt = pitch_of(N, P, lddyt);
+  ldxt = pitch_of(K, P, ldxt);
   const bool dr = rows_of(dyt, lddyt), xr = rows_of(xt, ldxt);
   const int st = check_ws(workspace, ws_bytes, mcemu_fp8_grouped_wgrad_workspace(P, E, N, K, dr, xr));
   if (st != MCEMU_OK) return st;

@@ -100,3 +100,20 @@ def test_check_reports_each_wait_that_gave_up_once(L):
         L.fake_raise(i, 1)                         # grows after the first copy
         assert TIMEOUT in (L.mcemu_fp8_check(None), L.mcemu_fp8_check(None))
         assert L.mcemu_fp8_check(None) == OK
+
+
+@pytest.mark.parametrize("N,K,ldd,ldx", [(1, 32, 257, 256), (32, 1, 256, 257), (1, 1, 999, 257)])
+def test_single_columns_of_a_weight_gradient_are_read_in_place(L, N, K, ldd, ldx):
+    """A single row of an operand has no next one: its pointer decides, as in the other products.  Where that is
+    odd, the row is copied."""
+    def call(d, x, ws=0, nws=0):
+        L.fake_reset(-1)
+        st = L.mcemu_fp8_grouped_wgrad(256, 3, N, K, E4M3, d, ldd, P, 2, E4M3, x, ldx, P, 2, P, FP32, 0, P, K, N * K, ws, nws, None)
+        return st, [L.fake_name(i).decode() for i in range(L.fake_launches())]
+
+    assert L.mcemu_fp8_grouped_wgrad_workspace(256, 3, N, K, 1, 1) == 0
+    st, names = call(P, P)
+    assert st == OK and len(names) == 1 and "pair_kernel" in names[0]
+    assert call(P + 1, P) == (7, [])
+    st, names = call(P + 1, P, P, L.mcemu_fp8_grouped_wgrad_workspace(256, 3, N, K, 0, 1))
+    assert st == OK and len(names) == 2 and "align_kernel" in names[0]

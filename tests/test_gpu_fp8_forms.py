@@ -30,3 +30,21 @@ def test_joins_of_several_units_to_a_cluster(F, rows, N, K, tile, parts, out):
     for y in got:
         assert same(y, want)
     F.check()
+
+
+@pytest.mark.parametrize("N,K", [(1, 300), (300, 1), (1, 1)])
+def test_single_columns_of_a_weight_gradient_are_read_in_place(F, N, K):
+    """Of an operand of one row the leading dimension is that of no next row: any will do, without a workspace."""
+    T, g = 300, gen(N + K)
+    o = offsets_of([100, 0, 200])
+    dy, x = (torch.randint(-2, 3, (T, n), generator=g, device="cuda").bfloat16() for n in (N, K))
+    (_, _, dt, edt), (_, _, xt, ext) = (F.quantize(t, rows=False, columns=True, offsets=o) for t in (dy, x))
+    P, dW = dt.shape[1], torch.full((3, N, K), 7.0, device="cuda")
+    ld = lambda t: P + 1 if len(t) == 1 else P
+    st = F.lib().mcemu_fp8_grouped_wgrad(P, 3, N, K, F.FMT["e4m3"], dt.data_ptr(), ld(dt), edt.data_ptr(), P // 128, F.FMT["e4m3"],
+                                         xt.data_ptr(), ld(xt), ext.data_ptr(), P // 128, o.data_ptr(), F.FMT["fp32"], 0, dW.data_ptr(), K,
+                                         N * K, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    at = o.tolist()
+    assert same(dW, rounded(torch.stack([dy[a:b].double().T @ x[a:b].double() for a, b in zip(at, at[1:])]), "fp32"))
+    F.check()
