@@ -332,6 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
       if (row0 >= (TURNED ? p.a.rows : r.end) || dead) continue;
+      if (p.accumulate && r.k0 == r.k1) continue;      // nothing to add: even a zero would change -0 and, by the copy engine, subnormals
       if constexpr (TURNED) {
         T *y = (T *)p.y + z * p.stride_y + (int64_t)col0 * p.ldy + row0 + lane;
 #pragma unroll

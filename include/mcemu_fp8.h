@@ -109,7 +109,7 @@ size_t mcemu_fp8_grouped_linear_workspace(int T, int E, int N, int K, int x_rows
  * accumulate = 1, FP32 only).  dy and x are the columns that mcemu_fp8_quantize gives
  * with the same T, E and offsets: dyt [N][P], edyt [N][P/128], xt [K][P], ext [K][P/128],
  * P a multiple of 128.  dW [E][N][K] in FP32, FP16 or BF16, dw_stride elements between
- * matrices; a group without rows gets zeros (or keeps dW).  dy_rows, x_rows as above. */
+ * matrices; a group without rows gets zeros (accumulate = 1: keeps dW, bit for bit).  dy_rows, x_rows as above. */
 int mcemu_fp8_grouped_wgrad(int P, int E, int N, int K, int dy_fmt, const uint8_t *dyt, int64_t lddyt,
                             const int8_t *edyt, int64_t ldedyt, int x_fmt, const uint8_t *xt, int64_t ldxt,
                             const int8_t *ext, int64_t ldext, const int32_t *offsets, int out_fmt, int accumulate,

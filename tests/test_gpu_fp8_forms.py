@@ -48,3 +48,21 @@ def test_single_columns_of_a_weight_gradient_are_read_in_place(F, N, K):
     at = o.tolist()
     assert same(dW, rounded(torch.stack([dy[a:b].double().T @ x[a:b].double() for a, b in zip(at, at[1:])]), "fp32"))
     F.check()
+
+
+def test_a_group_without_rows_keeps_what_it_adds_to(F):
+    """To the last bit, negative zeros, subnormal numbers and NaNs' payloads too; in rows that the copy engine writes and in others."""
+    N, K, g = 264, 300, gen(11)
+    for lead, offsets in ((0, [0, 0, 200, 200, 200]), (0, [200, 200, 200, 200, 200]), (1, [0, 0, 77, 77, 200]), (0, [0, 130, 5, 130, 200])):
+        o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        dy, x = (torch.randint(-2, 3, (200, n), generator=g, device="cuda").bfloat16() for n in (N, K))
+        (_, _, dt, edt), (_, _, xt, ext) = (F.quantize(t, rows=False, columns=True, offsets=o) for t in (dy, x))
+        bits = torch.tensor([-2 ** 31, 1, -2 ** 31 + 5, 0x007FFFFF, 0x7FC00123, 0x7F800000, 0, 0x3F800000], dtype=torch.int32, device="cuda")
+        was = bits[torch.randint(0, 8, (4, N, K), generator=g, device="cuda")].view(torch.float32)
+        dW = strided(was, 0, lead)
+        F.grouped_wgrad(dt, edt, xt, ext, o, dW=dW, accumulate=True)
+        at = [max(offsets[:i + 1]) for i in range(5)]
+        for i, (a, b) in enumerate(zip(at, at[1:])):
+            if a == b:
+                assert torch.equal(dW[i].contiguous().view(torch.int32), was[i].view(torch.int32)), (offsets, i)
+    F.check()
