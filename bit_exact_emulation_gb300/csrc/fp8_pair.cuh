@@ -308,11 +308,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // gradients of 8 experts, 2048 x 4096 x 2048 each in fp32, not TURNED, 127 us; by the threads themselves 16 bytes of 32
       // rows at a time for every other piece 157, by rows 132; with larger pieces and fewer slots 130.  TURNED 114, by
       // the threads themselves 119).  What the copy engine cannot write (rows that end a group amid the warp's, or TURNED
-      // amid a piece; other alignments) leaves by rows.
+      // amid a piece; other alignments; the end of a row of y amid 16 bytes, which it fills with zeros to the end of
+      // them, beside y) leaves by rows.
       constexpr int kPiece = S::kPieceBytes / sizeof(T), kVec = 16 / sizeof(T);
       const int row0 = r.a + (int)rank * 128 + (warp & 3) * 32, col0 = r.b + (warp >> 2) * kCols, z = p.by_k ? r.g : 0;
       const uint32_t place = out + warp * 32 * S::kPieceBytes;
       const bool whole = boxes && (row0 + 32 <= r.end || r.end == p.a.rows);
+      const int row = TURNED ? p.a.rows : p.b.rows, inside = row * (int64_t)sizeof(T) % 16 ? row : INT32_MAX;     // of y
       if constexpr (TURNED) {                 // a lane's row of a is a column of y
         if (p.bias) {
           const float b = row0 + lane < p.a.rows ? __ldg(p.bias + row0 + lane) : 0.f;
@@ -338,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int j = 0; j < kCols; j += kPiece) {
           if (col0 + j >= r.end) break;
-          if (boxes && (col0 + j + kPiece <= r.end || r.end == p.b.rows)) {
+          if (boxes && row0 + 32 <= inside && (col0 + j + kPiece <= r.end || r.end == p.b.rows)) {
             if (lane == 0) boxes_left();
             __syncwarp();
 #pragma unroll
@@ -366,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                        "r"(v.y), "r"(v.z), "r"(v.w)
                        : "memory");
         }
-        if (whole) {
+        if (whole && col0 + j + kPiece <= inside) {
           tc::fence_async_smem();
           __syncwarp();
           if (lane == 0) box_store(&my, place, col0 + j, row0, z, p.accumulate);

@@ -79,7 +79,8 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
   return a;
 }
 // A box of shared memory to global memory, or added to what is there (fp32); by one thread, which also counts
-// them in groups.  What lies outside the tensor is not written.
+// them in groups.  Rows outside the tensor are not written; a row is, with zeros, up to the end of its last 16 bytes, which
+// is for the caller to avoid.
 __device__ __forceinline__ void box_store(const CUtensorMap *map, uint32_t from, int x, int y, int z, bool add) {
   if (add)
     asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),

@@ -74,3 +74,45 @@ def test_joins_take_several_units_to_a_cluster(L, rows, N, K, tile, parts, out):
     got = linear(L, rows, N, K, out) if isinstance(rows, int) else grouped(L, sum(counts), len(counts), N, K, out)
     assert got[:2] == ("few", tile) and got[3] == parts
     assert sum(-(-n // tile) for n in counts) * blocks(N) > got[4]
+
+
+# Pairs of CTAs: rows of b to a tile, operands exchanged or not.  With fewer tiles than pairs and with several to each; sums of
+# one run of 1024 along k and of more.
+LINEAR_PAIRS = [(104, 101, 2409, 128, True), (300, 700, 3000, 128, True), (2405, 924, 4534, 128, True), (3328, 1400, 4742, 128, False),
+                (2738, 1313, 1346, 224, False), (918, 4147, 1390, 224, False), (4096, 4099, 1300, 224, False), (562, 4019, 802, 224, True),
+                (2845, 2490, 412, 224, True), (2300, 2100, 2400, 224, True)]
+# Of grouped rows: offsets, which leave rows outside, T, N, K.
+GROUPED_PAIRS = [([1, 120, 120, 299], 300, 700, 3000, 128, True), ([0, 5, 60, 61, 61, 200, 260, 261, 400, 426], 426, 2173, 211, 128, True),
+                 ([3, 2200, 2201, 6400, 8471], 8471, 269, 1543, 224, False), ([0, 900, 900, 901, 1300, 1301, 1700, 2100, 2300, 2450], 2458, 1037, 1392, 224, False),
+                 ([7, 1000, 1400, 1400, 2700, 2704, 3900, 4500, 4660], 4672, 408, 791, 224, True),
+                 ([3, 1000, 1001, 1001, 3303, 5000, 8991], 9000, 2064, 1300, 224, True), ([0, 700, 2000, 2000, 4099, 7777, 9000], 9000, 4099, 1100, 224, True)]
+# Weight gradients: T, groups, N, K.
+WGRAD_PAIRS = [(231, 9, 1146, 101, 128, False), (328, 4, 187, 2432, 128, False), (107, 2, 110, 114, 128, True), (107, 6, 129, 1563, 128, True),
+               (5018, 5, 237, 1935, 224, False), (4978, 7, 2495, 273, 224, False), (2306, 5, 129, 1964, 224, True), (247, 9, 799, 874, 224, True)]
+# Results that pairs of this form give in 16 bits alone: in fp32 a few rows' form takes the call.
+SHORT = (3328, 1400, 4742)
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+def test_pairs_take_the_sizes_of_their_tests(L, out):
+    for M, N, K, tile, turned in LINEAR_PAIRS:
+        if (M, N, K) != SHORT or out != "fp32":
+            assert linear(L, M, N, K, out)[:3] == ("pair", tile, turned), (M, N, K)
+    for offsets, T, N, K, tile, turned in GROUPED_PAIRS:
+        assert grouped(L, T, len(offsets) - 1, N, K, out)[:3] == ("pair", tile, turned), (offsets, N, K)
+    for T, E, N, K, tile, turned in WGRAD_PAIRS:
+        L.fake_reset(-1)
+        C = fp8.columns(T, E)
+        got = last(L, L.mcemu_fp8_grouped_wgrad(C, E, N, K, E4M3, P, C, P, C // 128, E4M3, P, C, P, C // 128, P, FMT[out], 0, P, K, N * K, *WS, None))
+        assert got[:3] == ("pair", tile, turned), (T, E, N, K)
+
+
+# Products whose sums are held against the emulated unit's: M, N, K, kernel, tile, CTAs that share K.
+SUMS = [(7, 300, 9000, "few", 16, 8), (20, 200, 3000, "few", 32, 6), (40, 200, 5000, "few", 64, 7), (600, 200, 2100, "few", 128, 1),
+        (104, 101, 2409, "pair", 128, 1), (300, 700, 3000, "pair", 128, 1), (2738, 1313, 1346, "pair", 224, 1), (2300, 2100, 2400, "pair", 224, 1)]
+
+
+@pytest.mark.parametrize("M,N,K,kernel,tile,parts", SUMS)
+def test_sums_are_cut_as_their_test_says(L, M, N, K, kernel, tile, parts):
+    got = linear(L, M, N, K, "fp32")
+    assert got[:2] == (kernel, tile) and got[3] == parts

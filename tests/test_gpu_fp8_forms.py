@@ -6,7 +6,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from test_fp8_forms import JOINS  # noqa: E402
-from test_gpu_fp8 import DT, F, blocks, exps, gen, of_rows, of_tiles, rounded, same, strided, whole  # noqa: E402,F401
+from test_gpu_fp8 import DT, F, blocks, exps, gen, of_rows, of_tiles, raw, rounded, same, strided, whole  # noqa: E402,F401
 
 
 def offsets_of(counts):
@@ -65,4 +65,55 @@ def test_a_group_without_rows_keeps_what_it_adds_to(F):
         for i, (a, b) in enumerate(zip(at, at[1:])):
             if a == b:
                 assert torch.equal(dW[i].contiguous().view(torch.int32), was[i].view(torch.int32)), (offsets, i)
+    F.check()
+
+
+# Rows of y that begin on 16-byte boundaries and end between two, in products by pairs of CTAs and by single ones.
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(104, 97, 2409), (104, 101, 2409), (104, 103, 2409), (2738, 1313, 1346), (918, 4147, 1390), (562, 4019, 802),
+                                   (5, 203, 700), (300, 230, 400)])
+def test_nothing_is_written_beside_a_row_that_ends_between_boundaries(F, M, N, K, out):
+    g = gen(M + N)
+    x, w = (strided(whole(g, (r, K), "e4m3"), -K % 16) for r in (M, N))
+    ex, ew = exps(g, M, blocks(K)), exps(g, N, blocks(K))
+    product = of_rows(x, ex) @ of_rows(w, ew).T
+    # subnormal numbers beside the rows, which even a zero added by the copy engine would change
+    buf = torch.full((M + 2, -(-N // 8) * 8 + 8), 2.0 ** -24 if out == "fp16" else 2.0 ** -130, device="cuda").to(DT[out])
+    was = buf.clone()
+    y = buf[1:M + 1, :N]
+    for accumulate in (False, True) if out == "fp32" else (False,):
+        y.fill_(3.0)
+        F.linear(x, ex, w, ew, out=out, y=y, accumulate=accumulate)
+        assert same(y.contiguous(), rounded(product + 3.0 * accumulate, out))
+        y.copy_(was[1:M + 1, :N])
+        assert same(buf, was)
+    offsets, E = [0, M // 3, M // 3, M], 3
+    o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    w = strided(torch.stack([raw(w)] * E).view(w.dtype), -K % 16)
+    tiles = exps(g, E, blocks(N), blocks(K))
+    F.grouped_linear(x, ex, w, tiles, o, out=out, y=y)
+    for i, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        assert same(y[a:b].contiguous(), rounded(of_rows(x, ex)[a:b] @ of_tiles(w[i], tiles[i]).T, out))
+    y.copy_(was[1:M + 1, :N])
+    assert same(buf, was)
+    F.check()
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,N,K", [(200, 107, 113), (300, 129, 1563), (2000, 799, 874), (900, 264, 1)])
+def test_nothing_is_written_beside_the_rows_of_a_weight_gradient(F, T, N, K, out):
+    g, offsets = gen(T + N), [0, T // 2, T // 2, T - 7, T]
+    o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    dy, x = (torch.randint(-2, 3, (T, n), generator=g, device="cuda").bfloat16() for n in (N, K))
+    (_, _, dt, edt), (_, _, xt, ext) = (F.quantize(t, rows=False, columns=True, offsets=o) for t in (dy, x))
+    want = torch.stack([dy[a:b].double().T @ x[a:b].double() for a, b in zip(offsets, offsets[1:])])
+    buf = torch.full((4, N + 2, -(-K // 8) * 8 + 8), 2.0 ** -24 if out == "fp16" else 2.0 ** -130, device="cuda").to(DT[out])
+    was = buf.clone()
+    dW = buf[:, 1:N + 1, :K]
+    for accumulate in (False, True) if out == "fp32" else (False,):
+        dW.fill_(3.0)
+        F.grouped_wgrad(dt, edt, xt, ext, o, out=out, dW=dW, accumulate=accumulate)
+        assert same(dW.contiguous(), rounded(want + 3.0 * accumulate, out))
+        dW.copy_(was[:, 1:N + 1, :K])
+        assert same(buf, was)
     F.check()
