@@ -6,7 +6,8 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from test_fp8_forms import GROUPED_PAIRS, JOINS, LINEAR_PAIRS, SHORT, SUMS, WGRAD_PAIRS  # noqa: E402
-from test_gpu_fp8 import CODE, DT, F, blocks, exps, gen, of_rows, of_tiles, raw, rounded, same, strided, whole  # noqa: E402,F401
+from test_gpu_fp8 import CODE, DT, F, blocks, columns_host, exps, gen, of_rows, of_tiles, raw, rounded, rows_host, same  # noqa: E402,F401
+from test_gpu_fp8 import strided, values, whole  # noqa: E402
 
 
 def offsets_of(counts):
@@ -282,3 +283,35 @@ def test_sums_are_the_emulated_units_of_one_cut(F, fx, fw, M, N, K, kernel, tile
             part = part + run(b, min(b + length, a + per, blocks(K)))
         total = total + part
     assert torch.equal(y[r][:, c], total)
+
+
+# Columns of more tiles of 128 x 128 than blocks of threads run at a time, so that each takes several: in fp32 one after the other
+# along the rows and on to the next 128 places (304 blocks of threads), in 16 bits blocks of columns apart (from 1824 tiles on).  Rows of whole
+# vectors and odd ones; groups of all sizes, some empty, rows outside them.
+@pytest.mark.parametrize("fmt,out,T,H", [("fp32", "e4m3", 3000, 4096), ("fp32", "e5m2", 3000, 4099), ("fp32", "e4m3", 40000, 130), ("bf16", "e4m3", 4500, 7168),
+                                         ("fp16", "e4m3", 4500, 7171), ("bf16", "e5m2", 30000, 1026)])
+@pytest.mark.parametrize("ragged", [True, False])
+def test_columns_of_more_tiles_than_run_at_a_time(F, fmt, out, T, H, ragged):
+    x = values(T + H, T, H, fmt)
+    offsets = [T // 9, T // 9, T // 9 + 1, T // 5, T // 5 + 128, T // 2, T // 2, T // 2 + 300, T - 200] if ragged else None
+    o = torch.tensor(offsets, dtype=torch.int32, device="cuda") if ragged else None
+    P = F.columns(T, len(offsets) - 1 if ragged else 1)
+    assert P // 128 * blocks(H) >= 2 * (304 if fmt == "fp32" else 912)
+    qt0, et0 = columns_host(x, out, offsets)
+    q0, e0 = rows_host(x, out)
+    x = x.cuda()
+    for rows in (True, False):
+        q, e, qt, et = F.quantize(x, out=out, rows=rows, columns=True, offsets=o)
+        assert torch.equal(et.cpu(), et0) and same(qt.cpu(), qt0)
+        assert not rows or (torch.equal(e.cpu(), e0) and same(q.cpu(), q0))
+
+
+@pytest.mark.parametrize("less", [0, 3])
+def test_rows_longer_than_two_dimensions_of_a_grid_hold(F, less):
+    """65535 times sixteen blocks of 128 and more, against the same numbers in shorter rows."""
+    H = 65535 * 2048 + 3 * 2048 + 5 * 128
+    x = (torch.randn(H, generator=gen(less), device="cuda") * torch.exp2((torch.arange(H, device="cuda") // 128 % 19).float())).bfloat16()
+    x[H - less:] = 0
+    q, e, _, _ = F.quantize(x[None, :H - less])
+    q0, e0, _, _ = F.quantize(x.view(-1, 128))
+    assert torch.equal(e[0], e0[:, 0]) and torch.equal(raw(q)[0], raw(q0).view(-1)[:H - less])
