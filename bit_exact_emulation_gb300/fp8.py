@@ -133,7 +133,7 @@ def columns(T: int, groups: int = 1) -> int:
 
 
 def quantize(x, out: str = "e4m3", rows: bool = True, columns: bool = False, offsets=None, q=None, e=None, qt=None, et=None):
-    """(q, e, qt, et) of x [T, H]; what is not asked for is None.
+    """(q, e, qt, et) of x [T, H], H at least 1; what is not asked for is None.
 
     ``rows``: q [T, H] and e [T, ceil(H / 128)], blocks of 128 along each row.
     ``columns``: the transposed codes qt [H, P] and et [H, P / 128], blocks of 128 rows of each

@@ -47,7 +47,7 @@ extern "C" {
  * even).  A block of zeros has e = -120.  A block that holds a NaN or an infinity
  * has e = MCEMU_FP8_NAN and codes 0x7F (NaN).
  *
- * x [T][H] in fmt (FP16, BF16 or FP32).
+ * x [T][H] in fmt (FP16, BF16 or FP32), H >= 1.
  * Rows (q and e, both NULL when not wanted): q [T][H], e [T][ceil(H / 128)], blocks
  * of 128 along a row.
  * Columns (qt and et, both NULL when not wanted): the transposed matrix qt [H][P],
@@ -78,10 +78,13 @@ int mcemu_fp8_quantize_weight(int fmt, int out_fmt, int E, int N, int K, const v
  * w_tiles = 1 (ew[n/128][k/128]), [N][ceil(K/128)] with 0 (ew[n][k/128]).  Products
  * are exact; the matrix unit adds up runs of whole blocks, at most 512 along k (few
  * rows) or 1024 (many), with the sums of the emulated unit MCEMU_PRESET_B200_FP8, bit for
- * bit where the exponents are 0; the runs are added in fp32, in an order that goes by the
- * sizes alone, then bias (fp32, may be NULL), and the result is rounded once to out_fmt (FP16, BF16 or FP32).  accumulate = 1: the sum is added to y
- * (FP32 only, without bias; where the copy engine adds, numbers below 2^-126 count as
- * zeros).  K = 0 gives sums of 0.
+ * bit where the exponents are 0; the runs are added in fp32, then bias (fp32, may be
+ * NULL), and the result is rounded once to out_fmt (FP16, BF16 or FP32).  How K is cut
+ * into runs, and their order, go by the sizes, the width of the results, whether rows
+ * are grouped and the device's number of multiprocessors, and by nothing else: a
+ * 16-bit result need not be the fp32 call's, rounded.  accumulate = 1: the sum is added
+ * to y (FP32 only, without bias; where the copy engine adds, numbers below 2^-126 count
+ * as zeros).  K = 0 gives sums of 0.
  *   forward            x = activations' rows, w = weight's blocks
  *   input's gradient   x = dY's rows, w = the weight's transposed blocks
  *   weight's gradient  x = dY's columns, w = the activations' columns, w_tiles = 0

@@ -116,3 +116,14 @@ SUMS = [(7, 300, 9000, "few", 16, 8), (20, 200, 3000, "few", 32, 6), (40, 200, 5
 def test_sums_are_cut_as_their_test_says(L, M, N, K, kernel, tile, parts):
     got = linear(L, M, N, K, "fp32")
     assert got[:2] == (kernel, tile) and got[3] == parts
+
+
+def test_the_form_goes_by_more_than_sizes(L):
+    """By the width of the results and by groups, as the header says."""
+    M, N, K = SHORT
+    assert linear(L, M, N, K, "bf16")[0] == linear(L, M, N, K, "fp16")[0] == "pair" and linear(L, M, N, K, "fp32")[0] == "few"
+    assert linear(L, 300, 700, 3000)[0] == "pair" and grouped(L, 300, 9, 700, 3000)[0] == "few"
+    for out in ("bf16", "fp32"):                     # not by strides, addresses or what y holds
+        forms = {linear(L, 300, 700, 3000, out, ldy=ldy)[:4] for ldy in (700, 701, 704)}
+        assert len(forms) == 1
+    assert linear(L, 300, 700, 3000, "fp32", acc=1) == linear(L, 300, 700, 3000, "fp32")
