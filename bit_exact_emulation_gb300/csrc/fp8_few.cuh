@@ -9,7 +9,7 @@
 // than 32 tokens a cluster that shares K has one unit, whose sums leave through the stages' memory.
 //
 // Bound by HBM where there are weights enough: 128 rows through 32 experts of 2048 x 4096 take 43.7 us (6.1 TB/s, 0.89 of
-// the measured rate).  One token by 4096 x 4096 takes 5.1 us, 2.5 of them for the bytes: setting up (barriers,
+// the measured rate).  One token by 4096 x 4096 takes 5.0 us, 2.5 of them for the bytes: setting up (barriers,
 // tensor memory, a cluster's meeting), one memory latency, the join and the parting take 2000 cycles each or less.
 #pragma once
 #include "fp8_tc.cuh"

@@ -12,14 +12,18 @@
 //
 // TURNED: the operands have changed places, so that a lane's row is a column of y.  A piece of results then leaves as
 // rows of 32 neighbours, 128 bytes in fp32, from any row on: groups that begin amid a tile of tokens need no other
-// way out, and only the pieces at their ends go by lanes.  Turned and not, us: 16384 rows of 16 experts of 4096 x 2048
-// 106 and 120, weight gradients of 8 experts, 4096 x 2048 each in fp32, 120 and 131, 8192 x 8192 x 4096 183 and 190,
-// all under the power limit.
+// way out, and only the pieces at their ends go by lanes.  Turned and not, us, a few launches and under the power limit:
+// 16384 rows of 16 experts of 4096 x 2048 99 and 105, 114 and 120; weight gradients of 8 experts, 4096 x 2048 each in
+// fp32, 113 and 123, 124 and 131; 8192 x 8192 x 4096 163 and 165, 187 and 190.
 //
-// Bound by power where there is much work: 8192 x 8192 x 4096 takes 165 us in a burst (3.3 PFLOP/s), 177 to 193
+// Bound by power where there is much work: 8192 x 8192 x 4096 takes 163 us in a burst (3.4 PFLOP/s), 177 to 193
 // under the 1.4 kW limit, at 1.5 GHz.  Of 177, copies without a use would take away 18, results without a
 // place 20, both 28; two warps that issue in place of one took away 40, copies by two whole warps in place of a
 // lane 15.  A library's product with a scale for each 32 of k, measured beside it: 172.
+//
+// Weight gradients of few rows an expert wait for their way out: for 8 experts of 4096 x 2048 in fp32, 16 rounds of tiles,
+// 8192, 16384 and 32768 rows take 77, 113 and 190 us, so that a block of a tile takes 0.29 us and no blocks at all 40, as long
+// as HBM takes for the 268 MB (28 with results in bf16).  A tile's two chunks are too little to hide them behind.
 #pragma once
 #include "fp8_tc.cuh"
 
@@ -305,9 +309,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (lane == 0) tc::mbar_arrive_lead(acc_empty + 8 * set);
       }
       // Out through shared memory, where the copy engine takes over while the matrix unit goes on with both sets (weight
-      // gradients of 8 experts, 2048 x 4096 x 2048 each in fp32, not TURNED, 127 us; by the threads themselves 16 bytes of 32
-      // rows at a time for every other piece 157, by rows 132; with larger pieces and fewer slots 130.  TURNED 114, by
-      // the threads themselves 119).  What the copy engine cannot write (rows that end a group amid the warp's, or TURNED
+      // gradients of 8 experts, 2048 x 4096 x 2048 each in fp32: not TURNED by the threads themselves 16 bytes of 32 rows at a
+      // time for every other piece 1.24 of its time, by rows 1.04, with larger pieces and fewer slots 1.02; TURNED by the
+      // threads themselves 1.04).  What the copy engine cannot write (rows that end a group amid the warp's, or TURNED
       // amid a piece; other alignments; the end of a row of y amid 16 bytes, which it fills with zeros to the end of
       // them, beside y) leaves by rows.
       constexpr int kPiece = S::kPieceBytes / sizeof(T), kVec = 16 / sizeof(T);

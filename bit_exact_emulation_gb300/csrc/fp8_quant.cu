@@ -1,8 +1,10 @@
 // fp8_quant.cu -- FP8 operands with a power-of-two scale for each block of 128 (include/mcemu_fp8.h).
 //
 // Bound by HBM: 3 bytes an element from bf16, 4 where the transposed codes are wanted too; both
-// come from one reading.  8192 x 8192 bf16: rows 33 us (6.0 TB/s), rows and columns 49.8 us (5.4), weights
-// both ways 42.0 us (6.4, 0.94 of the measured rate); instructions issue in 0.63 of the cycles.
+// come from one reading.  8192 x 8192 bf16: rows 33 us (6.0 TB/s), rows and columns 46.4 us (5.8), of 8
+// groups 49.6 us (5.4; instructions issue in 0.63 of the cycles), weights both ways 42.0 us (6.4, 0.94 of the measured rate).
+// fp32, 8192 x 4096: rows 26.3 us, rows and columns 40.5 (5.0): a tile is 64 registers of a thread, so that 128 hold two blocks of
+// threads an SM and a few words spill, and nothing is asked for ahead.
 #include "fp8.h"
 #include "ops_common.cuh"
 
@@ -220,7 +222,7 @@ __device__ __forceinline__ void load_tile(Vec<T, 8> (&v)[8], const T *x, int64_t
   }
 }
 // The same of 16-bit elements by copies into places of the thread's own, which are under way while it works on
-// the tile before (loaded when they are needed, 8192 x 8192 took 53.1 us in place of 49.8).
+// the tile before (loaded when they are needed, 8192 x 8192 in 8 groups took 53.1 us in place of 49.8).
 template <class T>
 __device__ __forceinline__ void ask_tile(uint4 *places, const T *x, int64_t ld, int rows, int c, int H) {
   const int r0 = 8 * (threadIdx.x >> 4);
@@ -375,7 +377,7 @@ __device__ __forceinline__ uint32_t column_peak(const Vec<T, 8> (&v)[8]) {
 
 // Columns, and with a.q rows.  Of 16-bit elements a block of threads takes one block of 128 places and every gridDim.y-th
 // block of columns; of fp32 (ALONG) as many tiles as every other, one after the other along the rows: 8192 x 4096 in
-// fp32 40.0 us, by the former way 52.8; bf16 8192 x 8192 50.7, by the former 46.5.  Rows outside all groups (rarely any)
+// fp32 40.0 us, by the former way 52.8; bf16 8192 x 8192, without groups as before, 50.7, by the former 46.5.  Rows outside all groups (rarely any)
 // are dealt out over the blocks for their row codes.
 template <class T, class F, bool WIDE>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) columns_kernel(const QuantArgs a, int64_t tiles) {
@@ -513,7 +515,7 @@ int quantize_typed(const QuantArgs &a, cudaStream_t st) {
     grid = dim3((unsigned)(tiles < most ? tiles : most));
   } else {
     // two rounds of the blocks of threads that run at a time, with so many tiles each, one's copies under way while
-    // the one before is worked on.  8192 x 8192: tiles each and microseconds 2 49.7, 4 49.8, 5 49.3, 8 55.2, 10 60.1.
+    // the one before is worked on.  8192 x 8192 in 8 groups: tiles each and microseconds 2 49.7, 4 49.8, 5 49.3, 8 55.2, 10 60.1.
     int64_t turns = tiles / (6 * sm_count());
     turns = turns < 1 ? 1 : turns < blocks ? turns : blocks;
     const int64_t across = (blocks + turns - 1) / turns;
